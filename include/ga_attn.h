@@ -102,8 +102,10 @@ unsigned long long ga_debug_cuda_calls(void);
 
 /* Reads the current device's status word, written by kernels whose bounded waits gave
  * up or whose inputs failed a device-side check (0 = no error, 1 = wait timeout, 2 = bad
- * launch configuration, 3 = a page-table entry outside the page pool, see
- * ga_attn_verify_paged). Synchronises the device. clear != 0 resets the word afterwards. */
+ * launch configuration, 3 = a page-table entry or slot outside the page pool, see
+ * ga_attn_verify_paged and ga_kv_quantize_q4, 4 = a rotary position outside the table or a
+ * cached length outside the page table, see ga_qk_prologue_axes and ga_attn_verify_q4).
+ * Synchronises the device. clear != 0 resets the word afterwards. */
 int ga_device_status(int* status_out, int clear);
 
 /* Test hook for failure detection (no counterpart in the pages): launches a one-thread
@@ -495,6 +497,148 @@ int ga_attn_prefill_batch(const ga_bf16* qg, const int* row_start, const int* q_
                           int page_size, const int* page_table, int max_pages,
                           const ga_bf16* w_q, const ga_bf16* cos_tab, const ga_bf16* sin_tab,
                           int table_rows, ga_bf16* out, ga_stream stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Serving over a 4-bit paged cache, with every length on the device. The pages have no
+ * counterpart beyond paged caches and decode (pegainfer PR #1151, §Summary and §Limits); the
+ * calls below are additions. One step of a server is
+ *   ga_page_plan          pages, slots and positions of the step's tokens
+ *   ga_qk_prologue_axes   their prepared keys and queries
+ *   ga_kv_quantize_q4     their keys and values into the cache
+ *   ga_attn_verify_q4     attention of every sequence's window over its cache
+ * and reads no length on the host, so it can be captured once and replayed as they change.
+ * ------------------------------------------------------------------------------------------ */
+
+#define GA_PLAN_MAX_SEQ 2048 /* sequences of one ga_page_plan call */
+#define GA_Q4_PAGE_TOKENS 32 /* pages of a 4-bit cache hold a multiple of this many tokens */
+#define GA_Q4_ROW_BYTES 128  /* code bytes of one (token, KV head) row of 256 values */
+#define GA_Q4_SCALE_BYTES 16 /* scale bytes of one row */
+
+/* Page tables, slot maps and positions of one step, from the sequences' lengths. Sequence b
+ * holds held[b] pages (page_table row b, columns 0 .. held[b] - 1) and seq_len[b] cached
+ * tokens, and adds new_len[b] tokens at positions seq_len[b] ..:
+ *   new_len[b] >= 0, seq_len[b] >= 0: it needs ceil((seq_len + new_len) / page_size) pages; those
+ *           it lacks are taken from the top of the stack of free pages, in order of sequence and
+ *           then of page (the i-th is free_pages[count - 1 - i]), and appended to its row
+ *   new_len[b] < 0:  it is finished: its held pages go back on the stack, on top of what the step
+ *           left, in order of sequence and then of column, and it holds none. (Pages that other
+ *           rows share must not be given back this way.)
+ *   seq_len[b] < 0 (and new_len[b] >= 0): the row is unused and left as it is
+ * All arrays are DEVICE int32:
+ *   seq_len, new_len, held [n_seq]; page_table [n_seq][max_pages], updated in place
+ *   held_out [n_seq], may be held itself
+ *   free_pages [n_free]: the stack, n_free the pages of the pool; free_count [1]: pages on it;
+ *           free_count_out [1], may be free_count itself
+ *   pos_delta NULL or [n_seq]: added to the positions of sequence b's tokens (text after images
+ *           sits at other rotary positions than cache slots)
+ *   row_start [n_seq + 1]: packed row of each sequence's first new token; the last is the total
+ *   slot_map [max_tokens]: packed token t's cache slot, page * page_size + offset; -1 from the
+ *           total on
+ *   positions NULL or [max_tokens]: packed token t's position (seq_len + index + pos_delta); 0
+ *           from the total on
+ *   info    [4]: status, tokens, pages taken, pages given back. Status 0: done; 1: more than
+ *           max_tokens tokens; 2: a sequence past max_pages * page_size or GA_MAX_TOKENS; 3: not
+ *           enough free pages; 4: held or free_count out of range, or more pages given back than
+ *           the stack has room for. When it is not 0 nothing is planned: page_table and
+ *           free_pages keep their contents, held_out and free_count_out are copies, row_start
+ *           and the totals are 0, every slot is -1.
+ * Other than those pairs, no output may overlap an input or another output. The call takes one
+ * launch up to 8,192 slots, two above.
+ * Rules: 0 <= n_seq <= GA_PLAN_MAX_SEQ, page_size >= 1, 1 <= max_pages, max_pages * page_size
+ * < 2^31, n_free * page_size < 2^31, 0 <= max_tokens < 2^30; every array 4-byte aligned. With
+ * n_seq = 0, row_start, slot_map, positions and info are still written.
+ * Errors: NULL, SHAPE, RANGE, ALIGN, DEVICE, CUDA. */
+int ga_page_plan(const int* seq_len, const int* new_len, int n_seq, int page_size,
+                 int* page_table, int max_pages, const int* held, int* held_out, int* free_pages,
+                 int n_free, const int* free_count, int* free_count_out, const int* pos_delta,
+                 int max_tokens, int* row_start, int* slot_map, int* positions, int* info,
+                 ga_stream stream);
+
+/* ga_qk_prologue with positions from device memory, on up to four axes (time, height and width
+ * of image and video tokens; all axes alike for text): rotary pair i (dims i and i + 32) of
+ * token t turns by the angle of position positions[axis][t], axis = pair_axis[i]. The rounding
+ * points are ga_qk_prologue's, and so are the bits where a token's positions are all the same.
+ *   k_raw, w_k, k_prep  as in ga_qk_prologue, for n_tok tokens; or all three NULL
+ *   qg, w_q, q_prep     as in ga_qk_prologue, for the same n_tok tokens; or all three NULL
+ *   positions DEVICE int32 [n_axes][ld_pos], 4-byte aligned; ld_pos >= n_tok. A position outside
+ *             0 .. table_rows - 1 is not a fault: status 4 is recorded (ga_device_status) and
+ *             the pair turns by position 0.
+ *   pair_axis HOST array of 32 bytes, each below n_axes (contiguous or interleaved sections)
+ *   cos_tab, sin_tab [table_rows][32]
+ * Rules: 1 <= n_axes <= 4, 0 <= n_tok <= GA_MAX_TOKENS, table_rows >= 1; no output may overlap an
+ * input or the other output.
+ * Errors: NULL, SHAPE, RANGE, TABLE (table_rows < 1), ALIGN, DEVICE, CUDA. */
+int ga_qk_prologue_axes(const ga_bf16* k_raw, const ga_bf16* w_k, ga_bf16* k_prep,
+                        const ga_bf16* qg, const ga_bf16* w_q, ga_bf16* q_prep, int n_tok,
+                        const int* positions, long long ld_pos, int n_axes,
+                        const uint8_t* pair_axis, const ga_bf16* cos_tab, const ga_bf16* sin_tab,
+                        int table_rows, ga_stream stream);
+
+/* 4-bit cache rows. A row of 256 values has 16 groups of 16; a group's scale is
+ *   s = fp32(max|x| / 7), clamped to [2^-20, 3840] and rounded to 4 significant bits (ties to
+ *       even), stored as the byte 8 E + m for s = 2^(E - 20) (1 + m / 8)
+ * and a value's code is clamp(round(x / s), -8, 7) + 8 (ties to even), 4 bits. The widened value
+ * (code - 8) * s is a bf16 value exactly. A NaN is stored as 0; values beyond the largest scale's
+ * reach saturate. Any bytes are finite rows, so hidden positions need no initial contents.
+ * Eight dims make a little-endian 32-bit word: bits 4p .. 4p+3 hold dim 2p for p < 4, dim
+ * 2(p - 4) + 1 for p >= 4. Pools, per keys and values:
+ *   codes   [n_pages][2][page_size][128] uint8, 16-byte aligned (head-major within a page)
+ *   scales  [n_pages][2][page_size][16] uint8, 16-byte aligned
+ * Slot x is position x % page_size of page x / page_size.
+ * ga_kv_quantize_q4 stores token t's key and value rows at slots[t]:
+ *   k, v    bf16 rows of two heads' 256 values, token t at t * ld_k (ld_v) values; 16-byte
+ *           aligned, leading dimensions >= 512 and multiples of 8 (a slice of a fused projection)
+ *   slots   DEVICE int32 [n_tok], 4-byte aligned, or NULL: token t goes to slot t. A negative
+ *           slot stores nothing; one past the pool stores nothing and records status 3. Slots of
+ *           one call must differ (two tokens of one slot leave an unspecified mixture).
+ * Rules: page_size a multiple of 32, n_pages * page_size < 2^30, 0 <= n_tok <= 64 *
+ * GA_MAX_TOKENS; with slots NULL, n_tok <= n_pages * page_size.
+ * Errors: NULL, SHAPE, RANGE, ALIGN, DEVICE, CUDA. */
+int ga_kv_quantize_q4(const ga_bf16* k, long long ld_k, const ga_bf16* v, long long ld_v,
+                      long long n_tok, const int* slots, uint8_t* k_codes, uint8_t* k_scales,
+                      uint8_t* v_codes, uint8_t* v_scales, int n_pages, int page_size,
+                      ga_stream stream);
+
+/* The widened rows of the tokens at slots[0 .. n_tok - 1] (or slots 0 .. n_tok - 1 with NULL), as
+ * the other entry points read them: a prefix of a 4-bit cache for ga_attn_prefill, say.
+ *   k_out, v_out [n_tok][2][256] bf16, 16-byte aligned. Rows of negative or refused slots are
+ *           left as they were. The same slot may appear more than once.
+ * Everything else as in ga_kv_quantize_q4.
+ * Errors: NULL, SHAPE, RANGE, ALIGN, DEVICE, CUDA. */
+int ga_kv_dequantize_q4(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                        const uint8_t* v_scales, int n_pages, int page_size, const int* slots,
+                        long long n_tok, ga_bf16* k_out, ga_bf16* v_out, ga_stream stream);
+
+/* Bytes of workspace ga_attn_verify_q4 needs, whatever the sequences and lengths. */
+size_t ga_verify_q4_workspace_bytes(void);
+
+/* Few-row verify windows, and decode (rows = 1), over 4-bit paged caches. Unlike the other
+ * verify calls it takes prepared queries (their positions need not be their cache slots) and
+ * lengths on the DEVICE, and it rounds the softmax weights and the output only: scores, O and
+ * the gate stay in fp32. The same call gives the same bits; where a sequence's keys are cut
+ * among the SMs, and so its last bits, depends on all the lengths of the call.
+ *   q_prep   [n_seq][rows][24][256] prepared queries (ga_qk_prologue_axes or ga_q_prologue)
+ *   qg       [n_seq][rows][24][512] fused rows, read for their gate halves
+ *   k_codes, k_scales, v_codes, v_scales, n_pages, page_size: the pools, as ga_kv_quantize_q4
+ *            writes them (prepared keys); the window's own keys included
+ *   page_table DEVICE int32 [n_seq][max_pages]: as in ga_attn_verify_paged; the entries that
+ *            cover keys 0 .. L + rows - 1 are read, one outside the pool records status 3 and
+ *            reads zeros
+ *   seq_len  DEVICE int32 [n_seq]: L, the cached tokens before the window. Negative: an unused
+ *            row, of which nothing is read and whose outputs are left as they were; L + rows
+ *            past max_pages * page_size or GA_MAX_TOKENS records status 4 and is treated so too
+ *   out      [n_seq][rows][24 * 256], row r over keys 0 .. L + r; may not overlap any input
+ *   workspace >= ga_verify_q4_workspace_bytes() bytes, 256-byte aligned, not shared with a
+ *            concurrent call (captured graphs that may run at once need one each); it needs no
+ *            initial contents
+ * Rules: 0 <= rows <= 16, page_size a multiple of 32 up to GA_MAX_TOKENS, n_pages * page_size
+ * < 2^30. Nothing is allocated; the call keeps no pointer. n_seq = 0 or rows = 0 is a no-op.
+ * Errors: NULL, SHAPE, RANGE, ALIGN, WORKSPACE, DEVICE, CUDA. */
+int ga_attn_verify_q4(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k_codes,
+                      const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                      int n_pages, int page_size, const int* page_table, int max_pages,
+                      const int* seq_len, int n_seq, int rows, ga_bf16* out, void* workspace,
+                      size_t ws_bytes, ga_stream stream);
 
 #ifdef __cplusplus
 }

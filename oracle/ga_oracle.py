@@ -458,3 +458,138 @@ def verify_paged(qg_seq, k_pages, v_pages, page_table, page_size, seq_len, w_q, 
                             heads))
     return np.stack(outs)
 
+
+# ----------------------------------------------------------------------------------
+# Serving over a 4-bit paged cache (additions: no counterpart in the pages)
+# ----------------------------------------------------------------------------------
+Q4_GROUP = 16
+Q4_MIN_SCALE, Q4_MAX_SCALE = 2.0 ** -20, 3840.0
+
+
+def quantize_q4_rows(x):
+    """4-bit cache rows [..., 256] -> (codes 0..15 [..., 256], scale bytes [..., 16]).
+
+    Per group of 16: s = max|x| / 7 clamped to [2^-20, 3840] and rounded to 4 significant
+    bits (ties to even), byte 8 E + m for s = 2^(E - 20) (1 + m / 8); code = clamp(round(x / s),
+    -8, 7) + 8, ties to even. NaN counts as 0 and infinities saturate. In float64 every
+    quotient that is a rounding boundary is exact (it needs 8 significant bits)."""
+    x = np.asarray(x, np.float64)
+    x = np.where(np.isnan(x), 0.0, x)
+    g = x.reshape(x.shape[:-1] + (x.shape[-1] // Q4_GROUP, Q4_GROUP))
+    a = np.clip(np.max(np.abs(g), axis=-1) / 7.0, Q4_MIN_SCALE, Q4_MAX_SCALE)
+    m, e = np.frexp(a)
+    s = np.ldexp(np.rint(np.ldexp(m, 4)), e - 4)
+    m, e = np.frexp(s)                              # s = m 2^e, m in [0.5, 1)
+    byte = (e - 1 + 20) * 8 + (np.ldexp(m, 4) - 8)
+    q = np.clip(np.rint(g / s[..., None]), -8, 7) + 8
+    return q.reshape(x.shape).astype(np.int64), byte.astype(np.int64)
+
+
+def widen_q4_rows(codes, scale_bytes):
+    """The values (code - 8) * 2^(E - 20) (1 + m / 8) of 4-bit rows (each a bf16 value)."""
+    b = np.asarray(scale_bytes, np.int64)
+    s = np.ldexp(1.0 + (b % 8) / 8.0, b // 8 - 20)
+    return (np.asarray(codes, np.float64) - 8.0) * np.repeat(s, Q4_GROUP, axis=-1)
+
+
+def pack_q4(codes):
+    """Code bytes [..., 128] of codes [..., 256]: each 8 dims a little-endian 32-bit word, bits
+    4p .. 4p+3 holding dim 2p for p < 4 and dim 2(p - 4) + 1 for p >= 4."""
+    c = np.asarray(codes, np.uint64).reshape(np.shape(codes)[:-1] + (-1, 8))
+    word = np.zeros(c.shape[:-1], np.uint64)
+    for p in range(8):
+        dim = 2 * p if p < 4 else 2 * (p - 4) + 1
+        word |= c[..., dim] << np.uint64(4 * p)
+    out = np.stack([(word >> np.uint64(8 * i)) & np.uint64(255) for i in range(4)], axis=-1)
+    return out.reshape(out.shape[:-2] + (-1,)).astype(np.uint8)
+
+
+def prep_axes(x, w, cos, sin, positions, pair_axis, mode="R1"):
+    """(1+w) norm and partial RoPE of rows x [n, heads, 256]: pair i of token t turns by table
+    row positions[pair_axis[i]][t]. Rounding points as in prep_keys."""
+    rounded = mode != "F64"
+    positions = np.asarray(positions)
+    pair = np.arange(HALF_ROT)
+    rows = positions[np.asarray(pair_axis)].T          # [n, 32]
+    xn = rms_norm_1pw(x, w, rounded=rounded)
+    return rope_partial(xn, cos[rows, pair][:, None, :], sin[rows, pair][:, None, :],
+                        rounded=rounded)
+
+
+def page_plan(seq_len, new_len, page_table, held, free_pages, free_count, page_size, max_tokens,
+              pos_delta=None, max_total=1 << 20):
+    """One step's pages, slots and positions: (page_table, held, free_pages, free_count,
+    row_start, slot_map, positions, info), info = [status, tokens, taken, given back]."""
+    n = len(seq_len)
+    table = np.array(page_table, np.int64)
+    held = [int(x) for x in held]
+    stack = [int(x) for x in free_pages]
+    cap, width = len(stack), table.shape[1]
+    count = int(free_count)
+
+    def refuse(status):
+        return (table, np.array(held, np.int64), np.array(stack, np.int64), count,
+                np.zeros(n + 1, np.int64), np.full(max_tokens, -1, np.int64),
+                np.zeros(max_tokens, np.int64), np.array([status, 0, 0, 0]))
+
+    if not 0 <= count <= cap or any(not 0 <= h <= width for h in held):
+        return refuse(4)
+    need, rel, tok = [], [], []
+    for b in range(n):
+        L, a = int(seq_len[b]), int(new_len[b])
+        grows = a >= 0 and L >= 0
+        if grows and (L + a > width * page_size or L + a > max_total):
+            return refuse(2)   # (before the totals, which it would be part of)
+        tok.append(a if grows else 0)
+        need.append(max(0, -(-(L + a) // page_size) - held[b]) if grows else 0)
+        rel.append(held[b] if a < 0 else 0)
+    if count - sum(need) + sum(rel) > cap:
+        return refuse(4)
+    if sum(tok) > max_tokens:
+        return refuse(1)
+    if sum(need) > count:
+        return refuse(3)
+    taken = [stack[count - 1 - i] for i in range(sum(need))]
+    back = []
+    i = 0
+    for b in range(n):
+        table[b, held[b]:held[b] + need[b]] = taken[i:i + need[b]]
+        i += need[b]
+        back += [int(x) for x in table[b, :rel[b]]]
+    for j, p in enumerate(back):
+        stack[count - len(taken) + j] = p
+    start = np.concatenate([[0], np.cumsum(tok)]).astype(np.int64)
+    slots = np.full(max_tokens, -1, np.int64)
+    pos = np.zeros(max_tokens, np.int64)
+    for b in range(n):
+        for k in range(tok[b]):
+            p = int(seq_len[b]) + k
+            slots[start[b] + k] = table[b, p // page_size] * page_size + p % page_size
+            pos[start[b] + k] = p + (0 if pos_delta is None else int(pos_delta[b]))
+    held = np.array([0 if rel[b] else held[b] + need[b] for b in range(n)], np.int64)
+    return (table, held, np.array(stack, np.int64), count - len(taken) + len(back), start, slots,
+            pos, np.array([0, sum(tok), len(taken), len(back)]))
+
+
+def verify_q4(q_prep, gate, k, v, seq_len, heads=None):
+    """Decode / verify windows over widened rows: q_prep, gate [n, R, 24, 256]; k, v lists of
+    [>= L + R, 2, 256]; float64, nothing rounded. Returns (out [n, R, 24, 256], mass of the same
+    shape: sum_j w_j |v_j| times the gate, the scale of the weights' rounding errors)."""
+    q = np.asarray(q_prep, np.float64)
+    sig = sigmoid_gate(gate, "F64")
+    out, mass = np.zeros(q.shape), np.zeros(q.shape)
+    for b in range(q.shape[0]):
+        L = int(seq_len[b])
+        if L < 0:
+            continue
+        kb, vb = np.asarray(k[b], np.float64), np.asarray(v[b], np.float64)
+        for r in range(q.shape[1]):
+            T = L + r + 1
+            for h in (range(N_Q_HEADS) if heads is None else heads):
+                kv = h // GROUP
+                s = kb[:T, kv] @ q[b, r, h] / 16.0
+                w = np.exp(s - s.max())
+                w /= w.sum()
+                out[b, r, h] = (w @ vb[:T, kv]) * sig[b, r, h]
+                mass[b, r, h] = (w @ np.abs(vb[:T, kv])) * sig[b, r, h]
+    return out, mass

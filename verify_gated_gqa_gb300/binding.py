@@ -69,6 +69,14 @@ _SIGS = {
     "ga_prefill_e4m3_workspace_bytes": (_SZ, [_I]),
     "ga_attn_prefill_e4m3": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P,
                                   _SZ, _P]),
+    "ga_page_plan": (_I, [_P, _P, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P,
+                          _P]),
+    "ga_qk_prologue_axes": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _LL, _I, _P, _P, _P, _I, _P]),
+    "ga_kv_quantize_q4": (_I, [_P, _LL, _P, _LL, _LL, _P, _P, _P, _P, _P, _I, _I, _P]),
+    "ga_kv_dequantize_q4": (_I, [_P, _P, _P, _P, _I, _I, _P, _LL, _P, _P, _P]),
+    "ga_verify_q4_workspace_bytes": (_SZ, []),
+    "ga_attn_verify_q4": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _SZ,
+                               _P]),
 }
 
 
@@ -553,4 +561,228 @@ def ga_attn_verify_e4m3(qg, k_codes, k_scale, v_codes, v_scale, seq_len, w_q, co
                                      _ptr(cos_tab), _ptr(sin_tab), cos_tab.shape[0], _ptr(out),
                                      _ptr(workspace), workspace.numel(), _stream()),
            "ga_attn_verify_e4m3")
+    return out
+
+
+# ------------------------------------------------------------------ serving over 4-bit pages
+Q4_ROW_BYTES, Q4_SCALE_BYTES, Q4_PAGE_TOKENS = 128, 16, 32
+
+
+def _on_device(**tensors):
+    """The given tensors (None passes) live on the current CUDA device."""
+    for n, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+            raise ValueError(f"{n} must be a tensor on the current CUDA device")
+
+
+def _int32(name, t, *shape):
+    """A contiguous int32 tensor of the given shape (None entries: any extent)."""
+    if (t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or
+            any(s is not None and s != d for s, d in zip(shape, t.shape))):
+        raise ValueError(f"{name} must be a contiguous int32 tensor "
+                         f"[{', '.join('...' if s is None else str(s) for s in shape)}]")
+
+
+def _ptr_any(t):
+    """The address of a tensor; of an empty one, a stand-in that is aligned and never read."""
+    return _ptr(t) if t.numel() else ctypes.c_void_p(256)
+
+
+def _q4_pools(k_codes, k_scales, v_codes, v_scales):
+    """(n_pages, page_size) of four pool tensors that belong together."""
+    _on_device(k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales)
+    for n, t, last in (("k_codes", k_codes, Q4_ROW_BYTES), ("v_codes", v_codes, Q4_ROW_BYTES),
+                       ("k_scales", k_scales, Q4_SCALE_BYTES),
+                       ("v_scales", v_scales, Q4_SCALE_BYTES)):
+        if (t.dtype != torch.uint8 or not t.is_contiguous() or t.dim() != 4 or
+                t.shape[1] != N_KV_HEADS or t.shape[3] != last or
+                t.shape[0] != k_codes.shape[0] or t.shape[2] != k_codes.shape[2]):
+            raise ValueError(f"{n} must be a contiguous uint8 tensor "
+                             f"[n_pages, {N_KV_HEADS}, page_size, {last}], n_pages and page_size "
+                             "those of k_codes")
+    return k_codes.shape[0], k_codes.shape[2]
+
+
+def ga_page_plan(seq_len, new_len, page_table, held, free_pages, free_count, page_size,
+                 max_tokens, pos_delta=None, held_out=None, free_count_out=None, row_start=None,
+                 slot_map=None, positions=None, info=None):
+    """Pages, slots and positions of one step (all int32, on the device): takes pages from the
+    stack free_pages[:free_count] into page_table for seq_len + new_len tokens a sequence.
+    page_table is updated in place, and so are held and free_count unless held_out and
+    free_count_out are given. Returns (row_start [n + 1], slot_map [max_tokens], positions
+    [max_tokens], info [4])."""
+    n = seq_len.shape[0]
+    held_out = held if held_out is None else held_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    dev = seq_len.device
+    new = lambda k: torch.empty(k, dtype=torch.int32, device=dev)  # noqa: E731
+    row_start = new(n + 1) if row_start is None else row_start
+    slot_map = new(max_tokens) if slot_map is None else slot_map
+    positions = new(max_tokens) if positions is None else positions
+    info = new(4) if info is None else info
+    _on_device(seq_len=seq_len, new_len=new_len, page_table=page_table, held=held,
+               free_pages=free_pages, free_count=free_count, pos_delta=pos_delta,
+               held_out=held_out, free_count_out=free_count_out, row_start=row_start,
+               slot_map=slot_map, positions=positions, info=info)
+    for name, t, shape in (("seq_len", seq_len, (n,)), ("new_len", new_len, (n,)),
+                           ("page_table", page_table, (n, None)), ("held", held, (n,)),
+                           ("held_out", held_out, (n,)), ("free_pages", free_pages, (None,)),
+                           ("free_count", free_count, (1,)),
+                           ("free_count_out", free_count_out, (1,)),
+                           ("row_start", row_start, (n + 1,)), ("slot_map", slot_map, (max_tokens,)),
+                           ("positions", positions, (max_tokens,)), ("info", info, (4,))):
+        _int32(name, t, *shape)
+    if pos_delta is not None:
+        _int32("pos_delta", pos_delta, n)
+    _check(lib().ga_page_plan(_ptr_any(seq_len), _ptr_any(new_len), n, page_size,
+                              _ptr_any(page_table), page_table.shape[1], _ptr_any(held),
+                              _ptr_any(held_out), _ptr_any(free_pages), free_pages.shape[0],
+                              _ptr(free_count), _ptr(free_count_out), _ptr(pos_delta), max_tokens,
+                              _ptr(row_start), _ptr_any(slot_map), _ptr_any(positions), _ptr(info),
+                              _stream()),
+           "ga_page_plan")
+    return row_start, slot_map, positions, info
+
+
+def ga_qk_prologue_axes(k_raw, w_k, qg, w_q, positions, pair_axis, cos_tab, sin_tab, k_prep=None,
+                        q_prep=None):
+    """Both prologues at positions of their own: positions int32 [n_tok] or [n_axes, >= n_tok]
+    (unit column stride) on the device, pair_axis 32 axis numbers (rotary pair i turns by axis
+    pair_axis[i]; None: axis 0). k_raw (with w_k) or qg (with w_q) may be None. Returns (k_prep
+    [n_tok, 2, 256], q_prep [n_tok, 24, 256]), None for a side not given."""
+    if k_raw is None and qg is None:
+        raise ValueError("k_raw or qg must be given")
+    n_tok = (qg if k_raw is None else k_raw).shape[0]
+    dev = (qg if k_raw is None else k_raw).device
+    _on_device(k_raw=k_raw, w_k=w_k, qg=qg, w_q=w_q, positions=positions, cos_tab=cos_tab,
+               sin_tab=sin_tab, k_prep=k_prep, q_prep=q_prep)
+    if k_raw is not None:
+        _bf16_cuda("k_raw", k_raw, (n_tok, N_KV_HEADS, HEAD_DIM))
+        _bf16_cuda("w_k", w_k, (HEAD_DIM,))
+        k_prep = torch.empty_like(k_raw) if k_prep is None else k_prep
+        _bf16_cuda("k_prep", k_prep, tuple(k_raw.shape))
+    elif w_k is not None or k_prep is not None:
+        raise ValueError("w_k and k_prep come with k_raw")
+    if qg is not None:
+        _bf16_cuda("qg", qg, (n_tok, N_Q_HEADS, 2 * HEAD_DIM))
+        _bf16_cuda("w_q", w_q, (HEAD_DIM,))
+        if q_prep is None:
+            q_prep = torch.empty(n_tok, N_Q_HEADS, HEAD_DIM, dtype=torch.bfloat16, device=dev)
+        _bf16_cuda("q_prep", q_prep, (n_tok, N_Q_HEADS, HEAD_DIM))
+    elif w_q is not None or q_prep is not None:
+        raise ValueError("w_q and q_prep come with qg")
+    if positions.dim() == 1:
+        positions = positions[None]
+    if (positions.dtype != torch.int32 or positions.dim() != 2 or positions.shape[1] < n_tok or
+            (positions.shape[1] > 1 and positions.stride(1) != 1)):
+        raise ValueError("positions must be int32 [n_tok] or [n_axes, >= n_tok] with unit column "
+                         "stride")
+    axes = [0] * (ROPE_DIMS // 2) if pair_axis is None else [int(x) for x in pair_axis]
+    n_axes = positions.shape[0]
+    if len(axes) != ROPE_DIMS // 2 or min(axes) < 0 or max(axes) > 255:
+        raise ValueError("pair_axis must be 32 axis numbers")
+    _bf16_cuda("cos_tab", cos_tab, (cos_tab.shape[0], ROPE_DIMS // 2))
+    _bf16_cuda("sin_tab", sin_tab, tuple(cos_tab.shape))
+    ld = positions.stride(0) if n_axes > 1 else max(positions.shape[1], n_tok)
+    _check(lib().ga_qk_prologue_axes(_opt(k_raw), _ptr(w_k), _opt(k_prep), _opt(qg), _ptr(w_q),
+                                     _opt(q_prep), n_tok, _ptr_any(positions), ld, n_axes,
+                                     (ctypes.c_uint8 * len(axes))(*axes), _ptr(cos_tab),
+                                     _ptr(sin_tab), cos_tab.shape[0], _stream()),
+           "ga_qk_prologue_axes")
+    return k_prep, q_prep
+
+
+def _opt(t):
+    """_ptr_any of a tensor that may be None."""
+    return None if t is None else _ptr_any(t)
+
+
+def _kv_rows(name, x):
+    """(pointer, token stride in values) of bf16 rows [n_tok, 2, 256], heads and dims dense."""
+    if (x.dtype != torch.bfloat16 or x.dim() != 3 or tuple(x.shape[1:]) != (N_KV_HEADS, HEAD_DIM)
+            or x.stride(2) != 1 or x.stride(1) != HEAD_DIM):
+        raise ValueError(f"{name} must be bfloat16 [n_tok, {N_KV_HEADS}, {HEAD_DIM}] with dense "
+                         "heads and dims")
+    return _ptr_any(x), (x.stride(0) if x.shape[0] > 1 else N_KV_HEADS * HEAD_DIM)
+
+
+def ga_kv_quantize_q4(k, v, k_codes, k_scales, v_codes, v_scales, slots=None):
+    """Stores bf16 rows k, v [n_tok, 2, 256] (the token stride may be larger: a slice of a fused
+    projection) as 4-bit rows at slots int32 [n_tok] (None: token t at slot t) of the pools
+    k_codes, v_codes uint8 [n_pages, 2, page_size, 128], k_scales, v_scales uint8
+    [n_pages, 2, page_size, 16]. Negative slots are skipped."""
+    n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    _on_device(k=k, v=v, slots=slots)
+    kp, ld_k = _kv_rows("k", k)
+    vp, ld_v = _kv_rows("v", v)
+    n_tok = k.shape[0]
+    if v.shape[0] != n_tok:
+        raise ValueError("k and v must have the same tokens")
+    if slots is not None:
+        _int32("slots", slots, n_tok)
+    _check(lib().ga_kv_quantize_q4(kp, ld_k, vp, ld_v, n_tok, _opt(slots), _ptr(k_codes),
+                                   _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), n_pages,
+                                   page_size, _stream()),
+           "ga_kv_quantize_q4")
+
+
+def ga_kv_dequantize_q4(k_codes, k_scales, v_codes, v_scales, slots=None, n_tok=None, k_out=None,
+                        v_out=None):
+    """The widened rows at slots int32 [n_tok] (None: slots 0 .. n_tok - 1, by default the whole
+    pool) of 4-bit pools, (k_out, v_out) bf16 [n_tok, 2, 256]. Rows of negative slots are left as
+    they were (unspecified in outputs allocated here)."""
+    n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    if slots is not None:
+        n_tok = slots.shape[0]
+        _int32("slots", slots, n_tok)
+    elif n_tok is None:
+        n_tok = n_pages * page_size
+    shape = (n_tok, N_KV_HEADS, HEAD_DIM)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_codes.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_codes.device)
+    _on_device(slots=slots, k_out=k_out, v_out=v_out)
+    _bf16_cuda("k_out", k_out, shape)
+    _bf16_cuda("v_out", v_out, shape)
+    _check(lib().ga_kv_dequantize_q4(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
+                                     n_pages, page_size, _opt(slots), n_tok, _ptr_any(k_out),
+                                     _ptr_any(v_out), _stream()),
+           "ga_kv_dequantize_q4")
+    return k_out, v_out
+
+
+def ga_verify_q4_workspace_bytes() -> int:
+    return lib().ga_verify_q4_workspace_bytes()
+
+
+def ga_attn_verify_q4(q_prep, qg, k_codes, k_scales, v_codes, v_scales, page_table, seq_len,
+                      out=None, workspace=None):
+    """Decode (rows = 1) or verify windows over 4-bit paged caches: q_prep [n_seq, rows, 24, 256]
+    prepared queries; qg [n_seq, rows, 24, 512] fused rows (their gates); the pools; page_table
+    int32 [n_seq, max_pages] and seq_len int32 [n_seq] on the device (negative: unused, its rows
+    of out are left as they were). Returns out [n_seq, rows, 24*256]."""
+    n_seq, rows = q_prep.shape[0], q_prep.shape[1]
+    n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    if out is None:
+        out = torch.empty(n_seq, rows, N_Q_HEADS * HEAD_DIM, dtype=torch.bfloat16,
+                          device=q_prep.device)
+    if workspace is None:
+        workspace = torch.empty(ga_verify_q4_workspace_bytes(), dtype=torch.uint8,
+                                device=q_prep.device)
+    _on_device(q_prep=q_prep, qg=qg, page_table=page_table, seq_len=seq_len, out=out,
+               workspace=workspace)
+    _bf16_cuda("q_prep", q_prep, (n_seq, rows, N_Q_HEADS, HEAD_DIM))
+    _bf16_cuda("qg", qg, (n_seq, rows, N_Q_HEADS, 2 * HEAD_DIM))
+    _bf16_cuda("out", out, (n_seq, rows, N_Q_HEADS * HEAD_DIM))
+    _int32("page_table", page_table, n_seq, None)
+    _int32("seq_len", seq_len, n_seq)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check(lib().ga_attn_verify_q4(_ptr_any(q_prep), _ptr_any(qg), _ptr(k_codes), _ptr(k_scales),
+                                   _ptr(v_codes), _ptr(v_scales), n_pages, page_size,
+                                   _ptr_any(page_table), page_table.shape[1], _ptr_any(seq_len),
+                                   n_seq, rows, _ptr_any(out), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream()),
+           "ga_attn_verify_q4")
     return out

@@ -89,6 +89,7 @@ int current_device(DeviceState** out) {
       void* sw = nullptr;
       if ((e = GA_CUDA(attn_set_smem_attribute())) != cudaSuccess) return fail_cuda(e);
       if ((e = GA_CUDA(probe_set_smem_attribute())) != cudaSuccess) return fail_cuda(e);
+      if ((e = GA_CUDA(verify4_set_attributes())) != cudaSuccess) return fail_cuda(e);
       if ((e = GA_CUDA(attn_max_pair_clusters(&d.pair_clusters))) != cudaSuccess) return fail_cuda(e);
       if ((e = GA_CUDA(attn_max_gated_pair_clusters(&d.gated_pair_clusters))) != cudaSuccess)
         return fail_cuda(e);
@@ -202,6 +203,28 @@ int encode_kv8_map(CUtensorMap* map, const void* base, long long cap, long long 
                            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
+  if (r != CUDA_SUCCESS) {
+    t_last_cuda_error = (int)r;
+    return GA_ERR_CUDA;
+  }
+  return GA_OK;
+}
+
+// A 4-bit cache pool's rows, [n_rows][row_bytes] bytes, as a TMA tensor: box = 32 rows (a page
+// holds a multiple of that), code rows (128 bytes) with the 128-byte swizzle, scale rows (16
+// bytes) as they are; rows past the pool read as zeros.
+int encode_q4_map(CUtensorMap* map, const void* base, long long n_rows, int row_bytes) {
+  EncodeTiledFn enc;
+  int st = get_encode(&enc);
+  if (st != GA_OK) return st;
+  cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)n_rows};
+  cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  cuuint32_t box[2] = {(cuuint32_t)row_bytes, GA_Q4_PAGE_TOKENS};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = GA_CUDA(enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                           strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
   if (r != CUDA_SUCCESS) {
     t_last_cuda_error = (int)r;
     return GA_ERR_CUDA;
@@ -1180,6 +1203,201 @@ int ga_attn_masked_static(const ga_bf16* qg, const ga_bf16* k_prep, const ga_bf1
   }
   return masked_run(nullptr, qg, k_prep, v, w_q, cos_tab, sin_tab, rows, T, q_base, mask,
                     ld_mask, 0, kKvHeads, out, weights, hidden_rows, scratch, stream);
+}
+
+// ---------------------------------------------------------------- 4-bit paged serving
+int ga_page_plan(const int* seq_len, const int* new_len, int n_seq, int page_size,
+                 int* page_table, int max_pages, const int* held, int* held_out, int* free_pages,
+                 int n_free, const int* free_count, int* free_count_out, const int* pos_delta,
+                 int max_tokens, int* row_start, int* slot_map, int* positions, int* info,
+                 ga_stream stream) {
+  if (!seq_len || !new_len || !page_table || !held || !held_out || !free_pages || !free_count ||
+      !free_count_out || !row_start || !slot_map || !info)
+    return GA_ERR_NULL;
+  if (n_seq < 0 || page_size < 1 || max_pages < 1 || n_free < 0 || max_tokens < 0)
+    return GA_ERR_SHAPE;
+  if (n_seq > GA_PLAN_MAX_SEQ || (long long)max_pages * page_size > 0x7FFFFFFFLL ||
+      (long long)n_free * page_size > 0x7FFFFFFFLL || max_tokens >= (1 << 30))
+    return GA_ERR_RANGE;
+  const void* arrays[] = {seq_len, new_len, page_table, held, held_out, free_pages, free_count,
+                          free_count_out, pos_delta, row_start, slot_map, positions, info};
+  for (const void* p : arrays)
+    if (p && !aligned(p, 4)) return GA_ERR_ALIGN;
+  DeviceState* dev = nullptr;
+  const int st = current_device(&dev);
+  if (st != GA_OK) return st;
+  PlanArgs a{};
+  a.seq_len = seq_len; a.new_len = new_len;
+  a.n_seq = n_seq; a.page_size = page_size; a.max_pages = max_pages;
+  a.page_table = page_table; a.held = held; a.held_out = held_out;
+  a.free_pages = free_pages; a.n_free = n_free;
+  a.free_count = free_count; a.free_count_out = free_count_out;
+  a.pos_delta = pos_delta; a.max_tokens = max_tokens;
+  a.row_start = row_start; a.slot_map = slot_map; a.positions = positions; a.info = info;
+  const cudaError_t e = GA_CUDA(launch_plan(a, (cudaStream_t)stream));
+  return e == cudaSuccess ? GA_OK : fail_cuda(e);
+}
+
+int ga_qk_prologue_axes(const ga_bf16* k_raw, const ga_bf16* w_k, ga_bf16* k_prep,
+                        const ga_bf16* qg, const ga_bf16* w_q, ga_bf16* q_prep, int n_tok,
+                        const int* positions, long long ld_pos, int n_axes,
+                        const uint8_t* pair_axis, const ga_bf16* cos_tab, const ga_bf16* sin_tab,
+                        int table_rows, ga_stream stream) {
+  // each side whole or absent, one at least
+  if ((!k_raw != !w_k) || (!k_raw != !k_prep) || (!qg != !w_q) || (!qg != !q_prep) ||
+      (!k_raw && !qg) || !positions || !pair_axis || !cos_tab || !sin_tab)
+    return GA_ERR_NULL;
+  if (n_tok < 0 || n_axes < 1 || table_rows < 0) return GA_ERR_SHAPE;
+  if (n_tok > GA_MAX_TOKENS || n_axes > 4 || ld_pos < n_tok || ld_pos > (1LL << 40))
+    return GA_ERR_RANGE;
+  AxisPositions ap{};
+  for (int i = 0; i < kHalfRot; ++i) {
+    if (pair_axis[i] >= n_axes) return GA_ERR_RANGE;
+    ap.pair_axis |= (uint64_t)pair_axis[i] << (2 * i);
+  }
+  if (table_rows < 1) return GA_ERR_TABLE;
+  const void* arrays[] = {k_raw, w_k, k_prep, qg, w_q, q_prep, cos_tab, sin_tab};
+  for (const void* p : arrays)
+    if (p && !aligned(p, 16)) return GA_ERR_ALIGN;
+  if (!aligned(positions, 4)) return GA_ERR_ALIGN;
+  if (n_tok == 0) return GA_OK;
+  DeviceState* dev = nullptr;
+  const int st = current_device(&dev);
+  if (st != GA_OK) return st;
+  ap.pos = positions;
+  ap.ld = ld_pos;
+  ap.table_rows = table_rows;
+  ap.status = dev->status_word;
+  const cudaError_t e =
+      GA_CUDA(launch_qk_prologue_axes(k_raw, w_k, k_prep, qg, w_q, q_prep, n_tok, ap, cos_tab,
+                                      sin_tab, dev->sm_count, (cudaStream_t)stream));
+  return e == cudaSuccess ? GA_OK : fail_cuda(e);
+}
+
+}  // extern "C"
+
+namespace ga {
+namespace {
+// The checks that the 4-bit cache calls share (no CUDA call).
+int check_q4_pools(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                   const uint8_t* v_scales, int n_pages, int page_size) {
+  if (!k_codes || !k_scales || !v_codes || !v_scales) return GA_ERR_NULL;
+  if (n_pages < 1 || page_size < 1) return GA_ERR_SHAPE;
+  if (page_size % GA_Q4_PAGE_TOKENS != 0 || page_size > GA_MAX_TOKENS ||
+      (long long)n_pages * page_size >= (1LL << 30))
+    return GA_ERR_RANGE;
+  if (!aligned(k_codes, 16) || !aligned(k_scales, 16) || !aligned(v_codes, 16) ||
+      !aligned(v_scales, 16))
+    return GA_ERR_ALIGN;
+  return GA_OK;
+}
+int check_q4_tokens(long long n_tok, const int* slots, int n_pages, int page_size) {
+  if (n_tok < 0) return GA_ERR_SHAPE;
+  if (n_tok > 64LL * GA_MAX_TOKENS || (!slots && n_tok > (long long)n_pages * page_size))
+    return GA_ERR_RANGE;
+  if (slots && !aligned(slots, 4)) return GA_ERR_ALIGN;
+  return GA_OK;
+}
+}  // namespace
+}  // namespace ga
+
+extern "C" {
+
+int ga_kv_quantize_q4(const ga_bf16* k, long long ld_k, const ga_bf16* v, long long ld_v,
+                      long long n_tok, const int* slots, uint8_t* k_codes, uint8_t* k_scales,
+                      uint8_t* v_codes, uint8_t* v_scales, int n_pages, int page_size,
+                      ga_stream stream) {
+  if (!k || !v) return GA_ERR_NULL;
+  int st = check_q4_pools(k_codes, k_scales, v_codes, v_scales, n_pages, page_size);
+  if (st != GA_OK) return st;
+  st = check_q4_tokens(n_tok, slots, n_pages, page_size);
+  if (st != GA_OK) return st;
+  if (ld_k < kKvHeads * kDim || ld_v < kKvHeads * kDim || ld_k > (1LL << 32) || ld_v > (1LL << 32))
+    return GA_ERR_RANGE;
+  if (!aligned(k, 16) || !aligned(v, 16) || ld_k % 8 != 0 || ld_v % 8 != 0) return GA_ERR_ALIGN;
+  if (n_tok == 0) return GA_OK;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != GA_OK) return st;
+  Kv4Args a{};
+  a.k = k; a.v = v; a.ld_k = ld_k; a.ld_v = ld_v;
+  a.k_codes = k_codes; a.k_scales = k_scales; a.v_codes = v_codes; a.v_scales = v_scales;
+  a.slots = slots; a.n_tok = n_tok;
+  a.n_slots = (long long)n_pages * page_size; a.page_size = page_size;
+  a.status = dev->status_word;
+  const cudaError_t e = GA_CUDA(launch_quantize_q4(a, (cudaStream_t)stream));
+  return e == cudaSuccess ? GA_OK : fail_cuda(e);
+}
+
+int ga_kv_dequantize_q4(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                        const uint8_t* v_scales, int n_pages, int page_size, const int* slots,
+                        long long n_tok, ga_bf16* k_out, ga_bf16* v_out, ga_stream stream) {
+  if (!k_out || !v_out) return GA_ERR_NULL;
+  int st = check_q4_pools(k_codes, k_scales, v_codes, v_scales, n_pages, page_size);
+  if (st != GA_OK) return st;
+  st = check_q4_tokens(n_tok, slots, n_pages, page_size);
+  if (st != GA_OK) return st;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return GA_ERR_ALIGN;
+  if (n_tok == 0) return GA_OK;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != GA_OK) return st;
+  Kv4Args a{};
+  a.k_codes = const_cast<uint8_t*>(k_codes); a.k_scales = const_cast<uint8_t*>(k_scales);
+  a.v_codes = const_cast<uint8_t*>(v_codes); a.v_scales = const_cast<uint8_t*>(v_scales);
+  a.slots = slots; a.n_tok = n_tok;
+  a.n_slots = (long long)n_pages * page_size; a.page_size = page_size;
+  a.k_out = k_out; a.v_out = v_out;
+  a.status = dev->status_word;
+  const cudaError_t e = GA_CUDA(launch_dequantize_q4(a, (cudaStream_t)stream));
+  return e == cudaSuccess ? GA_OK : fail_cuda(e);
+}
+
+size_t ga_verify_q4_workspace_bytes(void) { return verify4_ws_bytes(); }
+
+int ga_attn_verify_q4(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k_codes,
+                      const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                      int n_pages, int page_size, const int* page_table, int max_pages,
+                      const int* seq_len, int n_seq, int rows, ga_bf16* out, void* workspace,
+                      size_t ws_bytes, ga_stream stream) {
+  if (!q_prep || !qg || !page_table || !seq_len || !out) return GA_ERR_NULL;
+  int st = check_q4_pools(k_codes, k_scales, v_codes, v_scales, n_pages, page_size);
+  if (st != GA_OK) return st;
+  if (n_seq < 0 || rows < 0 || max_pages < 1) return GA_ERR_SHAPE;
+  if (rows > kVerifyMaxRows || n_seq > GA_MAX_TOKENS) return GA_ERR_RANGE;
+  if (!aligned(q_prep, 16) || !aligned(qg, 16) || !aligned(out, 16) || !aligned(page_table, 4) ||
+      !aligned(seq_len, 4))
+    return GA_ERR_ALIGN;
+  if (n_seq == 0 || rows == 0) return GA_OK;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < verify4_ws_bytes())
+    return GA_ERR_WORKSPACE;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != GA_OK) return st;
+  const long long n_rows = (long long)n_pages * kKvHeads * page_size;
+  CUtensorMap kc, vc, ks, vs;
+  if ((st = encode_q4_map(&kc, k_codes, n_rows, GA_Q4_ROW_BYTES)) != GA_OK ||
+      (st = encode_q4_map(&vc, v_codes, n_rows, GA_Q4_ROW_BYTES)) != GA_OK ||
+      (st = encode_q4_map(&ks, k_scales, n_rows, GA_Q4_SCALE_BYTES)) != GA_OK ||
+      (st = encode_q4_map(&vs, v_scales, n_rows, GA_Q4_SCALE_BYTES)) != GA_OK)
+    return st;
+  for (int g0 = 0; g0 < n_seq; g0 += kV4MaxSeq) {
+    Verify4Args a{};
+    a.n_seq = n_seq - g0 < kV4MaxSeq ? n_seq - g0 : kV4MaxSeq;
+    a.rows = rows; a.page_size = page_size; a.max_pages = max_pages; a.n_pages = n_pages;
+    a.q_prep = q_prep + (size_t)g0 * rows * kOutRow;
+    a.qg = qg + (size_t)g0 * rows * kRowElems;
+    a.out = out + (size_t)g0 * rows * kOutRow;
+    a.page_table = page_table + (size_t)g0 * max_pages;
+    a.seq_len = seq_len + g0;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = a.part_o + (size_t)2 * kV4MaxCtas * 128 * kDim;
+    a.status = dev->status_word;
+    const cudaError_t e =
+        GA_CUDA(launch_verify4(kc, vc, ks, vs, a, dev->sm_count, (cudaStream_t)stream));
+    if (e != cudaSuccess) return fail_cuda(e);
+  }
+  return GA_OK;
 }
 
 }  // extern "C"

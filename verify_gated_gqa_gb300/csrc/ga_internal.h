@@ -145,6 +145,75 @@ cudaError_t launch_dequantize_e4m3(const uint8_t* q, const float* scale, long lo
 cudaError_t launch_select_mask(const float* scores, long long ld_scores, int rows, int T,
                                int q_base, int top_k, uint8_t* mask, long long ld_mask,
                                cudaStream_t s);
+// Positions of tokens 0 .. on several axes: token t's position on axis x is pos[x * ld + t];
+// rotary pair i turns by axis (pair_axis >> 2i) & 3. Positions lie in [0, table_rows).
+struct AxisPositions {
+  const int* pos;
+  long long ld;
+  uint64_t pair_axis;
+  int table_rows;
+  int* status;
+};
+// The key rows and (or) all query heads' rows of n_tok tokens at positions of their own.
+cudaError_t launch_qk_prologue_axes(const uint16_t* k_raw, const uint16_t* w_k, uint16_t* k_prep,
+                                    const uint16_t* qg, const uint16_t* w_q, uint16_t* q_prep,
+                                    int n_tok, const AxisPositions& ap, const uint16_t* cos_tab,
+                                    const uint16_t* sin_tab, int sm_count, cudaStream_t s);
+
+// A step's pages, slots and positions (ga_plan.cu).
+constexpr int kPlanFusedTokens = 8192;   // slots the single CTA of a small step writes itself
+struct PlanArgs {
+  const int *seq_len, *new_len;
+  int n_seq, page_size, max_pages;
+  int* page_table;
+  const int* held;
+  int* held_out;
+  int* free_pages;
+  int n_free;
+  const int* free_count;
+  int* free_count_out;
+  const int* pos_delta;   // nullable
+  int max_tokens;
+  int *row_start, *slot_map, *positions, *info;   // positions nullable
+};
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s);
+
+// 4-bit cache rows of n_tok tokens by slot (ga_kv4.cu; slots null: token t is slot t).
+struct Kv4Args {
+  const uint16_t *k, *v;      // storing: rows of 2 x 256 values, ld_k / ld_v values apart
+  long long ld_k, ld_v;
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const int* slots;
+  long long n_tok, n_slots;
+  int page_size;
+  uint16_t *k_out, *v_out;    // widening: [n_tok][2][256]
+  int* status;
+};
+cudaError_t launch_quantize_q4(const Kv4Args& a, cudaStream_t s);
+cudaError_t launch_dequantize_q4(const Kv4Args& a, cudaStream_t s);
+
+// Attention over 4-bit paged caches (ga_verify4.cu).
+constexpr int kV4MaxCtas = 160;        // CTAs of the attention kernel at most
+constexpr int kV4MaxSeq = 1024;        // sequences per launch (the host loops over groups)
+struct Verify4Args {
+  const uint16_t* q_prep;   // [n_seq][rows][24][256]
+  const uint16_t* qg;       // [n_seq][rows][24][512], read for the gates
+  uint16_t* out;            // [n_seq][rows][24 * 256]
+  const int* page_table;    // [n_seq][max_pages]
+  const int* seq_len;       // [n_seq]
+  int n_seq, rows, page_size, max_pages, n_pages;
+  float* part_o;            // [2 * kV4MaxCtas][128][256]
+  float* part_ml;           // [2 * kV4MaxCtas][128][2]
+  int* status;
+};
+size_t verify4_ws_bytes();
+cudaError_t verify4_set_attributes();
+// Maps: the code pools as [rows][128] bytes (box 32 rows, 128-byte swizzle) and the scale pools
+// as [rows][16] bytes (box 32 rows).
+cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
+                           const CUtensorMap& k_scales, const CUtensorMap& v_scales,
+                           const Verify4Args& a, int sm_count, cudaStream_t s);
+
 cudaError_t attn_set_smem_attribute();
 // Clusters of two attention CTAs (the e4m3 verify variant) that can run at once.
 cudaError_t attn_max_pair_clusters(int* n);

@@ -80,7 +80,7 @@ __device__ __forceinline__ void load_row(const uint16_t* p, int l, RowVals& v) {
 // token that has heads_per_tok heads. Row r is token r / n_heads, head head0 + r % n_heads;
 // it reads 256 values at src + (token * heads_per_tok + head) * src_stride and writes 256 at
 // dst + (token * heads_per_tok + head) * 256, normed with w_norm. Token t sits at position
-// pos_base + t, or, with kSeq, at the position its sequence gives (SeqPositions).
+// pos_base + t, or at the position that the launch's position rule gives (below).
 struct PrologueRows {
   const uint16_t* src;
   uint16_t* dst;
@@ -89,16 +89,103 @@ struct PrologueRows {
   int src_stride, heads_per_tok, head0, n_heads, pos_base;
 };
 
+// A position rule gives the cos and sin of a lane's two rotary pairs (2l and 2l + 1, low and
+// high half of a word) for the row in hand. fetch(t) is called for a row's token one row ahead,
+// so that what it loads is in flight while the row before is computed; step() makes it current.
+__device__ __forceinline__ uint32_t table_word(const uint16_t* tab, int pos, int l) {
+  return __ldg(reinterpret_cast<const uint32_t*>(tab + (long long)pos * kHalfRot) + l);
+}
+// Token t at pos_base + t.
+struct BasePositions {
+  struct At {
+    int base, tok, next;
+    __device__ __forceinline__ At(const BasePositions&, const PrologueRows& run, int)
+        : base(run.pos_base), tok(0), next(0) {}
+    __device__ __forceinline__ void fetch(int t) { next = t; }
+    __device__ __forceinline__ void step() { tok = next; }
+    __device__ __forceinline__ void words(const uint16_t* cos_tab, const uint16_t* sin_tab, int l,
+                                          uint32_t& cw, uint32_t& sw) const {
+      cw = table_word(cos_tab, base + tok, l);
+      sw = table_word(sin_tab, base + tok, l);
+    }
+  };
+};
+// Token t at the position its sequence gives.
+struct SeqRule {
+  SeqPositions sp;
+  struct At {
+    const SeqPositions& sp;
+    int tok, next;
+    __device__ __forceinline__ At(const SeqRule& r, const PrologueRows&, int)
+        : sp(r.sp), tok(0), next(0) {}
+    __device__ __forceinline__ void fetch(int t) { next = t; }
+    __device__ __forceinline__ void step() { tok = next; }
+    __device__ __forceinline__ int position(int t) const {
+      if (sp.n_seq > 0) {
+        // the sequence holding packed token t: the last b with row_start[b] <= t
+        int lo = 0, hi = sp.n_seq - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (sp.row_start[mid] <= t) lo = mid;
+          else hi = mid - 1;
+        }
+        return sp.seq_base[lo] + (t - sp.row_start[lo]);
+      }
+      return sp.seq_base[t / sp.rows_per_seq] + t % sp.rows_per_seq;
+    }
+    __device__ __forceinline__ void words(const uint16_t* cos_tab, const uint16_t* sin_tab, int l,
+                                          uint32_t& cw, uint32_t& sw) const {
+      const int pos = position(tok);
+      cw = table_word(cos_tab, pos, l);
+      sw = table_word(sin_tab, pos, l);
+    }
+  };
+};
+// Every rotary pair at its own axis's position of the token, from device memory. A position
+// outside the table is recorded in the status word and rotated as position 0.
+struct AxisRule {
+  AxisPositions ap;
+  struct At {
+    const AxisPositions& ap;
+    const int *p0, *p1;   // the positions of the lane's two pairs' axes
+    int a, b, na, nb;
+    __device__ __forceinline__ At(const AxisRule& r, const PrologueRows&, int l)
+        : ap(r.ap), a(0), b(0), na(0), nb(0) {
+      p0 = ap.pos + (long long)((ap.pair_axis >> (4 * l)) & 3u) * ap.ld;
+      p1 = ap.pos + (long long)((ap.pair_axis >> (4 * l + 2)) & 3u) * ap.ld;
+    }
+    __device__ __forceinline__ void fetch(int t) {
+      na = __ldg(p0 + t);
+      nb = __ldg(p1 + t);
+    }
+    __device__ __forceinline__ int checked(int p) const {
+      if ((unsigned)p < (unsigned)ap.table_rows) return p;
+      atomicCAS(ap.status, 0, (int)kDevBadPosition);
+      return 0;
+    }
+    __device__ __forceinline__ void step() {
+      a = checked(na);
+      b = checked(nb);
+    }
+    __device__ __forceinline__ void words(const uint16_t* cos_tab, const uint16_t* sin_tab, int l,
+                                          uint32_t& cw, uint32_t& sw) const {
+      // the low half from the first pair's row, the high half from the second's
+      cw = prmt_b32(table_word(cos_tab, a, l), table_word(cos_tab, b, l), 0x7610u);
+      sw = prmt_b32(table_word(sin_tab, a, l), table_word(sin_tab, b, l), 0x7610u);
+    }
+  };
+};
+
 // The rows first, first + stride, ... of one run, by this half-warp.
-template <bool kSeq>
+template <class Rule>
 __device__ __forceinline__ void prologue_walk(const PrologueRows& run, int first, int stride,
                                               const uint16_t* __restrict__ cos_tab,
                                               const uint16_t* __restrict__ sin_tab,
-                                              const SeqPositions& sp) {
+                                              const Rule& rule) {
   const uint16_t* __restrict__ src = run.src;
   uint16_t* __restrict__ dst = run.dst;
   const int src_stride = run.src_stride, heads_per_tok = run.heads_per_tok;
-  const int head0 = run.head0, n_heads = run.n_heads, pos_base = run.pos_base;
+  const int head0 = run.head0, n_heads = run.n_heads;
   const int l = threadIdx.x & 15;
   const unsigned hmask = 0xFFFFu << (threadIdx.x & 16);   // this half-warp's lanes
   // rows are walked as (token, head) pairs: no division inside the loop
@@ -115,23 +202,11 @@ __device__ __forceinline__ void prologue_walk(const PrologueRows& run, int first
   auto row_off = [&](int t, int hd, int stride_el) -> long long {
     return ((long long)t * heads_per_tok + head0 + hd) * stride_el;
   };
-  auto position = [&](int t) -> int {
-    if (!kSeq) return pos_base + t;
-    if (sp.n_seq > 0) {
-      // the sequence holding packed token t: the last b with row_start[b] <= t
-      int lo = 0, hi = sp.n_seq - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (sp.row_start[mid] <= t) lo = mid;
-        else hi = mid - 1;
-      }
-      return sp.seq_base[lo] + (t - sp.row_start[lo]);
-    }
-    return sp.seq_base[t / sp.rows_per_seq] + t % sp.rows_per_seq;
-  };
+  typename Rule::At at(rule, run, l);
 
   RowVals cur;
   load_row(src + row_off(tok, head, src_stride), l, cur);
+  at.fetch(tok);
   while (true) {
     int ntok = tok + stride_tok, nhead = head + stride_head;
     if (nhead >= n_heads) {
@@ -140,10 +215,13 @@ __device__ __forceinline__ void prologue_walk(const PrologueRows& run, int first
     }
     const bool more = row + stride < n_rows32;
     RowVals nxt;
-    if (more) load_row(src + row_off(ntok, nhead, src_stride), l, nxt);
-    const int pos = position(tok);
-    const uint32_t cw = __ldg(reinterpret_cast<const uint32_t*>(cos_tab + (long long)pos * kHalfRot) + l);
-    const uint32_t sw = __ldg(reinterpret_cast<const uint32_t*>(sin_tab + (long long)pos * kHalfRot) + l);
+    at.step();
+    if (more) {
+      load_row(src + row_off(ntok, nhead, src_stride), l, nxt);
+      at.fetch(ntok);
+    }
+    uint32_t cw, sw;
+    at.words(cos_tab, sin_tab, l, cw, sw);
 
     // fast sum of squares: pairs by one fma (the second square is exact), then a tree
     float t8[8];
@@ -237,19 +315,19 @@ __device__ __forceinline__ void prologue_walk(const PrologueRows& run, int first
 // One persistent grid over up to two runs of rows: every half-warp walks its rows of run0,
 // then its rows of run1 (n_rows 0: none), the two runs dealt as one sequence of rows so that
 // the half-warps' shares differ by one row at most.
-template <bool kSeq>
+template <class Rule>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     prologue_kernel(const __grid_constant__ PrologueRows run0,
                     const __grid_constant__ PrologueRows run1,
                     const uint16_t* __restrict__ cos_tab, const uint16_t* __restrict__ sin_tab,
-                    const __grid_constant__ SeqPositions sp) {
+                    const __grid_constant__ Rule rule) {
   const int stride = gridDim.x * (kThreads / 16);
   const int hw = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
-  prologue_walk<kSeq>(run0, hw, stride, cos_tab, sin_tab, sp);
+  prologue_walk(run0, hw, stride, cos_tab, sin_tab, rule);
   if (run1.n_rows > 0) {
     // the first row of run1 in this half-warp's share of the joined sequence
     const int first = (int)((((long long)hw - run0.n_rows) % stride + stride) % stride);
-    prologue_walk<kSeq>(run1, first, stride, cos_tab, sin_tab, sp);
+    prologue_walk(run1, first, stride, cos_tab, sin_tab, rule);
   }
 }
 
@@ -277,8 +355,8 @@ cudaError_t launch_k_prologue(const uint16_t* k_raw, const uint16_t* w_k, const 
                               const uint16_t* sin_tab, int n_tok, int pos_base, uint16_t* k_prep,
                               int sm_count, cudaStream_t s) {
   const PrologueRows run = k_rows(k_raw, w_k, n_tok, pos_base, k_prep);
-  prologue_kernel<false><<<prologue_grid(run.n_rows, sm_count), kThreads, 0, s>>>(
-      run, no_rows(), cos_tab, sin_tab, SeqPositions{});
+  prologue_kernel<BasePositions><<<prologue_grid(run.n_rows, sm_count), kThreads, 0, s>>>(
+      run, no_rows(), cos_tab, sin_tab, BasePositions{});
   return cudaGetLastError();
 }
 
@@ -286,8 +364,8 @@ cudaError_t launch_q_prologue(const uint16_t* qg, const uint16_t* w_q, const uin
                               const uint16_t* sin_tab, int rows, int q_base, int head0,
                               int n_heads, uint16_t* q_prep, int sm_count, cudaStream_t s) {
   const PrologueRows run = q_rows(qg, w_q, rows, q_base, head0, n_heads, q_prep);
-  prologue_kernel<false><<<prologue_grid(run.n_rows, sm_count), kThreads, 0, s>>>(
-      run, no_rows(), cos_tab, sin_tab, SeqPositions{});
+  prologue_kernel<BasePositions><<<prologue_grid(run.n_rows, sm_count), kThreads, 0, s>>>(
+      run, no_rows(), cos_tab, sin_tab, BasePositions{});
   return cudaGetLastError();
 }
 
@@ -298,8 +376,8 @@ cudaError_t launch_qk_prologue(const uint16_t* k_raw, const uint16_t* w_k, int n
                                cudaStream_t s) {
   const PrologueRows rk = k_rows(k_raw, w_k, n_tok, k_pos_base, k_prep);
   const PrologueRows rq = q_rows(qg, w_q, rows, q_base, 0, kHeads, q_prep);
-  prologue_kernel<false><<<prologue_grid(rk.n_rows + rq.n_rows, sm_count), kThreads, 0, s>>>(
-      rk, rq, cos_tab, sin_tab, SeqPositions{});
+  prologue_kernel<BasePositions><<<prologue_grid(rk.n_rows + rq.n_rows, sm_count), kThreads, 0, s>>>(
+      rk, rq, cos_tab, sin_tab, BasePositions{});
   return cudaGetLastError();
 }
 
@@ -307,8 +385,19 @@ cudaError_t launch_q_prologue_seq(const uint16_t* qg, const uint16_t* w_q, const
                                   const uint16_t* sin_tab, int n_tok, const SeqPositions& sp,
                                   uint16_t* q_prep, int sm_count, cudaStream_t s) {
   const PrologueRows run = q_rows(qg, w_q, n_tok, 0, 0, kHeads, q_prep);
-  prologue_kernel<true><<<prologue_grid(run.n_rows, sm_count), kThreads, 0, s>>>(
-      run, no_rows(), cos_tab, sin_tab, sp);
+  prologue_kernel<SeqRule><<<prologue_grid(run.n_rows, sm_count), kThreads, 0, s>>>(
+      run, no_rows(), cos_tab, sin_tab, SeqRule{sp});
+  return cudaGetLastError();
+}
+
+cudaError_t launch_qk_prologue_axes(const uint16_t* k_raw, const uint16_t* w_k, uint16_t* k_prep,
+                                    const uint16_t* qg, const uint16_t* w_q, uint16_t* q_prep,
+                                    int n_tok, const AxisPositions& ap, const uint16_t* cos_tab,
+                                    const uint16_t* sin_tab, int sm_count, cudaStream_t s) {
+  const PrologueRows rk = k_raw ? k_rows(k_raw, w_k, n_tok, 0, k_prep) : no_rows();
+  const PrologueRows rq = qg ? q_rows(qg, w_q, n_tok, 0, 0, kHeads, q_prep) : no_rows();
+  prologue_kernel<AxisRule><<<prologue_grid(rk.n_rows + rq.n_rows, sm_count), kThreads, 0, s>>>(
+      rk, rq, cos_tab, sin_tab, AxisRule{ap});
   return cudaGetLastError();
 }
 

@@ -19,7 +19,8 @@ enum DeviceStatus : int {
   kDevOk = 0,
   kDevWaitTimeout = 1,
   kDevBadLaunch = 2,
-  kDevBadPage = 3,   // a page-table entry outside the page pool (the tile reads zeros)
+  kDevBadPage = 3,   // a page-table entry or slot outside the page pool (the tile reads zeros)
+  kDevBadPosition = 4,   // a rotary position outside the table, a length outside the page table
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -174,6 +175,16 @@ __device__ __forceinline__ void mbar_expect_tx_warp(uint64_t* bar, uint32_t byte
       "elect.sync _|e, 0xffffffff;\n\t"
       "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(smem_u32(bar)),
       "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_warp(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                                 int c0, int c1) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
       : "memory");
 }
 __device__ __forceinline__ void tma_load_3d_warp(void* dst, const CUtensorMap* map, uint64_t* bar,

@@ -1,0 +1,707 @@
+// Decode and verify attention over 4-bit paged caches (format: ga_q4.cuh).
+//
+// Per sequence with L cached tokens before the window, window row r (position L + r) sees keys
+// 0 .. L + r; with s_j = q . k_j / 16, out = (sum_j e^(s_j) v_j / sum_j e^(s_j)) sigmoid(gate).
+// Keys and values are widened from their codes without rounding; scores, maxima, sums and O are
+// fp32; the weights e^(s - M) are rounded to bf16 for the tensor cores (and summed as rounded,
+// so their normalisation is consistent); the output is rounded once.
+//
+// Work. A stream is (sequence, KV head, query-row block): the 12 query heads of the group and
+// every window row when that makes at most 128 rows, else two blocks of 6 heads. A stream's
+// keys are tiles of 128. The streams' tiles, end to end, are cut into equal runs, one per CTA
+// (one CTA per SM), so any mix of lengths fills the device evenly: a CTA may end one stream
+// and begin another. The lengths are read on the device; every role of every CTA derives the
+// same cut from them. A stream that one CTA runs whole is written out by it; a stream cut
+// across CTAs leaves partial O, M, l per CTA (at most two per CTA: its first and its last
+// segment), merged by the combine kernel.
+//
+// Structure (640 threads, 20 warps):
+//   warp 0      issues S = Q K^T (tcgen05, M=128, N=128, K=256; Q dims 0..127 in tensor
+//               memory, 128..255 in shared memory)
+//   warp 1      issues O += P V (M=128, N=256, K=32 per V unit; P in tensor memory)
+//   warps 4-11  softmax: two warpgroups, one per 64-key half of a tile, a query row a thread;
+//               they also load Q and write the segment's result
+//   warps 12-15 widen K, warps 16-19 widen V: warp w owns keys 32w .. 32w+31 of every tile. It
+//               loads their codes and scales itself by TMA (a ring of its own: no exchange
+//               with other warps), takes a lane's row into registers, refills the ring and
+//               writes bf16 rows in the 128-byte-swizzled layout that the tensor cores read.
+// K is handed over in halves of 128 dims and V in units of 32 keys, so the tensor cores start
+// on the first piece of a tile while the rest is being widened.
+// Tensor memory: O [0, 256), S [256, 384), Q dims 0..127 [384, 448), P [448, 512).
+// Every wait is bounded; a wait that gives up raises the CTA's abort flag, which the others see.
+#include "ga_internal.h"
+#include "ga_q4.cuh"
+#include "ga_sm100.cuh"
+
+namespace ga {
+namespace {
+
+constexpr int kThreads = 640;
+constexpr int kBlockBytes = 128 * 128;    // 128 rows x 64 dims of bf16
+constexpr int kGranule = 32;              // keys per widening warp and tile; TMA box rows
+constexpr int kKStages = 2, kVStages = 1;
+constexpr int kRings = 4 * (kKStages + kVStages);
+constexpr int kRawBytes = kGranule * kQ4RowBytes, kRawScaleBytes = kGranule * kQ4ScaleBytes;
+constexpr int kMaxRowsWhole = 10;         // window rows up to which 12 heads fit in 128 lanes
+// Registers: launched at 96 a thread (640 x 96 = 61,440). The issuing warpgroup keeps 56, the
+// softmax warpgroups take 112, the widening ones keep 96: 128 x (56 + 2 x 112 + 2 x 96) = 60,416.
+constexpr int kRegsIssue = 56, kRegsSoftmax = 112;
+static_assert(128 * (kRegsIssue + 2 * kRegsSoftmax + 2 * 96) <= kThreads * 96, "register split");
+constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemQ = 384, kTmemP = 448;
+constexpr float kLog2eOver16 = 1.4426950408889634f / 16.0f;
+constexpr float kLazyRescale = 8.0f;   // O and l are rescaled when the maximum grows by > 2^8
+
+struct V4Smem {
+  uint8_t kt[4][kBlockBytes];              // K tile: 64-dim blocks of 128 keys
+  uint8_t vt[4][kBlockBytes];              // V units: 32 keys, four 64-dim blocks of 4 KiB each
+  uint8_t qhi[2][kBlockBytes];             // Q dims 128..255
+  uint8_t raw[kRings][kRawBytes];          // codes: the K warps' stages, then the V warps'
+  uint8_t rsc[kRings][kRawScaleBytes];
+  uint16_t tiles[kV4MaxSeq];               // key tiles of each sequence
+  float mx[2][2][128];                     // tile g: each half's row maximum, by g % 2
+  float stat_l[2][128];
+  uint64_t raw_full[kRings];
+  uint64_t k_full[2], k_empty[2], v_full[4], v_empty[4];
+  uint64_t q_full, s_full, s_free, p_full[2], p_empty[2], o_done, o_free, mx_bar;
+  uint64_t drain_qk, drain_pv;
+  int units, plane0, b0, tile0;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(V4Smem) <= 232448, "227 KiB of shared memory per CTA");
+
+__device__ __forceinline__ void record(int* status, int code) {
+  if (code) atomicCAS(status, 0, code);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const bool ok = mbar_wait(bar, parity, abort);
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// ------------------------------------------------------------------ the cut of the work
+// Key tiles (of `tile` keys) of a sequence: none when its slot is unused (negative length) or
+// its window passes the end of its page-table row, which is recorded.
+__device__ __forceinline__ int seq_tiles(const Verify4Args& a, int b, int tile, bool report) {
+  const int L = a.seq_len[b];
+  if (L < 0) return 0;
+  const long long keys = (long long)L + a.rows;
+  if (keys > (long long)a.max_pages * a.page_size || keys > GA_MAX_TOKENS) {
+    if (report) record(a.status, kDevBadPosition);
+    return 0;
+  }
+  return (int)((keys + tile - 1) / tile);
+}
+__host__ __device__ __forceinline__ int row_blocks(int rows) { return rows > kMaxRowsWhole ? 2 : 1; }
+
+// Tiles of every sequence into shared memory, by a block of kBlock threads.
+template <int kBlock>
+__device__ __forceinline__ void load_tiles(const Verify4Args& a, uint16_t* tiles, int tile, bool report) {
+  for (int b = threadIdx.x; b < a.n_seq; b += kBlock)
+    tiles[b] = (uint16_t)seq_tiles(a, b, tile, report);
+}
+// Sum of tiles[0 .. n - 1] by one warp (every lane gets it).
+__device__ __forceinline__ int warp_sum_tiles(const uint16_t* tiles, int n) {
+  int s = 0;
+  for (int b = threadIdx.x & 31; b < n; b += 32) s += tiles[b];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  return s;
+}
+
+// A CTA's share of the streams' tiles: `left` tiles from tile `tile` of stream (plane, b) on.
+// plane = 2 x row block + KV head; streams are ordered by plane, then sequence.
+struct Seg {
+  int plane, b, kt0, n;   // tiles kt0 .. kt0 + n - 1 of the stream
+  bool whole;             // all of the stream's tiles
+  int slot;               // partial slot of a segment that is not whole
+};
+struct Walk {
+  int plane, b, tile, left, seen;
+  __device__ __forceinline__ explicit Walk(const V4Smem& sm)
+      : plane(sm.plane0), b(sm.b0), tile(sm.tile0), left(sm.units), seen(0) {}
+  __device__ __forceinline__ bool next(const V4Smem& sm, const Verify4Args& a, Seg& s) {
+    if (left <= 0) return false;
+    int total = sm.tiles[b];
+    while (tile >= total) {   // the next stream with tiles
+      tile = 0;
+      if (++b == a.n_seq) {
+        b = 0;
+        ++plane;
+      }
+      total = sm.tiles[b];
+    }
+    s.plane = plane;
+    s.b = b;
+    s.kt0 = tile;
+    s.n = min(left, total - tile);
+    s.whole = s.n == total;
+    // of a CTA's segments only the first and the last can be parts of a stream
+    s.slot = 2 * (int)blockIdx.x + (seen ? 1 : 0);
+    ++seen;
+    tile += s.n;
+    left -= s.n;
+    return true;
+  }
+};
+
+// This CTA's part of the cut, by one warp: its first tile and number of tiles, into sm.
+__device__ __forceinline__ void find_share(V4Smem& sm, const Verify4Args& a) {
+  const int lane = threadIdx.x & 31;
+  const int planes = kKvHeads * row_blocks(a.rows);
+  const int per_plane = warp_sum_tiles(sm.tiles, a.n_seq);
+  const int total = per_plane * planes;
+  const int share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  const long long u0 = (long long)share * blockIdx.x;
+  const int units = (int)min((long long)share, max(0LL, (long long)total - u0));
+  int plane = 0, b0 = 0, tile0 = 0;
+  if (units > 0) {
+    plane = (int)(u0 / per_plane);
+    int rem = (int)(u0 - (long long)plane * per_plane);
+    // the sequence holding tile `rem` of the plane: sums of 32 sequences at a time
+    for (int base = 0; base < a.n_seq; base += 32) {
+      const int t = base + lane < a.n_seq ? sm.tiles[base + lane] : 0;
+      int inc = t;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += o;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, inc > rem);
+      if (past) {
+        const int k = __ffs((int)past) - 1;
+        b0 = base + k;
+        tile0 = rem - __shfl_sync(0xffffffffu, inc - t, k);
+        break;
+      }
+      rem -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  if (lane == 0) {
+    sm.units = units;
+    sm.plane0 = plane;
+    sm.b0 = b0;
+    sm.tile0 = tile0;
+  }
+}
+
+// ------------------------------------------------------------------ widening warps
+// One granule (32 keys x 128 code bytes and 32 x 16 scale bytes) per tile and warp.
+template <bool kV>
+__device__ void widen_worker(V4Smem& sm, const CUtensorMap* tm_c, const CUtensorMap* tm_s,
+                             const Verify4Args& a, volatile int* abort) {
+  constexpr int kStages = kV ? kVStages : kKStages;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+  const int st0 = kV ? 4 * kKStages + w * kVStages : w * kKStages;
+  const long long n_rows = (long long)a.n_pages * kKvHeads * a.page_size;
+  Walk ahead(sm);
+  Seg as{};
+  int aj = 0;            // next tile of `as` to load
+  int win_b = -1, win0 = 0, win_page = 0;   // 32 page-table entries of a sequence, one per lane
+  uint32_t issued = 0;
+  // the next granule of this warp, in the CTA's tile order, into its ring
+  auto issue = [&]() {
+    if (aj >= as.n) {
+      if (!ahead.next(sm, a, as)) return;
+      aj = 0;
+    }
+    const int key0 = (as.kt0 + aj) * kTileN + kGranule * w;
+    ++aj;
+    long long row = n_rows;   // past the pool: reads zeros (a granule with no key of the sequence)
+    if (key0 < a.seq_len[as.b] + a.rows) {
+      const int e = key0 / a.page_size;
+      if (win_b != as.b || e < win0 || e >= win0 + 32) {
+        win_b = as.b;
+        win0 = e;
+        const int idx = e + lane;
+        win_page = idx < a.max_pages ? __ldg(a.page_table + (size_t)as.b * a.max_pages + idx) : -1;
+      }
+      const int page = __shfl_sync(0xffffffffu, win_page, e - win0);
+      if (page >= 0 && page < a.n_pages)
+        row = ((long long)page * kKvHeads + (as.plane & 1)) * a.page_size + (key0 - e * a.page_size);
+      else if (lane == 0)
+        record(a.status, kDevBadPage);
+    }
+    const int st = st0 + (int)(issued % kStages);
+    mbar_expect_tx_warp(&sm.raw_full[st], kRawBytes + kRawScaleBytes);
+    tma_load_2d_warp(sm.raw[st], tm_c, &sm.raw_full[st], 0, (int)row);
+    tma_load_2d_warp(sm.rsc[st], tm_s, &sm.raw_full[st], 0, (int)row);
+    ++issued;
+  };
+  for (int i = 0; i < kStages; ++i) issue();
+  uint32_t g = 0;   // tiles done
+  const int units = sm.units;
+  bool ok = true;
+  for (; ok && (int)g < units; ++g) {
+    const int st = st0 + (int)(g % kStages);
+    if (!warp_wait(&sm.raw_full[st], (g / kStages) & 1, abort)) break;
+    // this lane's row: eight 16-byte chunks (swizzled by the copy) and 16 scale bytes
+    uint4 c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      c[i] = *reinterpret_cast<const uint4*>(sm.raw[st] + lane * kQ4RowBytes + ((i ^ (lane & 7)) << 4));
+    const uint4 sc = *reinterpret_cast<const uint4*>(sm.rsc[st] + lane * kQ4ScaleBytes);
+    const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
+    fence_async_smem();   // the reads come before the refill by the copy engine
+    __syncwarp();
+    issue();
+    // chunk i (dims 32i .. 32i + 31) is half a row of the 64-dim block i / 2
+    auto widen_chunk = [&](int i, uint8_t* block, uint32_t row) {
+      const uint32_t wd[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+      const uint32_t pair = scw[i >> 1] >> (16 * (i & 1));
+      const Q4Scale q0 = q4_scale(pair & 0xFFu), q1 = q4_scale((pair >> 8) & 0xFFu);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t o[4];
+        q4_widen(wd[j], j < 2 ? q0 : q1, o);
+        *reinterpret_cast<uint4*>(block + sw128_offset(row, (uint32_t)(4 * (i & 1) + j))) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    };
+    if (kV) {
+      if (!warp_wait(&sm.v_empty[w], (g & 1) ^ 1, abort)) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        widen_chunk(i, sm.vt[w] + (i >> 1) * (kGranule * 128), (uint32_t)lane);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.v_full[w]);
+    } else {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        if (!warp_wait(&sm.k_empty[hf], (g & 1) ^ 1, abort)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int i = 4 * hf; i < 4 * hf + 4; ++i)
+          widen_chunk(i, sm.kt[i >> 1], (uint32_t)(kGranule * w + lane));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.k_full[hf]);
+      }
+    }
+  }
+  if (*abort) {   // the copies in flight land before the CTA leaves
+    for (uint32_t f = issued > kStages ? issued - kStages : 0; f < issued; ++f)
+      mbar_wait_quiet(&sm.raw_full[st0 + (int)(f % kStages)], (f / kStages) & 1, 100000000LL);
+  }
+}
+
+// ------------------------------------------------------------------ MMA issue
+__device__ void qk_issue(V4Smem& sm, const Verify4Args& a, uint32_t tmem, volatile int* abort) {
+  constexpr uint32_t kId = idesc_bf16(128, kTileN, false, false);
+  const uint64_t k_desc = sdesc_sw128(smem_u32(sm.kt[0]), 16, 1024);
+  const uint64_t q_desc = sdesc_sw128(smem_u32(sm.qhi[0]), 16, 1024);
+  Walk walk(sm);
+  Seg seg;
+  uint32_t g = 0, done = 0;
+  while (walk.next(sm, a, seg)) {
+    if (!warp_wait(&sm.q_full, done & 1, abort)) return;
+    for (int j = 0; j < seg.n; ++j, ++g) {
+      if (g > 0 && !warp_wait(&sm.s_free, (g - 1) & 1, abort)) return;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        if (!warp_wait(&sm.k_full[hf], g & 1, abort)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const int blk = kk >> 2;
+          const uint64_t bd = k_desc + (uint64_t)((2 * hf + blk) * (kBlockBytes >> 4) + (kk & 3) * 2);
+          if (hf == 0)
+            umma_ts_warp(tmem + kTmemS, tmem + kTmemQ + kk * 8, bd, kId, kk > 0 ? 1u : 0u);
+          else
+            umma_ss_warp(tmem + kTmemS, q_desc + (uint64_t)(blk * (kBlockBytes >> 4) + (kk & 3) * 2),
+                         bd, kId, 1u);
+        }
+        umma_commit_warp(&sm.k_empty[hf]);
+      }
+      umma_commit_warp(&sm.s_full);
+    }
+    ++done;
+  }
+}
+
+__device__ void pv_issue(V4Smem& sm, const Verify4Args& a, uint32_t tmem, volatile int* abort) {
+  constexpr uint32_t kId = idesc_bf16(128, kDim, false, true);
+  const uint64_t v_desc = sdesc_sw128(smem_u32(sm.vt[0]), kGranule * 128, 1024);
+  Walk walk(sm);
+  Seg seg;
+  uint32_t g = 0, done = 0;
+  while (walk.next(sm, a, seg)) {
+    if (done > 0 && !warp_wait(&sm.o_free, (done - 1) & 1, abort)) return;
+    for (int j = 0; j < seg.n; ++j, ++g) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if ((u & 1) == 0 && !warp_wait(&sm.p_full[u >> 1], g & 1, abort)) return;
+        if (!warp_wait(&sm.v_full[u], g & 1, abort)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2)
+          umma_ts_warp(tmem + kTmemO, tmem + kTmemP + 16 * u + 8 * k2,
+                       v_desc + (uint64_t)(u * (kBlockBytes >> 4) + k2 * (2048 >> 4)), kId,
+                       (j > 0 || u > 0 || k2 > 0) ? 1u : 0u);
+        umma_commit_warp(&sm.v_empty[u]);
+        if (u & 1) umma_commit_warp(&sm.p_empty[u >> 1]);   // [1]: O holds every P V so far
+      }
+    }
+    umma_commit_warp(&sm.o_done);
+    ++done;
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+__device__ __forceinline__ float sigmoid_f(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// Warpgroup hf takes keys 64 hf .. + 63 of every tile, and dims 128 hf .. + 127 of Q and O.
+__device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, int hf,
+                               volatile int* abort) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = (warp & 3) * 32 + lane;
+  const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t s_taddr = tmem + kTmemS + lane_off + 64 * hf;
+  const uint32_t o_taddr = tmem + kTmemO + lane_off + 128 * hf;
+  const int heads = kGroup / row_blocks(a.rows);       // query heads of a row block
+  const int rr = r / heads, hh = r - rr * heads;
+  const bool valid = rr < a.rows;
+  uint32_t g = 0, done = 0, mxn = 0;
+  // one exchange between the two warpgroups: what each wrote before is read after
+  auto exchange = [&]() -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.mx_bar);
+    const bool ok = warp_wait(&sm.mx_bar, mxn & 1, abort);
+    ++mxn;
+    return ok;
+  };
+  Walk walk(sm);
+  Seg seg;
+  while (walk.next(sm, a, seg)) {
+    const int L = a.seq_len[seg.b];
+    const int limit = L + min(rr, a.rows - 1);   // the row's last visible key
+    const int h = (seg.plane & 1) * kGroup + (seg.plane >> 1) * heads + hh;
+    const size_t row = (size_t)seg.b * a.rows + rr;
+    {   // Q: dims 0..127 to tensor memory, 128..255 to shared memory. Both places are free: this
+        // warp has seen the last S of the segment before, so its Q K^T are done.
+      const uint4* qp = reinterpret_cast<const uint4*>(a.q_prep + (row * kHeads + h) * kDim) + 16 * hf;
+#pragma unroll
+      for (int c0 = 0; c0 < 16; c0 += 8) {
+        uint32_t x[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 t = valid ? __ldg(qp + c0 + i) : make_uint4(0u, 0u, 0u, 0u);
+          x[4 * i] = t.x; x[4 * i + 1] = t.y; x[4 * i + 2] = t.z; x[4 * i + 3] = t.w;
+        }
+        if (hf == 0) {
+          tc_fence_after();
+          tmem_st32(tmem + kTmemQ + lane_off + 4 * c0, x);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(sm.qhi[c0 >> 3] + sw128_offset((uint32_t)r, (uint32_t)i)) =
+                make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        }
+      }
+      if (hf == 0) {
+        tmem_wait_st();
+        tc_fence_before();
+      } else {
+        fence_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+    }
+    float M = -INFINITY, l = 0.f;
+    for (int j = 0; j < seg.n; ++j, ++g) {
+      const int key0 = (seg.kt0 + j) * kTileN + 64 * hf;
+      if (!warp_wait(&sm.s_full, g & 1, abort)) return;
+      tc_fence_after();
+      uint32_t sb[64];
+      tmem_ld32(s_taddr, *reinterpret_cast<uint32_t(*)[32]>(sb));
+      tmem_ld32(s_taddr + 32, *reinterpret_cast<uint32_t(*)[32]>(sb + 32));
+      tmem_wait_ld(sb);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.s_free);
+      if (key0 + 63 > L) {   // some key of the half is hidden from some row
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (key0 + k > limit) sb[k] = 0xFF800000u;   // -inf: weight 0, never the maximum
+      }
+      auto f = [&](int k) { return __uint_as_float(sb[k]); };
+      float m0 = f(0), m1 = f(1), m2 = f(2), m3 = f(3);
+#pragma unroll
+      for (int k = 4; k + 7 < 64; k += 8) {
+        m0 = max3(m0, f(k), f(k + 1));
+        m1 = max3(m1, f(k + 2), f(k + 3));
+        m2 = max3(m2, f(k + 4), f(k + 5));
+        m3 = max3(m3, f(k + 6), f(k + 7));
+      }
+      m0 = max3(m0, f(60), f(61));
+      m1 = max3(m1, f(62), f(63));
+      const float mine = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+      sm.mx[g & 1][hf][r] = mine;
+      if (!exchange()) return;
+      const float top = fmaxf(mine, sm.mx[g & 1][hf ^ 1][r]) * kLog2eOver16;
+      // M starts at the first visible tile's maximum and grows when that is passed by > 2^8
+      const bool grow = top > M + kLazyRescale;
+      const float newM = grow ? top : M;
+      if (__any_sync(0xffffffffu, grow && M != -INFINITY)) {
+        // O must hold every P V before it is scaled (the other half's last store waited for the
+        // P V before the last, and the exchange came after it, so this phase is the next one)
+        if (!warp_wait(&sm.p_empty[1], (g - 1) & 1, abort)) return;
+        tc_fence_after();
+        const float sc = (grow && M != -INFINITY) ? exp2f(M - newM) : 1.0f;
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_taddr + c0, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sc);
+          tmem_st32(o_taddr + c0, o);
+        }
+        tmem_wait_st();
+        l *= sc;
+      }
+      M = newM;
+      const float mf = M == -INFINITY ? 0.f : M;
+      float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float p0 = ex2_approx(fmaf(f(2 * k), kLog2eOver16, -mf));
+        const float p1 = ex2_approx(fmaf(f(2 * k + 1), kLog2eOver16, -mf));
+        sb[k] = pack_bf16x2(p0, p1);   // an index already read
+        if (k & 1) add_bf16x2(l2, l3, sb[k]);
+        else add_bf16x2(l0, l1, sb[k]);
+      }
+      l += (l0 + l2) + (l1 + l3);
+      if (g > 0 && !warp_wait(&sm.p_empty[hf], (g - 1) & 1, abort)) return;
+      tc_fence_after();
+      tmem_st32(tmem + kTmemP + lane_off + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(sb));
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_full[hf]);
+    }
+    // the segment's result
+    sm.stat_l[hf][r] = l;
+    if (!exchange()) return;
+    l += sm.stat_l[hf ^ 1][r];
+    if (!warp_wait(&sm.o_done, done & 1, abort)) return;
+    tc_fence_after();
+    const float inv = l > 0.f ? 1.0f / l : (l != l ? l : 0.f);
+    const size_t prow = (size_t)seg.slot * 128 + r;
+    float4* po = reinterpret_cast<float4*>(a.part_o + prow * kDim + 128 * hf);
+    const uint4* gp = reinterpret_cast<const uint4*>(a.qg + (row * kHeads + h) * kQgStride + kDim + 128 * hf);
+    uint4* op = reinterpret_cast<uint4*>(a.out + (row * kHeads + h) * kDim + 128 * hf);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      tmem_ld32(o_taddr + 32 * c, o);
+      tmem_wait_ld(o);
+      if (valid && seg.whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 gt = __ldg(gp + 4 * c + i);
+          const uint32_t gw[4] = {gt.x, gt.y, gt.z, gt.w};
+          uint32_t res[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            res[q] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * q]) * inv * sigmoid_f(lo_f(gw[q])),
+                                 __uint_as_float(o[8 * i + 2 * q + 1]) * inv * sigmoid_f(hi_f(gw[q])));
+          op[4 * c + i] = make_uint4(res[0], res[1], res[2], res[3]);
+        }
+      } else if (valid) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          po[8 * c + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                      __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+      }
+    }
+    if (valid && !seg.whole && hf == 0)
+      reinterpret_cast<float2*>(a.part_ml)[prow] = make_float2(M, l);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.o_free);
+    ++done;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    verify4_kernel(const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
+                   const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
+                   const __grid_constant__ Verify4Args a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if ((smem_u32(smem_raw) & 1023u) != 0u) {
+    if (threadIdx.x == 0) record(a.status, kDevBadLaunch);
+    return;
+  }
+  V4Smem& sm = *reinterpret_cast<V4Smem*>(smem_raw);
+  const int warp = threadIdx.x >> 5;
+  volatile int* abort = &sm.abort;
+  load_tiles<kThreads>(a, sm.tiles, kTileN, blockIdx.x == 0);
+  if (threadIdx.x == 0) {
+    sm.abort = 0;
+    for (int i = 0; i < kRings; ++i) mbar_init(&sm.raw_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.k_full[i], 4);    // one arrival per widening warp
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.p_full[i], 4);    // per softmax warp of the half
+      mbar_init(&sm.p_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_empty[i], 1);
+    }
+    mbar_init(&sm.q_full, 8);         // per softmax warp
+    mbar_init(&sm.s_full, 1);
+    mbar_init(&sm.s_free, 8);
+    mbar_init(&sm.o_done, 1);
+    mbar_init(&sm.o_free, 8);
+    mbar_init(&sm.mx_bar, 8);
+    mbar_init(&sm.drain_qk, 1);
+    mbar_init(&sm.drain_pv, 1);
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) find_share(sm, a);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 0 && sm.units > 0) {
+      qk_issue(sm, a, tmem, abort);
+      umma_commit_warp(&sm.drain_qk);
+      mbar_wait_quiet(&sm.drain_qk, 0, 100000000LL);
+    }
+    if (warp == 1 && sm.units > 0) {
+      pv_issue(sm, a, tmem, abort);
+      umma_commit_warp(&sm.drain_pv);
+      mbar_wait_quiet(&sm.drain_pv, 0, 100000000LL);
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    softmax_worker(sm, a, tmem, (warp - 4) >> 2, abort);
+  } else {
+    if (warp < 16) widen_worker<false>(sm, &tm_kc, &tm_ks, a, abort);
+    else widen_worker<true>(sm, &tm_vc, &tm_vs, a, abort);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && sm.abort) record(a.status, sm.abort);
+}
+
+// ------------------------------------------------------------------ combine
+// A block per (sequence, window row, query head): the partials of its stream, if the cut left
+// it in parts. Four warps take every fourth part, eight dims a lane, and join in shared memory.
+constexpr int kCombineThreads = 128;
+__global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
+    const __grid_constant__ Verify4Args a, int ctas) {
+  __shared__ uint16_t tiles[kV4MaxSeq];
+  __shared__ float so[4][kDim], sml[4][2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = blockIdx.x % kHeads, rr = (blockIdx.x / kHeads) % a.rows;
+  const int b = blockIdx.x / (kHeads * a.rows);
+  load_tiles<kCombineThreads>(a, tiles, kTileN, false);
+  __syncthreads();
+  if (tiles[b] == 0) return;
+  const int blocks = row_blocks(a.rows), heads = kGroup / blocks;
+  const int per_plane = warp_sum_tiles(tiles, a.n_seq);
+  const int before = warp_sum_tiles(tiles, b);
+  const int total = per_plane * kKvHeads * blocks;
+  const int share = (total + ctas - 1) / ctas;
+  const int kvh = h / kGroup, hg = h % kGroup;
+  const int plane = 2 * (hg / heads) + kvh;
+  const long long u0 = (long long)plane * per_plane + before, u1 = u0 + tiles[b] - 1;
+  const int c0 = (int)(u0 / share), c1 = (int)(u1 / share);
+  if (c0 == c1) return;   // one CTA ran the whole stream and wrote it
+  const int r = rr * heads + hg % heads;
+  // CTA c's part is its first segment unless the stream began inside the CTA's run
+  auto part_row = [&](int c) -> size_t {
+    const int slot = 2 * c + ((long long)c * share < u0 ? 1 : 0);
+    return (size_t)slot * 128 + r;
+  };
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+  float M = -INFINITY, L = 0.f, o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  for (int c = c0 + warp; c <= c1; c += 4) {
+    const size_t pr = part_row(c);
+    const float2 x = ml[pr];
+    const float4* p = reinterpret_cast<const float4*>(a.part_o + pr * kDim + 8 * lane);
+    const float4 v0 = p[0], v1 = p[1];
+    if (x.x == -INFINITY && x.y == 0.f) continue;   // no key of the part is visible to the row
+    const float newM = fmaxf(M, x.x);
+    const float fa = M == -INFINITY ? 0.f : exp2f(M - newM), fb = exp2f(x.x - newM);
+    const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], fb, o[i] * fa);
+    L = fmaf(x.y, fb, L * fa);
+    M = newM;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) so[warp][8 * lane + i] = o[i];
+  if (lane == 0) {
+    sml[warp][0] = M;
+    sml[warp][1] = L;
+  }
+  __syncthreads();
+  float Mt = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) Mt = fmaxf(Mt, sml[w][0]);
+  float Lt = 0.f, x0 = 0.f, x1 = 0.f;
+  const int d = 2 * threadIdx.x;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = sml[w][0] == -INFINITY ? 0.f : exp2f(sml[w][0] - Mt);
+    Lt = fmaf(sml[w][1], f, Lt);
+    x0 = fmaf(so[w][d], f, x0);
+    x1 = fmaf(so[w][d + 1], f, x1);
+  }
+  const float inv = Lt > 0.f ? 1.0f / Lt : (Lt != Lt ? Lt : 0.f);
+  const size_t row = ((size_t)b * a.rows + rr) * kHeads + h;
+  const uint32_t gw = __ldg(reinterpret_cast<const uint32_t*>(a.qg + row * kQgStride + kDim + d));
+  reinterpret_cast<uint32_t*>(a.out + row * kDim + d)[0] =
+      pack_bf16x2(x0 * inv * sigmoid_f(lo_f(gw)), x1 * inv * sigmoid_f(hi_f(gw)));
+}
+
+}  // namespace
+
+size_t verify4_ws_bytes() {
+  return (size_t)2 * kV4MaxCtas * 128 * (kDim + 2) * sizeof(float);
+}
+
+cudaError_t verify4_set_attributes() {
+  return cudaFuncSetAttribute(verify4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)sizeof(V4Smem));
+}
+
+cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
+                           const CUtensorMap& k_scales, const CUtensorMap& v_scales,
+                           const Verify4Args& a, int sm_count, cudaStream_t s) {
+  const int ctas = sm_count < kV4MaxCtas ? sm_count : kV4MaxCtas;
+  verify4_kernel<<<ctas, kThreads, sizeof(V4Smem), s>>>(k_codes, v_codes, k_scales, v_scales, a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  verify4_combine_kernel<<<a.n_seq * a.rows * kHeads, kCombineThreads, 0, s>>>(a, ctas);
+  return cudaGetLastError();
+}
+
+}  // namespace ga
