@@ -1391,7 +1391,7 @@ int ga_attn_verify_q4(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k
     a.page_table = page_table + (size_t)g0 * max_pages;
     a.seq_len = seq_len + g0;
     a.part_o = static_cast<float*>(workspace);
-    a.part_ml = a.part_o + (size_t)2 * kV4MaxCtas * 128 * kDim;
+    a.part_ml = a.part_o + (size_t)2 * kV4MaxCtas * kV4Lanes * kDim;
     a.status = dev->status_word;
     const cudaError_t e =
         GA_CUDA(launch_verify4(kc, vc, ks, vs, a, dev->sm_count, (cudaStream_t)stream));

@@ -7,7 +7,7 @@
 // so their normalisation is consistent); the output is rounded once.
 //
 // Work. A stream is (sequence, KV head, query-row block): the 12 query heads of the group and
-// every window row when that makes at most 128 rows, else two blocks of 6 heads. A stream's
+// every window row when that makes at most 96 rows, else two blocks of 6 heads. A stream's
 // keys are tiles of 128. The streams' tiles, end to end, are cut into equal runs, one per CTA
 // (one CTA per SM), so any mix of lengths fills the device evenly: a CTA may end one stream
 // and begin another. The lengths are read on the device; every role of every CTA derives the
@@ -17,16 +17,20 @@
 //
 // Structure (640 threads, 20 warps):
 //   warp 0      issues S = Q K^T (tcgen05, M=128, N=128, K=256; Q dims 0..127 in tensor
-//               memory, 128..255 in shared memory)
-//   warp 1      issues O += P V (M=128, N=256, K=32 per V unit; P in tensor memory)
-//   warps 4-11  softmax: two warpgroups, one per 64-key half of a tile, a query row a thread;
-//               they also load Q and write the segment's result
-//   warps 12-15 widen K, warps 16-19 widen V: warp w owns keys 32w .. 32w+31 of every tile. It
-//               loads their codes and scales itself by TMA (a ring of its own: no exchange
-//               with other warps), takes a lane's row into registers, refills the ring and
-//               writes bf16 rows in the 128-byte-swizzled layout that the tensor cores read.
-// K is handed over in halves of 128 dims and V in units of 32 keys, so the tensor cores start
-// on the first piece of a tile while the rest is being widened.
+//               memory, 128..255 in shared memory; lanes past the 96 rows hold whatever is there, and
+//               nothing reads their results)
+//   warp 1      issues O += P V (M=128, N=256, K=32 per piece of V; P in tensor memory)
+//   warps 4-11  softmax: two warpgroups, one per 64-key half of a tile, a query row a thread
+//               (warps without rows are idle); they also load Q and write the segment's result
+//   warps 2, 3  load the codes and scales of K and V tiles by TMA, a granule of 32 keys a lane
+//               (a page holds a multiple of that), through two stages each
+//   warps 12-15 widen K, warps 16-19 widen V: a lane turns 64 codes of one row into the 128 bytes
+//               of a row of the 128-byte-swizzled blocks that the tensor cores read
+// K is handed over in four pieces of 64 dims and V in four of 32 keys (16 KiB each), so the
+// tensor cores start on the first piece of a tile while the rest is being widened, and give
+// its place back as soon as they have read it. The roles run different code at
+// once and share the instruction cache: the widening loop is one short body for K and V (with
+// the rows unrolled through registers the widening alone took 3,500 cycles a tile).
 // Tensor memory: O [0, 256), S [256, 384), Q dims 0..127 [384, 448), P [448, 512).
 // Every wait is bounded; a wait that gives up raises the CTA's abort flag, which the others see.
 #include "ga_internal.h"
@@ -38,30 +42,30 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kBlockBytes = 128 * 128;    // 128 rows x 64 dims of bf16
-constexpr int kGranule = 32;              // keys per widening warp and tile; TMA box rows
-constexpr int kKStages = 2, kVStages = 1;
-constexpr int kRings = 4 * (kKStages + kVStages);
-constexpr int kRawBytes = kGranule * kQ4RowBytes, kRawScaleBytes = kGranule * kQ4ScaleBytes;
-constexpr int kMaxRowsWhole = 10;         // window rows up to which 12 heads fit in 128 lanes
-// Registers: launched at 96 a thread (640 x 96 = 61,440). The issuing warpgroup keeps 56, the
-// softmax warpgroups take 112, the widening ones keep 96: 128 x (56 + 2 x 112 + 2 x 96) = 60,416.
-constexpr int kRegsIssue = 56, kRegsSoftmax = 112;
-static_assert(128 * (kRegsIssue + 2 * kRegsSoftmax + 2 * 96) <= kThreads * 96, "register split");
+constexpr int kGranule = 32;              // keys per TMA box
+constexpr int kStages = 2;                // raw tiles in flight, for K and for V
+constexpr int kRawBytes = kTileN * kQ4RowBytes, kRawScaleBytes = kTileN * kQ4ScaleBytes;
+constexpr int kQBlockBytes = kV4Lanes * 128;      // 64 dims of the query rows
+constexpr int kMaxRowsWhole = kV4Lanes / kGroup;  // window rows up to which 12 heads fit
+// Registers: launched at 96 a thread (640 x 96 = 61,440). The issuing warpgroup keeps 64, the
+// softmax warpgroups take 136, the widening ones keep 72: 128 x (64 + 2 x 136 + 2 x 72) = 61,440.
+constexpr int kRegsIssue = 64, kRegsSoftmax = 136, kRegsWiden = 72;
+static_assert(128 * (kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsWiden) <= kThreads * 96,
+              "register split");
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemQ = 384, kTmemP = 448;
 constexpr float kLog2eOver16 = 1.4426950408889634f / 16.0f;
 constexpr float kLazyRescale = 8.0f;   // O and l are rescaled when the maximum grows by > 2^8
 
 struct V4Smem {
   uint8_t kt[4][kBlockBytes];              // K tile: 64-dim blocks of 128 keys
-  uint8_t vt[4][kBlockBytes];              // V units: 32 keys, four 64-dim blocks of 4 KiB each
-  uint8_t qhi[2][kBlockBytes];             // Q dims 128..255
-  uint8_t raw[kRings][kRawBytes];          // codes: the K warps' stages, then the V warps'
-  uint8_t rsc[kRings][kRawScaleBytes];
+  uint8_t vt[4][kBlockBytes];              // V tile: pieces of 32 keys, four 64-dim blocks each
+  uint8_t qhi[2][kQBlockBytes];            // Q dims 128..255 (the MMA reads 32 rows past each block)
+  uint8_t raw[2 * kStages][kRawBytes];     // code rows: K's stages, then V's
+  uint8_t rsc[2 * kStages][kRawScaleBytes];
   uint16_t tiles[kV4MaxSeq];               // key tiles of each sequence
-  float mx[2][2][128];                     // tile g: each half's row maximum, by g % 2
-  float stat_l[2][128];
-  uint64_t raw_full[kRings];
-  uint64_t k_full[2], k_empty[2], v_full[4], v_empty[4];
+  float mx[2][2][kV4Lanes];                // exchange i: each half's row value, by i % 2
+  uint64_t raw_full[2 * kStages], raw_empty[2 * kStages];
+  uint64_t full[8], empty[8];              // pieces of the K tile, then of the V tile
   uint64_t q_full, s_full, s_free, p_full[2], p_empty[2], o_done, o_free, mx_bar;
   uint64_t drain_qk, drain_pv;
   int units, plane0, b0, tile0;
@@ -76,6 +80,32 @@ __device__ __forceinline__ void record(int* status, int code) {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const bool ok = mbar_wait(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_v4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+// A tensor load by the calling thread alone.
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -189,106 +219,111 @@ __device__ __forceinline__ void find_share(V4Smem& sm, const Verify4Args& a) {
   }
 }
 
-// ------------------------------------------------------------------ widening warps
-// One granule (32 keys x 128 code bytes and 32 x 16 scale bytes) per tile and warp.
-template <bool kV>
-__device__ void widen_worker(V4Smem& sm, const CUtensorMap* tm_c, const CUtensorMap* tm_s,
-                             const Verify4Args& a, volatile int* abort) {
-  constexpr int kStages = kV ? kVStages : kKStages;
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
-  const int st0 = kV ? 4 * kKStages + w * kVStages : w * kKStages;
+// ------------------------------------------------------------------ loading codes
+// Tiles of K (is_v 0) or V (1): four boxes of 32 code rows and four of 32 scale rows, by lanes
+// 0 .. 3. A granule with no key of the sequence, or on a page outside the pool (recorded), is
+// read past the pool's end, which gives zeros.
+__device__ void raw_loader(V4Smem& sm, const CUtensorMap* tm_c, const CUtensorMap* tm_s, int is_v,
+                           const Verify4Args& a, volatile int* abort) {
+  const int lane = threadIdx.x & 31;
   const long long n_rows = (long long)a.n_pages * kKvHeads * a.page_size;
-  Walk ahead(sm);
-  Seg as{};
-  int aj = 0;            // next tile of `as` to load
-  int win_b = -1, win0 = 0, win_page = 0;   // 32 page-table entries of a sequence, one per lane
-  uint32_t issued = 0;
-  // the next granule of this warp, in the CTA's tile order, into its ring
-  auto issue = [&]() {
-    if (aj >= as.n) {
-      if (!ahead.next(sm, a, as)) return;
-      aj = 0;
-    }
-    const int key0 = (as.kt0 + aj) * kTileN + kGranule * w;
-    ++aj;
-    long long row = n_rows;   // past the pool: reads zeros (a granule with no key of the sequence)
-    if (key0 < a.seq_len[as.b] + a.rows) {
+  uint32_t f = 0;   // tiles issued
+  Walk walk(sm);
+  Seg seg;
+  while (walk.next(sm, a, seg)) {
+    const int end = a.seq_len[seg.b] + a.rows;
+    const int* table = a.page_table + (size_t)seg.b * a.max_pages;
+    // the pool row of this lane's granule of tile kt
+    auto row_of = [&](int kt) -> int {
+      const int key0 = kt * kTileN + kGranule * (lane & 3);
+      if (key0 >= end) return (int)n_rows;
       const int e = key0 / a.page_size;
-      if (win_b != as.b || e < win0 || e >= win0 + 32) {
-        win_b = as.b;
-        win0 = e;
-        const int idx = e + lane;
-        win_page = idx < a.max_pages ? __ldg(a.page_table + (size_t)as.b * a.max_pages + idx) : -1;
+      const int page = __ldg(table + e);
+      if (page < 0 || page >= a.n_pages) {
+        if (lane < 4) record(a.status, kDevBadPage);
+        return (int)n_rows;
       }
-      const int page = __shfl_sync(0xffffffffu, win_page, e - win0);
-      if (page >= 0 && page < a.n_pages)
-        row = ((long long)page * kKvHeads + (as.plane & 1)) * a.page_size + (key0 - e * a.page_size);
-      else if (lane == 0)
-        record(a.status, kDevBadPage);
-    }
-    const int st = st0 + (int)(issued % kStages);
-    mbar_expect_tx_warp(&sm.raw_full[st], kRawBytes + kRawScaleBytes);
-    tma_load_2d_warp(sm.raw[st], tm_c, &sm.raw_full[st], 0, (int)row);
-    tma_load_2d_warp(sm.rsc[st], tm_s, &sm.raw_full[st], 0, (int)row);
-    ++issued;
-  };
-  for (int i = 0; i < kStages; ++i) issue();
-  uint32_t g = 0;   // tiles done
-  const int units = sm.units;
-  bool ok = true;
-  for (; ok && (int)g < units; ++g) {
-    const int st = st0 + (int)(g % kStages);
-    if (!warp_wait(&sm.raw_full[st], (g / kStages) & 1, abort)) break;
-    // this lane's row: eight 16-byte chunks (swizzled by the copy) and 16 scale bytes
-    uint4 c[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      c[i] = *reinterpret_cast<const uint4*>(sm.raw[st] + lane * kQ4RowBytes + ((i ^ (lane & 7)) << 4));
-    const uint4 sc = *reinterpret_cast<const uint4*>(sm.rsc[st] + lane * kQ4ScaleBytes);
-    const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
-    fence_async_smem();   // the reads come before the refill by the copy engine
-    __syncwarp();
-    issue();
-    // chunk i (dims 32i .. 32i + 31) is half a row of the 64-dim block i / 2
-    auto widen_chunk = [&](int i, uint8_t* block, uint32_t row) {
-      const uint32_t wd[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-      const uint32_t pair = scw[i >> 1] >> (16 * (i & 1));
-      const Q4Scale q0 = q4_scale(pair & 0xFFu), q1 = q4_scale((pair >> 8) & 0xFFu);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t o[4];
-        q4_widen(wd[j], j < 2 ? q0 : q1, o);
-        *reinterpret_cast<uint4*>(block + sw128_offset(row, (uint32_t)(4 * (i & 1) + j))) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-      }
+      return (int)(((long long)page * kKvHeads + (seg.plane & 1)) * a.page_size) + key0 - e * a.page_size;
     };
-    if (kV) {
-      if (!warp_wait(&sm.v_empty[w], (g & 1) ^ 1, abort)) break;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        widen_chunk(i, sm.vt[w] + (i >> 1) * (kGranule * 128), (uint32_t)lane);
-      fence_async_smem();
+    int row = row_of(seg.kt0);
+    for (int j = 0; j < seg.n; ++j, ++f) {
+      const int here = row;
+      if (j + 1 < seg.n) row = row_of(seg.kt0 + j + 1);   // in flight during the wait
+      const int st = kStages * is_v + (int)(f % kStages);
+      if (!warp_wait(&sm.raw_empty[st], ((f / kStages) & 1) ^ 1, abort)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[st], kRawBytes + kRawScaleBytes);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_full[w]);
-    } else {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (!warp_wait(&sm.k_empty[hf], (g & 1) ^ 1, abort)) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int i = 4 * hf; i < 4 * hf + 4; ++i)
-          widen_chunk(i, sm.kt[i >> 1], (uint32_t)(kGranule * w + lane));
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.k_full[hf]);
+      if (lane < 4) {
+        tma_load_2d(sm.raw[st] + lane * (kGranule * kQ4RowBytes), tm_c, &sm.raw_full[st], 0, here);
+        tma_load_2d(sm.rsc[st] + lane * (kGranule * kQ4ScaleBytes), tm_s, &sm.raw_full[st], 0, here);
       }
     }
+    if (*abort) break;
   }
   if (*abort) {   // the copies in flight land before the CTA leaves
-    for (uint32_t f = issued > kStages ? issued - kStages : 0; f < issued; ++f)
-      mbar_wait_quiet(&sm.raw_full[st0 + (int)(f % kStages)], (f / kStages) & 1, 100000000LL);
+    for (uint32_t i = f > kStages ? f - kStages : 0; i < f; ++i)
+      mbar_wait_quiet(&sm.raw_full[kStages * is_v + (int)(i % kStages)], (i / kStages) & 1, 100000000LL);
+  }
+}
+
+// ------------------------------------------------------------------ widening
+// Warp w of four. K, piece u (64-dim block u): keys 32w .. 32w+31, a key a lane. V, piece u (keys
+// 32u ..): keys 32u + 8w .. + 7, four lanes a key, a 64-dim block each. Eight neighbouring lanes
+// always hold eight neighbouring rows, so the swizzle keeps reads and writes free of bank
+// conflicts.
+__device__ void widen_worker(V4Smem& sm, int is_v, volatile int* abort) {
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+  const uint32_t row0 = is_v ? 8 * w + (lane & 7) : 32 * w + lane;   // the lane's row in piece 0
+  const uint32_t blk0 = is_v ? (uint32_t)lane >> 3 : 0;              // and 64-dim block of it
+  const uint32_t xr = row0 & 7;
+  const uint32_t src_u = is_v ? kGranule * kQ4RowBytes : 0u;         // from piece to piece
+  const uint32_t scs_u = is_v ? kGranule * kQ4ScaleBytes : 4u;
+  const uint32_t ch_u = is_v ? 0u : 2u;
+  const uint32_t dst0 = smem_u32(is_v ? sm.vt[0] : sm.kt[0]) + (row0 >> 3) * 1024u + xr * 128u +
+                        blk0 * (kGranule * 128u);
+  uint64_t* full = sm.full + 4 * is_v;
+  uint64_t* empty = sm.empty + 4 * is_v;
+  const int n = sm.units;
+  for (int g = 0; g < n; ++g) {
+    const int st = kStages * is_v + g % kStages;
+    if (!warp_wait(&sm.raw_full[st], (g / kStages) & 1, abort)) return;
+    uint32_t src = smem_u32(sm.raw[st]) + row0 * kQ4RowBytes;
+    uint32_t scs = smem_u32(sm.rsc[st]) + row0 * kQ4ScaleBytes + 4 * blk0;
+    uint32_t ch = 2 * blk0, dst = dst0;   // 16-byte chunk of the row; destination row
+    uint32_t sc = lds_u32(scs);
+    uint4 c0 = lds_v4(src + ((ch ^ xr) << 4)), c1 = lds_v4(src + (((ch + 1) ^ xr) << 4));
+#pragma unroll 1
+    for (int u = 0; u < 4; ++u) {
+      if (!warp_wait(&empty[u], (g & 1) ^ 1, abort)) return;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 c = i ? c1 : c0;
+        const uint32_t wd[4] = {c.x, c.y, c.z, c.w};
+        const Q4Scale q0 = q4_scale((sc >> (16 * i)) & 0xFFu);
+        const Q4Scale q1 = q4_scale((sc >> (16 * i + 8)) & 0xFFu);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t o[4];
+          q4_widen(wd[j], j < 2 ? q0 : q1, o);
+          sts_v4(dst + (((uint32_t)(4 * i + j) ^ xr) << 4), o);
+        }
+      }
+      if (u < 3) {   // the next piece's codes, while the stores drain
+        src += src_u;
+        scs += scs_u;
+        ch += ch_u;
+        dst += kBlockBytes;
+        sc = lds_u32(scs);
+        c0 = lds_v4(src + ((ch ^ xr) << 4));
+        c1 = lds_v4(src + (((ch + 1) ^ xr) << 4));
+      }
+      fence_async_smem();   // the tensor cores read what the lanes wrote
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&full[u]);
+        if (u == 3) mbar_arrive(&sm.raw_empty[st]);
+      }
+    }
   }
 }
 
@@ -305,20 +340,20 @@ __device__ void qk_issue(V4Smem& sm, const Verify4Args& a, uint32_t tmem, volati
     for (int j = 0; j < seg.n; ++j, ++g) {
       if (g > 0 && !warp_wait(&sm.s_free, (g - 1) & 1, abort)) return;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (!warp_wait(&sm.k_full[hf], g & 1, abort)) return;
+      for (int u = 0; u < 4; ++u) {
+        if (!warp_wait(&sm.full[u], g & 1, abort)) return;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const int blk = kk >> 2;
-          const uint64_t bd = k_desc + (uint64_t)((2 * hf + blk) * (kBlockBytes >> 4) + (kk & 3) * 2);
-          if (hf == 0)
-            umma_ts_warp(tmem + kTmemS, tmem + kTmemQ + kk * 8, bd, kId, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t bd = k_desc + (uint64_t)(u * (kBlockBytes >> 4) + kk * 2);
+          if (u < 2)
+            umma_ts_warp(tmem + kTmemS, tmem + kTmemQ + 32 * u + 8 * kk, bd, kId,
+                         (u > 0 || kk > 0) ? 1u : 0u);
           else
-            umma_ss_warp(tmem + kTmemS, q_desc + (uint64_t)(blk * (kBlockBytes >> 4) + (kk & 3) * 2),
+            umma_ss_warp(tmem + kTmemS, q_desc + (uint64_t)((u - 2) * (kQBlockBytes >> 4) + kk * 2),
                          bd, kId, 1u);
         }
-        umma_commit_warp(&sm.k_empty[hf]);
+        umma_commit_warp(&sm.empty[u]);
       }
       umma_commit_warp(&sm.s_full);
     }
@@ -338,14 +373,14 @@ __device__ void pv_issue(V4Smem& sm, const Verify4Args& a, uint32_t tmem, volati
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if ((u & 1) == 0 && !warp_wait(&sm.p_full[u >> 1], g & 1, abort)) return;
-        if (!warp_wait(&sm.v_full[u], g & 1, abort)) return;
+        if (!warp_wait(&sm.full[4 + u], g & 1, abort)) return;
         tc_fence_after();
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2)
-          umma_ts_warp(tmem + kTmemO, tmem + kTmemP + 16 * u + 8 * k2,
-                       v_desc + (uint64_t)(u * (kBlockBytes >> 4) + k2 * (2048 >> 4)), kId,
-                       (j > 0 || u > 0 || k2 > 0) ? 1u : 0u);
-        umma_commit_warp(&sm.v_empty[u]);
+        for (int kk = 0; kk < 2; ++kk)
+          umma_ts_warp(tmem + kTmemO, tmem + kTmemP + 16 * u + 8 * kk,
+                       v_desc + (uint64_t)(u * (kBlockBytes >> 4) + kk * (2048 >> 4)), kId,
+                       (j > 0 || u > 0 || kk > 0) ? 1u : 0u);
+        umma_commit_warp(&sm.empty[4 + u]);
         if (u & 1) umma_commit_warp(&sm.p_empty[u >> 1]);   // [1]: O holds every P V so far
       }
     }
@@ -371,11 +406,14 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
   const int rr = r / heads, hh = r - rr * heads;
   const bool valid = rr < a.rows;
   uint32_t g = 0, done = 0, mxn = 0;
-  // one exchange between the two warpgroups: what each wrote before is read after
-  auto exchange = [&]() -> bool {
+  // one exchange of a value with the other warpgroup's thread of the same row (a buffer is
+  // written again two exchanges on, after the reader has arrived at the next)
+  auto exchange = [&](float mine, float& other) -> bool {
+    sm.mx[mxn & 1][hf][r] = mine;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.mx_bar);
     const bool ok = warp_wait(&sm.mx_bar, mxn & 1, abort);
+    other = sm.mx[mxn & 1][hf ^ 1][r];
     ++mxn;
     return ok;
   };
@@ -445,9 +483,9 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
       m0 = max3(m0, f(60), f(61));
       m1 = max3(m1, f(62), f(63));
       const float mine = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-      sm.mx[g & 1][hf][r] = mine;
-      if (!exchange()) return;
-      const float top = fmaxf(mine, sm.mx[g & 1][hf ^ 1][r]) * kLog2eOver16;
+      float other;
+      if (!exchange(mine, other)) return;
+      const float top = fmaxf(mine, other) * kLog2eOver16;
       // M starts at the first visible tile's maximum and grows when that is passed by > 2^8
       const bool grow = top > M + kLazyRescale;
       const float newM = grow ? top : M;
@@ -490,13 +528,13 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
       if (lane == 0) mbar_arrive(&sm.p_full[hf]);
     }
     // the segment's result
-    sm.stat_l[hf][r] = l;
-    if (!exchange()) return;
-    l += sm.stat_l[hf ^ 1][r];
+    float other_l;
+    if (!exchange(l, other_l)) return;
+    l += other_l;
     if (!warp_wait(&sm.o_done, done & 1, abort)) return;
     tc_fence_after();
     const float inv = l > 0.f ? 1.0f / l : (l != l ? l : 0.f);
-    const size_t prow = (size_t)seg.slot * 128 + r;
+    const size_t prow = (size_t)seg.slot * kV4Lanes + r;
     float4* po = reinterpret_cast<float4*>(a.part_o + prow * kDim + 128 * hf);
     const uint4* gp = reinterpret_cast<const uint4*>(a.qg + (row * kHeads + h) * kQgStride + kDim + 128 * hf);
     uint4* op = reinterpret_cast<uint4*>(a.out + (row * kHeads + h) * kDim + 128 * hf);
@@ -545,26 +583,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   V4Smem& sm = *reinterpret_cast<V4Smem*>(smem_raw);
   const int warp = threadIdx.x >> 5;
   volatile int* abort = &sm.abort;
+  // softmax warps with query rows, of each warpgroup's four
+  const uint32_t act = (uint32_t)(a.rows * (kGroup / row_blocks(a.rows)) + 31) / 32;
   load_tiles<kThreads>(a, sm.tiles, kTileN, blockIdx.x == 0);
   if (threadIdx.x == 0) {
     sm.abort = 0;
-    for (int i = 0; i < kRings; ++i) mbar_init(&sm.raw_full[i], 1);
+    for (int i = 0; i < 2 * kStages; ++i) {
+      mbar_init(&sm.raw_full[i], 1);
+      mbar_init(&sm.raw_empty[i], 4);   // one arrival per widening warp
+    }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&sm.full[i], 4);         // per widening warp
+      mbar_init(&sm.empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.k_full[i], 4);    // one arrival per widening warp
-      mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.p_full[i], 4);    // per softmax warp of the half
+      mbar_init(&sm.p_full[i], act);      // per softmax warp of the half
       mbar_init(&sm.p_empty[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_empty[i], 1);
-    }
-    mbar_init(&sm.q_full, 8);         // per softmax warp
+    mbar_init(&sm.q_full, 2 * act);       // per softmax warp
     mbar_init(&sm.s_full, 1);
-    mbar_init(&sm.s_free, 8);
+    mbar_init(&sm.s_free, 2 * act);
     mbar_init(&sm.o_done, 1);
-    mbar_init(&sm.o_free, 8);
-    mbar_init(&sm.mx_bar, 8);
+    mbar_init(&sm.o_free, 2 * act);
+    mbar_init(&sm.mx_bar, 2 * act);
     mbar_init(&sm.drain_qk, 1);
     mbar_init(&sm.drain_pv, 1);
     mbar_fence_init();
@@ -591,12 +632,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit_warp(&sm.drain_pv);
       mbar_wait_quiet(&sm.drain_pv, 0, 100000000LL);
     }
+    if (warp >= 2)
+      raw_loader(sm, warp == 2 ? &tm_kc : &tm_vc, warp == 2 ? &tm_ks : &tm_vs, warp - 2, a, abort);
   } else if (warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_worker(sm, a, tmem, (warp - 4) >> 2, abort);
+    if ((uint32_t)(warp & 3) < act) softmax_worker(sm, a, tmem, (warp - 4) >> 2, abort);
   } else {
-    if (warp < 16) widen_worker<false>(sm, &tm_kc, &tm_ks, a, abort);
-    else widen_worker<true>(sm, &tm_vc, &tm_vs, a, abort);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
+    widen_worker(sm, warp >= 16 ? 1 : 0, abort);
   }
   tc_fence_before();
   __syncthreads();
@@ -636,7 +679,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   // CTA c's part is its first segment unless the stream began inside the CTA's run
   auto part_row = [&](int c) -> size_t {
     const int slot = 2 * c + ((long long)c * share < u0 ? 1 : 0);
-    return (size_t)slot * 128 + r;
+    return (size_t)slot * kV4Lanes + r;
   };
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
   float M = -INFINITY, L = 0.f, o[8];
@@ -685,7 +728,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
 }  // namespace
 
 size_t verify4_ws_bytes() {
-  return (size_t)2 * kV4MaxCtas * 128 * (kDim + 2) * sizeof(float);
+  return (size_t)2 * kV4MaxCtas * kV4Lanes * (kDim + 2) * sizeof(float);
 }
 
 cudaError_t verify4_set_attributes() {
