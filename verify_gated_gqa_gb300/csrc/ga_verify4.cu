@@ -15,7 +15,7 @@
 // across CTAs leaves partial O, M, l per CTA (at most two per CTA: its first and its last
 // segment), merged by the combine kernel.
 //
-// Structure (640 threads, 20 warps):
+// Structure (896 threads, 28 warps):
 //   warp 0      issues S = Q K^T (tcgen05, M=128, N=128, K=256; Q dims 0..127 in tensor
 //               memory, 128..255 in shared memory; lanes past the 96 rows hold whatever is there, and
 //               nothing reads their results)
@@ -24,8 +24,8 @@
 //               (warps without rows are idle); they also load Q and write the segment's result
 //   warps 2, 3  load the codes and scales of K and V tiles by TMA, a granule of 32 keys a lane
 //               (a page holds a multiple of that), through two stages each
-//   warps 12-15 widen K, warps 16-19 widen V: a lane turns 64 codes of one row into the 128 bytes
-//               of a row of the 128-byte-swizzled blocks that the tensor cores read
+//   warps 12-19 widen K, warps 20-27 widen V: a lane turns 32 codes of one row into 64 bytes of a
+//               row of the 128-byte-swizzled blocks that the tensor cores read
 // K is handed over in four pieces of 64 dims and V in four of 32 keys (16 KiB each), so the
 // tensor cores start on the first piece of a tile while the rest is being widened, and give
 // its place back as soon as they have read it. The roles run different code at
@@ -40,17 +40,18 @@
 namespace ga {
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 896;
 constexpr int kBlockBytes = 128 * 128;    // 128 rows x 64 dims of bf16
 constexpr int kGranule = 32;              // keys per TMA box
 constexpr int kStages = 2;                // raw tiles in flight, for K and for V
 constexpr int kRawBytes = kTileN * kQ4RowBytes, kRawScaleBytes = kTileN * kQ4ScaleBytes;
 constexpr int kQBlockBytes = kV4Lanes * 128;      // 64 dims of the query rows
 constexpr int kMaxRowsWhole = kV4Lanes / kGroup;  // window rows up to which 12 heads fit
-// Registers: launched at 96 a thread (640 x 96 = 61,440). The issuing warpgroup keeps 64, the
-// softmax warpgroups take 136, the widening ones keep 72: 128 x (64 + 2 x 136 + 2 x 72) = 61,440.
-constexpr int kRegsIssue = 64, kRegsSoftmax = 136, kRegsWiden = 72;
-static_assert(128 * (kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsWiden) <= kThreads * 96,
+// Registers: launched at 72 a thread (896 x 72 = 64,512). The issuing warpgroup keeps 64, the
+// softmax warpgroups take 120, the four widening ones keep 48: 128 x (64 + 2 x 120 + 4 x 48) =
+// 63,488.
+constexpr int kRegsIssue = 64, kRegsSoftmax = 120, kRegsWiden = 48;
+static_assert(128 * (kRegsIssue + 2 * kRegsSoftmax + 4 * kRegsWiden) <= kThreads * 72,
               "register split");
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemQ = 384, kTmemP = 448;
 constexpr float kLog2eOver16 = 1.4426950408889634f / 16.0f;
@@ -81,9 +82,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   const bool ok = mbar_wait(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
 }
-__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
@@ -267,20 +268,25 @@ __device__ void raw_loader(V4Smem& sm, const CUtensorMap* tm_c, const CUtensorMa
 }
 
 // ------------------------------------------------------------------ widening
-// Warp w of four. K, piece u (64-dim block u): keys 32w .. 32w+31, a key a lane. V, piece u (keys
-// 32u ..): keys 32u + 8w .. + 7, four lanes a key, a 64-dim block each. Eight neighbouring lanes
-// always hold eight neighbouring rows, so the swizzle keeps reads and writes free of bank
-// conflicts.
+// Warp w of eight. K, piece u (64-dim block u): keys 32 (w % 4) .. + 31, a key a lane, dims 32
+// (w / 4) .. + 31 of the block. V, piece u (keys 32u ..): keys 32u + 8 (w % 4) .. + 7, four lanes
+// a key, 32 dims each, those of warps 4 .. 7 in the upper 128. Eight neighbouring lanes always
+// hold eight neighbouring rows, so the swizzle keeps reads and writes free of bank conflicts.
 __device__ void widen_worker(V4Smem& sm, int is_v, volatile int* abort) {
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
-  const uint32_t row0 = is_v ? 8 * w + (lane & 7) : 32 * w + lane;   // the lane's row in piece 0
-  const uint32_t blk0 = is_v ? (uint32_t)lane >> 3 : 0;              // and 64-dim block of it
+  const int lane = threadIdx.x & 31, w = ((int)(threadIdx.x >> 5) - 12) & 7;
+  const uint32_t row0 = is_v ? 8 * (w & 3) + (lane & 7) : 32 * (w & 3) + lane;   // row in piece 0
   const uint32_t xr = row0 & 7;
+  uint32_t ch = is_v ? (uint32_t)(4 * (w >> 2) + (lane >> 3)) : (uint32_t)(w >> 2);   // 32-dim chunk
   const uint32_t src_u = is_v ? kGranule * kQ4RowBytes : 0u;         // from piece to piece
   const uint32_t scs_u = is_v ? kGranule * kQ4ScaleBytes : 4u;
   const uint32_t ch_u = is_v ? 0u : 2u;
+  // this lane's four 16-byte places in piece 0: in row xr of an 8-row atom
   const uint32_t dst0 = smem_u32(is_v ? sm.vt[0] : sm.kt[0]) + (row0 >> 3) * 1024u + xr * 128u +
-                        blk0 * (kGranule * 128u);
+                        (is_v ? (ch >> 1) * (kGranule * 128u) : 0u);
+  uint32_t at[4];
+#pragma unroll
+  for (uint32_t j = 0; j < 4; ++j) at[j] = dst0 + (((4 * (ch & 1) + j) ^ xr) << 4);
+  const uint32_t ch0 = ch;
   uint64_t* full = sm.full + 4 * is_v;
   uint64_t* empty = sm.empty + 4 * is_v;
   const int n = sm.units;
@@ -288,34 +294,27 @@ __device__ void widen_worker(V4Smem& sm, int is_v, volatile int* abort) {
     const int st = kStages * is_v + g % kStages;
     if (!warp_wait(&sm.raw_full[st], (g / kStages) & 1, abort)) return;
     uint32_t src = smem_u32(sm.raw[st]) + row0 * kQ4RowBytes;
-    uint32_t scs = smem_u32(sm.rsc[st]) + row0 * kQ4ScaleBytes + 4 * blk0;
-    uint32_t ch = 2 * blk0, dst = dst0;   // 16-byte chunk of the row; destination row
-    uint32_t sc = lds_u32(scs);
-    uint4 c0 = lds_v4(src + ((ch ^ xr) << 4)), c1 = lds_v4(src + (((ch + 1) ^ xr) << 4));
+    uint32_t scs = smem_u32(sm.rsc[st]) + row0 * kQ4ScaleBytes + 2 * ch0;
+    ch = ch0;
+    uint32_t sc = lds_u16(scs);
+    uint4 c = lds_v4(src + ((ch ^ xr) << 4));
 #pragma unroll 1
     for (int u = 0; u < 4; ++u) {
       if (!warp_wait(&empty[u], (g & 1) ^ 1, abort)) return;
+      const uint32_t wd[4] = {c.x, c.y, c.z, c.w};
+      const Q4Scale q0 = q4_scale(sc & 0xFFu), q1 = q4_scale(sc >> 8);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 c = i ? c1 : c0;
-        const uint32_t wd[4] = {c.x, c.y, c.z, c.w};
-        const Q4Scale q0 = q4_scale((sc >> (16 * i)) & 0xFFu);
-        const Q4Scale q1 = q4_scale((sc >> (16 * i + 8)) & 0xFFu);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t o[4];
-          q4_widen(wd[j], j < 2 ? q0 : q1, o);
-          sts_v4(dst + (((uint32_t)(4 * i + j) ^ xr) << 4), o);
-        }
+      for (int j = 0; j < 4; ++j) {
+        uint32_t o[4];
+        q4_widen(wd[j], j < 2 ? q0 : q1, o);
+        sts_v4(at[j] + u * kBlockBytes, o);
       }
       if (u < 3) {   // the next piece's codes, while the stores drain
         src += src_u;
         scs += scs_u;
         ch += ch_u;
-        dst += kBlockBytes;
-        sc = lds_u32(scs);
-        c0 = lds_v4(src + ((ch ^ xr) << 4));
-        c1 = lds_v4(src + (((ch + 1) ^ xr) << 4));
+        sc = lds_u16(scs);
+        c = lds_v4(src + ((ch ^ xr) << 4));
       }
       fence_async_smem();   // the tensor cores read what the lanes wrote
       __syncwarp();
@@ -590,10 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.abort = 0;
     for (int i = 0; i < 2 * kStages; ++i) {
       mbar_init(&sm.raw_full[i], 1);
-      mbar_init(&sm.raw_empty[i], 4);   // one arrival per widening warp
+      mbar_init(&sm.raw_empty[i], 8);   // one arrival per widening warp
     }
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&sm.full[i], 4);         // per widening warp
+      mbar_init(&sm.full[i], 8);         // per widening warp
       mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -639,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if ((uint32_t)(warp & 3) < act) softmax_worker(sm, a, tmem, (warp - 4) >> 2, abort);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
-    widen_worker(sm, warp >= 16 ? 1 : 0, abort);
+    widen_worker(sm, warp >= 20 ? 1 : 0, abort);
   }
   tc_fence_before();
   __syncthreads();
