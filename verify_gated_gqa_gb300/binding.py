@@ -7,6 +7,7 @@ current stream. There is no CPU fallback: if the library is not built, every cal
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -565,42 +566,45 @@ def ga_attn_verify_e4m3(qg, k_codes, k_scale, v_codes, v_scale, seq_len, w_q, co
 
 
 # ------------------------------------------------------------------ serving over 4-bit pages
+# These calls run once a decode step, where the host's microseconds count: one pass of plain
+# comparisons per tensor, addresses as integers, the stream's handle without a Stream object.
 Q4_ROW_BYTES, Q4_SCALE_BYTES, Q4_PAGE_TOKENS = 128, 16, 32
+_BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on_device(**tensors):
-    """The given tensors (None passes) live on the current CUDA device."""
-    for n, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
-            raise ValueError(f"{n} must be a tensor on the current CUDA device")
+def _device(t, name):
+    """The current CUDA device's index, which must be the tensor's."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a tensor on the current CUDA device")
+    return dev
 
 
-def _int32(name, t, *shape):
-    """A contiguous int32 tensor of the given shape (None entries: any extent)."""
-    if (t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or
-            any(s is not None and s != d for s, d in zip(shape, t.shape))):
-        raise ValueError(f"{name} must be a contiguous int32 tensor "
-                         f"[{', '.join('...' if s is None else str(s) for s in shape)}]")
+def _stream_of(dev):
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
-def _ptr_any(t):
-    """The address of a tensor; of an empty one, a stand-in that is aligned and never read."""
-    return _ptr(t) if t.numel() else ctypes.c_void_p(256)
+def _addr(name, t, dtype, shape, dev):
+    """The address of a contiguous tensor of the given type, shape and device (of an empty one, a
+    stand-in that is aligned and never read)."""
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev or
+            not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on CUDA device "
+                         f"{dev}, not {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr() or 256
 
 
-def _q4_pools(k_codes, k_scales, v_codes, v_scales):
-    """(n_pages, page_size) of four pool tensors that belong together."""
-    _on_device(k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales)
-    for n, t, last in (("k_codes", k_codes, Q4_ROW_BYTES), ("v_codes", v_codes, Q4_ROW_BYTES),
-                       ("k_scales", k_scales, Q4_SCALE_BYTES),
-                       ("v_scales", v_scales, Q4_SCALE_BYTES)):
-        if (t.dtype != torch.uint8 or not t.is_contiguous() or t.dim() != 4 or
-                t.shape[1] != N_KV_HEADS or t.shape[3] != last or
-                t.shape[0] != k_codes.shape[0] or t.shape[2] != k_codes.shape[2]):
-            raise ValueError(f"{n} must be a contiguous uint8 tensor "
-                             f"[n_pages, {N_KV_HEADS}, page_size, {last}], n_pages and page_size "
-                             "those of k_codes")
-    return k_codes.shape[0], k_codes.shape[2]
+def _q4_pools(k_codes, k_scales, v_codes, v_scales, dev):
+    """(addresses of the four pools, n_pages, page_size)."""
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes must be [n_pages, 2, page_size, 128]")
+    n_pages, page_size = k_codes.shape[0], k_codes.shape[2]
+    codes = (n_pages, N_KV_HEADS, page_size, Q4_ROW_BYTES)
+    scales = (n_pages, N_KV_HEADS, page_size, Q4_SCALE_BYTES)
+    return (_addr("k_codes", k_codes, _U8, codes, dev), _addr("k_scales", k_scales, _U8, scales, dev),
+            _addr("v_codes", v_codes, _U8, codes, dev), _addr("v_scales", v_scales, _U8, scales, dev),
+            n_pages, page_size)
 
 
 def ga_page_plan(seq_len, new_len, page_table, held, free_pages, free_count, page_size,
@@ -611,37 +615,46 @@ def ga_page_plan(seq_len, new_len, page_table, held, free_pages, free_count, pag
     page_table is updated in place, and so are held and free_count unless held_out and
     free_count_out are given. Returns (row_start [n + 1], slot_map [max_tokens], positions
     [max_tokens], info [4])."""
+    dev = _device(seq_len, "seq_len")
     n = seq_len.shape[0]
-    held_out = held if held_out is None else held_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    dev = seq_len.device
-    new = lambda k: torch.empty(k, dtype=torch.int32, device=dev)  # noqa: E731
-    row_start = new(n + 1) if row_start is None else row_start
-    slot_map = new(max_tokens) if slot_map is None else slot_map
-    positions = new(max_tokens) if positions is None else positions
-    info = new(4) if info is None else info
-    _on_device(seq_len=seq_len, new_len=new_len, page_table=page_table, held=held,
-               free_pages=free_pages, free_count=free_count, pos_delta=pos_delta,
-               held_out=held_out, free_count_out=free_count_out, row_start=row_start,
-               slot_map=slot_map, positions=positions, info=info)
-    for name, t, shape in (("seq_len", seq_len, (n,)), ("new_len", new_len, (n,)),
-                           ("page_table", page_table, (n, None)), ("held", held, (n,)),
-                           ("held_out", held_out, (n,)), ("free_pages", free_pages, (None,)),
-                           ("free_count", free_count, (1,)),
-                           ("free_count_out", free_count_out, (1,)),
-                           ("row_start", row_start, (n + 1,)), ("slot_map", slot_map, (max_tokens,)),
-                           ("positions", positions, (max_tokens,)), ("info", info, (4,))):
-        _int32(name, t, *shape)
-    if pos_delta is not None:
-        _int32("pos_delta", pos_delta, n)
-    _check(lib().ga_page_plan(_ptr_any(seq_len), _ptr_any(new_len), n, page_size,
-                              _ptr_any(page_table), page_table.shape[1], _ptr_any(held),
-                              _ptr_any(held_out), _ptr_any(free_pages), free_pages.shape[0],
-                              _ptr(free_count), _ptr(free_count_out), _ptr(pos_delta), max_tokens,
-                              _ptr(row_start), _ptr_any(slot_map), _ptr_any(positions), _ptr(info),
-                              _stream()),
-           "ga_page_plan")
+    where = seq_len.device
+    if row_start is None:
+        row_start = torch.empty(n + 1, dtype=_I32, device=where)
+    if slot_map is None:
+        slot_map = torch.empty(max_tokens, dtype=_I32, device=where)
+    if positions is None:
+        positions = torch.empty(max_tokens, dtype=_I32, device=where)
+    if info is None:
+        info = torch.empty(4, dtype=_I32, device=where)
+    if page_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("page_table must be [n_seq, max_pages] and free_pages [n_free]")
+    width, n_free = page_table.shape[1], free_pages.shape[0]
+    held_at = _addr("held", held, _I32, (n,), dev)
+    count_at = _addr("free_count", free_count, _I32, (1,), dev)
+    st = lib().ga_page_plan(
+        _addr("seq_len", seq_len, _I32, (n,), dev), _addr("new_len", new_len, _I32, (n,), dev), n,
+        page_size, _addr("page_table", page_table, _I32, (n, width), dev), width, held_at,
+        held_at if held_out is None else _addr("held_out", held_out, _I32, (n,), dev),
+        _addr("free_pages", free_pages, _I32, (n_free,), dev), n_free, count_at,
+        count_at if free_count_out is None else
+        _addr("free_count_out", free_count_out, _I32, (1,), dev),
+        None if pos_delta is None else _addr("pos_delta", pos_delta, _I32, (n,), dev), max_tokens,
+        _addr("row_start", row_start, _I32, (n + 1,), dev),
+        _addr("slot_map", slot_map, _I32, (max_tokens,), dev),
+        _addr("positions", positions, _I32, (max_tokens,), dev), _addr("info", info, _I32, (4,), dev),
+        _stream_of(dev))
+    _check(st, "ga_page_plan")
     return row_start, slot_map, positions, info
+
+
+@functools.lru_cache(maxsize=64)
+def _axis_bytes(pair_axis):
+    if len(pair_axis) != ROPE_DIMS // 2 or min(pair_axis) < 0 or max(pair_axis) > 255:
+        raise ValueError("pair_axis must be 32 axis numbers")
+    return (ctypes.c_uint8 * len(pair_axis))(*pair_axis)
+
+
+_ONE_AXIS = (0,) * (ROPE_DIMS // 2)
 
 
 def ga_qk_prologue_axes(k_raw, w_k, qg, w_q, positions, pair_axis, cos_tab, sin_tab, k_prep=None,
@@ -652,58 +665,54 @@ def ga_qk_prologue_axes(k_raw, w_k, qg, w_q, positions, pair_axis, cos_tab, sin_
     [n_tok, 2, 256], q_prep [n_tok, 24, 256]), None for a side not given."""
     if k_raw is None and qg is None:
         raise ValueError("k_raw or qg must be given")
-    n_tok = (qg if k_raw is None else k_raw).shape[0]
-    dev = (qg if k_raw is None else k_raw).device
-    _on_device(k_raw=k_raw, w_k=w_k, qg=qg, w_q=w_q, positions=positions, cos_tab=cos_tab,
-               sin_tab=sin_tab, k_prep=k_prep, q_prep=q_prep)
+    if (k_raw is None and (w_k is not None or k_prep is not None) or
+            qg is None and (w_q is not None or q_prep is not None)):
+        raise ValueError("w_k and k_prep come with k_raw, w_q and q_prep with qg")
+    some = qg if k_raw is None else k_raw
+    dev = _device(some, "qg" if k_raw is None else "k_raw")
+    n_tok = some.shape[0]
+    k = wk = kp = q = wq = qp = None
     if k_raw is not None:
-        _bf16_cuda("k_raw", k_raw, (n_tok, N_KV_HEADS, HEAD_DIM))
-        _bf16_cuda("w_k", w_k, (HEAD_DIM,))
-        k_prep = torch.empty_like(k_raw) if k_prep is None else k_prep
-        _bf16_cuda("k_prep", k_prep, tuple(k_raw.shape))
-    elif w_k is not None or k_prep is not None:
-        raise ValueError("w_k and k_prep come with k_raw")
+        rows = (n_tok, N_KV_HEADS, HEAD_DIM)
+        if k_prep is None:
+            k_prep = torch.empty(rows, dtype=_BF16, device=some.device)
+        k = _addr("k_raw", k_raw, _BF16, rows, dev)
+        wk = _addr("w_k", w_k, _BF16, (HEAD_DIM,), dev)
+        kp = _addr("k_prep", k_prep, _BF16, rows, dev)
     if qg is not None:
-        _bf16_cuda("qg", qg, (n_tok, N_Q_HEADS, 2 * HEAD_DIM))
-        _bf16_cuda("w_q", w_q, (HEAD_DIM,))
+        rows = (n_tok, N_Q_HEADS, HEAD_DIM)
         if q_prep is None:
-            q_prep = torch.empty(n_tok, N_Q_HEADS, HEAD_DIM, dtype=torch.bfloat16, device=dev)
-        _bf16_cuda("q_prep", q_prep, (n_tok, N_Q_HEADS, HEAD_DIM))
-    elif w_q is not None or q_prep is not None:
-        raise ValueError("w_q and q_prep come with qg")
-    if positions.dim() == 1:
-        positions = positions[None]
-    if (positions.dtype != torch.int32 or positions.dim() != 2 or positions.shape[1] < n_tok or
-            (positions.shape[1] > 1 and positions.stride(1) != 1)):
+            q_prep = torch.empty(rows, dtype=_BF16, device=some.device)
+        q = _addr("qg", qg, _BF16, (n_tok, N_Q_HEADS, 2 * HEAD_DIM), dev)
+        wq = _addr("w_q", w_q, _BF16, (HEAD_DIM,), dev)
+        qp = _addr("q_prep", q_prep, _BF16, rows, dev)
+    dims = positions.dim()
+    n_axes, cols = (1, positions.shape[0]) if dims == 1 else positions.shape if dims == 2 else (0, 0)
+    if (n_axes < 1 or positions.dtype is not _I32 or positions.get_device() != dev or cols < n_tok or
+            (cols > 1 and positions.stride(-1) != 1)):
         raise ValueError("positions must be int32 [n_tok] or [n_axes, >= n_tok] with unit column "
-                         "stride")
-    axes = [0] * (ROPE_DIMS // 2) if pair_axis is None else [int(x) for x in pair_axis]
-    n_axes = positions.shape[0]
-    if len(axes) != ROPE_DIMS // 2 or min(axes) < 0 or max(axes) > 255:
-        raise ValueError("pair_axis must be 32 axis numbers")
-    _bf16_cuda("cos_tab", cos_tab, (cos_tab.shape[0], ROPE_DIMS // 2))
-    _bf16_cuda("sin_tab", sin_tab, tuple(cos_tab.shape))
-    ld = positions.stride(0) if n_axes > 1 else max(positions.shape[1], n_tok)
-    _check(lib().ga_qk_prologue_axes(_opt(k_raw), _ptr(w_k), _opt(k_prep), _opt(qg), _ptr(w_q),
-                                     _opt(q_prep), n_tok, _ptr_any(positions), ld, n_axes,
-                                     (ctypes.c_uint8 * len(axes))(*axes), _ptr(cos_tab),
-                                     _ptr(sin_tab), cos_tab.shape[0], _stream()),
-           "ga_qk_prologue_axes")
+                         f"stride, on CUDA device {dev}")
+    table = (cos_tab.shape[0], ROPE_DIMS // 2)
+    st = lib().ga_qk_prologue_axes(
+        k, wk, kp, q, wq, qp, n_tok, positions.data_ptr() or 256,
+        positions.stride(0) if n_axes > 1 else cols, n_axes,
+        _axis_bytes(_ONE_AXIS if pair_axis is None else tuple(pair_axis)),
+        _addr("cos_tab", cos_tab, _BF16, table, dev), _addr("sin_tab", sin_tab, _BF16, table, dev),
+        table[0], _stream_of(dev))
+    _check(st, "ga_qk_prologue_axes")
     return k_prep, q_prep
 
 
-def _opt(t):
-    """_ptr_any of a tensor that may be None."""
-    return None if t is None else _ptr_any(t)
-
-
-def _kv_rows(name, x):
-    """(pointer, token stride in values) of bf16 rows [n_tok, 2, 256], heads and dims dense."""
-    if (x.dtype != torch.bfloat16 or x.dim() != 3 or tuple(x.shape[1:]) != (N_KV_HEADS, HEAD_DIM)
-            or x.stride(2) != 1 or x.stride(1) != HEAD_DIM):
-        raise ValueError(f"{name} must be bfloat16 [n_tok, {N_KV_HEADS}, {HEAD_DIM}] with dense "
-                         "heads and dims")
-    return _ptr_any(x), (x.stride(0) if x.shape[0] > 1 else N_KV_HEADS * HEAD_DIM)
+def _kv_rows(name, x, n_tok, dev):
+    """(address, token stride in values) of bf16 rows [n_tok, 2, 256], heads and dims dense."""
+    if (x.dtype is not _BF16 or x.shape != (n_tok, N_KV_HEADS, HEAD_DIM) or
+            x.get_device() != dev):
+        raise ValueError(f"{name} must be bfloat16 [{n_tok}, {N_KV_HEADS}, {HEAD_DIM}] on CUDA "
+                         f"device {dev}")
+    tok, head, dim = x.stride()
+    if dim != 1 or head != HEAD_DIM:
+        raise ValueError(f"{name} must have dense heads and dims")
+    return x.data_ptr() or 256, tok if n_tok > 1 else N_KV_HEADS * HEAD_DIM
 
 
 def ga_kv_quantize_q4(k, v, k_codes, k_scales, v_codes, v_scales, slots=None):
@@ -711,19 +720,16 @@ def ga_kv_quantize_q4(k, v, k_codes, k_scales, v_codes, v_scales, slots=None):
     projection) as 4-bit rows at slots int32 [n_tok] (None: token t at slot t) of the pools
     k_codes, v_codes uint8 [n_pages, 2, page_size, 128], k_scales, v_scales uint8
     [n_pages, 2, page_size, 16]. Negative slots are skipped."""
-    n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales)
-    _on_device(k=k, v=v, slots=slots)
-    kp, ld_k = _kv_rows("k", k)
-    vp, ld_v = _kv_rows("v", v)
+    dev = _device(k, "k")
     n_tok = k.shape[0]
-    if v.shape[0] != n_tok:
-        raise ValueError("k and v must have the same tokens")
-    if slots is not None:
-        _int32("slots", slots, n_tok)
-    _check(lib().ga_kv_quantize_q4(kp, ld_k, vp, ld_v, n_tok, _opt(slots), _ptr(k_codes),
-                                   _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), n_pages,
-                                   page_size, _stream()),
-           "ga_kv_quantize_q4")
+    kc, ks, vc, vs, n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales, dev)
+    k_at, ld_k = _kv_rows("k", k, n_tok, dev)
+    v_at, ld_v = _kv_rows("v", v, n_tok, dev)
+    st = lib().ga_kv_quantize_q4(
+        k_at, ld_k, v_at, ld_v, n_tok,
+        None if slots is None else _addr("slots", slots, _I32, (n_tok,), dev), kc, ks, vc, vs,
+        n_pages, page_size, _stream_of(dev))
+    _check(st, "ga_kv_quantize_q4")
 
 
 def ga_kv_dequantize_q4(k_codes, k_scales, v_codes, v_scales, slots=None, n_tok=None, k_out=None,
@@ -731,24 +737,23 @@ def ga_kv_dequantize_q4(k_codes, k_scales, v_codes, v_scales, slots=None, n_tok=
     """The widened rows at slots int32 [n_tok] (None: slots 0 .. n_tok - 1, by default the whole
     pool) of 4-bit pools, (k_out, v_out) bf16 [n_tok, 2, 256]. Rows of negative slots are left as
     they were (unspecified in outputs allocated here)."""
-    n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    dev = _device(k_codes, "k_codes")
+    kc, ks, vc, vs, n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales, dev)
     if slots is not None:
         n_tok = slots.shape[0]
-        _int32("slots", slots, n_tok)
     elif n_tok is None:
         n_tok = n_pages * page_size
     shape = (n_tok, N_KV_HEADS, HEAD_DIM)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_codes.device)
+        k_out = torch.empty(shape, dtype=_BF16, device=k_codes.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_codes.device)
-    _on_device(slots=slots, k_out=k_out, v_out=v_out)
-    _bf16_cuda("k_out", k_out, shape)
-    _bf16_cuda("v_out", v_out, shape)
-    _check(lib().ga_kv_dequantize_q4(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
-                                     n_pages, page_size, _opt(slots), n_tok, _ptr_any(k_out),
-                                     _ptr_any(v_out), _stream()),
-           "ga_kv_dequantize_q4")
+        v_out = torch.empty(shape, dtype=_BF16, device=k_codes.device)
+    st = lib().ga_kv_dequantize_q4(
+        kc, ks, vc, vs, n_pages, page_size,
+        None if slots is None else _addr("slots", slots, _I32, (n_tok,), dev), n_tok,
+        _addr("k_out", k_out, _BF16, shape, dev), _addr("v_out", v_out, _BF16, shape, dev),
+        _stream_of(dev))
+    _check(st, "ga_kv_dequantize_q4")
     return k_out, v_out
 
 
@@ -762,27 +767,26 @@ def ga_attn_verify_q4(q_prep, qg, k_codes, k_scales, v_codes, v_scales, page_tab
     prepared queries; qg [n_seq, rows, 24, 512] fused rows (their gates); the pools; page_table
     int32 [n_seq, max_pages] and seq_len int32 [n_seq] on the device (negative: unused, its rows
     of out are left as they were). Returns out [n_seq, rows, 24*256]."""
+    dev = _device(q_prep, "q_prep")
     n_seq, rows = q_prep.shape[0], q_prep.shape[1]
-    n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales)
+    kc, ks, vc, vs, n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seq, max_pages]")
+    L = lib()
+    o_shape = (n_seq, rows, N_Q_HEADS * HEAD_DIM)
     if out is None:
-        out = torch.empty(n_seq, rows, N_Q_HEADS * HEAD_DIM, dtype=torch.bfloat16,
-                          device=q_prep.device)
+        out = torch.empty(o_shape, dtype=_BF16, device=q_prep.device)
     if workspace is None:
-        workspace = torch.empty(ga_verify_q4_workspace_bytes(), dtype=torch.uint8,
-                                device=q_prep.device)
-    _on_device(q_prep=q_prep, qg=qg, page_table=page_table, seq_len=seq_len, out=out,
-               workspace=workspace)
-    _bf16_cuda("q_prep", q_prep, (n_seq, rows, N_Q_HEADS, HEAD_DIM))
-    _bf16_cuda("qg", qg, (n_seq, rows, N_Q_HEADS, 2 * HEAD_DIM))
-    _bf16_cuda("out", out, (n_seq, rows, N_Q_HEADS * HEAD_DIM))
-    _int32("page_table", page_table, n_seq, None)
-    _int32("seq_len", seq_len, n_seq)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _check(lib().ga_attn_verify_q4(_ptr_any(q_prep), _ptr_any(qg), _ptr(k_codes), _ptr(k_scales),
-                                   _ptr(v_codes), _ptr(v_scales), n_pages, page_size,
-                                   _ptr_any(page_table), page_table.shape[1], _ptr_any(seq_len),
-                                   n_seq, rows, _ptr_any(out), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream()),
-           "ga_attn_verify_q4")
+        workspace = torch.empty(L.ga_verify_q4_workspace_bytes(), dtype=_U8, device=q_prep.device)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on CUDA device {dev}")
+    width = page_table.shape[1]
+    st = L.ga_attn_verify_q4(
+        _addr("q_prep", q_prep, _BF16, (n_seq, rows, N_Q_HEADS, HEAD_DIM), dev),
+        _addr("qg", qg, _BF16, (n_seq, rows, N_Q_HEADS, 2 * HEAD_DIM), dev), kc, ks, vc, vs, n_pages,
+        page_size, _addr("page_table", page_table, _I32, (n_seq, width), dev), width,
+        _addr("seq_len", seq_len, _I32, (n_seq,), dev), n_seq, rows,
+        _addr("out", out, _BF16, o_shape, dev), workspace.data_ptr(), workspace.nbytes,
+        _stream_of(dev))
+    _check(st, "ga_attn_verify_q4")
     return out
