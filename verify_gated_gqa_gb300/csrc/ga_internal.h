@@ -214,6 +214,11 @@ cudaError_t verify4_set_attributes();
 cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
                            const CUtensorMap& k_scales, const CUtensorMap& v_scales,
                            const Verify4Args& a, int sm_count, cudaStream_t s);
+// The form for one row per sequence (ga_decode4.cu), called by launch_verify4.
+cudaError_t decode4_set_attributes();
+cudaError_t launch_decode4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
+                           const CUtensorMap& k_scales, const CUtensorMap& v_scales,
+                           const Verify4Args& a, int ctas, cudaStream_t s);
 
 cudaError_t attn_set_smem_attribute();
 // Clusters of two attention CTAs (the e4m3 verify variant) that can run at once.

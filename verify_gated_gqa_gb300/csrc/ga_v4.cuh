@@ -1,0 +1,168 @@
+// The attention kernels over 4-bit paged caches (ga_verify4.cu, ga_decode4.cu): how the work is
+// cut among the CTAs, and small helpers.
+#pragma once
+#include "ga_internal.h"
+#include "ga_q4.cuh"
+#include "ga_sm100.cuh"
+
+namespace ga {
+
+__device__ __forceinline__ void record(int* status, int code) {
+  if (code) atomicCAS(status, 0, code);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const bool ok = mbar_wait(bar, parity, abort);
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_v4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+// A tensor load by the calling thread alone.
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ float sigmoid_f(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+
+// ------------------------------------------------------------------ the cut of the work
+// Key tiles (of `tile` keys) of a sequence: none when its slot is unused (negative length) or
+// its window passes the end of its page-table row, which is recorded.
+__device__ __forceinline__ int seq_tiles(const Verify4Args& a, int b, int tile, bool report) {
+  const int L = a.seq_len[b];
+  if (L < 0) return 0;
+  const long long keys = (long long)L + a.rows;
+  if (keys > (long long)a.max_pages * a.page_size || keys > GA_MAX_TOKENS) {
+    if (report) record(a.status, kDevBadPosition);
+    return 0;
+  }
+  return (int)((keys + tile - 1) / tile);
+}
+// Query-row blocks of a (sequence, KV head): one while all heads' rows fit in kV4Lanes.
+__host__ __device__ __forceinline__ int row_blocks(int rows) {
+  return rows * kGroup > kV4Lanes ? 2 : 1;
+}
+
+// Tiles of every sequence into shared memory, by a block of kBlock threads.
+template <int kBlock>
+__device__ __forceinline__ void load_tiles(const Verify4Args& a, uint16_t* tiles, int tile, bool report) {
+  for (int b = threadIdx.x; b < a.n_seq; b += kBlock)
+    tiles[b] = (uint16_t)seq_tiles(a, b, tile, report);
+}
+// Sum of tiles[0 .. n - 1] by one warp (every lane gets it).
+__device__ __forceinline__ int warp_sum_tiles(const uint16_t* tiles, int n) {
+  int s = 0;
+  for (int b = threadIdx.x & 31; b < n; b += 32) s += tiles[b];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  return s;
+}
+
+// A CTA's share of the streams' tiles: `left` tiles from tile `tile` of stream (plane, b) on.
+// plane = 2 x row block + KV head; streams are ordered by plane, then sequence.
+struct Seg {
+  int plane, b, kt0, n;   // tiles kt0 .. kt0 + n - 1 of the stream
+  bool whole;             // all of the stream's tiles
+  int slot;               // partial slot of a segment that is not whole
+};
+// What every role of a CTA derives its share from, in shared memory.
+struct V4Cut {
+  uint16_t tiles[kV4MaxSeq];   // key tiles of each sequence
+  int units, plane0, b0, tile0;
+};
+struct Walk {
+  int plane, b, tile, left, seen;
+  __device__ __forceinline__ explicit Walk(const V4Cut& c)
+      : plane(c.plane0), b(c.b0), tile(c.tile0), left(c.units), seen(0) {}
+  __device__ __forceinline__ bool next(const V4Cut& c, int n_seq, Seg& s) {
+    if (left <= 0) return false;
+    int total = c.tiles[b];
+    while (tile >= total) {   // the next stream with tiles
+      tile = 0;
+      if (++b == n_seq) {
+        b = 0;
+        ++plane;
+      }
+      total = c.tiles[b];
+    }
+    s.plane = plane;
+    s.b = b;
+    s.kt0 = tile;
+    s.n = min(left, total - tile);
+    s.whole = s.n == total;
+    // of a CTA's segments only the first and the last can be parts of a stream
+    s.slot = 2 * (int)blockIdx.x + (seen ? 1 : 0);
+    ++seen;
+    tile += s.n;
+    left -= s.n;
+    return true;
+  }
+};
+
+// Tiles per CTA of a cut of `total` tiles over `ctas` CTAs.
+__device__ __forceinline__ int v4_share(int total, int ctas) { return (total + ctas - 1) / ctas; }
+
+// This CTA's part of the cut, by one warp: its first tile and number of tiles, into c.
+__device__ __forceinline__ void find_share(V4Cut& sm, int n_seq, int planes) {
+  const int lane = threadIdx.x & 31;
+  const int per_plane = warp_sum_tiles(sm.tiles, n_seq);
+  const int total = per_plane * planes;
+  const int share = v4_share(total, (int)gridDim.x);
+  const long long u0 = (long long)share * blockIdx.x;
+  const int units = (int)min((long long)share, max(0LL, (long long)total - u0));
+  int plane = 0, b0 = 0, tile0 = 0;
+  if (units > 0) {
+    plane = (int)(u0 / per_plane);
+    int rem = (int)(u0 - (long long)plane * per_plane);
+    // the sequence holding tile `rem` of the plane: sums of 32 sequences at a time
+    for (int base = 0; base < n_seq; base += 32) {
+      const int t = base + lane < n_seq ? sm.tiles[base + lane] : 0;
+      int inc = t;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += o;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, inc > rem);
+      if (past) {
+        const int k = __ffs((int)past) - 1;
+        b0 = base + k;
+        tile0 = rem - __shfl_sync(0xffffffffu, inc - t, k);
+        break;
+      }
+      rem -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  if (lane == 0) {
+    sm.units = units;
+    sm.plane0 = plane;
+    sm.b0 = b0;
+    sm.tile0 = tile0;
+  }
+}
+
+// The log-sum-exp merge of the streams that the cut left in parts, after either kernel with
+// tiles of `tile` keys.
+cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, cudaStream_t s);
+
+}  // namespace ga

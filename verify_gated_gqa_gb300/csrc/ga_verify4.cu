@@ -33,9 +33,7 @@
 // the rows unrolled through registers the widening alone took 3,500 cycles a tile).
 // Tensor memory: O [0, 256), S [256, 384), Q dims 0..127 [384, 448), P [448, 512).
 // Every wait is bounded; a wait that gives up raises the CTA's abort flag, which the others see.
-#include "ga_internal.h"
-#include "ga_q4.cuh"
-#include "ga_sm100.cuh"
+#include "ga_v4.cuh"
 
 namespace ga {
 namespace {
@@ -46,7 +44,6 @@ constexpr int kGranule = 32;              // keys per TMA box
 constexpr int kStages = 2;                // raw tiles in flight, for K and for V
 constexpr int kRawBytes = kTileN * kQ4RowBytes, kRawScaleBytes = kTileN * kQ4ScaleBytes;
 constexpr int kQBlockBytes = kV4Lanes * 128;      // 64 dims of the query rows
-constexpr int kMaxRowsWhole = kV4Lanes / kGroup;  // window rows up to which 12 heads fit
 // Registers: launched at 72 a thread (896 x 72 = 64,512). The issuing warpgroup keeps 64, the
 // softmax warpgroups take 120, the four widening ones keep 48: 128 x (64 + 2 x 120 + 4 x 48) =
 // 63,488.
@@ -63,161 +60,21 @@ struct V4Smem {
   uint8_t qhi[2][kQBlockBytes];            // Q dims 128..255 (the MMA reads 32 rows past each block)
   uint8_t raw[2 * kStages][kRawBytes];     // code rows: K's stages, then V's
   uint8_t rsc[2 * kStages][kRawScaleBytes];
-  uint16_t tiles[kV4MaxSeq];               // key tiles of each sequence
+  V4Cut cut;
   float mx[2][2][kV4Lanes];                // exchange i: each half's row value, by i % 2
   uint64_t raw_full[2 * kStages], raw_empty[2 * kStages];
   uint64_t full[8], empty[8];              // pieces of the K tile, then of the V tile
   uint64_t q_full, s_full, s_free, p_full[2], p_empty[2], o_done, o_free, mx_bar;
   uint64_t drain_qk, drain_pv;
-  int units, plane0, b0, tile0;
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(V4Smem) <= 232448, "227 KiB of shared memory per CTA");
 
-__device__ __forceinline__ void record(int* status, int code) {
-  if (code) atomicCAS(status, 0, code);
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const bool ok = mbar_wait(bar, parity, abort);
-  return __all_sync(0xffffffffu, ok);
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts_v4(uint32_t addr, const uint32_t (&v)[4]) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3])
-               : "memory");
-}
-// A tensor load by the calling thread alone.
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
-      : "memory");
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-// ------------------------------------------------------------------ the cut of the work
-// Key tiles (of `tile` keys) of a sequence: none when its slot is unused (negative length) or
-// its window passes the end of its page-table row, which is recorded.
-__device__ __forceinline__ int seq_tiles(const Verify4Args& a, int b, int tile, bool report) {
-  const int L = a.seq_len[b];
-  if (L < 0) return 0;
-  const long long keys = (long long)L + a.rows;
-  if (keys > (long long)a.max_pages * a.page_size || keys > GA_MAX_TOKENS) {
-    if (report) record(a.status, kDevBadPosition);
-    return 0;
-  }
-  return (int)((keys + tile - 1) / tile);
-}
-__host__ __device__ __forceinline__ int row_blocks(int rows) { return rows > kMaxRowsWhole ? 2 : 1; }
-
-// Tiles of every sequence into shared memory, by a block of kBlock threads.
-template <int kBlock>
-__device__ __forceinline__ void load_tiles(const Verify4Args& a, uint16_t* tiles, int tile, bool report) {
-  for (int b = threadIdx.x; b < a.n_seq; b += kBlock)
-    tiles[b] = (uint16_t)seq_tiles(a, b, tile, report);
-}
-// Sum of tiles[0 .. n - 1] by one warp (every lane gets it).
-__device__ __forceinline__ int warp_sum_tiles(const uint16_t* tiles, int n) {
-  int s = 0;
-  for (int b = threadIdx.x & 31; b < n; b += 32) s += tiles[b];
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  return s;
-}
-
-// A CTA's share of the streams' tiles: `left` tiles from tile `tile` of stream (plane, b) on.
-// plane = 2 x row block + KV head; streams are ordered by plane, then sequence.
-struct Seg {
-  int plane, b, kt0, n;   // tiles kt0 .. kt0 + n - 1 of the stream
-  bool whole;             // all of the stream's tiles
-  int slot;               // partial slot of a segment that is not whole
-};
-struct Walk {
-  int plane, b, tile, left, seen;
-  __device__ __forceinline__ explicit Walk(const V4Smem& sm)
-      : plane(sm.plane0), b(sm.b0), tile(sm.tile0), left(sm.units), seen(0) {}
-  __device__ __forceinline__ bool next(const V4Smem& sm, const Verify4Args& a, Seg& s) {
-    if (left <= 0) return false;
-    int total = sm.tiles[b];
-    while (tile >= total) {   // the next stream with tiles
-      tile = 0;
-      if (++b == a.n_seq) {
-        b = 0;
-        ++plane;
-      }
-      total = sm.tiles[b];
-    }
-    s.plane = plane;
-    s.b = b;
-    s.kt0 = tile;
-    s.n = min(left, total - tile);
-    s.whole = s.n == total;
-    // of a CTA's segments only the first and the last can be parts of a stream
-    s.slot = 2 * (int)blockIdx.x + (seen ? 1 : 0);
-    ++seen;
-    tile += s.n;
-    left -= s.n;
-    return true;
-  }
-};
-
-// This CTA's part of the cut, by one warp: its first tile and number of tiles, into sm.
-__device__ __forceinline__ void find_share(V4Smem& sm, const Verify4Args& a) {
-  const int lane = threadIdx.x & 31;
-  const int planes = kKvHeads * row_blocks(a.rows);
-  const int per_plane = warp_sum_tiles(sm.tiles, a.n_seq);
-  const int total = per_plane * planes;
-  const int share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-  const long long u0 = (long long)share * blockIdx.x;
-  const int units = (int)min((long long)share, max(0LL, (long long)total - u0));
-  int plane = 0, b0 = 0, tile0 = 0;
-  if (units > 0) {
-    plane = (int)(u0 / per_plane);
-    int rem = (int)(u0 - (long long)plane * per_plane);
-    // the sequence holding tile `rem` of the plane: sums of 32 sequences at a time
-    for (int base = 0; base < a.n_seq; base += 32) {
-      const int t = base + lane < a.n_seq ? sm.tiles[base + lane] : 0;
-      int inc = t;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += o;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, inc > rem);
-      if (past) {
-        const int k = __ffs((int)past) - 1;
-        b0 = base + k;
-        tile0 = rem - __shfl_sync(0xffffffffu, inc - t, k);
-        break;
-      }
-      rem -= __shfl_sync(0xffffffffu, inc, 31);
-    }
-  }
-  if (lane == 0) {
-    sm.units = units;
-    sm.plane0 = plane;
-    sm.b0 = b0;
-    sm.tile0 = tile0;
-  }
 }
 
 // ------------------------------------------------------------------ loading codes
@@ -229,9 +86,9 @@ __device__ void raw_loader(V4Smem& sm, const CUtensorMap* tm_c, const CUtensorMa
   const int lane = threadIdx.x & 31;
   const long long n_rows = (long long)a.n_pages * kKvHeads * a.page_size;
   uint32_t f = 0;   // tiles issued
-  Walk walk(sm);
+  Walk walk(sm.cut);
   Seg seg;
-  while (walk.next(sm, a, seg)) {
+  while (walk.next(sm.cut, a.n_seq, seg)) {
     const int end = a.seq_len[seg.b] + a.rows;
     const int* table = a.page_table + (size_t)seg.b * a.max_pages;
     // the pool row of this lane's granule of tile kt
@@ -289,7 +146,7 @@ __device__ void widen_worker(V4Smem& sm, int is_v, volatile int* abort) {
   const uint32_t ch0 = ch;
   uint64_t* full = sm.full + 4 * is_v;
   uint64_t* empty = sm.empty + 4 * is_v;
-  const int n = sm.units;
+  const int n = sm.cut.units;
   for (int g = 0; g < n; ++g) {
     const int st = kStages * is_v + g % kStages;
     if (!warp_wait(&sm.raw_full[st], (g / kStages) & 1, abort)) return;
@@ -331,10 +188,10 @@ __device__ void qk_issue(V4Smem& sm, const Verify4Args& a, uint32_t tmem, volati
   constexpr uint32_t kId = idesc_bf16(128, kTileN, false, false);
   const uint64_t k_desc = sdesc_sw128(smem_u32(sm.kt[0]), 16, 1024);
   const uint64_t q_desc = sdesc_sw128(smem_u32(sm.qhi[0]), 16, 1024);
-  Walk walk(sm);
+  Walk walk(sm.cut);
   Seg seg;
   uint32_t g = 0, done = 0;
-  while (walk.next(sm, a, seg)) {
+  while (walk.next(sm.cut, a.n_seq, seg)) {
     if (!warp_wait(&sm.q_full, done & 1, abort)) return;
     for (int j = 0; j < seg.n; ++j, ++g) {
       if (g > 0 && !warp_wait(&sm.s_free, (g - 1) & 1, abort)) return;
@@ -363,10 +220,10 @@ __device__ void qk_issue(V4Smem& sm, const Verify4Args& a, uint32_t tmem, volati
 __device__ void pv_issue(V4Smem& sm, const Verify4Args& a, uint32_t tmem, volatile int* abort) {
   constexpr uint32_t kId = idesc_bf16(128, kDim, false, true);
   const uint64_t v_desc = sdesc_sw128(smem_u32(sm.vt[0]), kGranule * 128, 1024);
-  Walk walk(sm);
+  Walk walk(sm.cut);
   Seg seg;
   uint32_t g = 0, done = 0;
-  while (walk.next(sm, a, seg)) {
+  while (walk.next(sm.cut, a.n_seq, seg)) {
     if (done > 0 && !warp_wait(&sm.o_free, (done - 1) & 1, abort)) return;
     for (int j = 0; j < seg.n; ++j, ++g) {
 #pragma unroll
@@ -389,10 +246,6 @@ __device__ void pv_issue(V4Smem& sm, const Verify4Args& a, uint32_t tmem, volati
 }
 
 // ------------------------------------------------------------------ softmax
-__device__ __forceinline__ float sigmoid_f(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
-__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-
 // Warpgroup hf takes keys 64 hf .. + 63 of every tile, and dims 128 hf .. + 127 of Q and O.
 __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, int hf,
                                volatile int* abort) {
@@ -416,9 +269,9 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
     ++mxn;
     return ok;
   };
-  Walk walk(sm);
+  Walk walk(sm.cut);
   Seg seg;
-  while (walk.next(sm, a, seg)) {
+  while (walk.next(sm.cut, a.n_seq, seg)) {
     const int L = a.seq_len[seg.b];
     const int limit = L + min(rr, a.rows - 1);   // the row's last visible key
     const int h = (seg.plane & 1) * kGroup + (seg.plane >> 1) * heads + hh;
@@ -584,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &sm.abort;
   // softmax warps with query rows, of each warpgroup's four
   const uint32_t act = (uint32_t)(a.rows * (kGroup / row_blocks(a.rows)) + 31) / 32;
-  load_tiles<kThreads>(a, sm.tiles, kTileN, blockIdx.x == 0);
+  load_tiles<kThreads>(a, sm.cut.tiles, kTileN, blockIdx.x == 0);
   if (threadIdx.x == 0) {
     sm.abort = 0;
     for (int i = 0; i < 2 * kStages; ++i) {
@@ -615,18 +468,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) find_share(sm, a);
+  if (warp == 0) find_share(sm.cut, a.n_seq, kKvHeads * row_blocks(a.rows));
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 0 && sm.units > 0) {
+    if (warp == 0 && sm.cut.units > 0) {
       qk_issue(sm, a, tmem, abort);
       umma_commit_warp(&sm.drain_qk);
       mbar_wait_quiet(&sm.drain_qk, 0, 100000000LL);
     }
-    if (warp == 1 && sm.units > 0) {
+    if (warp == 1 && sm.cut.units > 0) {
       pv_issue(sm, a, tmem, abort);
       umma_commit_warp(&sm.drain_pv);
       mbar_wait_quiet(&sm.drain_pv, 0, 100000000LL);
@@ -655,20 +508,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // it in parts. Four warps take every fourth part, eight dims a lane, and join in shared memory.
 constexpr int kCombineThreads = 128;
 __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
-    const __grid_constant__ Verify4Args a, int ctas) {
+    const __grid_constant__ Verify4Args a, int ctas, int tile) {
   __shared__ uint16_t tiles[kV4MaxSeq];
   __shared__ float so[4][kDim], sml[4][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.x % kHeads, rr = (blockIdx.x / kHeads) % a.rows;
   const int b = blockIdx.x / (kHeads * a.rows);
-  load_tiles<kCombineThreads>(a, tiles, kTileN, false);
+  load_tiles<kCombineThreads>(a, tiles, tile, false);
   __syncthreads();
   if (tiles[b] == 0) return;
   const int blocks = row_blocks(a.rows), heads = kGroup / blocks;
   const int per_plane = warp_sum_tiles(tiles, a.n_seq);
   const int before = warp_sum_tiles(tiles, b);
   const int total = per_plane * kKvHeads * blocks;
-  const int share = (total + ctas - 1) / ctas;
+  const int share = v4_share(total, ctas);
   const int kvh = h / kGroup, hg = h % kGroup;
   const int plane = 2 * (hg / heads) + kvh;
   const long long u0 = (long long)plane * per_plane + before, u1 = u0 + tiles[b] - 1;
@@ -731,19 +584,24 @@ size_t verify4_ws_bytes() {
 }
 
 cudaError_t verify4_set_attributes() {
-  return cudaFuncSetAttribute(verify4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)sizeof(V4Smem));
+  const cudaError_t e = cudaFuncSetAttribute(
+      verify4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(V4Smem));
+  return e != cudaSuccess ? e : decode4_set_attributes();
+}
+
+cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, cudaStream_t s) {
+  verify4_combine_kernel<<<a.n_seq * a.rows * kHeads, kCombineThreads, 0, s>>>(a, ctas, tile);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
                            const CUtensorMap& k_scales, const CUtensorMap& v_scales,
                            const Verify4Args& a, int sm_count, cudaStream_t s) {
   const int ctas = sm_count < kV4MaxCtas ? sm_count : kV4MaxCtas;
+  if (a.rows == 1) return launch_decode4(k_codes, v_codes, k_scales, v_scales, a, ctas, s);
   verify4_kernel<<<ctas, kThreads, sizeof(V4Smem), s>>>(k_codes, v_codes, k_scales, v_scales, a);
   const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  verify4_combine_kernel<<<a.n_seq * a.rows * kHeads, kCombineThreads, 0, s>>>(a, ctas);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : launch_verify4_combine(a, ctas, kTileN, s);
 }
 
 }  // namespace ga
