@@ -38,7 +38,7 @@ constexpr float kLazyRescale = 8.0f;
 struct D4Smem {
   uint8_t codes[kWarps][kStages][2][kCodeBytes];   // K, V
   uint8_t scales[kWarps][kStages][2][kScaleBytes];
-  uint4 q[16][32];                                 // Q fragments: (chunk, word, row half) x lane
+  uint4 q[16][32];                                 // Q fragments: k-step x lane
   float join[kWarps][8][kJoinStride];              // a segment's O by warp, eight rows at a time
   float m[kWarps][16], l[kWarps][16];
   V4Cut cut;
@@ -61,7 +61,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 }
 // A pair of codes at nibble p of both halves of w, widened.
 __device__ __forceinline__ uint32_t widen_pair(uint32_t w, int p, Q4Scale q) {
-  return q4_fma_bf16x2(((w >> (4 * p)) & 0x000F000Fu) | 0x43004300u, q.s, q.off);
+  return q4_fma_bf16x2(q4_codes(w, p), q.s, q.off);
 }
 // Multipliers of two keys' groups: bytes b of ua and ub in the low and the high half.
 __device__ __forceinline__ Q4Scale scale_pair(uint32_t ua, uint32_t ub, int b) {
@@ -142,17 +142,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   Seg seg;
   while (walk.next(sm.cut, a.n_seq, seg)) {
     const int L = a.seq_len[seg.b];
-    // Q fragments: item (chunk cc, word j, row half rh) of a lane is dims 64 t + 32 cc + 8 j .. + 7
-    // of row g + 8 rh; rows 12 .. 15 are zeros
+    // Q fragments of k-step i (of lane t's dims 64 t + 4 i .. + 3): rows g, g + 8 at the first two
+    // of them, then at the last two; rows 12 .. 15 are zeros
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int item = (tid >> 5) * 2 + i;   // 16 items of 32 lanes
-      const int row = g + 8 * (item & 1), d = 64 * t + 32 * (item >> 3) + 8 * ((item >> 1) & 3);
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (row < kGroup)
-        x = __ldg(reinterpret_cast<const uint4*>(
-            a.q_prep + ((size_t)seg.b * kHeads + seg.plane * kGroup + row) * kDim + d));
-      sm.q[item][lane] = x;
+    for (int i = 2 * warp; i < 2 * warp + 2; ++i) {
+      const uint2* x = reinterpret_cast<const uint2*>(
+          a.q_prep + ((size_t)seg.b * kHeads + seg.plane * kGroup + g) * kDim + 64 * t + 4 * i);
+      const uint2 lo = __ldg(x);
+      const uint2 hi = g < kGroup - 8 ? __ldg(x + 8 * kDim / 4) : make_uint2(0u, 0u);
+      sm.q[i][lane] = make_uint4(lo.x, hi.x, lo.y, hi.y);
     }
     __syncthreads();
     const uint32_t q_at = smem_u32(&sm.q[0][lane]);
@@ -188,16 +186,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           kw[n] = lds_v4(kc + (8 * n + g) * kQ4RowBytes + (((2 * t + cc) ^ g) << 4));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint4 qa = lds_v4(q_at + (8 * cc + 2 * j) * 512);
-          const uint4 qb = lds_v4(q_at + (8 * cc + 2 * j + 1) * 512);
+          const uint4 q0 = lds_v4(q_at + (8 * cc + 2 * j) * 512);       // two k-steps
+          const uint4 q1 = lds_v4(q_at + (8 * cc + 2 * j + 1) * 512);
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
             const uint32_t w = j == 0 ? kw[n].x : j == 1 ? kw[n].y : j == 2 ? kw[n].z : kw[n].w;
             const Q4Scale sc = q4_scale((ksc[n] >> (16 * cc + 8 * (j >> 1))) & 0xFFu);
             uint32_t b[4];
             q4_widen(w, sc, b);
-            mma_16816(s[n], qa.x, qb.x, qa.y, qb.y, b[0], b[1]);
-            mma_16816(s[n], qa.z, qb.z, qa.w, qb.w, b[2], b[3]);
+            mma_16816(s[n], q0.x, q0.y, q0.z, q0.w, b[0], b[1]);
+            mma_16816(s[n], q1.x, q1.y, q1.z, q1.w, b[2], b[3]);
           }
         }
       }

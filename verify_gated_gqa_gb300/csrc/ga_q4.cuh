@@ -48,12 +48,18 @@ __device__ __forceinline__ Q4Scale q4_scale(uint32_t b) {
   return q;
 }
 
+// The pair of codes at nibble p of both halves of w as bf16 128 + n: one shift and one
+// three-input logic operation (the compiler by itself makes the AND and the OR two).
+__device__ __forceinline__ uint32_t q4_codes(uint32_t w, int p) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * p)), "r"(0x000F000Fu), "r"(0x43004300u));
+  return r;
+}
 // The eight bf16 values of one word, in dim order: two per register.
 __device__ __forceinline__ void q4_widen(uint32_t w, Q4Scale q, uint32_t (&o)[4]) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    const uint32_t n = ((w >> (4 * p)) & 0x000F000Fu) | 0x43004300u;
-    o[p] = q4_fma_bf16x2(n, q.s, q.off);
+    o[p] = q4_fma_bf16x2(q4_codes(w, p), q.s, q.off);
   }
 }
 
