@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   volatile int* abort = &sm.abort;
+  grid_launch_dependents();
   load_tiles<kThreads>(a, sm.cut.tiles, kKeys, blockIdx.x == 0);
   if (tid == 0) {
     sm.abort = 0;
@@ -104,9 +105,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   Seg as{};
   int aj = 0;                // next granule of `as` of this warp
   uint32_t issued = 0;
-  int next_row = -1;         // pool row of the granule to issue next (-1: none is left)
+  // the granule to issue next: its page-table entry (in flight until the issue reads it) and place
+  // in the page; next_at < 0: none is left
+  int next_page = 0, next_at = -1;
   auto find_next = [&]() {
-    next_row = -1;
+    next_at = -1;
     while (aj >= as.n) {
       if (!ahead.next(sm.cut, a.n_seq, as)) return;
       aj = warp;
@@ -114,22 +117,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key0 = (as.kt0 + aj) * kKeys;
     aj += kWarps;
     const int e = key0 / a.page_size;
-    const int page = __ldg(a.page_table + (size_t)as.b * a.max_pages + e);
-    if (page >= 0 && page < a.n_pages) {
-      next_row = (page * kKvHeads + as.plane) * a.page_size + key0 - e * a.page_size;
-    } else {
-      if (lane == 0) record(a.status, kDevBadPage);
-      next_row = n_rows;
-    }
+    next_page = __ldg(a.page_table + (size_t)as.b * a.max_pages + e);
+    next_at = as.plane * a.page_size + key0 - e * a.page_size;
   };
   auto issue = [&]() {
-    if (next_row < 0) return;
+    if (next_at < 0) return;
+    int row = n_rows;
+    if (next_page >= 0 && next_page < a.n_pages) row = next_page * kKvHeads * a.page_size + next_at;
+    else if (lane == 0) record(a.status, kDevBadPage);
     const int st = (int)(issued % kStages);
     if (lane == 0) mbar_arrive_expect_tx(&sm.full[warp][st], kStageBytes);
     __syncwarp();
     if (lane < 4)
       tma_load_2d(lane < 2 ? sm.codes[warp][st][lane] : sm.scales[warp][st][lane - 2], my_map,
-                  &sm.full[warp][st], 0, next_row);
+                  &sm.full[warp][st], 0, row);
     ++issued;
     find_next();
   };
@@ -365,7 +366,7 @@ cudaError_t launch_decode4(const CUtensorMap& k_codes, const CUtensorMap& v_code
                            const Verify4Args& a, int ctas, cudaStream_t s) {
   decode4_kernel<<<ctas, kThreads, sizeof(D4Smem), s>>>(k_codes, v_codes, k_scales, v_scales, a);
   const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_verify4_combine(a, ctas, kKeys, s);
+  return e != cudaSuccess ? e : launch_verify4_combine(a, ctas, kKeys, ctas, s);
 }
 
 }  // namespace ga

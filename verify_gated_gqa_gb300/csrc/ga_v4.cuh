@@ -40,6 +40,12 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
       : "memory");
 }
+// Programmatic dependent launch: the next kernel's blocks may be placed from here on; they wait
+// (grid_wait) for this one's end before they read what it wrote.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ float sigmoid_f(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
@@ -91,6 +97,7 @@ struct V4Cut {
   int units, plane0, b0, tile0;
 };
 struct Walk {
+  Walk() = default;
   int plane, b, tile, left, seen;
   __device__ __forceinline__ explicit Walk(const V4Cut& c)
       : plane(c.plane0), b(c.b0), tile(c.tile0), left(c.units), seen(0) {}
@@ -163,6 +170,7 @@ __device__ __forceinline__ void find_share(V4Cut& sm, int n_seq, int planes) {
 
 // The log-sum-exp merge of the streams that the cut left in parts, after either kernel with
 // tiles of `tile` keys.
-cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, cudaStream_t s);
+cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, int sm_count,
+                                   cudaStream_t s);
 
 }  // namespace ga

@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   V4Smem& sm = *reinterpret_cast<V4Smem*>(smem_raw);
   const int warp = threadIdx.x >> 5;
   volatile int* abort = &sm.abort;
+  grid_launch_dependents();
   // softmax warps with query rows, of each warpgroup's four
   const uint32_t act = (uint32_t)(a.rows * (kGroup / row_blocks(a.rows)) + 31) / 32;
   load_tiles<kThreads>(a, sm.cut.tiles, kTileN, blockIdx.x == 0);
@@ -504,19 +505,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ combine
-// A block per (sequence, window row, query head): the partials of its stream, if the cut left
-// it in parts. Four warps take every fourth part, eight dims a lane, and join in shared memory.
-constexpr int kCombineThreads = 128;
-__global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
+// A block per (sequence, window row, query head): the parts of its stream, if the cut left it in
+// parts. Every part's weight first (a part a thread), then each of kWarps warps takes every
+// kWarps-th part, eight dims a lane, four parts' loads in flight, and they join in shared memory.
+// Eight warps when the rows are too few to fill the device (one sequence over 65,536 keys has 76
+// parts a row: 21 us with four warps that formed the weights on the way and loaded nothing
+// ahead, 7.6 us so), two when they fill it, where a stream has a few parts and the blocks'
+// number counts (64 sequences: 14 us with eight).
+template <int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) verify4_combine_kernel(
     const __grid_constant__ Verify4Args a, int ctas, int tile) {
+  constexpr int kCombineThreads = 32 * kWarps, kDims = kDim / kCombineThreads;
   __shared__ uint16_t tiles[kV4MaxSeq];
-  __shared__ float so[4][kDim], sml[4][2];
+  __shared__ float so[kWarps][kDim], f[kV4MaxCtas], red[kWarps], red_l[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.x % kHeads, rr = (blockIdx.x / kHeads) % a.rows;
   const int b = blockIdx.x / (kHeads * a.rows);
   load_tiles<kCombineThreads>(a, tiles, tile, false);
   __syncthreads();
-  if (tiles[b] == 0) return;
   const int blocks = row_blocks(a.rows), heads = kGroup / blocks;
   const int per_plane = warp_sum_tiles(tiles, a.n_seq);
   const int before = warp_sum_tiles(tiles, b);
@@ -524,57 +530,84 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   const int share = v4_share(total, ctas);
   const int kvh = h / kGroup, hg = h % kGroup;
   const int plane = 2 * (hg / heads) + kvh;
-  const long long u0 = (long long)plane * per_plane + before, u1 = u0 + tiles[b] - 1;
-  const int c0 = (int)(u0 / share), c1 = (int)(u1 / share);
-  if (c0 == c1) return;   // one CTA ran the whole stream and wrote it
+  const long long u0 = (long long)plane * per_plane + before, u1 = u0 + max((int)tiles[b], 1) - 1;
+  const int c0 = (int)(u0 / share), n = (int)(u1 / share) - c0 + 1;
   const int r = rr * heads + hg % heads;
-  // CTA c's part is its first segment unless the stream began inside the CTA's run
-  auto part_row = [&](int c) -> size_t {
-    const int slot = 2 * c + ((long long)c * share < u0 ? 1 : 0);
-    return (size_t)slot * kV4Lanes + r;
+  // part i is of CTA c0 + i: its first segment unless the stream began inside the CTA's run
+  const bool inside = (long long)c0 * share < u0;
+  auto part_row = [&](int i) -> size_t {
+    return (size_t)(2 * (c0 + i) + (i == 0 && inside ? 1 : 0)) * kV4Lanes + r;
   };
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-  float M = -INFINITY, L = 0.f, o[8];
+  grid_wait();   // in every block: the grid's end then stands for the attention kernel's too
+  if (tiles[b] == 0 || n == 1) return;   // unused, or one CTA ran the whole stream and wrote it
+  float2 x[(kV4MaxCtas + kCombineThreads - 1) / kCombineThreads];
+  constexpr int kPer = sizeof(x) / sizeof(x[0]);   // parts a thread weighs
+  float M = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = threadIdx.x + k * kCombineThreads;
+    x[k] = i < n ? reinterpret_cast<const float2*>(a.part_ml)[part_row(i)] : make_float2(-INFINITY, 0.f);
+    M = fmaxf(M, x[k].x);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if (lane == 0) red[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[w]);
+  float L = 0.f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = threadIdx.x + k * kCombineThreads;
+    const float fx = x[k].x == -INFINITY ? 0.f : exp2f(x[k].x - M);   // no visible key: none
+    L = fmaf(fx, x[k].y, L);
+    if (i < n) f[i] = fx;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  if (lane == 0) red_l[warp] = L;
+  __syncthreads();
+  float o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  for (int c = c0 + warp; c <= c1; c += 4) {
-    const size_t pr = part_row(c);
-    const float2 x = ml[pr];
-    const float4* p = reinterpret_cast<const float4*>(a.part_o + pr * kDim + 8 * lane);
-    const float4 v0 = p[0], v1 = p[1];
-    if (x.x == -INFINITY && x.y == 0.f) continue;   // no key of the part is visible to the row
-    const float newM = fmaxf(M, x.x);
-    const float fa = M == -INFINITY ? 0.f : exp2f(M - newM), fb = exp2f(x.x - newM);
-    const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  for (int i0 = warp; i0 < n; i0 += 4 * kWarps) {
+    float4 v[4][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], fb, o[i] * fa);
-    L = fmaf(x.y, fb, L * fa);
-    M = newM;
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * kWarps;
+      if (i >= n) continue;
+      const float4* p = reinterpret_cast<const float4*>(a.part_o + part_row(i) * kDim + 8 * lane);
+      v[k][0] = p[0];
+      v[k][1] = p[1];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * kWarps;
+      if (i >= n) continue;
+      const float w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                          v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+      const float fi = f[i];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) o[q] = fmaf(fi, w[q], o[q]);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) so[warp][8 * lane + i] = o[i];
-  if (lane == 0) {
-    sml[warp][0] = M;
-    sml[warp][1] = L;
-  }
+  for (int q = 0; q < 8; ++q) so[warp][8 * lane + q] = o[q];
   __syncthreads();
-  float Mt = -INFINITY;
+  float Lt = 0.f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) Mt = fmaxf(Mt, sml[w][0]);
-  float Lt = 0.f, x0 = 0.f, x1 = 0.f;
-  const int d = 2 * threadIdx.x;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = sml[w][0] == -INFINITY ? 0.f : exp2f(sml[w][0] - Mt);
-    Lt = fmaf(sml[w][1], f, Lt);
-    x0 = fmaf(so[w][d], f, x0);
-    x1 = fmaf(so[w][d + 1], f, x1);
-  }
+  for (int w = 0; w < kWarps; ++w) Lt += red_l[w];
   const float inv = Lt > 0.f ? 1.0f / Lt : (Lt != Lt ? Lt : 0.f);
   const size_t row = ((size_t)b * a.rows + rr) * kHeads + h;
-  const uint32_t gw = __ldg(reinterpret_cast<const uint32_t*>(a.qg + row * kQgStride + kDim + d));
-  reinterpret_cast<uint32_t*>(a.out + row * kDim + d)[0] =
-      pack_bf16x2(x0 * inv * sigmoid_f(lo_f(gw)), x1 * inv * sigmoid_f(hi_f(gw)));
+#pragma unroll
+  for (int k = 0; k < kDims; ++k) {
+    const int d = threadIdx.x + k * kCombineThreads;
+    float y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) y += so[w][d];
+    const float g = __uint_as_float((uint32_t)a.qg[row * kQgStride + kDim + d] << 16);
+    a.out[row * kDim + d] = (uint16_t)(pack_bf16x2(y * inv * sigmoid_f(g), 0.f) & 0xFFFFu);
+  }
 }
 
 }  // namespace
@@ -589,9 +622,21 @@ cudaError_t verify4_set_attributes() {
   return e != cudaSuccess ? e : decode4_set_attributes();
 }
 
-cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, cudaStream_t s) {
-  verify4_combine_kernel<<<a.n_seq * a.rows * kHeads, kCombineThreads, 0, s>>>(a, ctas, tile);
-  return cudaGetLastError();
+cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, int sm_count,
+                                   cudaStream_t s) {
+  const int blocks = a.n_seq * a.rows * kHeads;
+  const bool few = blocks < 4 * sm_count;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(few ? 256 : 64);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return few ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<8>, a, ctas, tile)
+             : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<2>, a, ctas, tile);
 }
 
 cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
@@ -601,7 +646,7 @@ cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_code
   if (a.rows == 1) return launch_decode4(k_codes, v_codes, k_scales, v_scales, a, ctas, s);
   verify4_kernel<<<ctas, kThreads, sizeof(V4Smem), s>>>(k_codes, v_codes, k_scales, v_scales, a);
   const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_verify4_combine(a, ctas, kTileN, s);
+  return e != cudaSuccess ? e : launch_verify4_combine(a, ctas, kTileN, sm_count, s);
 }
 
 }  // namespace ga
