@@ -1348,6 +1348,7 @@ int ga_kv_dequantize_q4(const uint8_t* k_codes, const uint8_t* k_scales, const u
   a.slots = slots; a.n_tok = n_tok;
   a.n_slots = (long long)n_pages * page_size; a.page_size = page_size;
   a.k_out = k_out; a.v_out = v_out;
+  a.out32 = aligned(k_out, 32) && aligned(v_out, 32);
   a.status = dev->status_word;
   const cudaError_t e = GA_CUDA(launch_dequantize_q4(a, (cudaStream_t)stream));
   return e == cudaSuccess ? GA_OK : fail_cuda(e);

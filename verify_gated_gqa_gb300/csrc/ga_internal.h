@@ -187,6 +187,7 @@ struct Kv4Args {
   long long n_tok, n_slots;
   int page_size;
   uint16_t *k_out, *v_out;    // widening: [n_tok][2][256]
+  bool out32;                 // and both 32-byte aligned
   int* status;
 };
 cudaError_t launch_quantize_q4(const Kv4Args& a, cudaStream_t s);
