@@ -7,7 +7,6 @@ current stream. There is no CPU fallback: if the library is not built, every cal
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -566,45 +565,23 @@ def ga_attn_verify_e4m3(qg, k_codes, k_scale, v_codes, v_scale, seq_len, w_q, co
 
 
 # ------------------------------------------------------------------ serving over 4-bit pages
-# These calls run once a decode step, where the host's microseconds count: one pass of plain
-# comparisons per tensor, addresses as integers, the stream's handle without a Stream object.
+# These calls run once a decode step, where the host's microseconds count: the native module
+# (csrc/ga_native.cpp) checks their tensors, makes the outputs that were not given and calls the
+# library in one step. Tensors live on the current CUDA device; one that does not belong raises
+# ValueError.
 Q4_ROW_BYTES, Q4_SCALE_BYTES, Q4_PAGE_TOKENS = 128, 16, 32
-_BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_native_module = None
 
 
-def _device(t, name):
-    """The current CUDA device's index, which must be the tensor's."""
-    dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"{name} must be a tensor on the current CUDA device")
-    return dev
+def _native():
+    """The native module (raises if it has not been built)."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        from . import _native as module
 
-
-def _stream_of(dev):
-    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
-
-
-def _addr(name, t, dtype, shape, dev):
-    """The address of a contiguous tensor of the given type, shape and device (of an empty one, a
-    stand-in that is aligned and never read)."""
-    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev or
-            not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on CUDA device "
-                         f"{dev}, not {t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr() or 256
-
-
-def _q4_pools(k_codes, k_scales, v_codes, v_scales, dev):
-    """(addresses of the four pools, n_pages, page_size)."""
-    if k_codes.dim() != 4:
-        raise ValueError("k_codes must be [n_pages, 2, page_size, 128]")
-    n_pages, page_size = k_codes.shape[0], k_codes.shape[2]
-    codes = (n_pages, N_KV_HEADS, page_size, Q4_ROW_BYTES)
-    scales = (n_pages, N_KV_HEADS, page_size, Q4_SCALE_BYTES)
-    return (_addr("k_codes", k_codes, _U8, codes, dev), _addr("k_scales", k_scales, _U8, scales, dev),
-            _addr("v_codes", v_codes, _U8, codes, dev), _addr("v_scales", v_scales, _U8, scales, dev),
-            n_pages, page_size)
+        _native_module = module
+    return _native_module
 
 
 def ga_page_plan(seq_len, new_len, page_table, held, free_pages, free_count, page_size,
@@ -615,46 +592,11 @@ def ga_page_plan(seq_len, new_len, page_table, held, free_pages, free_count, pag
     page_table is updated in place, and so are held and free_count unless held_out and
     free_count_out are given. Returns (row_start [n + 1], slot_map [max_tokens], positions
     [max_tokens], info [4])."""
-    dev = _device(seq_len, "seq_len")
-    n = seq_len.shape[0]
-    where = seq_len.device
-    if row_start is None:
-        row_start = torch.empty(n + 1, dtype=_I32, device=where)
-    if slot_map is None:
-        slot_map = torch.empty(max_tokens, dtype=_I32, device=where)
-    if positions is None:
-        positions = torch.empty(max_tokens, dtype=_I32, device=where)
-    if info is None:
-        info = torch.empty(4, dtype=_I32, device=where)
-    if page_table.dim() != 2 or free_pages.dim() != 1:
-        raise ValueError("page_table must be [n_seq, max_pages] and free_pages [n_free]")
-    width, n_free = page_table.shape[1], free_pages.shape[0]
-    held_at = _addr("held", held, _I32, (n,), dev)
-    count_at = _addr("free_count", free_count, _I32, (1,), dev)
-    st = lib().ga_page_plan(
-        _addr("seq_len", seq_len, _I32, (n,), dev), _addr("new_len", new_len, _I32, (n,), dev), n,
-        page_size, _addr("page_table", page_table, _I32, (n, width), dev), width, held_at,
-        held_at if held_out is None else _addr("held_out", held_out, _I32, (n,), dev),
-        _addr("free_pages", free_pages, _I32, (n_free,), dev), n_free, count_at,
-        count_at if free_count_out is None else
-        _addr("free_count_out", free_count_out, _I32, (1,), dev),
-        None if pos_delta is None else _addr("pos_delta", pos_delta, _I32, (n,), dev), max_tokens,
-        _addr("row_start", row_start, _I32, (n + 1,), dev),
-        _addr("slot_map", slot_map, _I32, (max_tokens,), dev),
-        _addr("positions", positions, _I32, (max_tokens,), dev), _addr("info", info, _I32, (4,), dev),
-        _stream_of(dev))
+    st, *outputs = _native().page_plan(seq_len, new_len, page_table, held, free_pages, free_count,
+                                       page_size, max_tokens, pos_delta, held_out, free_count_out,
+                                       row_start, slot_map, positions, info)
     _check(st, "ga_page_plan")
-    return row_start, slot_map, positions, info
-
-
-@functools.lru_cache(maxsize=64)
-def _axis_bytes(pair_axis):
-    if len(pair_axis) != ROPE_DIMS // 2 or min(pair_axis) < 0 or max(pair_axis) > 255:
-        raise ValueError("pair_axis must be 32 axis numbers")
-    return (ctypes.c_uint8 * len(pair_axis))(*pair_axis)
-
-
-_ONE_AXIS = (0,) * (ROPE_DIMS // 2)
+    return tuple(outputs)
 
 
 def ga_qk_prologue_axes(k_raw, w_k, qg, w_q, positions, pair_axis, cos_tab, sin_tab, k_prep=None,
@@ -663,56 +605,10 @@ def ga_qk_prologue_axes(k_raw, w_k, qg, w_q, positions, pair_axis, cos_tab, sin_
     (unit column stride) on the device, pair_axis 32 axis numbers (rotary pair i turns by axis
     pair_axis[i]; None: axis 0). k_raw (with w_k) or qg (with w_q) may be None. Returns (k_prep
     [n_tok, 2, 256], q_prep [n_tok, 24, 256]), None for a side not given."""
-    if k_raw is None and qg is None:
-        raise ValueError("k_raw or qg must be given")
-    if (k_raw is None and (w_k is not None or k_prep is not None) or
-            qg is None and (w_q is not None or q_prep is not None)):
-        raise ValueError("w_k and k_prep come with k_raw, w_q and q_prep with qg")
-    some = qg if k_raw is None else k_raw
-    dev = _device(some, "qg" if k_raw is None else "k_raw")
-    n_tok = some.shape[0]
-    k = wk = kp = q = wq = qp = None
-    if k_raw is not None:
-        rows = (n_tok, N_KV_HEADS, HEAD_DIM)
-        if k_prep is None:
-            k_prep = torch.empty(rows, dtype=_BF16, device=some.device)
-        k = _addr("k_raw", k_raw, _BF16, rows, dev)
-        wk = _addr("w_k", w_k, _BF16, (HEAD_DIM,), dev)
-        kp = _addr("k_prep", k_prep, _BF16, rows, dev)
-    if qg is not None:
-        rows = (n_tok, N_Q_HEADS, HEAD_DIM)
-        if q_prep is None:
-            q_prep = torch.empty(rows, dtype=_BF16, device=some.device)
-        q = _addr("qg", qg, _BF16, (n_tok, N_Q_HEADS, 2 * HEAD_DIM), dev)
-        wq = _addr("w_q", w_q, _BF16, (HEAD_DIM,), dev)
-        qp = _addr("q_prep", q_prep, _BF16, rows, dev)
-    dims = positions.dim()
-    n_axes, cols = (1, positions.shape[0]) if dims == 1 else positions.shape if dims == 2 else (0, 0)
-    if (n_axes < 1 or positions.dtype is not _I32 or positions.get_device() != dev or cols < n_tok or
-            (cols > 1 and positions.stride(-1) != 1)):
-        raise ValueError("positions must be int32 [n_tok] or [n_axes, >= n_tok] with unit column "
-                         f"stride, on CUDA device {dev}")
-    table = (cos_tab.shape[0], ROPE_DIMS // 2)
-    st = lib().ga_qk_prologue_axes(
-        k, wk, kp, q, wq, qp, n_tok, positions.data_ptr() or 256,
-        positions.stride(0) if n_axes > 1 else cols, n_axes,
-        _axis_bytes(_ONE_AXIS if pair_axis is None else tuple(pair_axis)),
-        _addr("cos_tab", cos_tab, _BF16, table, dev), _addr("sin_tab", sin_tab, _BF16, table, dev),
-        table[0], _stream_of(dev))
+    st, k_prep, q_prep = _native().qk_prologue_axes(k_raw, w_k, qg, w_q, positions, pair_axis,
+                                                    cos_tab, sin_tab, k_prep, q_prep)
     _check(st, "ga_qk_prologue_axes")
     return k_prep, q_prep
-
-
-def _kv_rows(name, x, n_tok, dev):
-    """(address, token stride in values) of bf16 rows [n_tok, 2, 256], heads and dims dense."""
-    if (x.dtype is not _BF16 or x.shape != (n_tok, N_KV_HEADS, HEAD_DIM) or
-            x.get_device() != dev):
-        raise ValueError(f"{name} must be bfloat16 [{n_tok}, {N_KV_HEADS}, {HEAD_DIM}] on CUDA "
-                         f"device {dev}")
-    tok, head, dim = x.stride()
-    if dim != 1 or head != HEAD_DIM:
-        raise ValueError(f"{name} must have dense heads and dims")
-    return x.data_ptr() or 256, tok if n_tok > 1 else N_KV_HEADS * HEAD_DIM
 
 
 def ga_kv_quantize_q4(k, v, k_codes, k_scales, v_codes, v_scales, slots=None):
@@ -720,16 +616,8 @@ def ga_kv_quantize_q4(k, v, k_codes, k_scales, v_codes, v_scales, slots=None):
     projection) as 4-bit rows at slots int32 [n_tok] (None: token t at slot t) of the pools
     k_codes, v_codes uint8 [n_pages, 2, page_size, 128], k_scales, v_scales uint8
     [n_pages, 2, page_size, 16]. Negative slots are skipped."""
-    dev = _device(k, "k")
-    n_tok = k.shape[0]
-    kc, ks, vc, vs, n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales, dev)
-    k_at, ld_k = _kv_rows("k", k, n_tok, dev)
-    v_at, ld_v = _kv_rows("v", v, n_tok, dev)
-    st = lib().ga_kv_quantize_q4(
-        k_at, ld_k, v_at, ld_v, n_tok,
-        None if slots is None else _addr("slots", slots, _I32, (n_tok,), dev), kc, ks, vc, vs,
-        n_pages, page_size, _stream_of(dev))
-    _check(st, "ga_kv_quantize_q4")
+    _check(_native().kv_quantize_q4(k, v, k_codes, k_scales, v_codes, v_scales, slots)[0],
+           "ga_kv_quantize_q4")
 
 
 def ga_kv_dequantize_q4(k_codes, k_scales, v_codes, v_scales, slots=None, n_tok=None, k_out=None,
@@ -737,22 +625,8 @@ def ga_kv_dequantize_q4(k_codes, k_scales, v_codes, v_scales, slots=None, n_tok=
     """The widened rows at slots int32 [n_tok] (None: slots 0 .. n_tok - 1, by default the whole
     pool) of 4-bit pools, (k_out, v_out) bf16 [n_tok, 2, 256]. Rows of negative slots are left as
     they were (unspecified in outputs allocated here)."""
-    dev = _device(k_codes, "k_codes")
-    kc, ks, vc, vs, n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales, dev)
-    if slots is not None:
-        n_tok = slots.shape[0]
-    elif n_tok is None:
-        n_tok = n_pages * page_size
-    shape = (n_tok, N_KV_HEADS, HEAD_DIM)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=_BF16, device=k_codes.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=_BF16, device=k_codes.device)
-    st = lib().ga_kv_dequantize_q4(
-        kc, ks, vc, vs, n_pages, page_size,
-        None if slots is None else _addr("slots", slots, _I32, (n_tok,), dev), n_tok,
-        _addr("k_out", k_out, _BF16, shape, dev), _addr("v_out", v_out, _BF16, shape, dev),
-        _stream_of(dev))
+    st, k_out, v_out = _native().kv_dequantize_q4(k_codes, k_scales, v_codes, v_scales, slots, n_tok,
+                                                  k_out, v_out)
     _check(st, "ga_kv_dequantize_q4")
     return k_out, v_out
 
@@ -767,26 +641,7 @@ def ga_attn_verify_q4(q_prep, qg, k_codes, k_scales, v_codes, v_scales, page_tab
     prepared queries; qg [n_seq, rows, 24, 512] fused rows (their gates); the pools; page_table
     int32 [n_seq, max_pages] and seq_len int32 [n_seq] on the device (negative: unused, its rows
     of out are left as they were). Returns out [n_seq, rows, 24*256]."""
-    dev = _device(q_prep, "q_prep")
-    n_seq, rows = q_prep.shape[0], q_prep.shape[1]
-    kc, ks, vc, vs, n_pages, page_size = _q4_pools(k_codes, k_scales, v_codes, v_scales, dev)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [n_seq, max_pages]")
-    L = lib()
-    o_shape = (n_seq, rows, N_Q_HEADS * HEAD_DIM)
-    if out is None:
-        out = torch.empty(o_shape, dtype=_BF16, device=q_prep.device)
-    if workspace is None:
-        workspace = torch.empty(L.ga_verify_q4_workspace_bytes(), dtype=_U8, device=q_prep.device)
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on CUDA device {dev}")
-    width = page_table.shape[1]
-    st = L.ga_attn_verify_q4(
-        _addr("q_prep", q_prep, _BF16, (n_seq, rows, N_Q_HEADS, HEAD_DIM), dev),
-        _addr("qg", qg, _BF16, (n_seq, rows, N_Q_HEADS, 2 * HEAD_DIM), dev), kc, ks, vc, vs, n_pages,
-        page_size, _addr("page_table", page_table, _I32, (n_seq, width), dev), width,
-        _addr("seq_len", seq_len, _I32, (n_seq,), dev), n_seq, rows,
-        _addr("out", out, _BF16, o_shape, dev), workspace.data_ptr(), workspace.nbytes,
-        _stream_of(dev))
+    st, out = _native().attn_verify_q4(q_prep, qg, k_codes, k_scales, v_codes, v_scales, page_table,
+                                       seq_len, out, workspace)
     _check(st, "ga_attn_verify_q4")
     return out

@@ -1,10 +1,13 @@
 """Build libga_attn.so in-tree: one nvcc per translation unit (in parallel) for sm_103a,
-then one shared-library link. No CMake; a rebuild only recompiles changed units."""
+then one shared-library link, and beside it the native half of the torch binding
+(_native.so, plain C++ against torch's headers). No CMake; a rebuild only recompiles
+changed units."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -12,6 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libga_attn.so")
+NATIVE_SRC = os.path.join(CSRC, "ga_native.cpp")
+NATIVE = os.path.join(PKG, "_native.so")
 SOURCES = ["ga_host.cu", "ga_prologue.cu", "ga_attn.cu", "ga_mask.cu", "ga_quant.cu",
            "ga_select.cu", "ga_kv4.cu", "ga_plan.cu", "ga_verify4.cu", "ga_decode4.cu",
            "ga_debug.cu"]
@@ -31,6 +36,23 @@ def _newest_dep() -> float:
     return max(os.path.getmtime(p) for p in deps)
 
 
+def _native_commands(obj: str):
+    """Compile and link commands of the native binding against the installed torch."""
+    import torch
+
+    tdir = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", *[f"-I{d}" for d in inc],
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+                "-c", NATIVE_SRC, "-o", obj]
+    link = ["g++", "-shared", "-o", NATIVE, obj, "-L", PKG, "-l:libga_attn.so",
+            "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -44,18 +66,28 @@ def build(verbose: bool = False, force: bool = False) -> str:
         stale = force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(s), dep_time)
         if stale:
             jobs.append([nvcc, *ARCH, *FLAGS, "-c", s, "-o", o])
+    native_obj = os.path.join(BUILD, "ga_native.o")
+    native_dep = max(os.path.getmtime(NATIVE_SRC),
+                     os.path.getmtime(os.path.join(ROOT, "include", "ga_attn.h")))
+    native = (force or not os.path.exists(NATIVE) or not os.path.exists(native_obj) or
+              min(os.path.getmtime(NATIVE), os.path.getmtime(native_obj)) < native_dep)
+    if native:
+        native_compile, native_link = _native_commands(native_obj)
+        jobs.append(native_compile)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if verbose or r.returncode != 0:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {cmd[-3]}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {cmd[-3]}")
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
         list(ex.map(run, jobs))
     if jobs or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         run([nvcc, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"])
+    if native:
+        run(native_link)
     return LIB
 
 
