@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = lane >> 2, t = lane & 3;
   volatile int* abort = &sm.abort;
   grid_launch_dependents();
-  load_tiles<kThreads>(a, sm.cut.tiles, kKeys, blockIdx.x == 0);
+  load_cut<kKeys, kThreads>(a, sm.cut, blockIdx.x == 0);
   if (tid == 0) {
     sm.abort = 0;
     for (int w = 0; w < kWarps; ++w)
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk walk(sm.cut);
   Seg seg;
   while (walk.next(sm.cut, a.n_seq, seg)) {
-    const int L = a.seq_len[seg.b];
+    const int L = cut_len<kKeys>(sm.cut, seg.b, 1);
     // Q fragments of k-step i (of lane t's dims 64 t + 4 i .. + 3): rows g, g + 8 at the first two
     // of them, then at the last two; rows 12 .. 15 are zeros
 #pragma unroll
@@ -336,11 +336,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  x[2 * i + 1] * inv * sigmoid_f(hi_f(gw[i])));
           *reinterpret_cast<uint4*>(a.out + at * kDim + d) = make_uint4(res[0], res[1], res[2], res[3]);
         } else {
-          const size_t pr = (size_t)seg.slot * kV4Lanes + hr;
-          float4* po = reinterpret_cast<float4*>(a.part_o + pr * kDim + d);
-          po[0] = make_float4(x[0], x[1], x[2], x[3]);
-          po[1] = make_float4(x[4], x[5], x[6], x[7]);
-          if ((tid & 31) == 0) reinterpret_cast<float2*>(a.part_ml)[pr] = make_float2(mt, lt);
+          *part_at(a.part_o, seg.slot, d / 4, hr) = make_float4(x[0], x[1], x[2], x[3]);
+          *part_at(a.part_o, seg.slot, d / 4 + 1, hr) = make_float4(x[4], x[5], x[6], x[7]);
+          if ((tid & 31) == 0)
+            reinterpret_cast<float2*>(a.part_ml)[(size_t)seg.slot * kV4Lanes + hr] = make_float2(mt, lt);
         }
       }
       __syncthreads();

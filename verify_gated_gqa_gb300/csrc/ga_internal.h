@@ -195,7 +195,7 @@ cudaError_t launch_dequantize_q4(const Kv4Args& a, cudaStream_t s);
 
 // Attention over 4-bit paged caches (ga_verify4.cu).
 constexpr int kV4MaxCtas = 160;        // CTAs of the attention kernel at most
-constexpr int kV4MaxSeq = 512;         // sequences per launch (the host loops over groups)
+constexpr int kV4MaxSeq = 384;         // sequences per launch (the host loops over groups)
 constexpr int kV4Lanes = 96;           // query rows of a stream at most
 struct Verify4Args {
   const uint16_t* q_prep;   // [n_seq][rows][24][256]
@@ -204,7 +204,7 @@ struct Verify4Args {
   const int* page_table;    // [n_seq][max_pages]
   const int* seq_len;       // [n_seq]
   int n_seq, rows, page_size, max_pages, n_pages;
-  float* part_o;            // [2 * kV4MaxCtas][kV4Lanes][256]
+  float* part_o;            // [2 * kV4MaxCtas][256 / 4][kV4Lanes][4]
   float* part_ml;           // [2 * kV4MaxCtas][kV4Lanes][2]
   int* status;
 };

@@ -52,29 +52,19 @@ __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0
 
 
 // ------------------------------------------------------------------ the cut of the work
-// Key tiles (of `tile` keys) of a sequence: none when its slot is unused (negative length) or
-// its window passes the end of its page-table row, which is recorded.
-__device__ __forceinline__ int seq_tiles(const Verify4Args& a, int b, int tile, bool report) {
-  const int L = a.seq_len[b];
-  if (L < 0) return 0;
+// Key tiles (of kTile keys) of a sequence with L cached tokens and a window of `rows`: none when its
+// slot is unused (negative length) or the window passes the end of its page-table row.
+template <int kTile>
+__device__ __forceinline__ int seq_tiles(const Verify4Args& a, int L, bool& refused) {
   const long long keys = (long long)L + a.rows;
-  if (keys > (long long)a.max_pages * a.page_size || keys > GA_MAX_TOKENS) {
-    if (report) record(a.status, kDevBadPosition);
-    return 0;
-  }
-  return (int)((keys + tile - 1) / tile);
+  refused = L >= 0 && (keys > (long long)a.max_pages * a.page_size || keys > GA_MAX_TOKENS);
+  return L < 0 || refused ? 0 : (int)((keys + kTile - 1) / kTile);
 }
 // Query-row blocks of a (sequence, KV head): one while all heads' rows fit in kV4Lanes.
 __host__ __device__ __forceinline__ int row_blocks(int rows) {
   return rows * kGroup > kV4Lanes ? 2 : 1;
 }
 
-// Tiles of every sequence into shared memory, by a block of kBlock threads.
-template <int kBlock>
-__device__ __forceinline__ void load_tiles(const Verify4Args& a, uint16_t* tiles, int tile, bool report) {
-  for (int b = threadIdx.x; b < a.n_seq; b += kBlock)
-    tiles[b] = (uint16_t)seq_tiles(a, b, tile, report);
-}
 // Sum of tiles[0 .. n - 1] by one warp (every lane gets it).
 __device__ __forceinline__ int warp_sum_tiles(const uint16_t* tiles, int n) {
   int s = 0;
@@ -94,8 +84,26 @@ struct Seg {
 // What every role of a CTA derives its share from, in shared memory.
 struct V4Cut {
   uint16_t tiles[kV4MaxSeq];   // key tiles of each sequence
+  uint8_t spare[kV4MaxSeq];    // and what its keys lack of filling the last
   int units, plane0, b0, tile0;
 };
+// The sequences' tiles, by a block of kBlock threads; a refused length is recorded by `report`.
+template <int kTile, int kBlock>
+__device__ __forceinline__ void load_cut(const Verify4Args& a, V4Cut& c, bool report) {
+  for (int b = threadIdx.x; b < a.n_seq; b += kBlock) {
+    const int L = __ldg(a.seq_len + b);
+    bool refused;
+    const int n = seq_tiles<kTile>(a, L, refused);
+    if (refused && report) record(a.status, kDevBadPosition);
+    c.tiles[b] = (uint16_t)n;
+    c.spare[b] = (uint8_t)(n * kTile - L - a.rows);
+  }
+}
+// Cached tokens of a sequence that has tiles.
+template <int kTile>
+__device__ __forceinline__ int cut_len(const V4Cut& c, int b, int rows) {
+  return (int)c.tiles[b] * kTile - (int)c.spare[b] - rows;
+}
 struct Walk {
   Walk() = default;
   int plane, b, tile, left, seen;
@@ -168,8 +176,15 @@ __device__ __forceinline__ void find_share(V4Cut& sm, int n_seq, int planes) {
   }
 }
 
+// A part's O in the workspace: float4 of four dims at (slot, dims / 4, row), rows innermost, so that
+// the attention kernel, whose threads hold a row each, writes whole sectors (row after row of 1
+// KiB it wrote half sectors, 32 rows an instruction: 3 us a segment).
+__device__ __forceinline__ float4* part_at(float* part_o, int slot, int d4, int row) {
+  return reinterpret_cast<float4*>(part_o) + ((size_t)slot * (kDim / 4) + d4) * kV4Lanes + row;
+}
+
 // The log-sum-exp merge of the streams that the cut left in parts, after either kernel with
-// tiles of `tile` keys.
+// tiles of `tile` keys (128 or 32).
 cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, int sm_count,
                                    cudaStream_t s);
 

@@ -89,7 +89,7 @@ __device__ void raw_loader(V4Smem& sm, const CUtensorMap* tm_c, const CUtensorMa
   Walk walk(sm.cut);
   Seg seg;
   while (walk.next(sm.cut, a.n_seq, seg)) {
-    const int end = a.seq_len[seg.b] + a.rows;
+    const int end = cut_len<kTileN>(sm.cut, seg.b, a.rows) + a.rows;
     const int* table = a.page_table + (size_t)seg.b * a.max_pages;
     // the pool row of this lane's granule of tile kt
     auto row_of = [&](int kt) -> int {
@@ -272,7 +272,7 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
   Walk walk(sm.cut);
   Seg seg;
   while (walk.next(sm.cut, a.n_seq, seg)) {
-    const int L = a.seq_len[seg.b];
+    const int L = cut_len<kTileN>(sm.cut, seg.b, a.rows);
     const int limit = L + min(rr, a.rows - 1);   // the row's last visible key
     const int h = (seg.plane & 1) * kGroup + (seg.plane >> 1) * heads + hh;
     const size_t row = (size_t)seg.b * a.rows + rr;
@@ -387,7 +387,6 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
     tc_fence_after();
     const float inv = l > 0.f ? 1.0f / l : (l != l ? l : 0.f);
     const size_t prow = (size_t)seg.slot * kV4Lanes + r;
-    float4* po = reinterpret_cast<float4*>(a.part_o + prow * kDim + 128 * hf);
     const uint4* gp = reinterpret_cast<const uint4*>(a.qg + (row * kHeads + h) * kQgStride + kDim + 128 * hf);
     uint4* op = reinterpret_cast<uint4*>(a.out + (row * kHeads + h) * kDim + 128 * hf);
 #pragma unroll 1
@@ -410,7 +409,7 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
       } else if (valid) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          po[8 * c + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+          *part_at(a.part_o, seg.slot, 32 * hf + 8 * c + i, r) = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
       }
     }
@@ -438,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_launch_dependents();
   // softmax warps with query rows, of each warpgroup's four
   const uint32_t act = (uint32_t)(a.rows * (kGroup / row_blocks(a.rows)) + 31) / 32;
-  load_tiles<kThreads>(a, sm.cut.tiles, kTileN, blockIdx.x == 0);
+  load_cut<kTileN, kThreads>(a, sm.cut, blockIdx.x == 0);
   if (threadIdx.x == 0) {
     sm.abort = 0;
     for (int i = 0; i < 2 * kStages; ++i) {
@@ -505,108 +504,160 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ combine
-// A block per (sequence, window row, query head): the parts of its stream, if the cut left it in
-// parts. Every part's weight first (a part a thread), then each of kWarps warps takes every
-// kWarps-th part, eight dims a lane, four parts' loads in flight, and they join in shared memory.
-// Eight warps when the rows are too few to fill the device (one sequence over 65,536 keys has 76
-// parts a row: 21 us with four warps that formed the weights on the way and loaded nothing
-// ahead, 7.6 us so), two when they fill it, where a stream has a few parts and the blocks'
-// number counts (64 sequences: 14 us with eight).
-template <int kWarps>
-__global__ void __launch_bounds__(32 * kWarps) verify4_combine_kernel(
+// The streams that the cut left in parts: o = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i over a
+// stream's parts, times the gate. A block takes a slice of 4 kD4 dims of every query row of a
+// stream, a thread a float4 of a row, neighbouring threads neighbouring rows (as the parts lie). Up
+// to kDirectParts parts a thread loads the M, l and float4 of eight parts at a time and merges them as
+// they come, a trip to L2 for eight. More parts: all (M, l) into shared memory, a warp per row turns them into weights, and the
+// float4s come eight parts at a time; when a slice has fewer float4s than the block has threads,
+// the parts are dealt to several groups of threads, joined in shared memory. Thin slices when the streams are few (one sequence over 65,536 keys: two streams
+// of 76 parts), wide ones when they fill the device, where a stream has a few parts.
+constexpr int kCombineThreads = 384, kCombineWarps = kCombineThreads / 32;
+// A stream's parts are at most half the CTAs and two: there are two KV heads of the same tiles.
+constexpr int kMaxParts = kV4MaxCtas / 2 + 2;
+constexpr int kDirectParts = 24;
+template <int kD4>
+__global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     const __grid_constant__ Verify4Args a, int ctas, int tile) {
-  constexpr int kCombineThreads = 32 * kWarps, kDims = kDim / kCombineThreads;
+  constexpr int kSlices = kDim / 4 / kD4;
+  extern __shared__ float2 ml[];   // [parts][rows]: M, l, then the part's weight and l
   __shared__ uint16_t tiles[kV4MaxSeq];
-  __shared__ float so[kWarps][kDim], f[kV4MaxCtas], red[kWarps], red_l[kWarps];
+  __shared__ float4 join[kCombineThreads];
+  __shared__ float inv[kV4Lanes];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x % kHeads, rr = (blockIdx.x / kHeads) % a.rows;
-  const int b = blockIdx.x / (kHeads * a.rows);
-  load_tiles<kCombineThreads>(a, tiles, tile, false);
+  const int slice = blockIdx.x % kSlices, stream = blockIdx.x / kSlices;
+  const int b = stream % a.n_seq, plane = stream / a.n_seq;
+  for (int i = threadIdx.x; i < a.n_seq; i += kCombineThreads) {
+    bool refused;
+    const int L = __ldg(a.seq_len + i);
+    tiles[i] = (uint16_t)(tile == kTileN ? seq_tiles<kTileN>(a, L, refused) : seq_tiles<32>(a, L, refused));
+  }
   __syncthreads();
-  const int blocks = row_blocks(a.rows), heads = kGroup / blocks;
+  const int blocks = row_blocks(a.rows), heads = kGroup / blocks, rows = heads * a.rows;
   const int per_plane = warp_sum_tiles(tiles, a.n_seq);
-  const int before = warp_sum_tiles(tiles, b);
-  const int total = per_plane * kKvHeads * blocks;
-  const int share = v4_share(total, ctas);
-  const int kvh = h / kGroup, hg = h % kGroup;
-  const int plane = 2 * (hg / heads) + kvh;
-  const long long u0 = (long long)plane * per_plane + before, u1 = u0 + max((int)tiles[b], 1) - 1;
-  const int c0 = (int)(u0 / share), n = (int)(u1 / share) - c0 + 1;
-  const int r = rr * heads + hg % heads;
+  const int share = v4_share(per_plane * kKvHeads * blocks, ctas);
+  const long long u0 = (long long)plane * per_plane + warp_sum_tiles(tiles, b);
+  const int nt = tiles[b];
+  const int c0 = nt ? (int)(u0 / share) : 0, n = nt ? (int)((u0 + nt - 1) / share) - c0 + 1 : 1;
+  grid_wait();   // in every block: the grid's end then stands for the attention kernel's too
+  if (n == 1 || n > kMaxParts) return;   // unused, or one CTA ran the whole stream and wrote it
   // part i is of CTA c0 + i: its first segment unless the stream began inside the CTA's run
   const bool inside = (long long)c0 * share < u0;
-  auto part_row = [&](int i) -> size_t {
-    return (size_t)(2 * (c0 + i) + (i == 0 && inside ? 1 : 0)) * kV4Lanes + r;
+  auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 && inside ? 1 : 0); };
+  const int items = rows * kD4;
+  // o (relative to the weights' scale s) times the gate, to the output
+  auto finish = [&](int d4, int r, float4 o, float s) {
+    const int rr = r / heads, h = (plane & 1) * kGroup + (plane >> 1) * heads + r - rr * heads;
+    const size_t row = ((size_t)b * a.rows + rr) * kHeads + h;
+    const int d = 4 * (slice * kD4 + d4);
+    const uint2 g = __ldg(reinterpret_cast<const uint2*>(a.qg + row * kQgStride + kDim + d));
+    *reinterpret_cast<uint2*>(a.out + row * kDim + d) =
+        make_uint2(pack_bf16x2(o.x * s * sigmoid_f(lo_f(g.x)), o.y * s * sigmoid_f(hi_f(g.x))),
+                   pack_bf16x2(o.z * s * sigmoid_f(lo_f(g.y)), o.w * s * sigmoid_f(hi_f(g.y))));
   };
-  grid_wait();   // in every block: the grid's end then stands for the attention kernel's too
-  if (tiles[b] == 0 || n == 1) return;   // unused, or one CTA ran the whole stream and wrote it
-  float2 x[(kV4MaxCtas + kCombineThreads - 1) / kCombineThreads];
-  constexpr int kPer = sizeof(x) / sizeof(x[0]);   // parts a thread weighs
-  float M = -INFINITY;
+  if (n <= kDirectParts) {
+    for (int item = threadIdx.x; item < items; item += kCombineThreads) {
+      const int d4 = item / rows, r = item - d4 * rows;
+      float M = -INFINITY, L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = 0; i0 < n; i0 += 8) {
+        float2 x[8];
+        float4 v[8];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int i = threadIdx.x + k * kCombineThreads;
-    x[k] = i < n ? reinterpret_cast<const float2*>(a.part_ml)[part_row(i)] : make_float2(-INFINITY, 0.f);
-    M = fmaxf(M, x[k].x);
+        for (int k = 0; k < 8; ++k) {
+          const int i = i0 + k;
+          x[k] = make_float2(-INFINITY, 0.f);
+          if (i < n) {
+            x[k] = reinterpret_cast<const float2*>(a.part_ml)[(size_t)slot(i) * kV4Lanes + r];
+            v[k] = *part_at(a.part_o, slot(i), slice * kD4 + d4, r);
+          }
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k].x);
+        const float f0 = M == -INFINITY ? 0.f : exp2f(M - top);
+        M = top;
+        L *= f0;
+        o.x *= f0;
+        o.y *= f0;
+        o.z *= f0;
+        o.w *= f0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (x[k].x == -INFINITY) continue;   // no such part, or no key of it is visible
+          const float f = exp2f(x[k].x - M);
+          L = fmaf(f, x[k].y, L);
+          o.x = fmaf(f, v[k].x, o.x);
+          o.y = fmaf(f, v[k].y, o.y);
+          o.z = fmaf(f, v[k].z, o.z);
+          o.w = fmaf(f, v[k].w, o.w);
+        }
+      }
+      finish(d4, r, o, L > 0.f ? 1.0f / L : (L != L ? L : 0.f));
+    }
+    return;
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if (lane == 0) red[warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[w]);
-  float L = 0.f;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int i = threadIdx.x + k * kCombineThreads;
-    const float fx = x[k].x == -INFINITY ? 0.f : exp2f(x[k].x - M);   // no visible key: none
-    L = fmaf(fx, x[k].y, L);
-    if (i < n) f[i] = fx;
+  for (int k = threadIdx.x; k < n * rows; k += kCombineThreads) {
+    const int i = k / rows;
+    ml[k] = reinterpret_cast<const float2*>(a.part_ml)[(size_t)slot(i) * kV4Lanes + (k - i * rows)];
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-  if (lane == 0) red_l[warp] = L;
   __syncthreads();
-  float o[8];
+  for (int r = warp; r < rows; r += kCombineWarps) {
+    float M = -INFINITY, L = 0.f;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[i * rows + r].x);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  for (int i0 = warp; i0 < n; i0 += 4 * kWarps) {
-    float4 v[4][2];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k * kWarps;
-      if (i >= n) continue;
-      const float4* p = reinterpret_cast<const float4*>(a.part_o + part_row(i) * kDim + 8 * lane);
-      v[k][0] = p[0];
-      v[k][1] = p[1];
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    for (int i = lane; i < n; i += 32) {
+      const float2 x = ml[i * rows + r];
+      const float f = x.x == -INFINITY ? 0.f : exp2f(x.x - M);   // no visible key in the part: none
+      L = fmaf(f, x.y, L);
+      ml[i * rows + r].x = f;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k * kWarps;
-      if (i >= n) continue;
-      const float w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
-                          v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
-      const float fi = f[i];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) o[q] = fmaf(fi, w[q], o[q]);
-    }
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    if (lane == 0) inv[r] = L > 0.f ? 1.0f / L : (L != L ? L : 0.f);
   }
-#pragma unroll
-  for (int q = 0; q < 8; ++q) so[warp][8 * lane + q] = o[q];
   __syncthreads();
-  float Lt = 0.f;
+  const int groups = items < kCombineThreads ? kCombineThreads / items : 1;
+  const int group = items < kCombineThreads ? threadIdx.x / items : 0;
+  const int first = items < kCombineThreads ? threadIdx.x - group * items : threadIdx.x;
+  if (groups == 1 && group > 0) return;   // threads past the items (no barrier follows)
+  for (int item = first; item < items; item += kCombineThreads) {
+    const int d4 = item / rows, r = item - d4 * rows;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (group < groups) {
+      for (int i0 = group; i0 < n; i0 += 8 * groups) {
+        float4 v[8];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) Lt += red_l[w];
-  const float inv = Lt > 0.f ? 1.0f / Lt : (Lt != Lt ? Lt : 0.f);
-  const size_t row = ((size_t)b * a.rows + rr) * kHeads + h;
+        for (int k = 0; k < 8; ++k) {
+          const int i = i0 + k * groups;
+          if (i < n) v[k] = *part_at(a.part_o, slot(i), slice * kD4 + d4, r);
+        }
 #pragma unroll
-  for (int k = 0; k < kDims; ++k) {
-    const int d = threadIdx.x + k * kCombineThreads;
-    float y = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) y += so[w][d];
-    const float g = __uint_as_float((uint32_t)a.qg[row * kQgStride + kDim + d] << 16);
-    a.out[row * kDim + d] = (uint16_t)(pack_bf16x2(y * inv * sigmoid_f(g), 0.f) & 0xFFFFu);
+        for (int k = 0; k < 8; ++k) {
+          const int i = i0 + k * groups;
+          if (i >= n) continue;
+          const float f = ml[i * rows + r].x;
+          o.x = fmaf(f, v[k].x, o.x);
+          o.y = fmaf(f, v[k].y, o.y);
+          o.z = fmaf(f, v[k].z, o.z);
+          o.w = fmaf(f, v[k].w, o.w);
+        }
+      }
+    }
+    if (groups > 1) {   // items < threads: this loop runs once
+      join[threadIdx.x] = o;
+      __syncthreads();
+      if (group != 0) return;
+      for (int k = 1; k < groups; ++k) {
+        const float4 x = join[k * items + item];
+        o.x += x.x;
+        o.y += x.y;
+        o.z += x.z;
+        o.w += x.w;
+      }
+    }
+    finish(d4, r, o, inv[r]);
   }
 }
 
@@ -617,26 +668,33 @@ size_t verify4_ws_bytes() {
 }
 
 cudaError_t verify4_set_attributes() {
-  const cudaError_t e = cudaFuncSetAttribute(
-      verify4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(V4Smem));
+  const int ml_bytes = kMaxParts * kV4Lanes * (int)sizeof(float2);
+  cudaError_t e = cudaFuncSetAttribute(verify4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(V4Smem));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(verify4_combine_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, ml_bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(verify4_combine_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, ml_bytes);
   return e != cudaSuccess ? e : decode4_set_attributes();
 }
 
 cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, int sm_count,
                                    cudaStream_t s) {
-  const int blocks = a.n_seq * a.rows * kHeads;
-  const bool few = blocks < 4 * sm_count;
+  const int streams = a.n_seq * kKvHeads * row_blocks(a.rows);
+  const bool few = streams * 2 < sm_count;
+  const int parts = ctas / 2 + 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(few ? 256 : 64);
+  cfg.gridDim = dim3((unsigned)(streams * (few ? 16 : 2)));
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.dynamicSmemBytes = (size_t)parts * (a.rows * kGroup / row_blocks(a.rows)) * sizeof(float2);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<8>, a, ctas, tile)
-             : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<2>, a, ctas, tile);
+  return few ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<4>, a, ctas, tile)
+             : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<32>, a, ctas, tile);
 }
 
 cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
