@@ -85,14 +85,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   volatile int* abort = &sm.abort;
-  grid_launch_dependents();
-  load_cut<kKeys, kThreads>(a, sm.cut, blockIdx.x == 0);
   if (tid == 0) {
     sm.abort = 0;
     for (int w = 0; w < kWarps; ++w)
       for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[w][i], 1);
     mbar_fence_init();
   }
+  if (warp == 1 && lane == 0) {
+    tma_prefetch_desc(&tm_kc);
+    tma_prefetch_desc(&tm_vc);
+    tma_prefetch_desc(&tm_ks);
+    tma_prefetch_desc(&tm_vs);
+  }
+  grid_wait();
+  grid_launch_dependents();
+  load_cut<kKeys, kThreads>(a, sm.cut, blockIdx.x == 0);
   __syncthreads();
   if (warp == 0) find_share(sm.cut, a.n_seq, kKvHeads);
   __syncthreads();
@@ -363,8 +370,9 @@ cudaError_t decode4_set_attributes() {
 cudaError_t launch_decode4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
                            const CUtensorMap& k_scales, const CUtensorMap& v_scales,
                            const Verify4Args& a, int ctas, cudaStream_t s) {
-  decode4_kernel<<<ctas, kThreads, sizeof(D4Smem), s>>>(k_codes, v_codes, k_scales, v_scales, a);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)ctas, kThreads, sizeof(D4Smem), s, attr);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode4_kernel, k_codes, v_codes, k_scales, v_scales, a);
   return e != cudaSuccess ? e : launch_verify4_combine(a, ctas, kKeys, ctas, s);
 }
 

@@ -136,19 +136,21 @@ struct Walk {
 
 // Tiles per CTA of a cut of `total` tiles over `ctas` CTAs.
 __device__ __forceinline__ int v4_share(int total, int ctas) { return (total + ctas - 1) / ctas; }
+static_assert(4LL * kV4MaxSeq * (GA_MAX_TOKENS / 32) + (1 << 20) < (1LL << 31), "tile counts fit in 32 bits");
 
 // This CTA's part of the cut, by one warp: its first tile and number of tiles, into c.
 __device__ __forceinline__ void find_share(V4Cut& sm, int n_seq, int planes) {
   const int lane = threadIdx.x & 31;
+  // 32 bits hold it all: 4 planes x kV4MaxSeq sequences x 2^15 tiles
   const int per_plane = warp_sum_tiles(sm.tiles, n_seq);
   const int total = per_plane * planes;
   const int share = v4_share(total, (int)gridDim.x);
-  const long long u0 = (long long)share * blockIdx.x;
-  const int units = (int)min((long long)share, max(0LL, (long long)total - u0));
+  const int u0 = share * (int)blockIdx.x;
+  const int units = min(share, max(0, total - u0));
   int plane = 0, b0 = 0, tile0 = 0;
   if (units > 0) {
-    plane = (int)(u0 / per_plane);
-    int rem = (int)(u0 - (long long)plane * per_plane);
+    plane = u0 / per_plane;
+    int rem = u0 - plane * per_plane;
     // the sequence holding tile `rem` of the plane: sums of 32 sequences at a time
     for (int base = 0; base < n_seq; base += 32) {
       const int t = base + lane < n_seq ? sm.tiles[base + lane] : 0;
@@ -174,6 +176,22 @@ __device__ __forceinline__ void find_share(V4Cut& sm, int n_seq, int planes) {
     sm.b0 = b0;
     sm.tile0 = tile0;
   }
+}
+
+// Launch that may be placed while the kernel before it in the stream ends (its blocks call
+// grid_wait before they touch memory that one may use).
+inline cudaLaunchConfig_t overlapped_launch(unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                                            cudaLaunchAttribute (&attr)[1]) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
 }
 
 // A part's O in the workspace: float4 of four dims at (slot, dims / 4, row), rows innermost, so that

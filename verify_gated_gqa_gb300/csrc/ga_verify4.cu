@@ -434,10 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   V4Smem& sm = *reinterpret_cast<V4Smem*>(smem_raw);
   const int warp = threadIdx.x >> 5;
   volatile int* abort = &sm.abort;
-  grid_launch_dependents();
   // softmax warps with query rows, of each warpgroup's four
   const uint32_t act = (uint32_t)(a.rows * (kGroup / row_blocks(a.rows)) + 31) / 32;
-  load_cut<kTileN, kThreads>(a, sm.cut, blockIdx.x == 0);
   if (threadIdx.x == 0) {
     sm.abort = 0;
     for (int i = 0; i < 2 * kStages; ++i) {
@@ -462,10 +460,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.drain_pv, 1);
     mbar_fence_init();
   }
-  if (warp == 1) {
+  if (warp == 2 && (threadIdx.x & 31) == 0) {
+    tma_prefetch_desc(&tm_kc);
+    tma_prefetch_desc(&tm_vc);
+    tma_prefetch_desc(&tm_ks);
+    tma_prefetch_desc(&tm_vs);
+  }
+  grid_wait();
+  grid_launch_dependents();
+  if (warp == 1) {   // after the wait: the kernel before may still need tensor memory until it ends
     tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
   }
+  load_cut<kTileN, kThreads>(a, sm.cut, blockIdx.x == 0);
   tc_fence_before();
   __syncthreads();
   if (warp == 0) find_share(sm.cut, a.n_seq, kKvHeads * row_blocks(a.rows));
@@ -536,13 +543,13 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   const int blocks = row_blocks(a.rows), heads = kGroup / blocks, rows = heads * a.rows;
   const int per_plane = warp_sum_tiles(tiles, a.n_seq);
   const int share = v4_share(per_plane * kKvHeads * blocks, ctas);
-  const long long u0 = (long long)plane * per_plane + warp_sum_tiles(tiles, b);
+  const int u0 = plane * per_plane + warp_sum_tiles(tiles, b);
   const int nt = tiles[b];
-  const int c0 = nt ? (int)(u0 / share) : 0, n = nt ? (int)((u0 + nt - 1) / share) - c0 + 1 : 1;
+  const int c0 = nt ? u0 / share : 0, n = nt ? (u0 + nt - 1) / share - c0 + 1 : 1;
   grid_wait();   // in every block: the grid's end then stands for the attention kernel's too
   if (n == 1 || n > kMaxParts) return;   // unused, or one CTA ran the whole stream and wrote it
   // part i is of CTA c0 + i: its first segment unless the stream began inside the CTA's run
-  const bool inside = (long long)c0 * share < u0;
+  const bool inside = c0 * share < u0;
   auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 && inside ? 1 : 0); };
   const int items = rows * kD4;
   // o (relative to the weights' scale s) times the gate, to the output
@@ -683,16 +690,10 @@ cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, int
   const int streams = a.n_seq * kKvHeads * row_blocks(a.rows);
   const bool few = streams * 2 < sm_count;
   const int parts = ctas / 2 + 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(streams * (few ? 16 : 2)));
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.dynamicSmemBytes = (size_t)parts * (a.rows * kGroup / row_blocks(a.rows)) * sizeof(float2);
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const cudaLaunchConfig_t cfg = overlapped_launch(
+      (unsigned)(streams * (few ? 16 : 2)), kCombineThreads,
+      (size_t)parts * (a.rows * kGroup / row_blocks(a.rows)) * sizeof(float2), s, attr);
   return few ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<4>, a, ctas, tile)
              : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<32>, a, ctas, tile);
 }
@@ -702,8 +703,9 @@ cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_code
                            const Verify4Args& a, int sm_count, cudaStream_t s) {
   const int ctas = sm_count < kV4MaxCtas ? sm_count : kV4MaxCtas;
   if (a.rows == 1) return launch_decode4(k_codes, v_codes, k_scales, v_scales, a, ctas, s);
-  verify4_kernel<<<ctas, kThreads, sizeof(V4Smem), s>>>(k_codes, v_codes, k_scales, v_scales, a);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)ctas, kThreads, sizeof(V4Smem), s, attr);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify4_kernel, k_codes, v_codes, k_scales, v_scales, a);
   return e != cudaSuccess ? e : launch_verify4_combine(a, ctas, kTileN, sm_count, s);
 }
 
