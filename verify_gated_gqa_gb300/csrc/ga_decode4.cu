@@ -8,10 +8,12 @@
 // them, about equally (288 bytes and 550 warp instructions per 16 keys of a head).
 //
 // Work: streams (sequence, KV head) in granules of 32 keys, cut into equal runs, one per CTA, as in
-// ga_v4.cuh. Eight warps a CTA; warp w takes a segment's granules w, w + 8, ... on its own: it
-// loads them by TMA into two stages of its own (codes and scales of K and V, 9 KiB), forms S =
-// Q K^T, a running softmax and O += P V for all 16 rows and 256 dims in registers, and meets the
-// other warps only at the segment's end, where their O, M and l are joined in shared memory.
+// ga_v4.cuh. Eight computing warps a CTA; warp w takes a segment's granules w, w + 8, ... on its
+// own, through two stages of its own (codes and scales of K and V, 9 KiB): it forms S = Q K^T, a
+// running softmax and O += P V for all 16 rows and 256 dims in registers, and meets the other
+// warps only at the segment's end, where their O, M and l are joined in shared memory. Four more
+// warps fill the stages by TMA, each for two computing warps (done by the computing warps
+// themselves, the page lookups and copies took a fifth of a granule's time).
 //
 // Fragments (m16n8k16; lane = 4 g + t). The order of the dims within Q K^T is free as long as Q
 // and K agree: lane t of a key owns its dims 64t .. 64t + 63 (two 16-byte chunks of codes; the
@@ -26,7 +28,12 @@ namespace ga {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kLoaders = 4;                        // loading warps, each for kWarps / kLoaders
+constexpr int kThreads = 32 * (kWarps + kLoaders);
+// Registers: launched at 168 a thread (384 x 168 = 64,512); the computing warps take 232, the loading
+// ones keep 40: 128 x (2 x 232 + 40) = 64,512.
+constexpr int kRegsCompute = 232, kRegsLoad = 40;
+static_assert(128 * (2 * kRegsCompute + kRegsLoad) <= kThreads * 168, "register split");
 constexpr int kKeys = 32;                          // keys of a granule
 constexpr int kStages = 2;
 constexpr int kCodeBytes = kKeys * kQ4RowBytes, kScaleBytes = kKeys * kQ4ScaleBytes;
@@ -42,7 +49,7 @@ struct D4Smem {
   float join[kWarps][8][kJoinStride];              // a segment's O by warp, eight rows at a time
   float m[kWarps][16], l[kWarps][16];
   V4Cut cut;
-  uint64_t full[kWarps][kStages];
+  uint64_t full[kWarps][kStages], empty[kWarps][kStages];
   int abort;
 };
 static_assert(sizeof(D4Smem) <= 232448, "227 KiB of shared memory per CTA");
@@ -51,6 +58,9 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void compute_sync() {   // the computing warps
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
 }
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -72,80 +82,58 @@ __device__ __forceinline__ Q4Scale scale_pair(uint32_t ua, uint32_t ub, int b) {
   return q;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
-    decode4_kernel(const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
-                   const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
-                   const __grid_constant__ Verify4Args a) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  if ((smem_u32(smem_raw) & 1023u) != 0u) {
-    if (threadIdx.x == 0) record(a.status, kDevBadLaunch);
-    return;
+// ------------------------------------------------------------------ loading
+// Loading warp lw fills the stages of computing warps 2 lw and 2 lw + 1: lane 4 i + c copies, for
+// the i-th of them, c = 0: K codes, 1: V codes, 2, 3: their scales. A granule on a page outside the
+// pool (recorded) is read past the pool's end: zeros.
+__device__ void loader(D4Smem& sm, const CUtensorMap* tm_kc, const CUtensorMap* tm_vc,
+                       const CUtensorMap* tm_ks, const CUtensorMap* tm_vs, const Verify4Args& a, int lw,
+                       volatile int* abort) {
+  constexpr int kEach = kWarps / kLoaders;
+  const int lane = threadIdx.x & 31;
+  if (lane >= 4 * kEach) return;
+  const int w = kEach * lw + (lane >> 2), c = lane & 3;
+  const CUtensorMap* map = c == 0 ? tm_kc : c == 1 ? tm_vc : c == 2 ? tm_ks : tm_vs;
+  uint32_t issued = 0;
+  Walk walk(sm.cut);
+  Seg seg;
+  while (walk.next(sm.cut, a.n_seq, seg)) {
+    const int* table = a.page_table + (size_t)seg.b * a.max_pages;
+    int page = 0, at = 0;   // of granule j, looked up a round ahead
+    auto look_up = [&](int j) {
+      if (j >= seg.n) return;
+      const int key0 = (seg.kt0 + j) * kKeys, e = key0 / a.page_size;
+      page = __ldg(table + e);
+      at = seg.plane * a.page_size + key0 - e * a.page_size;
+    };
+    look_up(w);
+    for (int j = w; j < seg.n; j += kWarps) {
+      int row = a.n_pages * kKvHeads * a.page_size;
+      if (page >= 0 && page < a.n_pages) row = page * kKvHeads * a.page_size + at;
+      else record(a.status, kDevBadPage);
+      look_up(j + kWarps);
+      const int st = (int)(issued % kStages);
+      uint64_t* bar = &sm.full[w][st];
+      if (!mbar_wait(&sm.empty[w][st], ((issued / kStages) & 1) ^ 1, abort)) break;
+      if (c == 0) mbar_arrive_expect_tx(bar, kStageBytes);   // (a copy may report its bytes before)
+      tma_load_2d(c < 2 ? sm.codes[w][st][c] : sm.scales[w][st][c - 2], map, bar, 0, row);
+      ++issued;
+    }
+    if (*abort) break;
   }
-  D4Smem& sm = *reinterpret_cast<D4Smem*>(smem_raw);
+  if (*abort) {   // the copies in flight land before the CTA leaves
+    for (uint32_t f = issued > kStages ? issued - kStages : 0; f < issued; ++f)
+      mbar_wait_quiet(&sm.full[w][f % kStages], (f / kStages) & 1, 100000000LL);
+  }
+}
+
+// ------------------------------------------------------------------ computing
+// (A warp whose wait gave up goes on without computing, to meet the others at the barriers.)
+__device__ void compute(D4Smem& sm, const Verify4Args& a, volatile int* abort) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  volatile int* abort = &sm.abort;
-  if (tid == 0) {
-    sm.abort = 0;
-    for (int w = 0; w < kWarps; ++w)
-      for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[w][i], 1);
-    mbar_fence_init();
-  }
-  if (warp == 1 && lane == 0) {
-    tma_prefetch_desc(&tm_kc);
-    tma_prefetch_desc(&tm_vc);
-    tma_prefetch_desc(&tm_ks);
-    tma_prefetch_desc(&tm_vs);
-  }
-  grid_wait();
-  grid_launch_dependents();
-  load_cut<kKeys, kThreads>(a, sm.cut, blockIdx.x == 0);
-  __syncthreads();
-  if (warp == 0) find_share(sm.cut, a.n_seq, kKvHeads);
-  __syncthreads();
-
-  // ---- loading: this warp's granules in order, lanes 0 .. 3 a copy each (K and V codes, K and V
-  // scales). A granule on a page outside the pool (recorded) is read past the pool's end: zeros.
-  const int n_rows = (int)((long long)a.n_pages * kKvHeads * a.page_size);
-  const CUtensorMap* my_map = lane == 0 ? &tm_kc : lane == 1 ? &tm_vc : lane == 2 ? &tm_ks : &tm_vs;
-  Walk ahead(sm.cut);
-  Seg as{};
-  int aj = 0;                // next granule of `as` of this warp
-  uint32_t issued = 0;
-  // the granule to issue next: its page-table entry (in flight until the issue reads it) and place
-  // in the page; next_at < 0: none is left
-  int next_page = 0, next_at = -1;
-  auto find_next = [&]() {
-    next_at = -1;
-    while (aj >= as.n) {
-      if (!ahead.next(sm.cut, a.n_seq, as)) return;
-      aj = warp;
-    }
-    const int key0 = (as.kt0 + aj) * kKeys;
-    aj += kWarps;
-    const int e = key0 / a.page_size;
-    next_page = __ldg(a.page_table + (size_t)as.b * a.max_pages + e);
-    next_at = as.plane * a.page_size + key0 - e * a.page_size;
-  };
-  auto issue = [&]() {
-    if (next_at < 0) return;
-    int row = n_rows;
-    if (next_page >= 0 && next_page < a.n_pages) row = next_page * kKvHeads * a.page_size + next_at;
-    else if (lane == 0) record(a.status, kDevBadPage);
-    const int st = (int)(issued % kStages);
-    if (lane == 0) mbar_arrive_expect_tx(&sm.full[warp][st], kStageBytes);
-    __syncwarp();
-    if (lane < 4)
-      tma_load_2d(lane < 2 ? sm.codes[warp][st][lane] : sm.scales[warp][st][lane - 2], my_map,
-                  &sm.full[warp][st], 0, row);
-    ++issued;
-    find_next();
-  };
-  find_next();
-  for (int i = 0; i < kStages; ++i) issue();
-
   uint32_t taken = 0;
-  bool ok = true;   // a warp whose wait gave up goes on without computing, to meet the others
+  bool ok = true;
   Walk walk(sm.cut);
   Seg seg;
   while (walk.next(sm.cut, a.n_seq, seg)) {
@@ -160,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint2 hi = g < kGroup - 8 ? __ldg(x + 8 * kDim / 4) : make_uint2(0u, 0u);
       sm.q[i][lane] = make_uint4(lo.x, hi.x, lo.y, hi.y);
     }
-    __syncthreads();
+    compute_sync();
     const uint32_t q_at = smem_u32(&sm.q[0][lane]);
     float o[32][4];
 #pragma unroll
@@ -285,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_async_smem();   // the reads come before the refill by the copy engine
       __syncwarp();
-      issue();
+      if (lane == 0) mbar_arrive(&sm.empty[warp][st]);
     }
 
     // ---- join the warps: M, l first, then O eight rows at a time
@@ -298,8 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.l[warp][g + 8 * r] = l[r];
       }
     }
-    __syncthreads();
-    const bool whole = seg.whole;
+    compute_sync();
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float top = -INFINITY;
@@ -308,56 +295,92 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f = M[r] == -INFINITY ? 0.f : exp2f(M[r] - top);
       if (r == 0 || g < kGroup - 8) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)   // column 8 e + c of a row is dim 32 c + e
+        for (int e = 0; e < 32; ++e)   // place 8 e + c of a row is dim 32 c + e
           *reinterpret_cast<float2*>(&sm.join[warp][g][8 * e + 2 * t]) =
               make_float2(o[e][2 * r] * f, o[e][2 * r + 1] * f);
       }
-      __syncthreads();
-      // a thread sums eight dims of a row over the warps: dims 32 c + e0 .. + 7
-      const int row = tid >> 5, c = (tid & 31) >> 2, e0 = 8 * (tid & 3);
-      if (r == 0 || row < kGroup - 8) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] += sm.join[w][row][8 * (e0 + i) + c];
-        const int hr = row + 8 * r;   // query head of the group
+      compute_sync();
+      // a warp sums a row over the warps, a lane four neighbouring places at a time
+      const int hr = warp + 8 * r;   // query head of the group
+      if (hr < kGroup) {
         float mt = -INFINITY, lt = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, sm.m[w][hr]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
           lt += sm.m[w][hr] == -INFINITY ? 0.f : sm.l[w][hr] * exp2f(sm.m[w][hr] - mt);
-        const int d = 32 * c + e0;
-        if (whole) {
-          const size_t at = (size_t)seg.b * kHeads + seg.plane * kGroup + hr;
-          const float inv = lt > 0.f ? 1.0f / lt : (lt != lt ? lt : 0.f);
-          const uint4 gt = __ldg(reinterpret_cast<const uint4*>(a.qg + at * kQgStride + kDim + d));
-          const uint32_t gw[4] = {gt.x, gt.y, gt.z, gt.w};
-          uint32_t res[4];
+        const float inv = lt > 0.f ? 1.0f / lt : (lt != lt ? lt : 0.f);
+        const size_t out_row = (size_t)seg.b * kHeads + seg.plane * kGroup + hr;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            res[i] = pack_bf16x2(x[2 * i] * inv * sigmoid_f(lo_f(gw[i])),
-                                 x[2 * i + 1] * inv * sigmoid_f(hi_f(gw[i])));
-          *reinterpret_cast<uint4*>(a.out + at * kDim + d) = make_uint4(res[0], res[1], res[2], res[3]);
-        } else {
-          *part_at(a.part_o, seg.slot, d / 4, hr) = make_float4(x[0], x[1], x[2], x[3]);
-          *part_at(a.part_o, seg.slot, d / 4 + 1, hr) = make_float4(x[4], x[5], x[6], x[7]);
-          if ((tid & 31) == 0)
-            reinterpret_cast<float2*>(a.part_ml)[(size_t)seg.slot * kV4Lanes + hr] = make_float2(mt, lt);
+        for (int i = 0; i < 2; ++i) {
+          const int p = 128 * i + 4 * lane;
+          float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(&sm.join[w][warp][p]);
+            x[0] += v.x;
+            x[1] += v.y;
+            x[2] += v.z;
+            x[3] += v.w;
+          }
+          if (seg.whole) {
+            const int d = 32 * (p & 7) + (p >> 3);
+            const uint16_t* gt = a.qg + out_row * kQgStride + kDim + d;
+            uint16_t* to = a.out + out_row * kDim + d;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              to[32 * k] = (uint16_t)(pack_bf16x2(x[k] * inv * sigmoid_f(lo_f(__ldg(gt + 32 * k))), 0.f) & 0xFFFFu);
+          } else {
+            *part_at(a.part_o, seg.slot, p / 4, hr) = make_float4(x[0], x[1], x[2], x[3]);
+            if (p == 0)
+              reinterpret_cast<float2*>(a.part_ml)[(size_t)seg.slot * kV4Lanes + hr] = make_float2(mt, lt);
+          }
         }
       }
-      __syncthreads();
+      compute_sync();
     }
   }
-  if (*abort) {   // the copies in flight land before the CTA leaves
-    for (uint32_t f = issued > kStages ? issued - kStages : 0; f < issued; ++f)
-      mbar_wait_quiet(&sm.full[warp][f % kStages], (f / kStages) & 1, 100000000LL);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    decode4_kernel(const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
+                   const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
+                   const __grid_constant__ Verify4Args a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if ((smem_u32(smem_raw) & 1023u) != 0u) {
+    if (threadIdx.x == 0) record(a.status, kDevBadLaunch);
+    return;
+  }
+  D4Smem& sm = *reinterpret_cast<D4Smem*>(smem_raw);
+  const int warp = threadIdx.x >> 5;
+  volatile int* abort = &sm.abort;
+  if (threadIdx.x == 0) {
+    sm.abort = 0;
+    for (int w = 0; w < kWarps; ++w)
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&sm.full[w][i], 1);
+        mbar_init(&sm.empty[w][i], 1);
+      }
+    mbar_fence_init();
+  }
+  if (warp == kWarps && (threadIdx.x & 31) == 0) {
+    tma_prefetch_desc(&tm_kc);
+    tma_prefetch_desc(&tm_vc);
+    tma_prefetch_desc(&tm_ks);
+    tma_prefetch_desc(&tm_vs);
+  }
+  grid_wait();
+  grid_launch_dependents();
+  make_cut<kKeys>(a, sm.cut, kKvHeads, blockIdx.x == 0);   // two block barriers
+  if (warp < kWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
+    compute(sm, a, abort);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
+    loader(sm, &tm_kc, &tm_vc, &tm_ks, &tm_vs, a, warp - kWarps, abort);
   }
   __syncthreads();
-  if (tid == 0 && sm.abort) record(a.status, sm.abort);
+  if (threadIdx.x == 0 && sm.abort) record(a.status, sm.abort);
 }
 
 }  // namespace

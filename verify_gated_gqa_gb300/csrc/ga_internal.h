@@ -195,7 +195,7 @@ cudaError_t launch_dequantize_q4(const Kv4Args& a, cudaStream_t s);
 
 // Attention over 4-bit paged caches (ga_verify4.cu).
 constexpr int kV4MaxCtas = 160;        // CTAs of the attention kernel at most
-constexpr int kV4MaxSeq = 384;         // sequences per launch (the host loops over groups)
+constexpr int kV4MaxSeq = 256;         // sequences per launch (the host loops over groups)
 constexpr int kV4Lanes = 96;           // query rows of a stream at most
 struct Verify4Args {
   const uint16_t* q_prep;   // [n_seq][rows][24][256]

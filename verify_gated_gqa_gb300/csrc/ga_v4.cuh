@@ -65,15 +65,6 @@ __host__ __device__ __forceinline__ int row_blocks(int rows) {
   return rows * kGroup > kV4Lanes ? 2 : 1;
 }
 
-// Sum of tiles[0 .. n - 1] by one warp (every lane gets it).
-__device__ __forceinline__ int warp_sum_tiles(const uint16_t* tiles, int n) {
-  int s = 0;
-  for (int b = threadIdx.x & 31; b < n; b += 32) s += tiles[b];
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  return s;
-}
-
 // A CTA's share of the streams' tiles: `left` tiles from tile `tile` of stream (plane, b) on.
 // plane = 2 x row block + KV head; streams are ordered by plane, then sequence.
 struct Seg {
@@ -85,19 +76,61 @@ struct Seg {
 struct V4Cut {
   uint16_t tiles[kV4MaxSeq];   // key tiles of each sequence
   uint8_t spare[kV4MaxSeq];    // and what its keys lack of filling the last
+  int warp_sum[kV4MaxSeq / 32];
   int units, plane0, b0, tile0;
 };
-// The sequences' tiles, by a block of kBlock threads; a refused length is recorded by `report`.
-template <int kTile, int kBlock>
-__device__ __forceinline__ void load_cut(const Verify4Args& a, V4Cut& c, bool report) {
-  for (int b = threadIdx.x; b < a.n_seq; b += kBlock) {
-    const int L = __ldg(a.seq_len + b);
-    bool refused;
-    const int n = seq_tiles<kTile>(a, L, refused);
-    if (refused && report) record(a.status, kDevBadPosition);
-    c.tiles[b] = (uint16_t)n;
-    c.spare[b] = (uint8_t)(n * kTile - L - a.rows);
+static_assert(4LL * kV4MaxSeq * (GA_MAX_TOKENS / 32) + (1 << 20) < (1LL << 31),
+              "tile counts of a launch fit in 32 bits");
+// Tiles per CTA of a cut of `total` tiles over `ctas` CTAs.
+__device__ __forceinline__ int v4_share(int total, int ctas) { return (total + ctas - 1) / ctas; }
+
+// The sequences' tiles and this CTA's part of the cut, by the whole block (at least kV4MaxSeq
+// threads, a sequence each): planes x the sequences' tiles, end to end. A refused length is
+// recorded by `report`. Short on purpose: this code runs once, from a cold instruction cache,
+// before anything can be loaded (a warp's search over the sequences took 2.5 us here).
+template <int kTile>
+__device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int planes, bool report) {
+  const int b = threadIdx.x, warp = b >> 5;
+  int n = 0, sum = 0;
+  if (b < kV4MaxSeq) {
+    if (b < a.n_seq) {
+      const int L = __ldg(a.seq_len + b);
+      bool refused;
+      n = seq_tiles<kTile>(a, L, refused);
+      if (refused && report) record(a.status, kDevBadPosition);
+      c.tiles[b] = (uint16_t)n;
+      c.spare[b] = (uint8_t)(n * kTile - L - a.rows);
+    }
+    sum = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, off);
+      if ((b & 31) >= off) sum += o;
+    }
+    if ((b & 31) == 31) c.warp_sum[warp] = sum;
   }
+  __syncthreads();
+  int per_plane = 0, before = sum - n;
+#pragma unroll
+  for (int w = 0; w < kV4MaxSeq / 32; ++w) {
+    const int x = c.warp_sum[w];
+    per_plane += x;
+    if (w < warp) before += x;
+  }
+  const int total = per_plane * planes;
+  const int share = v4_share(total, (int)gridDim.x);
+  const int u0 = share * (int)blockIdx.x;
+  const int units = min(share, max(0, total - u0));
+  if (units > 0) {
+    const int plane = u0 / per_plane, rem = u0 - plane * per_plane;
+    if (before <= rem && rem < before + n) {   // one sequence's thread (n is 0 past the last)
+      c.plane0 = plane;
+      c.b0 = b;
+      c.tile0 = rem - before;
+    }
+  }
+  if (b == 0) c.units = units;
+  __syncthreads();
 }
 // Cached tokens of a sequence that has tiles.
 template <int kTile>
@@ -134,50 +167,6 @@ struct Walk {
   }
 };
 
-// Tiles per CTA of a cut of `total` tiles over `ctas` CTAs.
-__device__ __forceinline__ int v4_share(int total, int ctas) { return (total + ctas - 1) / ctas; }
-static_assert(4LL * kV4MaxSeq * (GA_MAX_TOKENS / 32) + (1 << 20) < (1LL << 31), "tile counts fit in 32 bits");
-
-// This CTA's part of the cut, by one warp: its first tile and number of tiles, into c.
-__device__ __forceinline__ void find_share(V4Cut& sm, int n_seq, int planes) {
-  const int lane = threadIdx.x & 31;
-  // 32 bits hold it all: 4 planes x kV4MaxSeq sequences x 2^15 tiles
-  const int per_plane = warp_sum_tiles(sm.tiles, n_seq);
-  const int total = per_plane * planes;
-  const int share = v4_share(total, (int)gridDim.x);
-  const int u0 = share * (int)blockIdx.x;
-  const int units = min(share, max(0, total - u0));
-  int plane = 0, b0 = 0, tile0 = 0;
-  if (units > 0) {
-    plane = u0 / per_plane;
-    int rem = u0 - plane * per_plane;
-    // the sequence holding tile `rem` of the plane: sums of 32 sequences at a time
-    for (int base = 0; base < n_seq; base += 32) {
-      const int t = base + lane < n_seq ? sm.tiles[base + lane] : 0;
-      int inc = t;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += o;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, inc > rem);
-      if (past) {
-        const int k = __ffs((int)past) - 1;
-        b0 = base + k;
-        tile0 = rem - __shfl_sync(0xffffffffu, inc - t, k);
-        break;
-      }
-      rem -= __shfl_sync(0xffffffffu, inc, 31);
-    }
-  }
-  if (lane == 0) {
-    sm.units = units;
-    sm.plane0 = plane;
-    sm.b0 = b0;
-    sm.tile0 = tile0;
-  }
-}
-
 // Launch that may be placed while the kernel before it in the stream ends (its blocks call
 // grid_wait before they touch memory that one may use).
 inline cudaLaunchConfig_t overlapped_launch(unsigned grid, unsigned block, size_t smem, cudaStream_t s,
@@ -196,7 +185,8 @@ inline cudaLaunchConfig_t overlapped_launch(unsigned grid, unsigned block, size_
 
 // A part's O in the workspace: float4 of four dims at (slot, dims / 4, row), rows innermost, so that
 // the attention kernel, whose threads hold a row each, writes whole sectors (row after row of 1
-// KiB it wrote half sectors, 32 rows an instruction: 3 us a segment).
+// KiB it wrote half sectors, 32 rows an instruction: 3 us a segment). The decode form keeps dims in
+// the order that its fragments leave them in: place p is dim 32 (p % 8) + p / 8.
 __device__ __forceinline__ float4* part_at(float* part_o, int slot, int d4, int row) {
   return reinterpret_cast<float4*>(part_o) + ((size_t)slot * (kDim / 4) + d4) * kV4Lanes + row;
 }

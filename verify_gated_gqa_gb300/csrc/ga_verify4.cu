@@ -472,11 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
   }
-  load_cut<kTileN, kThreads>(a, sm.cut, blockIdx.x == 0);
   tc_fence_before();
-  __syncthreads();
-  if (warp == 0) find_share(sm.cut, a.n_seq, kKvHeads * row_blocks(a.rows));
-  __syncthreads();
+  make_cut<kTileN>(a, sm.cut, kKvHeads * row_blocks(a.rows), blockIdx.x == 0);   // two block barriers
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   if (warp < 4) {
@@ -528,23 +525,30 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     const __grid_constant__ Verify4Args a, int ctas, int tile) {
   constexpr int kSlices = kDim / 4 / kD4;
   extern __shared__ float2 ml[];   // [parts][rows]: M, l, then the part's weight and l
-  __shared__ uint16_t tiles[kV4MaxSeq];
+  __shared__ int sums[2], own;
   __shared__ float4 join[kCombineThreads];
   __shared__ float inv[kV4Lanes];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int slice = blockIdx.x % kSlices, stream = blockIdx.x / kSlices;
   const int b = stream % a.n_seq, plane = stream / a.n_seq;
-  for (int i = threadIdx.x; i < a.n_seq; i += kCombineThreads) {
+  if (threadIdx.x < 2) sums[threadIdx.x] = 0;
+  __syncthreads();
+  if (threadIdx.x < kV4MaxSeq) {   // all tiles, those before sequence b, and its own
+    const int i = threadIdx.x;
     bool refused;
-    const int L = __ldg(a.seq_len + i);
-    tiles[i] = (uint16_t)(tile == kTileN ? seq_tiles<kTileN>(a, L, refused) : seq_tiles<32>(a, L, refused));
+    const int L = i < a.n_seq ? __ldg(a.seq_len + i) : -1;
+    const int t = tile == kTileN ? seq_tiles<kTileN>(a, L, refused) : seq_tiles<32>(a, L, refused);
+    const int all = __reduce_add_sync(0xffffffffu, t), first = __reduce_add_sync(0xffffffffu, i < b ? t : 0);
+    if (lane == 0) {
+      atomicAdd(&sums[0], all);
+      atomicAdd(&sums[1], first);
+    }
+    if (i == b) own = t;
   }
   __syncthreads();
   const int blocks = row_blocks(a.rows), heads = kGroup / blocks, rows = heads * a.rows;
-  const int per_plane = warp_sum_tiles(tiles, a.n_seq);
-  const int share = v4_share(per_plane * kKvHeads * blocks, ctas);
-  const int u0 = plane * per_plane + warp_sum_tiles(tiles, b);
-  const int nt = tiles[b];
+  const int share = v4_share(sums[0] * kKvHeads * blocks, ctas);
+  const int u0 = plane * sums[0] + sums[1], nt = own;
   const int c0 = nt ? u0 / share : 0, n = nt ? (u0 + nt - 1) / share - c0 + 1 : 1;
   grid_wait();   // in every block: the grid's end then stands for the attention kernel's too
   if (n == 1 || n > kMaxParts) return;   // unused, or one CTA ran the whole stream and wrote it
@@ -556,7 +560,18 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   auto finish = [&](int d4, int r, float4 o, float s) {
     const int rr = r / heads, h = (plane & 1) * kGroup + (plane >> 1) * heads + r - rr * heads;
     const size_t row = ((size_t)b * a.rows + rr) * kHeads + h;
-    const int d = 4 * (slice * kD4 + d4);
+    const int p = 4 * (slice * kD4 + d4);
+    if (tile != kTileN) {   // place p + k is dim 32 (p % 8 + k) + p / 8
+      const int d = 32 * (p & 7) + (p >> 3);
+      const uint16_t* g = a.qg + row * kQgStride + kDim + d;
+      uint16_t* to = a.out + row * kDim + d;
+      const float x[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        to[32 * k] = (uint16_t)(pack_bf16x2(x[k] * s * sigmoid_f(lo_f(__ldg(g + 32 * k))), 0.f) & 0xFFFFu);
+      return;
+    }
+    const int d = p;
     const uint2 g = __ldg(reinterpret_cast<const uint2*>(a.qg + row * kQgStride + kDim + d));
     *reinterpret_cast<uint2*>(a.out + row * kDim + d) =
         make_uint2(pack_bf16x2(o.x * s * sigmoid_f(lo_f(g.x)), o.y * s * sigmoid_f(hi_f(g.x))),
