@@ -114,7 +114,7 @@ __device__ void loader(D4Smem& sm, const CUtensorMap* tm_kc, const CUtensorMap* 
       look_up(j + kWarps);
       const int st = (int)(issued % kStages);
       uint64_t* bar = &sm.full[w][st];
-      if (!mbar_wait(&sm.empty[w][st], ((issued / kStages) & 1) ^ 1, abort)) break;
+      if (!v4_wait(&sm.empty[w][st], ((issued / kStages) & 1) ^ 1, abort)) break;
       if (c == 0) mbar_arrive_expect_tx(bar, kStageBytes);   // (a copy may report its bytes before)
       tma_load_2d(c < 2 ? sm.codes[w][st][c] : sm.scales[w][st][c - 2], map, bar, 0, row);
       ++issued;

@@ -10,8 +10,32 @@ namespace ga {
 __device__ __forceinline__ void record(int* status, int code) {
   if (code) atomicCAS(status, 0, code);
 }
+// mbar_wait with a time hint on every try after the first, so that a waiting warp is suspended by
+// the hardware: most warps of these kernels wait most of the time, and spinning they took a third of
+// the SM's issue slots.
+__device__ __forceinline__ bool v4_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)   // ns
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort = kDevWaitTimeout;
+      return false;
+    }
+  }
+}
+// The same in all 32 lanes, which agree on the outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const bool ok = mbar_wait(bar, parity, abort);
+  const bool ok = v4_wait(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
