@@ -54,11 +54,6 @@ struct D4Smem {
 };
 static_assert(sizeof(D4Smem) <= 232448, "227 KiB of shared memory per CTA");
 
-__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ void compute_sync() {   // the computing warps
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
 }

@@ -24,8 +24,8 @@
 //               (warps without rows are idle); they also load Q and write the segment's result
 //   warps 2, 3  load the codes and scales of K and V tiles by TMA, a granule of 32 keys a lane
 //               (a page holds a multiple of that), through two stages each
-//   warps 12-19 widen K, warps 20-27 widen V: a lane turns 32 codes of one row into 64 bytes of a
-//               row of the 128-byte-swizzled blocks that the tensor cores read
+//   warps 12-19 widen K, warps 20-27 widen V, four at even and four at odd pieces: a lane turns 64
+//               codes of one row into a 128-byte row of the swizzled blocks that the tensor cores read
 // K is handed over in four pieces of 64 dims and V in four of 32 keys (16 KiB each), so the
 // tensor cores start on the first piece of a tile while the rest is being widened, and give
 // its place back as soon as they have read it. The roles run different code at
@@ -71,6 +71,14 @@ struct V4Smem {
 };
 static_assert(sizeof(V4Smem) <= 232448, "227 KiB of shared memory per CTA");
 
+// Two multiply-adds by one operation: a x + b for both x.
+__device__ __forceinline__ void fma_f32x2(float& r0, float& r1, float x0, float x1, float a, float b) {
+  asm("{\n\t.reg .b64 x, m, c, r;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 m, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+      "fma.rn.f32x2 r, x, m, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r0), "=f"(r1)
+      : "f"(x0), "f"(x1), "f"(a), "f"(b));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -125,59 +133,61 @@ __device__ void raw_loader(V4Smem& sm, const CUtensorMap* tm_c, const CUtensorMa
 }
 
 // ------------------------------------------------------------------ widening
-// Warp w of eight. K, piece u (64-dim block u): keys 32 (w % 4) .. + 31, a key a lane, dims 32
-// (w / 4) .. + 31 of the block. V, piece u (keys 32u ..): keys 32u + 8 (w % 4) .. + 7, four lanes
-// a key, 32 dims each, those of warps 4 .. 7 in the upper 128. Eight neighbouring lanes always
-// hold eight neighbouring rows, so the swizzle keeps reads and writes free of bank conflicts.
+// Warps 0 .. 3 take pieces 0 and 2 of every tile, 4 .. 7 pieces 1 and 3 (all eight at every piece
+// cost a third more instructions for the same codes). Warp w of four. K, piece u (64-dim block u):
+// keys 32w .. 32w+31, a key a lane. V, piece u (keys 32u ..): keys 32u + 8w .. + 7, four lanes a
+// key, a 64-dim block each. Eight neighbouring lanes always hold eight neighbouring rows, so the
+// swizzle keeps reads and writes free of bank conflicts.
 __device__ void widen_worker(V4Smem& sm, int is_v, volatile int* abort) {
-  const int lane = threadIdx.x & 31, w = ((int)(threadIdx.x >> 5) - 12) & 7;
-  const uint32_t row0 = is_v ? 8 * (w & 3) + (lane & 7) : 32 * (w & 3) + lane;   // row in piece 0
+  const int lane = threadIdx.x & 31, w = ((int)(threadIdx.x >> 5) - 12) & 3;
+  const int u0 = (((int)(threadIdx.x >> 5) - 12) >> 2) & 1;           // first piece
+  const uint32_t row0 = is_v ? 8 * w + (lane & 7) : 32 * w + lane;   // the lane's row in piece 0
+  const uint32_t blk = is_v ? (uint32_t)lane >> 3 : 0;               // and 64-dim block of it
   const uint32_t xr = row0 & 7;
-  uint32_t ch = is_v ? (uint32_t)(4 * (w >> 2) + (lane >> 3)) : (uint32_t)(w >> 2);   // 32-dim chunk
   const uint32_t src_u = is_v ? kGranule * kQ4RowBytes : 0u;         // from piece to piece
   const uint32_t scs_u = is_v ? kGranule * kQ4ScaleBytes : 4u;
-  const uint32_t ch_u = is_v ? 0u : 2u;
-  // this lane's four 16-byte places in piece 0: in row xr of an 8-row atom
+  const uint32_t ch_u = is_v ? 0u : 2u;                              // 16-byte chunks of the row
   const uint32_t dst0 = smem_u32(is_v ? sm.vt[0] : sm.kt[0]) + (row0 >> 3) * 1024u + xr * 128u +
-                        (is_v ? (ch >> 1) * (kGranule * 128u) : 0u);
-  uint32_t at[4];
-#pragma unroll
-  for (uint32_t j = 0; j < 4; ++j) at[j] = dst0 + (((4 * (ch & 1) + j) ^ xr) << 4);
-  const uint32_t ch0 = ch;
+                        blk * (kGranule * 128u);
   uint64_t* full = sm.full + 4 * is_v;
   uint64_t* empty = sm.empty + 4 * is_v;
   const int n = sm.cut.units;
   for (int g = 0; g < n; ++g) {
     const int st = kStages * is_v + g % kStages;
     if (!warp_wait(&sm.raw_full[st], (g / kStages) & 1, abort)) return;
-    uint32_t src = smem_u32(sm.raw[st]) + row0 * kQ4RowBytes;
-    uint32_t scs = smem_u32(sm.rsc[st]) + row0 * kQ4ScaleBytes + 2 * ch0;
-    ch = ch0;
-    uint32_t sc = lds_u16(scs);
-    uint4 c = lds_v4(src + ((ch ^ xr) << 4));
-#pragma unroll 1
-    for (int u = 0; u < 4; ++u) {
-      if (!warp_wait(&empty[u], (g & 1) ^ 1, abort)) return;
-      const uint32_t wd[4] = {c.x, c.y, c.z, c.w};
-      const Q4Scale q0 = q4_scale(sc & 0xFFu), q1 = q4_scale(sc >> 8);
+    const uint32_t src = smem_u32(sm.raw[st]) + row0 * kQ4RowBytes;
+    const uint32_t scs = smem_u32(sm.rsc[st]) + row0 * kQ4ScaleBytes + 4 * blk;
+    uint32_t sc = lds_u32(scs + u0 * scs_u), ch = 2 * blk + u0 * ch_u;
+    uint4 c0 = lds_v4(src + u0 * src_u + ((ch ^ xr) << 4)), c1 = lds_v4(src + u0 * src_u + (((ch + 1) ^ xr) << 4));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t o[4];
-        q4_widen(wd[j], j < 2 ? q0 : q1, o);
-        sts_v4(at[j] + u * kBlockBytes, o);
+    for (int i = 0; i < 2; ++i) {
+      const int u = u0 + 2 * i;
+      if (!warp_wait(&empty[u], (g & 1) ^ 1, abort)) return;
+      const uint32_t dst = dst0 + u * kBlockBytes;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint4 c = k ? c1 : c0;
+        const uint32_t wd[4] = {c.x, c.y, c.z, c.w};
+        const Q4Scale q0 = q4_scale((sc >> (16 * k)) & 0xFFu);
+        const Q4Scale q1 = q4_scale((sc >> (16 * k + 8)) & 0xFFu);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t o[4];
+          q4_widen(wd[j], j < 2 ? q0 : q1, o);
+          sts_v4(dst + (((uint32_t)(4 * k + j) ^ xr) << 4), o);
+        }
       }
-      if (u < 3) {   // the next piece's codes, while the stores drain
-        src += src_u;
-        scs += scs_u;
-        ch += ch_u;
-        sc = lds_u16(scs);
-        c = lds_v4(src + ((ch ^ xr) << 4));
+      if (i == 0) {   // the next piece's codes, while the stores drain
+        sc = lds_u32(scs + (u0 + 2) * scs_u);
+        ch += 2 * ch_u;
+        c0 = lds_v4(src + (u0 + 2) * src_u + ((ch ^ xr) << 4));
+        c1 = lds_v4(src + (u0 + 2) * src_u + (((ch + 1) ^ xr) << 4));
       }
       fence_async_smem();   // the tensor cores read what the lanes wrote
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&full[u]);
-        if (u == 3) mbar_arrive(&sm.raw_empty[st]);
+        if (i == 1) mbar_arrive(&sm.raw_empty[st]);
       }
     }
   }
@@ -364,9 +374,9 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
       float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        const float p0 = ex2_approx(fmaf(f(2 * k), kLog2eOver16, -mf));
-        const float p1 = ex2_approx(fmaf(f(2 * k + 1), kLog2eOver16, -mf));
-        sb[k] = pack_bf16x2(p0, p1);   // an index already read
+        float t0, t1;
+        fma_f32x2(t0, t1, f(2 * k), f(2 * k + 1), kLog2eOver16, -mf);
+        sb[k] = pack_bf16x2(ex2_approx(t0), ex2_approx(t1));   // an index already read
         if (k & 1) add_bf16x2(l2, l3, sb[k]);
         else add_bf16x2(l0, l1, sb[k]);
       }
@@ -443,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.raw_empty[i], 8);   // one arrival per widening warp
     }
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&sm.full[i], 8);         // per widening warp
+      mbar_init(&sm.full[i], 4);         // per widening warp of the piece
       mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
