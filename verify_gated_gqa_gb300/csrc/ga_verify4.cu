@@ -147,8 +147,13 @@ __device__ void widen_worker(V4Smem& sm, int is_v, volatile int* abort) {
   const uint32_t src_u = is_v ? kGranule * kQ4RowBytes : 0u;         // from piece to piece
   const uint32_t scs_u = is_v ? kGranule * kQ4ScaleBytes : 4u;
   const uint32_t ch_u = is_v ? 0u : 2u;                              // 16-byte chunks of the row
-  const uint32_t dst0 = smem_u32(is_v ? sm.vt[0] : sm.kt[0]) + (row0 >> 3) * 1024u + xr * 128u +
+  // this lane's 128-byte row in its first piece, and the four 16-byte places of its first 32 codes in
+  // it (the last 32 codes' are 64 bytes across)
+  const uint32_t dst0 = smem_u32(is_v ? sm.vt[u0] : sm.kt[u0]) + (row0 >> 3) * 1024u + xr * 128u +
                         blk * (kGranule * 128u);
+  uint32_t at[4];
+#pragma unroll
+  for (uint32_t j = 0; j < 4; ++j) at[j] = dst0 + ((j ^ xr) << 4);
   uint64_t* full = sm.full + 4 * is_v;
   uint64_t* empty = sm.empty + 4 * is_v;
   const int n = sm.cut.units;
@@ -163,7 +168,6 @@ __device__ void widen_worker(V4Smem& sm, int is_v, volatile int* abort) {
     for (int i = 0; i < 2; ++i) {
       const int u = u0 + 2 * i;
       if (!warp_wait(&empty[u], (g & 1) ^ 1, abort)) return;
-      const uint32_t dst = dst0 + u * kBlockBytes;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint4 c = k ? c1 : c0;
@@ -174,7 +178,7 @@ __device__ void widen_worker(V4Smem& sm, int is_v, volatile int* abort) {
         for (int j = 0; j < 4; ++j) {
           uint32_t o[4];
           q4_widen(wd[j], j < 2 ? q0 : q1, o);
-          sts_v4(dst + (((uint32_t)(4 * k + j) ^ xr) << 4), o);
+          sts_v4((k ? at[j] ^ 64u : at[j]) + i * (2 * kBlockBytes), o);
         }
       }
       if (i == 0) {   // the next piece's codes, while the stores drain
