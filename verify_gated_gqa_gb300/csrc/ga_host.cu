@@ -1291,6 +1291,16 @@ int check_q4_pools(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_
     return GA_ERR_ALIGN;
   return GA_OK;
 }
+// Division of slots by the page size in the kernels (Kv4Args): with L = ceil(log2 d) the product's
+// excess over 2^(25 + L) x / d is below 2^L x / 2^(25 + L) < 1 / d for x < 2^25, so the quotient is
+// exact; pools have fewer than 2^30 slots.
+void set_page_division(Kv4Args& a) {
+  const unsigned d = (unsigned)a.page_size / GA_Q4_PAGE_TOKENS;
+  int log2 = 0;
+  while ((1u << log2) < d) ++log2;
+  a.page_shift = 25 + log2;
+  a.page_mul = (unsigned)(((1ULL << a.page_shift) + d - 1) / d);
+}
 int check_q4_tokens(long long n_tok, const int* slots, int n_pages, int page_size) {
   if (n_tok < 0) return GA_ERR_SHAPE;
   if (n_tok > 64LL * GA_MAX_TOKENS || (!slots && n_tok > (long long)n_pages * page_size))
@@ -1321,9 +1331,11 @@ int ga_kv_quantize_q4(const ga_bf16* k, long long ld_k, const ga_bf16* v, long l
   if (st != GA_OK) return st;
   Kv4Args a{};
   a.k = k; a.v = v; a.ld_k = ld_k; a.ld_v = ld_v;
+  a.in32 = aligned(k, 32) && aligned(v, 32) && ld_k % 16 == 0 && ld_v % 16 == 0;
   a.k_codes = k_codes; a.k_scales = k_scales; a.v_codes = v_codes; a.v_scales = v_scales;
   a.slots = slots; a.n_tok = n_tok;
   a.n_slots = (long long)n_pages * page_size; a.page_size = page_size;
+  set_page_division(a);
   a.status = dev->status_word;
   const cudaError_t e = GA_CUDA(launch_quantize_q4(a, (cudaStream_t)stream));
   return e == cudaSuccess ? GA_OK : fail_cuda(e);
@@ -1347,6 +1359,7 @@ int ga_kv_dequantize_q4(const uint8_t* k_codes, const uint8_t* k_scales, const u
   a.v_codes = const_cast<uint8_t*>(v_codes); a.v_scales = const_cast<uint8_t*>(v_scales);
   a.slots = slots; a.n_tok = n_tok;
   a.n_slots = (long long)n_pages * page_size; a.page_size = page_size;
+  set_page_division(a);
   a.k_out = k_out; a.v_out = v_out;
   a.out32 = aligned(k_out, 32) && aligned(v_out, 32);
   a.status = dev->status_word;

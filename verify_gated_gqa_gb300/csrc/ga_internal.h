@@ -185,7 +185,10 @@ struct Kv4Args {
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
   const int* slots;
   long long n_tok, n_slots;
-  int page_size;
+  int page_size;              // 32 d; x / d = (x page_mul) >> page_shift for x < 2^25:
+  unsigned page_mul;          // page_shift = 25 + ceil(log2 d), page_mul = ceil(2^page_shift / d)
+  int page_shift;
+  bool in32;                  // every one of them 32-byte aligned
   uint16_t *k_out, *v_out;    // widening: [n_tok][2][256]
   bool out32;                 // and both 32-byte aligned
   int* status;

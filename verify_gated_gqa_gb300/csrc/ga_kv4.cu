@@ -5,10 +5,10 @@
 // position x % page_size of page x / page_size, the same for both heads.
 //
 // 16 lanes per row, one 16-value group per lane, so a group's maximum needs no exchange between
-// lanes, a row's reads and writes are contiguous runs, and the four rows of a token (two heads of
-// K and of V) lie in one 64-thread stretch. Both kernels are bound by the bytes they move
-// (2,624 a token); a thread takes kTok tokens, with the slots and then the rows of all of them
-// in flight before the first is used, once there are enough tokens to fill the device so.
+// lanes and a row's reads and writes are contiguous runs. Both kernels are bound by the bytes they
+// move (2,624 a token), storing by its instructions nearly as much. A thread takes the same group
+// of a token's four rows (two heads of K and of V), all four in flight before the first is used
+// and the slot looked up and divided once for them; with few tokens, of one row.
 #include <cuda_bf16.h>
 
 #include "ga_internal.h"
@@ -18,48 +18,39 @@
 namespace ga {
 namespace {
 
-constexpr int kRowThreads = 16;                           // one 16-value group each
-constexpr int kTokThreads = 2 * kKvHeads * kRowThreads;   // K and V rows of a token
+constexpr int kRowThreads = 16;         // one 16-value group each
+constexpr int kTokRows = 2 * kKvHeads;  // K heads 0, 1, V heads 0, 1
 constexpr int kBlockThreads = 256;
-constexpr int kBlockToks = kBlockThreads / kTokThreads;   // tokens a block takes at a time
 
-// Row index in a pool of a slot's row of head h, or -1: a negative slot (the token is not
-// stored) or one outside the pool (recorded in the status word).
-__device__ __forceinline__ long long pool_row(const Kv4Args& a, long long slot, int h) {
+// Pool row of head 0 of a slot, or -1: a negative slot (the token is not stored) or one outside
+// the pool (recorded in the status word). Head 1's is page_size on.
+__device__ __forceinline__ long long pool_row(const Kv4Args& a, long long slot) {
   if (slot < 0) return -1;
   if (slot >= a.n_slots) {
     atomicCAS(a.status, 0, (int)kDevBadPage);
     return -1;
   }
-  const unsigned page = (unsigned)slot / (unsigned)a.page_size;
-  const unsigned off = (unsigned)slot - page * (unsigned)a.page_size;
-  return ((long long)page * kKvHeads + h) * a.page_size + off;
+  // pages of 32 d slots: slot / 32 / d by one multiplication, exact below 2^25 (Kv4Args)
+  const unsigned page = (unsigned)(((unsigned long long)((unsigned)slot >> 5) * a.page_mul) >> a.page_shift);
+  return (long long)page * (kKvHeads * a.page_size) + ((unsigned)slot - page * (unsigned)a.page_size);
 }
 
-// A thread's place in a token: a group of a head's K or V row.
+// A thread's place: group g of rows r0 .. r0 + kRows - 1 of token tok.
+template <int kRows>
 struct Place {
-  int g, h;
-  bool is_v;
-  long long tok;   // its first token; the next ones kBlockToks apart
-  __device__ __forceinline__ explicit Place(int n_per_thread) {
-    const int row = (threadIdx.x % kTokThreads) / kRowThreads;   // K head 0, 1, V head 0, 1
+  int g, r0;
+  long long tok;
+  __device__ __forceinline__ Place() {
+    constexpr int kPer = kTokRows / kRows;   // threads of a group of a token
     g = threadIdx.x % kRowThreads;
-    h = row % kKvHeads;
-    is_v = row >= kKvHeads;
-    tok = (long long)blockIdx.x * (kBlockToks * n_per_thread) + threadIdx.x / kTokThreads;
+    r0 = threadIdx.x / kRowThreads % kPer * kRows;
+    tok = (long long)blockIdx.x * (kBlockThreads / kRowThreads / kPer) + threadIdx.x / (kRowThreads * kPer);
+  }
+  __device__ __forceinline__ long long row(const Kv4Args& a) const {
+    if (tok >= a.n_tok) return -1;
+    return pool_row(a, a.slots ? (long long)__ldg(a.slots + tok) : tok);
   }
 };
-template <int kTok>
-__device__ __forceinline__ void pool_rows(const Kv4Args& a, const Place& at, long long (&row)[kTok]) {
-  long long slot[kTok];
-#pragma unroll
-  for (int k = 0; k < kTok; ++k) {
-    const long long t = at.tok + k * kBlockToks;
-    slot[k] = t >= a.n_tok ? -1 : a.slots ? (long long)__ldg(a.slots + t) : t;
-  }
-#pragma unroll
-  for (int k = 0; k < kTok; ++k) row[k] = pool_row(a, slot[k], at.h);
-}
 
 // The scale byte of a group whose largest magnitude is amax (an infinite one takes the
 // largest scale). The division is correctly rounded, and a bf16 maximum cannot put fp32(a/7)
@@ -77,11 +68,11 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
 
 // Codes without a division each. With x = X 2^a (X < 256) and s = S 2^b (8 <= S <= 15), a
 // quotient that is not on a half is at least 1/960 from the nearest one (for quotients of 0.5 and
-// more; smaller ones round to 0), while x times the reciprocal is within 2^-19 of it. Adding and
-// subtracting 3072 = 1.5 x 2^11 rounds that product to a multiple of 2^-12: a quotient on a half
-// comes out on it exactly, and none is carried to or past one. A last addition rounds to the
-// integer, ties to even, in the low bits of the sum.
-constexpr float kSnap = 1.5f * 2048.0f, kInt = 1.5f * 8388608.0f + 8.0f;
+// more; smaller ones round to 0), while x times the reciprocal is within 2^-19 of it. One
+// multiply-add onto 3072 = 1.5 x 2^11 rounds that product to a multiple of 2^-12: a quotient on a
+// half comes out on it exactly, and none is carried to or past one. One addition more rounds to
+// the integer, ties to even, in the low bits of the sum.
+constexpr float kSnap = 1.5f * 2048.0f, kInt = 1.5f * 8388608.0f + 8.0f - kSnap;
 __device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -92,9 +83,9 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 
@@ -109,15 +100,15 @@ __device__ __forceinline__ uint32_t quantize_group(const uint32_t (&xw)[8], uint
     const uint32_t byte = scale_byte(__uint_as_float(top << 16));
     const float inv = __fdividef(1.0f, scale_of(byte));
     const uint64_t inv2 = pack_f32x2(inv, inv), snap = pack_f32x2(kSnap, kSnap),
-                   back = pack_f32x2(-kSnap, -kSnap), whole = pack_f32x2(kInt, kInt);
+                   whole = pack_f32x2(kInt, kInt);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       uint32_t acc = 0u;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {   // dims 2j and 2j + 1: nibbles j and 4 + j
         const uint32_t v = xw[4 * k + j];
-        uint64_t q = mul_f32x2(pack_f32x2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u)), inv2);
-        q = add_f32x2(add_f32x2(add_f32x2(q, snap), back), whole);
+        const uint64_t x = pack_f32x2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+        const uint64_t q = add_f32x2(fma_f32x2(x, inv2, snap), whole);
         // the sums' low bits hold code and constant; the constants are taken off below
         acc += (uint32_t)q * (1u << (4 * j)) + (uint32_t)(q >> 32) * (1u << (4 * j + 16));
       }
@@ -146,65 +137,72 @@ __device__ __forceinline__ uint32_t quantize_group(const uint32_t (&xw)[8], uint
   return byte;
 }
 
-// 32 bytes of a row by one lane: two 16-byte loads (the rows are 16-byte aligned).
-__device__ __forceinline__ void load_group(const uint16_t* p, uint32_t (&x)[8]) {
+// 32 bytes of a row by one lane: one load where every row is 32-byte aligned, else two.
+__device__ __forceinline__ void load_group(const uint16_t* p, bool whole, uint32_t (&x)[8]) {
+  if (whole) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+                   "=r"(x[7])
+                 : "l"(p));
+    return;
+  }
   const uint4 x0 = __ldg(reinterpret_cast<const uint4*>(p));
   const uint4 x1 = __ldg(reinterpret_cast<const uint4*>(p) + 1);
   x[0] = x0.x; x[1] = x0.y; x[2] = x0.z; x[3] = x0.w;
   x[4] = x1.x; x[5] = x1.y; x[6] = x1.z; x[7] = x1.w;
 }
 
-template <int kTok>
+template <int kRows>
 __global__ void __launch_bounds__(kBlockThreads) quantize_q4_kernel(
     const __grid_constant__ Kv4Args a) {
-  const Place at(kTok);
-  const uint16_t* x = (at.is_v ? a.v : a.k) + at.h * kDim + at.g * kQ4Group;
-  const long long ld = at.is_v ? a.ld_v : a.ld_k;
-  uint32_t xw[kTok][8];
+  const Place<kRows> at;
+  uint32_t xw[kRows][8];
+  if (at.tok < a.n_tok) {   // the rows do not wait for the slot
 #pragma unroll
-  for (int k = 0; k < kTok; ++k) {   // the rows do not wait for the slots
-    const long long t = at.tok + k * kBlockToks;
-    if (t < a.n_tok) load_group(x + t * ld, xw[k]);
+    for (int k = 0; k < kRows; ++k) {
+      const int r = at.r0 + k;
+      const uint16_t* x = r < kKvHeads ? a.k + at.tok * a.ld_k : a.v + at.tok * a.ld_v;
+      load_group(x + r % kKvHeads * kDim + at.g * kQ4Group, a.in32, xw[k]);
+    }
   }
-  long long row[kTok];
-  pool_rows<kTok>(a, at, row);
-  uint8_t* codes = at.is_v ? a.v_codes : a.k_codes;
-  uint8_t* scales = at.is_v ? a.v_scales : a.k_scales;
+  const long long row0 = at.row(a);
+  if (row0 < 0) return;
 #pragma unroll
-  for (int k = 0; k < kTok; ++k) {
-    if (row[k] < 0) continue;
+  for (int k = 0; k < kRows; ++k) {
+    const int r = at.r0 + k;
+    const long long row = row0 + r % kKvHeads * a.page_size;
     uint32_t w[2];
     const uint32_t byte = quantize_group(xw[k], w);
-    *reinterpret_cast<uint2*>(codes + row[k] * kQ4RowBytes + at.g * 8) = make_uint2(w[0], w[1]);
-    scales[row[k] * kQ4ScaleBytes + at.g] = (uint8_t)byte;
+    uint8_t* codes = r < kKvHeads ? a.k_codes : a.v_codes;
+    uint8_t* scales = r < kKvHeads ? a.k_scales : a.v_scales;
+    *reinterpret_cast<uint2*>(codes + row * kQ4RowBytes + at.g * 8) = make_uint2(w[0], w[1]);
+    scales[row * kQ4ScaleBytes + at.g] = (uint8_t)byte;
   }
 }
 
-template <int kTok>
+template <int kRows>
 __global__ void __launch_bounds__(kBlockThreads) dequantize_q4_kernel(
     const __grid_constant__ Kv4Args a) {
-  const Place at(kTok);
-  long long row[kTok];
-  pool_rows<kTok>(a, at, row);
-  const uint8_t* codes = at.is_v ? a.v_codes : a.k_codes;
-  const uint8_t* scales = at.is_v ? a.v_scales : a.k_scales;
-  uint2 w[kTok];
-  uint32_t sc[kTok];
+  const Place<kRows> at;
+  const long long row0 = at.row(a);
+  if (row0 < 0) return;
+  uint2 w[kRows];
+  uint32_t sc[kRows];
 #pragma unroll
-  for (int k = 0; k < kTok; ++k) {
-    const long long r = row[k] < 0 ? 0 : row[k];
-    w[k] = *reinterpret_cast<const uint2*>(codes + r * kQ4RowBytes + at.g * 8);
-    sc[k] = scales[r * kQ4ScaleBytes + at.g];
+  for (int k = 0; k < kRows; ++k) {
+    const int r = at.r0 + k;
+    const long long row = row0 + r % kKvHeads * a.page_size;
+    w[k] = *reinterpret_cast<const uint2*>((r < kKvHeads ? a.k_codes : a.v_codes) + row * kQ4RowBytes + at.g * 8);
+    sc[k] = (r < kKvHeads ? a.k_scales : a.v_scales)[row * kQ4ScaleBytes + at.g];
   }
-  uint16_t* out = (at.is_v ? a.v_out : a.k_out) + at.h * kDim + at.g * kQ4Group;
 #pragma unroll
-  for (int k = 0; k < kTok; ++k) {
-    if (row[k] < 0) continue;
+  for (int k = 0; k < kRows; ++k) {
+    const int r = at.r0 + k;
     const Q4Scale q = q4_scale(sc[k]);
     uint32_t o0[4], o1[4];
     q4_widen(w[k].x, q, o0);
     q4_widen(w[k].y, q, o1);
-    uint16_t* to = out + (at.tok + k * kBlockToks) * (kKvHeads * kDim);
+    uint16_t* to = (r < kKvHeads ? a.k_out : a.v_out) + (at.tok * kKvHeads + r % kKvHeads) * kDim + at.g * kQ4Group;
     if (a.out32) {   // whole sectors by one store a lane (two 16-byte stores: half sectors twice)
       const uint32_t o[8] = {o0[0], o0[1], o0[2], o0[3], o1[0], o1[1], o1[2], o1[3]};
       st_global_v8(to, o);
@@ -215,11 +213,11 @@ __global__ void __launch_bounds__(kBlockThreads) dequantize_q4_kernel(
   }
 }
 
-unsigned kv4_grid(long long n_tok, int per_thread) {
-  const long long per = (long long)kBlockToks * per_thread;
+unsigned kv4_grid(long long n_tok, int rows) {
+  const long long per = (long long)(kBlockThreads / kRowThreads) * rows / kTokRows;
   return (unsigned)((n_tok + per - 1) / per);
 }
-// Four tokens a thread from here on (the blocks then still fill the device a few times over).
+// Four rows a thread from here on (the blocks then still fill the device a few times over).
 constexpr long long kManyToks = 16384;
 
 }  // namespace

@@ -708,6 +708,8 @@ cudaError_t verify4_set_attributes() {
   cudaError_t e = cudaFuncSetAttribute(verify4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)sizeof(V4Smem));
   if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(verify4_combine_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, ml_bytes);
+  if (e == cudaSuccess)
     e = cudaFuncSetAttribute(verify4_combine_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, ml_bytes);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(verify4_combine_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, ml_bytes);
@@ -717,12 +719,13 @@ cudaError_t verify4_set_attributes() {
 cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, int sm_count,
                                    cudaStream_t s) {
   const int streams = a.n_seq * kKvHeads * row_blocks(a.rows);
-  const bool few = streams * 2 < sm_count;
+  const bool few = streams * 2 < sm_count, very_few = streams * 16 < sm_count;
   const int parts = ctas / 2 + 2;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = overlapped_launch(
-      (unsigned)(streams * (few ? 16 : 2)), kCombineThreads,
+      (unsigned)(streams * (very_few ? 64 : few ? 16 : 2)), kCombineThreads,
       (size_t)parts * (a.rows * kGroup / row_blocks(a.rows)) * sizeof(float2), s, attr);
+  if (very_few) return cudaLaunchKernelEx(&cfg, verify4_combine_kernel<1>, a, ctas, tile);
   return few ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<4>, a, ctas, tile)
              : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<32>, a, ctas, tile);
 }
