@@ -218,7 +218,7 @@ unsigned kv4_grid(long long n_tok, int rows) {
   return (unsigned)((n_tok + per - 1) / per);
 }
 // Four rows a thread from here on (the blocks then still fill the device a few times over).
-constexpr long long kManyToks = 16384;
+constexpr long long kManyToks = 4096;
 
 }  // namespace
 
