@@ -277,6 +277,47 @@ def test_slots_outside_the_pool_are_recorded_and_skipped():
     assert B.ga_device_status() == 3 and bool((ko == 1).all()) and bool((vo == 1).all())
 
 
+@pytest.mark.parametrize("n", [4095, 4096, 4999])
+@pytest.mark.parametrize("offset", [0, 8])
+def test_store_and_widen_many_tokens(n, offset):
+    """Both splits of the work, and rows that begin 16 bytes past a 32-byte boundary."""
+    page, n_pages = 96, 60
+    flat = torch.zeros(n * 2 * 512 + 8, dtype=torch.bfloat16, device="cuda")
+    k = flat[offset:offset + n * 1024].view(n, 2, 2, 256)[:, 0]
+    v = flat[offset:offset + n * 1024].view(n, 2, 2, 256)[:, 1]
+    k.copy_(_special_rows(n, SEED + n))
+    v.copy_(_special_rows(n, SEED + n + 1))
+    rng = np.random.default_rng(n)
+    slots = rng.permutation(n_pages * page)[:n]
+    slots[rng.integers(0, n, 300)] = -1
+    pools = _pools(n_pages, page)
+    want = _expect_pool(pools, k, v, slots, page)
+    B.ga_kv_quantize_q4(k, v, *pools, slots=_i32(slots))
+    for g, w in zip(pools, want):
+        assert np.array_equal(g.cpu().numpy(), w)
+    out = torch.full((2 * n * 512 + 16,), 3.0, dtype=torch.bfloat16, device="cuda")
+    ko, vo = (out[offset + i * n * 512:][:n * 512].view(n, 2, 256) for i in (0, 1))
+    B.ga_kv_dequantize_q4(*pools, slots=_i32(slots), k_out=ko, v_out=vo)
+    for x, o in ((k, ko), (v, vo)):
+        w = O.widen_q4_rows(*O.quantize_q4_rows(np64(x)))
+        w[slots < 0] = 3.0
+        assert np.array_equal(np64(o), w)
+    rest = torch.cat((out[:offset], out[offset + 2 * n * 512:]))
+    assert bool((rest == 3).all())
+
+
+def test_store_rows_of_an_odd_stride():
+    """Token strides that are multiples of 16 bytes only."""
+    n = 70
+    k = torch.randn(n, 520, device="cuda").to(torch.bfloat16)[:, :512].unflatten(1, (2, 256))
+    v = torch.randn(n, 776, device="cuda").to(torch.bfloat16)[:, 256:768].unflatten(1, (2, 256))
+    pools = _pools(3, 32)
+    want = _expect_pool(pools, k, v, range(n), 32)
+    B.ga_kv_quantize_q4(k, v, *pools)
+    for g, w in zip(pools, want):
+        assert np.array_equal(g.cpu().numpy(), w)
+
+
 # ------------------------------------------------------------------ attention
 # The tolerance, per element, from the roundings: each weight is rounded to bf16 (at most 2^-8
 # of itself) above and below the quotient, so 2 x 2^-8 of sum w |v| times the gate; the output
@@ -383,6 +424,45 @@ def test_attention_many_sequences():
     want, mass = c.oracle(heads=[0, 11, 12, 23])
     hs = [0, 11, 12, 23]
     _check(out.view(1100, 1, 24, 256)[:, :, hs], want[:, :, hs], mass[:, :, hs], lens)
+
+
+@pytest.mark.parametrize("rows,lens,page", [
+    (8, [12000], 64), (2, [20000, 15], 128),             # more parts than the direct merge takes
+    (2, [700] * 90 + [3000] * 3, 64), (1, [40, 6000] + [50] * 80, 32),   # cut among many
+    (9, [300] * 40 + [5000], 32), (16, [130] * 60, 96)])
+def test_attention_merges_parts(rows, lens, page):
+    """Every form of the merge: many parts of one stream, and few parts among many streams."""
+    rng = np.random.default_rng(rows + len(lens))
+    heads = sorted(map(int, rng.choice(24, 4, replace=False)))
+    c = Cache(lens, rows, page, SEED + 80 + rows)
+    want, mass = c.oracle(heads=heads)
+    got = c.run().view(len(lens), rows, 24, 256)
+    _check(got[:, :, heads], want[:, :, heads], mass[:, :, heads])
+
+
+def test_attention_long_and_short_beyond_one_launch():
+    """More sequences than one launch takes, with long ones in each."""
+    lens = [int(x) for x in np.random.default_rng(8).integers(0, 60, 300)]
+    lens[17], lens[255], lens[256], lens[299] = 3000, 900, 2500, 1111
+    c = Cache(lens, 3, 32, SEED + 90)
+    heads = [0, 11, 12, 23]
+    want, mass = c.oracle(heads=heads)
+    _check(c.run().view(300, 3, 24, 256)[:, :, heads], want[:, :, heads], mass[:, :, heads])
+
+
+@pytest.mark.parametrize("rows", [1, 3, 16])
+def test_attention_nan_stays_in_its_row(rows):
+    """A NaN or infinite query makes its own head's row NaN and no other element."""
+    c = Cache([3000, 40], rows, 32, SEED + 91)
+    good = c.run().view(2, rows, 24, 256)
+    c.q[0, rows // 2, 5, 77] = float("nan")
+    c.q[1, 0, 20, 200] = float("inf")
+    c.q[1, rows - 1, 2] = -float("inf")            # every score NaN or infinite
+    got = c.run().view(2, rows, 24, 256)
+    hit = torch.zeros(2, rows, 24, dtype=torch.bool, device="cuda")
+    hit[0, rows // 2, 5] = hit[1, 0, 20] = hit[1, rows - 1, 2] = True
+    assert bool(got[hit].isnan().all())
+    assert torch.equal(got[~hit], good[~hit])
 
 
 def test_attention_gates_at_their_limits():

@@ -276,6 +276,7 @@ __device__ void compute(D4Smem& sm, const Verify4Args& a, volatile int* abort) {
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (l[r] != l[r]) M[r] = l[r];   // a NaN row weighs NaN, not nothing
       if (t == 0) {
         sm.m[warp][g + 8 * r] = M[r];
         sm.l[warp][g + 8 * r] = l[r];
@@ -304,7 +305,7 @@ __device__ void compute(D4Smem& sm, const Verify4Args& a, volatile int* abort) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
           lt += sm.m[w][hr] == -INFINITY ? 0.f : sm.l[w][hr] * exp2f(sm.m[w][hr] - mt);
-        const float inv = lt > 0.f ? 1.0f / lt : (lt != lt ? lt : 0.f);
+        const float inv = 1.0f / lt;
         const size_t out_row = (size_t)seg.b * kHeads + seg.plane * kGroup + hr;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -328,7 +329,7 @@ __device__ void compute(D4Smem& sm, const Verify4Args& a, volatile int* abort) {
           } else {
             *part_at(a.part_o, seg.slot, p / 4, hr) = make_float4(x[0], x[1], x[2], x[3]);
             if (p == 0)
-              reinterpret_cast<float2*>(a.part_ml)[(size_t)seg.slot * kV4Lanes + hr] = make_float2(mt, lt);
+              reinterpret_cast<float2*>(a.part_ml)[(size_t)seg.slot * kV4Lanes + hr] = make_float2(lt != lt ? lt : mt, lt);
           }
         }
       }

@@ -69,7 +69,7 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
 // Codes without a division each. With x = X 2^a (X < 256) and s = S 2^b (8 <= S <= 15), a
 // quotient that is not on a half is at least 1/960 from the nearest one (for quotients of 0.5 and
 // more; smaller ones round to 0), while x times the reciprocal is within 2^-19 of it. One
-// multiply-add onto 3072 = 1.5 x 2^11 rounds that product to a multiple of 2^-12: a quotient on a
+// multiply-add onto 1.5 x 2^11 rounds that product to a multiple of 2^-12: a quotient on a
 // half comes out on it exactly, and none is carried to or past one. One addition more rounds to
 // the integer, ties to even, in the low bits of the sum.
 constexpr float kSnap = 1.5f * 2048.0f, kInt = 1.5f * 8388608.0f + 8.0f - kSnap;

@@ -399,7 +399,7 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
     l += other_l;
     if (!warp_wait(&sm.o_done, done & 1, abort)) return;
     tc_fence_after();
-    const float inv = l > 0.f ? 1.0f / l : (l != l ? l : 0.f);
+    const float inv = 1.0f / l;   // (every row sees a key: 0 only if all its scores are -inf, then NaN)
     const size_t prow = (size_t)seg.slot * kV4Lanes + r;
     const uint4* gp = reinterpret_cast<const uint4*>(a.qg + (row * kHeads + h) * kQgStride + kDim + 128 * hf);
     uint4* op = reinterpret_cast<uint4*>(a.out + (row * kHeads + h) * kDim + 128 * hf);
@@ -428,7 +428,7 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
       }
     }
     if (valid && !seg.whole && hf == 0)
-      reinterpret_cast<float2*>(a.part_ml)[prow] = make_float2(M, l);
+      reinterpret_cast<float2*>(a.part_ml)[prow] = make_float2(l != l ? l : M, l);   // a NaN row's part weighs NaN, not nothing
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.o_free);
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
           o.w = fmaf(f, v[k].w, o.w);
         }
       }
-      finish(d4, r, o, L > 0.f ? 1.0f / L : (L != L ? L : 0.f));
+      finish(d4, r, o, 1.0f / L);
     }
     return;
   }
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    if (lane == 0) inv[r] = L > 0.f ? 1.0f / L : (L != L ? L : 0.f);
+    if (lane == 0) inv[r] = 1.0f / L;
   }
   __syncthreads();
   const int groups = items < kCombineThreads ? kCombineThreads / items : 1;
