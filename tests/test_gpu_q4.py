@@ -126,6 +126,16 @@ def test_plan_refuses_on_the_device(kind, status, pad):
         assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
 
 
+def test_plan_refuses_more_held_pages_than_32_bits_count():
+    n, width = 2048, 1 << 21                       # 2^32 pages in all
+    table = torch.empty(n, width, dtype=torch.int32, device="cuda")
+    held, count = torch.full((n,), width, dtype=torch.int32, device="cuda"), _i32([0])
+    stack, lens = torch.full((width,), 7, dtype=torch.int32, device="cuda"), _i32([0] * n)
+    start, slots, pos, info = B.ga_page_plan(lens, _i32([-1] * n), table, held, stack, count, 1, 4)
+    assert info.tolist() == [4, 0, 0, 0] and count.item() == 0 and slots.tolist() == [-1] * 4
+    assert bool((held == width).all()) and bool((stack == 7).all())
+
+
 def test_plan_without_sequences():
     e = torch.zeros(0, dtype=torch.int32, device="cuda")
     start, slots, pos, info = B.ga_page_plan(e, e, torch.zeros(0, 4, dtype=torch.int32, device="cuda"),
@@ -519,6 +529,24 @@ def test_attention_repeats_bit_for_bit_and_on_another_stream():
     c.check()
 
 
+@pytest.mark.parametrize("rows", [1, 5])
+def test_attention_calls_at_once(rows):
+    """Calls on two streams that may run together, each with a workspace of its own, beside a call
+    of the other kernel form."""
+    a, b = Cache([5000, 30], rows, 32, SEED + 92), Cache([70, 900, 4000], 6 - rows, 64, SEED + 93)
+    want = a.run(), b.run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, s) in enumerate(zip((a, b), streams)):
+            with torch.cuda.stream(s):
+                got[i].append(c.run())
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
 @pytest.mark.parametrize("rows", [1, 4])
 def test_captured_step_follows_its_lengths(rows):
     """One captured graph, replayed as the device lengths change."""
@@ -692,6 +720,8 @@ def test_calls_refuse_tensors_that_do_not_belong():
         B.ga_kv_quantize_q4(c.kw[..., ::2], c.vw, kc, ks, vc, vs)
     with pytest.raises(ValueError):
         B.ga_kv_quantize_q4(c.kw[:8], c.vw[:8], kc, ks, vc, vs, slots=l)
+    with pytest.raises(ValueError):
+        B.ga_kv_dequantize_q4(kc, ks, vc, vs, slots=l, n_tok=5)
     with pytest.raises(B.GaError):
         B.ga_attn_verify_q4(c.q, c.qg, kc, ks, vc, vs, t, l, workspace=torch.empty(
             64, dtype=torch.uint8, device="cuda"))

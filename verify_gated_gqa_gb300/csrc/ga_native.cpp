@@ -152,7 +152,7 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   int* held = c.at<int>(a[3], "held", kI32, {n});
   int* count = c.at<int>(a[5], "free_count", kI32, {1});
   const int st = without_gil(
-      ga_page_plan, 
+      ga_page_plan,
       c.at<int>(len, "seq_len", kI32, {n}), c.at<int>(a[1], "new_len", kI32, {n}), extent(n, "seq_len"),
       page_size, c.at<int>(table, "page_table", kI32, {n, width}), extent(width, "page_table"), held,
       a[9] == Py_None ? held : c.at<int>(a[9], "held_out", kI32, {n}),
@@ -217,7 +217,7 @@ PyObject* qk_prologue_axes(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   const int64_t rows = cos.size(0);
   const void* p = pos.data_ptr();
   const int st = without_gil(
-      ga_qk_prologue_axes, 
+      ga_qk_prologue_axes,
       k, wk, kp, q, wq, qp, extent(n, first), static_cast<const int*>(p ? p : reinterpret_cast<void*>(256)),
       n_axes > 1 ? pos.stride(0) : cols, extent(n_axes, "positions"), axes,
       c.at<uint16_t>(cos, "cos_tab", kBf16, {rows, kPairs}),
@@ -270,6 +270,7 @@ PyObject* kv_dequantize_q4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (s.dim() != 1) value_error("slots must be [n_tok]");
     n = s.size(0);
     slots = c.at<int>(s, "slots", kI32, {n});
+    if (a[5] != Py_None && to_int(a[5], "n_tok") != n) value_error("slots must be [n_tok]");
   } else if (a[5] != Py_None) {
     n = to_int(a[5], "n_tok");
     if (n < 0) value_error("n_tok must not be negative");
@@ -302,7 +303,7 @@ PyObject* attn_verify_q4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   if (!ws.is_cuda() || ws.get_device() != c.dev || !ws.is_contiguous())
     value_error("workspace must be a contiguous tensor on the current CUDA device");
   const int st = without_gil(
-      ga_attn_verify_q4, 
+      ga_attn_verify_q4,
       c.at<uint16_t>(q, "q_prep", kBf16, {n, rows, kHeadsQ, kDim}),
       c.at<uint16_t>(a[1], "qg", kBf16, {n, rows, kHeadsQ, 2 * kDim}), p.kc, p.ks, p.vc, p.vs, p.n_pages,
       p.page_size, c.at<int>(table, "page_table", kI32, {n, width}), extent(width, "page_table"),

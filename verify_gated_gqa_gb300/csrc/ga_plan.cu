@@ -54,8 +54,11 @@ __device__ __forceinline__ void write_slot(const PlanArgs& a, const unsigned* st
 struct Triple {
   unsigned tok, need, rel;
 };
+// (tok and need are at most 2^20 a sequence; what rows claim to hold is only bounded by the table's
+// width, so its sum stops at the largest value, which is then refused)
 __device__ __forceinline__ Triple add(Triple x, Triple y) {
-  return Triple{x.tok + y.tok, x.need + y.need, x.rel + y.rel};
+  const unsigned rel = x.rel + y.rel;
+  return Triple{x.tok + y.tok, x.need + y.need, rel < x.rel ? 0xFFFFFFFFu : rel};
 }
 // Inclusive sums over the lanes of a warp.
 __device__ __forceinline__ Triple warp_scan(Triple x, int lane) {
