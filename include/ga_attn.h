@@ -616,14 +616,15 @@ size_t ga_verify_q4_workspace_bytes(void);
  * verify calls it takes prepared queries (their positions need not be their cache slots) and
  * lengths on the DEVICE, and it rounds the softmax weights and the output only: scores, O and
  * the gate stay in fp32. The same call gives the same bits; where a sequence's keys are cut
- * among the SMs, and so its last bits, depends on all the lengths of the call.
+ * among the SMs, and so its last bits, depends on all the lengths of the call. A NaN query (or one
+ * whose scores are infinite) makes its own head's row NaN and no other.
  *   q_prep   [n_seq][rows][24][256] prepared queries (ga_qk_prologue_axes or ga_q_prologue)
  *   qg       [n_seq][rows][24][512] fused rows, read for their gate halves
  *   k_codes, k_scales, v_codes, v_scales, n_pages, page_size: the pools, as ga_kv_quantize_q4
  *            writes them (prepared keys); the window's own keys included
  *   page_table DEVICE int32 [n_seq][max_pages]: as in ga_attn_verify_paged; the entries that
  *            cover keys 0 .. L + rows - 1 are read, one outside the pool records status 3 and
- *            reads zeros
+ *            reads zero bytes
  *   seq_len  DEVICE int32 [n_seq]: L, the cached tokens before the window. Negative: an unused
  *            row, of which nothing is read and whose outputs are left as they were; L + rows
  *            past max_pages * page_size or GA_MAX_TOKENS records status 4 and is treated so too

@@ -5,7 +5,7 @@
 // still had to be widened through shared memory, so this form feeds mma.sync (16 rows) from
 // registers: a lane's codes become its operand fragments where it holds them, and nothing
 // widened is ever stored. What bounds it is the cache's bytes and the instructions that widen
-// them, about equally (288 bytes and 550 warp instructions per 16 keys of a head).
+// them, about equally (288 bytes and some 40 warp instructions a key of a head).
 //
 // Work: streams (sequence, KV head) in granules of 32 keys, cut into equal runs, one per CTA, as in
 // ga_v4.cuh. Eight computing warps a CTA; warp w takes a segment's granules w, w + 8, ... on its

@@ -217,7 +217,9 @@ unsigned kv4_grid(long long n_tok, int rows) {
   const long long per = (long long)(kBlockThreads / kRowThreads) * rows / kTokRows;
   return (unsigned)((n_tok + per - 1) / per);
 }
-// Four rows a thread from here on (the blocks then still fill the device a few times over).
+// Four rows a thread from here on, against one: storing 4,096 tokens 3.2 against 3.4 us, 65,536
+// tokens 26.6 against 34.3 (widening 28.3 against 33.5); 64 tokens 2.15 against 1.67, 3,000 tokens
+// 3.2 against 2.8 (a quarter of the threads, each with four times the chain of instructions).
 constexpr long long kManyToks = 4096;
 
 }  // namespace

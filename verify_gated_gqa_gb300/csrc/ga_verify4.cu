@@ -525,10 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The streams that the cut left in parts: o = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i over a
 // stream's parts, times the gate. A block takes a slice of 4 kD4 dims of every query row of a
 // stream, a thread a float4 of a row, neighbouring threads neighbouring rows (as the parts lie). Up
-// to kDirectParts parts a thread loads the M, l and float4 of eight parts at a time and merges them as
-// they come, a trip to L2 for eight. More parts: all (M, l) into shared memory, a warp per row turns them into weights, and the
-// float4s come eight parts at a time; when a slice has fewer float4s than the block has threads,
-// the parts are dealt to several groups of threads, joined in shared memory. Thin slices when the streams are few (one sequence over 65,536 keys: two streams
+// to kDirectParts parts a thread loads the M, l and float4 of eight parts at a time and merges
+// them as they come, a trip to L2 for eight. More parts: all (M, l) into shared memory, a warp per
+// row turns them into weights, and the float4s come eight parts at a time; when a slice has fewer
+// float4s than the block has threads, the parts are dealt to several groups of threads, joined in
+// shared memory. Thin slices when the streams are few (one sequence over 65,536 keys: two streams
 // of 76 parts), wide ones when they fill the device, where a stream has a few parts.
 constexpr int kCombineThreads = 384, kCombineWarps = kCombineThreads / 32;
 // A stream's parts are at most half the CTAs and two: there are two KV heads of the same tiles.
