@@ -90,7 +90,7 @@ __device__ void loader(D4Smem& sm, const CUtensorMap* tm_kc, const CUtensorMap* 
   const int w = kEach * lw + (lane >> 2), c = lane & 3;
   const CUtensorMap* map = c == 0 ? tm_kc : c == 1 ? tm_vc : c == 2 ? tm_ks : tm_vs;
   uint32_t issued = 0;
-  Walk walk(sm.cut);
+  Walk<kKeys> walk(sm.cut);
   Seg seg;
   while (walk.next(sm.cut, a.n_seq, seg)) {
     const int* table = a.page_table + (size_t)seg.b * a.max_pages;
@@ -129,7 +129,7 @@ __device__ void compute(D4Smem& sm, const Verify4Args& a, volatile int* abort) {
   const int g = lane >> 2, t = lane & 3;
   uint32_t taken = 0;
   bool ok = true;
-  Walk walk(sm.cut);
+  Walk<kKeys> walk(sm.cut);
   Seg seg;
   while (walk.next(sm.cut, a.n_seq, seg)) {
     const int L = cut_len<kKeys>(sm.cut, seg.b, 1);

@@ -94,7 +94,28 @@ __host__ __device__ __forceinline__ int row_blocks(int rows) {
   return rows * kGroup > kV4Lanes ? 2 : 1;
 }
 
-// A CTA's share of the streams' tiles: `left` tiles from tile `tile` of stream (plane, b) on.
+// A stream's units in the cut: its tiles after kLead units of no work, which stand for what a
+// segment costs beside its tiles (its queries, the first loads, its result). A boundary inside them,
+// or fewer than kFront tiles past them, moves to the stream's beginning: the CTA before is spared a
+// segment. Cut by tiles alone, a CTA that met several short streams took several times as long as one
+// inside a long one: 64 sequences of up to 8,192 keys, one row: 76 us against 61; of up to 300 keys
+// 26 against 15; 5 x 5 rows over up to 12,345 keys 22 against 19. (Kept from 64 x 4,095 keys: 52 us
+// against 54.)
+template <int kTile>
+constexpr int kLead = kTile == 32 ? 16 : 6;
+template <int kTile>
+constexpr int kFront = kTile == 32 ? 8 : 2;
+template <int kTile>
+__device__ __forceinline__ int stream_units(int tiles) {
+  return tiles ? tiles + kLead<kTile> : 0;
+}
+// A stream's units that no boundary cuts off from its beginning (few streams are cut finely).
+template <int kTile>
+__device__ __forceinline__ int uncut(int share) {
+  return kLead<kTile> + min(kFront<kTile>, share);
+}
+
+// A CTA's share of the streams' units: `left` units from unit `at` of stream (plane, b) on.
 // plane = 2 x row block + KV head; streams are ordered by plane, then sequence.
 struct Seg {
   int plane, b, kt0, n;   // tiles kt0 .. kt0 + n - 1 of the stream
@@ -105,12 +126,14 @@ struct Seg {
 struct V4Cut {
   uint16_t tiles[kV4MaxSeq];   // key tiles of each sequence
   uint8_t spare[kV4MaxSeq];    // and what its keys lack of filling the last
-  int warp_sum[kV4MaxSeq / 32];
-  int units, plane0, b0, tile0;
+  int warp_units[kV4MaxSeq / 32], warp_streams[kV4MaxSeq / 32];   // of 32 sequences, one plane
+  int at[2], tiles_at[2];      // the CTA's run of units, and the tiles before its ends
+  int plane0, b0, at0;         // the stream that it begins in
+  __device__ __forceinline__ int run_tiles() const { return tiles_at[1] - tiles_at[0]; }
 };
-static_assert(4LL * kV4MaxSeq * (GA_MAX_TOKENS / 32) + (1 << 20) < (1LL << 31),
-              "tile counts of a launch fit in 32 bits");
-// Tiles per CTA of a cut of `total` tiles over `ctas` CTAs.
+static_assert(4LL * kV4MaxSeq * (GA_MAX_TOKENS / 32 + kLead<32>) + (1 << 20) < (1LL << 31),
+              "unit counts of a launch fit in 32 bits");
+// Units per CTA of a cut of `total` units over `ctas` CTAs.
 __device__ __forceinline__ int v4_share(int total, int ctas) { return (total + ctas - 1) / ctas; }
 
 // The sequences' tiles and this CTA's part of the cut, by the whole block (at least kV4MaxSeq
@@ -120,15 +143,16 @@ __device__ __forceinline__ int v4_share(int total, int ctas) { return (total + c
 template <int kTile>
 __device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int planes, bool report) {
   const int b = threadIdx.x, warp = b >> 5;
-  int n = 0, sum = 0;
+  int n = 0, sum = 0, streams = 0;   // units of sequence b's streams; those and the streams up to b
   if (b < kV4MaxSeq) {
     if (b < a.n_seq) {
       const int L = __ldg(a.seq_len + b);
       bool refused;
-      n = seq_tiles<kTile>(a, L, refused);
+      const int tiles = seq_tiles<kTile>(a, L, refused);
       if (refused && report) record(a.status, kDevBadPosition);
-      c.tiles[b] = (uint16_t)n;
-      c.spare[b] = (uint8_t)(n * kTile - L - a.rows);
+      c.tiles[b] = (uint16_t)tiles;
+      c.spare[b] = (uint8_t)(tiles * kTile - L - a.rows);
+      n = stream_units<kTile>(tiles);
     }
     sum = n;
 #pragma unroll
@@ -136,29 +160,49 @@ __device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int pla
       const int o = __shfl_up_sync(0xffffffffu, sum, off);
       if ((b & 31) >= off) sum += o;
     }
-    if ((b & 31) == 31) c.warp_sum[warp] = sum;
-  }
-  __syncthreads();
-  int per_plane = 0, before = sum - n;
-#pragma unroll
-  for (int w = 0; w < kV4MaxSeq / 32; ++w) {
-    const int x = c.warp_sum[w];
-    per_plane += x;
-    if (w < warp) before += x;
-  }
-  const int total = per_plane * planes;
-  const int share = v4_share(total, (int)gridDim.x);
-  const int u0 = share * (int)blockIdx.x;
-  const int units = min(share, max(0, total - u0));
-  if (units > 0) {
-    const int plane = u0 / per_plane, rem = u0 - plane * per_plane;
-    if (before <= rem && rem < before + n) {   // one sequence's thread (n is 0 past the last)
-      c.plane0 = plane;
-      c.b0 = b;
-      c.tile0 = rem - before;
+    streams = __popc(__ballot_sync(0xffffffffu, n > 0) & (0xffffffffu >> (31 - (b & 31))));
+    if ((b & 31) == 31) {
+      c.warp_units[warp] = sum;
+      c.warp_streams[warp] = streams;
     }
   }
-  if (b == 0) c.units = units;
+  __syncthreads();
+  int per_plane = 0, all = 0, before = sum - n;
+  if (n) --streams;   // those before
+#pragma unroll
+  for (int w = 0; w < kV4MaxSeq / 32; ++w) {
+    const int x = c.warp_units[w], y = c.warp_streams[w];
+    per_plane += x;
+    all += y;
+    if (w < warp) {
+      before += x;
+      streams += y;
+    }
+  }
+  const int total = per_plane * planes, share = v4_share(total, (int)gridDim.x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int u = share * ((int)blockIdx.x + i);
+    if (u >= total) {
+      if (b == 0) {
+        c.at[i] = total;
+        c.tiles_at[i] = total - kLead<kTile> * planes * all;
+      }
+      continue;
+    }
+    const int plane = u / per_plane, rem = u - plane * per_plane;
+    if (before <= rem && rem < before + n) {   // one sequence's thread (n is 0 past the last)
+      const int rel = rem - before < uncut<kTile>(share) ? 0 : rem - before;
+      const int at = plane * per_plane + before + rel;
+      c.at[i] = at;
+      c.tiles_at[i] = at - kLead<kTile> * (plane * all + streams) - min(rel, kLead<kTile>);
+      if (i == 0) {
+        c.plane0 = plane;
+        c.b0 = b;
+        c.at0 = rel;
+      }
+    }
+  }
   __syncthreads();
 }
 // Cached tokens of a sequence that has tiles.
@@ -166,32 +210,33 @@ template <int kTile>
 __device__ __forceinline__ int cut_len(const V4Cut& c, int b, int rows) {
   return (int)c.tiles[b] * kTile - (int)c.spare[b] - rows;
 }
+template <int kTile>
 struct Walk {
-  Walk() = default;
-  int plane, b, tile, left, seen;
+  int plane, b, at, left, seen;
   __device__ __forceinline__ explicit Walk(const V4Cut& c)
-      : plane(c.plane0), b(c.b0), tile(c.tile0), left(c.units), seen(0) {}
+      : plane(c.plane0), b(c.b0), at(c.at0), left(c.at[1] - c.at[0]), seen(0) {}
   __device__ __forceinline__ bool next(const V4Cut& c, int n_seq, Seg& s) {
     if (left <= 0) return false;
-    int total = c.tiles[b];
-    while (tile >= total) {   // the next stream with tiles
-      tile = 0;
+    int total = stream_units<kTile>(c.tiles[b]);
+    while (at >= total) {   // the next stream with tiles
+      at = 0;
       if (++b == n_seq) {
         b = 0;
         ++plane;
       }
-      total = c.tiles[b];
+      total = stream_units<kTile>(c.tiles[b]);
     }
+    const int n = min(left, total - at);   // past the lead: no boundary lies in one
+    s.kt0 = max(at - kLead<kTile>, 0);
+    s.n = at + n - kLead<kTile> - s.kt0;
+    s.whole = n == total;
     s.plane = plane;
     s.b = b;
-    s.kt0 = tile;
-    s.n = min(left, total - tile);
-    s.whole = s.n == total;
     // of a CTA's segments only the first and the last can be parts of a stream
     s.slot = 2 * (int)blockIdx.x + (seen ? 1 : 0);
     ++seen;
-    tile += s.n;
-    left -= s.n;
+    at += n;
+    left -= n;
     return true;
   }
 };

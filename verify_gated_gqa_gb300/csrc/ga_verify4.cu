@@ -9,8 +9,8 @@
 // Work. A stream is (sequence, KV head, query-row block): the 12 query heads of the group and
 // every window row when that makes at most 96 rows, else two blocks of 6 heads. A stream's
 // keys are tiles of 128. The streams' tiles, end to end, are cut into equal runs, one per CTA
-// (one CTA per SM), so any mix of lengths fills the device evenly: a CTA may end one stream
-// and begin another. The lengths are read on the device; every role of every CTA derives the
+// (one CTA per SM), so any mix of lengths fills the device evenly (a stream counts for a few tiles
+// more than it has, its fixed cost): a CTA may end one stream and begin another. The lengths are read on the device; every role of every CTA derives the
 // same cut from them. A stream that one CTA runs whole is written out by it; a stream cut
 // across CTAs leaves partial O, M, l per CTA (at most two per CTA: its first and its last
 // segment), merged by the combine kernel.
@@ -94,7 +94,7 @@ __device__ void raw_loader(V4Smem& sm, const CUtensorMap* tm_c, const CUtensorMa
   const int lane = threadIdx.x & 31;
   const long long n_rows = (long long)a.n_pages * kKvHeads * a.page_size;
   uint32_t f = 0;   // tiles issued
-  Walk walk(sm.cut);
+  Walk<kTileN> walk(sm.cut);
   Seg seg;
   while (walk.next(sm.cut, a.n_seq, seg)) {
     const int end = cut_len<kTileN>(sm.cut, seg.b, a.rows) + a.rows;
@@ -156,7 +156,7 @@ __device__ void widen_worker(V4Smem& sm, int is_v, volatile int* abort) {
   for (uint32_t j = 0; j < 4; ++j) at[j] = dst0 + ((j ^ xr) << 4);
   uint64_t* full = sm.full + 4 * is_v;
   uint64_t* empty = sm.empty + 4 * is_v;
-  const int n = sm.cut.units;
+  const int n = sm.cut.run_tiles();
   for (int g = 0; g < n; ++g) {
     const int st = kStages * is_v + g % kStages;
     if (!warp_wait(&sm.raw_full[st], (g / kStages) & 1, abort)) return;
@@ -202,7 +202,7 @@ __device__ void qk_issue(V4Smem& sm, const Verify4Args& a, uint32_t tmem, volati
   constexpr uint32_t kId = idesc_bf16(128, kTileN, false, false);
   const uint64_t k_desc = sdesc_sw128(smem_u32(sm.kt[0]), 16, 1024);
   const uint64_t q_desc = sdesc_sw128(smem_u32(sm.qhi[0]), 16, 1024);
-  Walk walk(sm.cut);
+  Walk<kTileN> walk(sm.cut);
   Seg seg;
   uint32_t g = 0, done = 0;
   while (walk.next(sm.cut, a.n_seq, seg)) {
@@ -234,7 +234,7 @@ __device__ void qk_issue(V4Smem& sm, const Verify4Args& a, uint32_t tmem, volati
 __device__ void pv_issue(V4Smem& sm, const Verify4Args& a, uint32_t tmem, volatile int* abort) {
   constexpr uint32_t kId = idesc_bf16(128, kDim, false, true);
   const uint64_t v_desc = sdesc_sw128(smem_u32(sm.vt[0]), kGranule * 128, 1024);
-  Walk walk(sm.cut);
+  Walk<kTileN> walk(sm.cut);
   Seg seg;
   uint32_t g = 0, done = 0;
   while (walk.next(sm.cut, a.n_seq, seg)) {
@@ -283,7 +283,7 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
     ++mxn;
     return ok;
   };
-  Walk walk(sm.cut);
+  Walk<kTileN> walk(sm.cut);
   Seg seg;
   while (walk.next(sm.cut, a.n_seq, seg)) {
     const int L = cut_len<kTileN>(sm.cut, seg.b, a.rows);
@@ -491,13 +491,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   if (warp < 4) {
+    const int tiles = sm.cut.run_tiles();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 0 && sm.cut.units > 0) {
+    if (warp == 0 && tiles > 0) {
       qk_issue(sm, a, tmem, abort);
       umma_commit_warp(&sm.drain_qk);
       mbar_wait_quiet(&sm.drain_qk, 0, 100000000LL);
     }
-    if (warp == 1 && sm.cut.units > 0) {
+    if (warp == 1 && tiles > 0) {
       pv_issue(sm, a, tmem, abort);
       umma_commit_warp(&sm.drain_pv);
       mbar_wait_quiet(&sm.drain_pv, 0, 100000000LL);
@@ -548,23 +549,28 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   const int b = stream % a.n_seq, plane = stream / a.n_seq;
   if (threadIdx.x < 2) sums[threadIdx.x] = 0;
   __syncthreads();
-  if (threadIdx.x < kV4MaxSeq) {   // all tiles, those before sequence b, and its own
+  const int lead = tile == kTileN ? kLead<kTileN> : kLead<32>;
+  if (threadIdx.x < kV4MaxSeq) {   // all units, those before sequence b, and its own
     const int i = threadIdx.x;
     bool refused;
     const int L = i < a.n_seq ? __ldg(a.seq_len + i) : -1;
     const int t = tile == kTileN ? seq_tiles<kTileN>(a, L, refused) : seq_tiles<32>(a, L, refused);
-    const int all = __reduce_add_sync(0xffffffffu, t), first = __reduce_add_sync(0xffffffffu, i < b ? t : 0);
+    const int u = t ? t + lead : 0;
+    const int all = __reduce_add_sync(0xffffffffu, u), first = __reduce_add_sync(0xffffffffu, i < b ? u : 0);
     if (lane == 0) {
       atomicAdd(&sums[0], all);
       atomicAdd(&sums[1], first);
     }
-    if (i == b) own = t;
+    if (i == b) own = u;
   }
   __syncthreads();
   const int blocks = row_blocks(a.rows), heads = kGroup / blocks, rows = heads * a.rows;
   const int share = v4_share(sums[0] * kKvHeads * blocks, ctas);
-  const int u0 = plane * sums[0] + sums[1], nt = own;
-  const int c0 = nt ? u0 / share : 0, n = nt ? (u0 + nt - 1) / share - c0 + 1 : 1;
+  // the stream's units are u0 .. u1 - 1, its first tile is CTA c0's, and boundaries cut it from u0 +
+  // uncut on
+  const int u0 = plane * sums[0] + sums[1], u1 = u0 + own;
+  const int c0 = own ? (min(u0 + (tile == kTileN ? uncut<kTileN>(share) : uncut<32>(share)), u1) - 1) / share : 0;
+  const int n = own ? (u1 - 1) / share - c0 + 1 : 1;
   grid_wait();   // in every block: the grid's end then stands for the attention kernel's too
   if (n == 1 || n > kMaxParts) return;   // unused, or one CTA ran the whole stream and wrote it
   // part i is of CTA c0 + i: its first segment unless the stream began inside the CTA's run
