@@ -307,6 +307,14 @@ __device__ void compute(D4Smem& sm, const Verify4Args& a, volatile int* abort) {
           lt += sm.m[w][hr] == -INFINITY ? 0.f : sm.l[w][hr] * exp2f(sm.m[w][hr] - mt);
         const float inv = 1.0f / lt;
         const size_t out_row = (size_t)seg.b * kHeads + seg.plane * kGroup + hr;
+        float gate[2][4];
+        if (seg.whole) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              gate[i][k] = lo_f(__ldg(a.qg + out_row * kQgStride + kDim + 32 * (4 * (lane & 1) + k) + 16 * i + (lane >> 1)));
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int p = 128 * i + 4 * lane;
@@ -320,12 +328,10 @@ __device__ void compute(D4Smem& sm, const Verify4Args& a, volatile int* abort) {
             x[3] += v.w;
           }
           if (seg.whole) {
-            const int d = 32 * (p & 7) + (p >> 3);
-            const uint16_t* gt = a.qg + out_row * kQgStride + kDim + d;
-            uint16_t* to = a.out + out_row * kDim + d;
+            uint16_t* to = a.out + out_row * kDim + 32 * (p & 7) + (p >> 3);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              to[32 * k] = (uint16_t)(pack_bf16x2(x[k] * inv * sigmoid_f(lo_f(__ldg(gt + 32 * k))), 0.f) & 0xFFFFu);
+              to[32 * k] = (uint16_t)(pack_bf16x2(x[k] * inv * sigmoid_f(gate[i][k]), 0.f) & 0xFFFFu);
           } else {
             *part_at(a.part_o, seg.slot, p / 4, hr) = make_float4(x[0], x[1], x[2], x[3]);
             if (p == 0)
