@@ -99,7 +99,7 @@ __device__ void loader(D4Smem& sm, const CUtensorMap* tm_kc, const CUtensorMap* 
       if (j >= seg.n) return;
       const int key0 = (seg.kt0 + j) * kKeys, e = key0 / a.page_size;
       page = __ldg(table + e);
-      at = seg.plane * a.page_size + key0 - e * a.page_size;
+      at = seg.head * a.page_size + key0 - e * a.page_size;
     };
     look_up(w);
     for (int j = w; j < seg.n; j += kWarps) {
@@ -138,7 +138,7 @@ __device__ void compute(D4Smem& sm, const Verify4Args& a, volatile int* abort) {
 #pragma unroll
     for (int i = 2 * warp; i < 2 * warp + 2; ++i) {
       const uint2* x = reinterpret_cast<const uint2*>(
-          a.q_prep + ((size_t)seg.b * kHeads + seg.plane * kGroup + g) * kDim + 64 * t + 4 * i);
+          a.q_prep + ((size_t)seg.b * kHeads + seg.head * kGroup + g) * kDim + 64 * t + 4 * i);
       const uint2 lo = __ldg(x);
       const uint2 hi = g < kGroup - 8 ? __ldg(x + 8 * kDim / 4) : make_uint2(0u, 0u);
       sm.q[i][lane] = make_uint4(lo.x, hi.x, lo.y, hi.y);
@@ -306,7 +306,7 @@ __device__ void compute(D4Smem& sm, const Verify4Args& a, volatile int* abort) {
         for (int w = 0; w < kWarps; ++w)
           lt += sm.m[w][hr] == -INFINITY ? 0.f : sm.l[w][hr] * exp2f(sm.m[w][hr] - mt);
         const float inv = 1.0f / lt;
-        const size_t out_row = (size_t)seg.b * kHeads + seg.plane * kGroup + hr;
+        const size_t out_row = (size_t)seg.b * kHeads + seg.head * kGroup + hr;
         float gate[2][4];
         if (seg.whole) {
 #pragma unroll
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_wait();
   grid_launch_dependents();
-  make_cut<kKeys>(a, sm.cut, kKvHeads, blockIdx.x == 0);   // two block barriers
+  make_cut<kKeys>(a, sm.cut, (int)gridDim.x, (int)blockIdx.x);   // two block barriers
   if (warp < kWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
     compute(sm, a, abort);

@@ -89,7 +89,10 @@ __device__ __forceinline__ int seq_tiles(const Verify4Args& a, int L, bool& refu
   refused = L >= 0 && (keys > (long long)a.max_pages * a.page_size || keys > GA_MAX_TOKENS);
   return L < 0 || refused ? 0 : (int)((keys + kTile - 1) / kTile);
 }
-// Query-row blocks of a (sequence, KV head): one while all heads' rows fit in kV4Lanes.
+// Query-row blocks of a (sequence, KV head), of 12 or 6 heads each: one while all heads' rows fit in
+// kV4Lanes. Two blocks go to two neighbouring CTAs, which run the same share of the tiles at the
+// same time (a worker is a CTA, or these two) and so read them from memory once: 8 x 16 rows over
+// 65,536 keys read 607 MB when the blocks were streams of their own.
 __host__ __device__ __forceinline__ int row_blocks(int rows) {
   return rows * kGroup > kV4Lanes ? 2 : 1;
 }
@@ -115,10 +118,10 @@ __device__ __forceinline__ int uncut(int share) {
   return kLead<kTile> + min(kFront<kTile>, share);
 }
 
-// A CTA's share of the streams' units: `left` units from unit `at` of stream (plane, b) on.
-// plane = 2 x row block + KV head; streams are ordered by plane, then sequence.
+// A worker's share of the streams' units: `left` units from unit `at` of stream (head, b) on.
+// Streams are ordered by KV head, then sequence.
 struct Seg {
-  int plane, b, kt0, n;   // tiles kt0 .. kt0 + n - 1 of the stream
+  int head, b, kt0, n;    // tiles kt0 .. kt0 + n - 1 of the stream
   bool whole;             // all of the stream's tiles
   int slot;               // partial slot of a segment that is not whole
 };
@@ -126,22 +129,22 @@ struct Seg {
 struct V4Cut {
   uint16_t tiles[kV4MaxSeq];   // key tiles of each sequence
   uint8_t spare[kV4MaxSeq];    // and what its keys lack of filling the last
-  int warp_units[kV4MaxSeq / 32], warp_streams[kV4MaxSeq / 32];   // of 32 sequences, one plane
-  int at[2], tiles_at[2];      // the CTA's run of units, and the tiles before its ends
-  int plane0, b0, at0;         // the stream that it begins in
+  int warp_units[kV4MaxSeq / 32], warp_streams[kV4MaxSeq / 32];   // of 32 sequences, one head
+  int at[2], tiles_at[2];      // the worker's run of units, and the tiles before its ends
+  int head0, b0, at0;          // the stream that it begins in
   __device__ __forceinline__ int run_tiles() const { return tiles_at[1] - tiles_at[0]; }
 };
-static_assert(4LL * kV4MaxSeq * (GA_MAX_TOKENS / 32 + kLead<32>) + (1 << 20) < (1LL << 31),
+static_assert((long long)kKvHeads * kV4MaxSeq * (GA_MAX_TOKENS / 32 + kLead<32>) + (1 << 20) < (1LL << 31),
               "unit counts of a launch fit in 32 bits");
-// Units per CTA of a cut of `total` units over `ctas` CTAs.
-__device__ __forceinline__ int v4_share(int total, int ctas) { return (total + ctas - 1) / ctas; }
+// Units per worker of a cut of `total` units.
+__device__ __forceinline__ int v4_share(int total, int workers) { return (total + workers - 1) / workers; }
 
-// The sequences' tiles and this CTA's part of the cut, by the whole block (at least kV4MaxSeq
-// threads, a sequence each): planes x the sequences' tiles, end to end. A refused length is
-// recorded by `report`. Short on purpose: this code runs once, from a cold instruction cache,
+// The sequences' tiles and the part of the cut of worker `me` of `workers`, by the whole block (at
+// least kV4MaxSeq threads, a sequence each): both heads' sequences, end to end. A refused length is
+// recorded by the first block. Short on purpose: this code runs once, from a cold instruction cache,
 // before anything can be loaded (a warp's search over the sequences took 2.5 us here).
 template <int kTile>
-__device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int planes, bool report) {
+__device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int workers, int me) {
   const int b = threadIdx.x, warp = b >> 5;
   int n = 0, sum = 0, streams = 0;   // units of sequence b's streams; those and the streams up to b
   if (b < kV4MaxSeq) {
@@ -149,7 +152,7 @@ __device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int pla
       const int L = __ldg(a.seq_len + b);
       bool refused;
       const int tiles = seq_tiles<kTile>(a, L, refused);
-      if (refused && report) record(a.status, kDevBadPosition);
+      if (refused && blockIdx.x == 0) record(a.status, kDevBadPosition);
       c.tiles[b] = (uint16_t)tiles;
       c.spare[b] = (uint8_t)(tiles * kTile - L - a.rows);
       n = stream_units<kTile>(tiles);
@@ -167,37 +170,37 @@ __device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int pla
     }
   }
   __syncthreads();
-  int per_plane = 0, all = 0, before = sum - n;
+  int per_head = 0, all = 0, before = sum - n;
   if (n) --streams;   // those before
 #pragma unroll
   for (int w = 0; w < kV4MaxSeq / 32; ++w) {
     const int x = c.warp_units[w], y = c.warp_streams[w];
-    per_plane += x;
+    per_head += x;
     all += y;
     if (w < warp) {
       before += x;
       streams += y;
     }
   }
-  const int total = per_plane * planes, share = v4_share(total, (int)gridDim.x);
+  const int total = per_head * kKvHeads, share = v4_share(total, workers);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int u = share * ((int)blockIdx.x + i);
+    const int u = share * (me + i);
     if (u >= total) {
       if (b == 0) {
         c.at[i] = total;
-        c.tiles_at[i] = total - kLead<kTile> * planes * all;
+        c.tiles_at[i] = total - kLead<kTile> * kKvHeads * all;
       }
       continue;
     }
-    const int plane = u / per_plane, rem = u - plane * per_plane;
+    const int head = u / per_head, rem = u - head * per_head;
     if (before <= rem && rem < before + n) {   // one sequence's thread (n is 0 past the last)
       const int rel = rem - before < uncut<kTile>(share) ? 0 : rem - before;
-      const int at = plane * per_plane + before + rel;
+      const int at = head * per_head + before + rel;
       c.at[i] = at;
-      c.tiles_at[i] = at - kLead<kTile> * (plane * all + streams) - min(rel, kLead<kTile>);
+      c.tiles_at[i] = at - kLead<kTile> * (head * all + streams) - min(rel, kLead<kTile>);
       if (i == 0) {
-        c.plane0 = plane;
+        c.head0 = head;
         c.b0 = b;
         c.at0 = rel;
       }
@@ -212,9 +215,9 @@ __device__ __forceinline__ int cut_len(const V4Cut& c, int b, int rows) {
 }
 template <int kTile>
 struct Walk {
-  int plane, b, at, left, seen;
+  int head, b, at, left, seen;
   __device__ __forceinline__ explicit Walk(const V4Cut& c)
-      : plane(c.plane0), b(c.b0), at(c.at0), left(c.at[1] - c.at[0]), seen(0) {}
+      : head(c.head0), b(c.b0), at(c.at0), left(c.at[1] - c.at[0]), seen(0) {}
   __device__ __forceinline__ bool next(const V4Cut& c, int n_seq, Seg& s) {
     if (left <= 0) return false;
     int total = stream_units<kTile>(c.tiles[b]);
@@ -222,7 +225,7 @@ struct Walk {
       at = 0;
       if (++b == n_seq) {
         b = 0;
-        ++plane;
+        ++head;
       }
       total = stream_units<kTile>(c.tiles[b]);
     }
@@ -230,9 +233,9 @@ struct Walk {
     s.kt0 = max(at - kLead<kTile>, 0);
     s.n = at + n - kLead<kTile> - s.kt0;
     s.whole = n == total;
-    s.plane = plane;
+    s.head = head;
     s.b = b;
-    // of a CTA's segments only the first and the last can be parts of a stream
+    // of a worker's segments only the first and the last can be parts of a stream
     s.slot = 2 * (int)blockIdx.x + (seen ? 1 : 0);
     ++seen;
     at += n;
@@ -265,9 +268,9 @@ __device__ __forceinline__ float4* part_at(float* part_o, int slot, int d4, int 
   return reinterpret_cast<float4*>(part_o) + ((size_t)slot * (kDim / 4) + d4) * kV4Lanes + row;
 }
 
-// The log-sum-exp merge of the streams that the cut left in parts, after either kernel with
-// tiles of `tile` keys (128 or 32).
-cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, int sm_count,
+// The log-sum-exp merge of the streams that the cut over `workers` left in parts, after either
+// kernel with tiles of `tile` keys (128 or 32).
+cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, int sm_count,
                                    cudaStream_t s);
 
 }  // namespace ga

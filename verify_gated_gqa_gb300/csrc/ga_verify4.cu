@@ -6,10 +6,10 @@
 // fp32; the weights e^(s - M) are rounded to bf16 for the tensor cores (and summed as rounded,
 // so their normalisation is consistent); the output is rounded once.
 //
-// Work. A stream is (sequence, KV head, query-row block): the 12 query heads of the group and
-// every window row when that makes at most 96 rows, else two blocks of 6 heads. A stream's
-// keys are tiles of 128. The streams' tiles, end to end, are cut into equal runs, one per CTA
-// (one CTA per SM), so any mix of lengths fills the device evenly (a stream counts for a few tiles
+// Work. A stream is (sequence, KV head), its keys in tiles of 128, its rows the window's rows of the
+// 12 query heads of the group: one block when that makes at most 96 rows, else two of 6 heads, for
+// two neighbouring CTAs. The streams' tiles, end to end, are cut into equal runs, one per CTA or two
+// such (one CTA per SM), so any mix of lengths fills the device evenly (a stream counts for a few tiles
 // more than it has, its fixed cost): a CTA may end one stream and begin another. The lengths are read on the device; every role of every CTA derives the
 // same cut from them. A stream that one CTA runs whole is written out by it; a stream cut
 // across CTAs leaves partial O, M, l per CTA (at most two per CTA: its first and its last
@@ -109,7 +109,7 @@ __device__ void raw_loader(V4Smem& sm, const CUtensorMap* tm_c, const CUtensorMa
         if (lane < 4) record(a.status, kDevBadPage);
         return (int)n_rows;
       }
-      return (int)(((long long)page * kKvHeads + (seg.plane & 1)) * a.page_size) + key0 - e * a.page_size;
+      return (int)(((long long)page * kKvHeads + seg.head) * a.page_size) + key0 - e * a.page_size;
     };
     int row = row_of(seg.kt0);
     for (int j = 0; j < seg.n; ++j, ++f) {
@@ -288,7 +288,7 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
   while (walk.next(sm.cut, a.n_seq, seg)) {
     const int L = cut_len<kTileN>(sm.cut, seg.b, a.rows);
     const int limit = L + min(rr, a.rows - 1);   // the row's last visible key
-    const int h = (seg.plane & 1) * kGroup + (seg.plane >> 1) * heads + hh;
+    const int h = seg.head * kGroup + (row_blocks(a.rows) == 2 ? heads * (int)(blockIdx.x & 1) : 0) + hh;
     const size_t row = (size_t)seg.b * a.rows + rr;
     {   // Q: dims 0..127 to tensor memory, 128..255 to shared memory. Both places are free: this
         // warp has seen the last S of the segment before, so its Q K^T are done.
@@ -487,7 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  make_cut<kTileN>(a, sm.cut, kKvHeads * row_blocks(a.rows), blockIdx.x == 0);   // two block barriers
+  {   // two block barriers
+    const int blocks = row_blocks(a.rows);
+    make_cut<kTileN>(a, sm.cut, (int)gridDim.x / blocks, (int)blockIdx.x / blocks);
+  }
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   if (warp < 4) {
@@ -533,12 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // shared memory. Thin slices when the streams are few (one sequence over 65,536 keys: two streams
 // of 76 parts), wide ones when they fill the device, where a stream has a few parts.
 constexpr int kCombineThreads = 384, kCombineWarps = kCombineThreads / 32;
-// A stream's parts are at most half the CTAs and two: there are two KV heads of the same tiles.
+// A stream's parts are at most half the workers and two: there are two KV heads of the same tiles.
 constexpr int kMaxParts = kV4MaxCtas / 2 + 2;
 constexpr int kDirectParts = 24;
 template <int kD4>
 __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
-    const __grid_constant__ Verify4Args a, int ctas, int tile) {
+    const __grid_constant__ Verify4Args a, int workers, int tile) {
   constexpr int kSlices = kDim / 4 / kD4;
   extern __shared__ float2 ml[];   // [parts][rows]: M, l, then the part's weight and l
   __shared__ int sums[2], own;
@@ -565,21 +568,22 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   }
   __syncthreads();
   const int blocks = row_blocks(a.rows), heads = kGroup / blocks, rows = heads * a.rows;
-  const int share = v4_share(sums[0] * kKvHeads * blocks, ctas);
-  // the stream's units are u0 .. u1 - 1, its first tile is CTA c0's, and boundaries cut it from u0 +
+  const int share = v4_share(sums[0] * kKvHeads, workers);
+  const int head = plane % kKvHeads, block = plane / kKvHeads;
+  // the stream's units are u0 .. u1 - 1, its first tile is worker c0's, and boundaries cut it from u0 +
   // uncut on
-  const int u0 = plane * sums[0] + sums[1], u1 = u0 + own;
+  const int u0 = head * sums[0] + sums[1], u1 = u0 + own;
   const int c0 = own ? (min(u0 + (tile == kTileN ? uncut<kTileN>(share) : uncut<32>(share)), u1) - 1) / share : 0;
   const int n = own ? (u1 - 1) / share - c0 + 1 : 1;
   grid_wait();   // in every block: the grid's end then stands for the attention kernel's too
   if (n == 1 || n > kMaxParts) return;   // unused, or one CTA ran the whole stream and wrote it
-  // part i is of CTA c0 + i: its first segment unless the stream began inside the CTA's run
+  // part i is of worker c0 + i: its first segment unless the stream began inside the worker's run
   const bool inside = c0 * share < u0;
-  auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 && inside ? 1 : 0); };
+  auto slot = [&](int i) { return 2 * (blocks * (c0 + i) + block) + (i == 0 && inside ? 1 : 0); };
   const int items = rows * kD4;
   // o (relative to the weights' scale s) times the gate, to the output
   auto finish = [&](int d4, int r, float4 o, float s) {
-    const int rr = r / heads, h = (plane & 1) * kGroup + (plane >> 1) * heads + r - rr * heads;
+    const int rr = r / heads, h = head * kGroup + block * heads + r - rr * heads;
     const size_t row = ((size_t)b * a.rows + rr) * kHeads + h;
     const int p = 4 * (slice * kD4 + d4);
     if (tile != kTileN) {   // place p + k is dim 32 (p % 8 + k) + p / 8
@@ -723,18 +727,18 @@ cudaError_t verify4_set_attributes() {
   return e != cudaSuccess ? e : decode4_set_attributes();
 }
 
-cudaError_t launch_verify4_combine(const Verify4Args& a, int ctas, int tile, int sm_count,
+cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, int sm_count,
                                    cudaStream_t s) {
   const int streams = a.n_seq * kKvHeads * row_blocks(a.rows);
   const bool few = streams * 2 < sm_count, very_few = streams * 16 < sm_count;
-  const int parts = ctas / 2 + 2;
+  const int parts = workers / 2 + 2;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = overlapped_launch(
       (unsigned)(streams * (very_few ? 64 : few ? 16 : 2)), kCombineThreads,
       (size_t)parts * (a.rows * kGroup / row_blocks(a.rows)) * sizeof(float2), s, attr);
-  if (very_few) return cudaLaunchKernelEx(&cfg, verify4_combine_kernel<1>, a, ctas, tile);
-  return few ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<4>, a, ctas, tile)
-             : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<32>, a, ctas, tile);
+  if (very_few) return cudaLaunchKernelEx(&cfg, verify4_combine_kernel<1>, a, workers, tile);
+  return few ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<4>, a, workers, tile)
+             : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<32>, a, workers, tile);
 }
 
 cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
@@ -743,9 +747,10 @@ cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_code
   const int ctas = sm_count < kV4MaxCtas ? sm_count : kV4MaxCtas;
   if (a.rows == 1) return launch_decode4(k_codes, v_codes, k_scales, v_scales, a, ctas, s);
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)ctas, kThreads, sizeof(V4Smem), s, attr);
+  const int blocks = row_blocks(a.rows), workers = ctas / blocks;
+  const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)(workers * blocks), kThreads, sizeof(V4Smem), s, attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, verify4_kernel, k_codes, v_codes, k_scales, v_scales, a);
-  return e != cudaSuccess ? e : launch_verify4_combine(a, ctas, kTileN, sm_count, s);
+  return e != cudaSuccess ? e : launch_verify4_combine(a, workers, kTileN, sm_count, s);
 }
 
 }  // namespace ga
