@@ -10,10 +10,10 @@
 // 12 query heads of the group: one block when that makes at most 96 rows, else two of 6 heads, for
 // two neighbouring CTAs. The streams' tiles, end to end, are cut into equal runs, one per CTA or two
 // such (one CTA per SM), so any mix of lengths fills the device evenly (a stream counts for a few tiles
-// more than it has, its fixed cost): a CTA may end one stream and begin another. The lengths are read on the device; every role of every CTA derives the
-// same cut from them. A stream that one CTA runs whole is written out by it; a stream cut
-// across CTAs leaves partial O, M, l per CTA (at most two per CTA: its first and its last
-// segment), merged by the combine kernel.
+// more than it has, its fixed cost): a CTA may end one stream and begin another. The lengths are
+// read on the device; every role of every CTA derives the same cut from them. A stream that one CTA
+// runs whole is written out by it; a stream cut across CTAs leaves partial O, M, l per CTA (at most
+// two per CTA: its first and its last segment), merged by the combine kernel.
 //
 // Structure (896 threads, 28 warps):
 //   warp 0      issues S = Q K^T (tcgen05, M=128, N=128, K=256; Q dims 0..127 in tensor
