@@ -398,7 +398,7 @@ cudaError_t launch_decode4(const CUtensorMap& k_codes, const CUtensorMap& v_code
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)ctas, kThreads, sizeof(D4Smem), s, attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, decode4_kernel, k_codes, v_codes, k_scales, v_scales, a);
-  return e != cudaSuccess ? e : launch_verify4_combine(a, ctas, kKeys, ctas, s);
+  return e != cudaSuccess ? e : launch_verify4_combine(a, ctas, kKeys, s);
 }
 
 }  // namespace ga

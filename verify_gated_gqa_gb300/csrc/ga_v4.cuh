@@ -139,66 +139,79 @@ static_assert((long long)kKvHeads * kV4MaxSeq * (GA_MAX_TOKENS / 32 + kLead<32>)
 // Units per worker of a cut of `total` units.
 __device__ __forceinline__ int v4_share(int total, int workers) { return (total + workers - 1) / workers; }
 
-// The sequences' tiles and the part of the cut of worker `me` of `workers`, by the whole block (at
-// least kV4MaxSeq threads, a sequence each): both heads' sequences, end to end. A refused length is
-// recorded by the first block. Short on purpose: this code runs once, from a cold instruction cache,
-// before anything can be loaded (a warp's search over the sequences took 2.5 us here).
+// The units of sequence threadIdx.x's streams, and sums over the sequences, for one KV head.
+struct Units {
+  int n, before, per_head;    // its units, those of the sequences before it, all
+  int streams, all_streams;   // streams before it, all
+};
+// By a whole block of at least kV4MaxSeq threads, a sequence each (`tiles` is 0 past the last); one
+// block barrier. Short on purpose: this code runs once, from a cold instruction cache, before
+// anything can be loaded (a warp's search over the sequences took 2.5 us here).
 template <int kTile>
-__device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int workers, int me) {
-  const int b = threadIdx.x, warp = b >> 5;
-  int n = 0, sum = 0, streams = 0;   // units of sequence b's streams; those and the streams up to b
-  if (b < kV4MaxSeq) {
-    if (b < a.n_seq) {
-      const int L = __ldg(a.seq_len + b);
-      bool refused;
-      const int tiles = seq_tiles<kTile>(a, L, refused);
-      if (refused && blockIdx.x == 0) record(a.status, kDevBadPosition);
-      c.tiles[b] = (uint16_t)tiles;
-      c.spare[b] = (uint8_t)(tiles * kTile - L - a.rows);
-      n = stream_units<kTile>(tiles);
-    }
-    sum = n;
+__device__ __forceinline__ Units scan_units(int tiles, int (&warp_units)[kV4MaxSeq / 32],
+                                            int (&warp_streams)[kV4MaxSeq / 32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = stream_units<kTile>(tiles);
+  int sum = n, streams = 0;
+  if (threadIdx.x < kV4MaxSeq) {
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, sum, off);
-      if ((b & 31) >= off) sum += o;
+      if (lane >= off) sum += o;
     }
-    streams = __popc(__ballot_sync(0xffffffffu, n > 0) & (0xffffffffu >> (31 - (b & 31))));
-    if ((b & 31) == 31) {
-      c.warp_units[warp] = sum;
-      c.warp_streams[warp] = streams;
+    streams = __popc(__ballot_sync(0xffffffffu, n > 0) & (0xffffffffu >> (31 - lane)));
+    if (lane == 31) {
+      warp_units[warp] = sum;
+      warp_streams[warp] = streams;
     }
   }
   __syncthreads();
-  int per_head = 0, all = 0, before = sum - n;
-  if (n) --streams;   // those before
+  Units u = {n, sum - n, 0, n ? streams - 1 : streams, 0};
 #pragma unroll
   for (int w = 0; w < kV4MaxSeq / 32; ++w) {
-    const int x = c.warp_units[w], y = c.warp_streams[w];
-    per_head += x;
-    all += y;
+    const int x = warp_units[w], y = warp_streams[w];
+    u.per_head += x;
+    u.all_streams += y;
     if (w < warp) {
-      before += x;
-      streams += y;
+      u.before += x;
+      u.streams += y;
     }
   }
-  const int total = per_head * kKvHeads, share = v4_share(total, workers);
+  return u;
+}
+
+// The sequences' tiles and the part of the cut of worker `me` of `workers`: both heads' sequences,
+// end to end. A refused length is recorded by the first block. Two block barriers.
+template <int kTile>
+__device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int workers, int me) {
+  const int b = threadIdx.x;
+  int tiles = 0;
+  if (b < kV4MaxSeq && b < a.n_seq) {
+    const int L = __ldg(a.seq_len + b);
+    bool refused;
+    tiles = seq_tiles<kTile>(a, L, refused);
+    if (refused && blockIdx.x == 0) record(a.status, kDevBadPosition);
+    c.tiles[b] = (uint16_t)tiles;
+    c.spare[b] = (uint8_t)(tiles * kTile - L - a.rows);
+  }
+  const Units q = scan_units<kTile>(tiles, c.warp_units, c.warp_streams);
+  const int total = q.per_head * kKvHeads, share = v4_share(total, workers);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int u = share * (me + i);
     if (u >= total) {
       if (b == 0) {
         c.at[i] = total;
-        c.tiles_at[i] = total - kLead<kTile> * kKvHeads * all;
+        c.tiles_at[i] = total - kLead<kTile> * kKvHeads * q.all_streams;
       }
       continue;
     }
-    const int head = u / per_head, rem = u - head * per_head;
-    if (before <= rem && rem < before + n) {   // one sequence's thread (n is 0 past the last)
-      const int rel = rem - before < uncut<kTile>(share) ? 0 : rem - before;
-      const int at = head * per_head + before + rel;
+    const int head = u / q.per_head, rem = u - head * q.per_head - q.before;
+    if (0 <= rem && rem < q.n) {   // one sequence's thread (n is 0 past the last)
+      const int rel = rem < uncut<kTile>(share) ? 0 : rem;
+      const int at = head * q.per_head + q.before + rel;
       c.at[i] = at;
-      c.tiles_at[i] = at - kLead<kTile> * (head * all + streams) - min(rel, kLead<kTile>);
+      c.tiles_at[i] = at - kLead<kTile> * (head * q.all_streams + q.streams) - min(rel, kLead<kTile>);
       if (i == 0) {
         c.head0 = head;
         c.b0 = b;
@@ -270,7 +283,6 @@ __device__ __forceinline__ float4* part_at(float* part_o, int slot, int d4, int 
 
 // The log-sum-exp merge of the streams that the cut over `workers` left in parts, after either
 // kernel with tiles of `tile` keys (128 or 32).
-cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, int sm_count,
-                                   cudaStream_t s);
+cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, cudaStream_t s);
 
 }  // namespace ga

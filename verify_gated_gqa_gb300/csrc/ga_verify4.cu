@@ -527,184 +527,143 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ combine
 // The streams that the cut left in parts: o = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i over a
-// stream's parts, times the gate. A block takes a slice of 4 kD4 dims of every query row of a
-// stream, a thread a float4 of a row, neighbouring threads neighbouring rows (as the parts lie). Up
-// to kDirectParts parts a thread loads the M, l and float4 of eight parts at a time and merges
-// them as they come, a trip to L2 for eight. More parts: all (M, l) into shared memory, a warp per
-// row turns them into weights, and the float4s come eight parts at a time; when a slice has fewer
-// float4s than the block has threads, the parts are dealt to several groups of threads, joined in
-// shared memory. Thin slices when the streams are few (one sequence over 65,536 keys: two streams
-// of 76 parts), wide ones when they fill the device, where a stream has a few parts.
-constexpr int kCombineThreads = 384, kCombineWarps = kCombineThreads / 32;
-// A stream's parts are at most half the workers and two: there are two KV heads of the same tiles.
-constexpr int kMaxParts = kV4MaxCtas / 2 + 2;
-constexpr int kDirectParts = 24;
-template <int kD4>
+// stream's parts, times the gate.
+//
+// A stream's items are (row, four dims), rows innermost, as the parts lie; a block takes an equal
+// share of them. With few streams each has `slices` blocks, about twice the device's CTAs in all (32
+// sequences of up to 4,096 keys, one row: a whole call of 22 us; with twice the blocks 25). With many
+// (slices 0), most of them whole or of two parts, blocks go by the boundaries that cut streams, n - 1
+// to a stream of n parts, kSplit to each, so that one long stream among many short ones is not left to
+// few blocks (5 rows of one sequence of 65,536 keys and 63 of 200: 34 us, by streams 76). A thread merges eight parts of an item at
+// a time, as they come; where a share has fewer items than the block has threads, a stream of more
+// than eight parts is dealt to groups of threads, merged through shared memory. (With all (M, l)
+// turned into weights in shared memory first, 76 parts of 96 rows took 28 us.)
+constexpr int kCombineThreads = 384, kSplit = 2;
+static_assert(kCombineThreads >= kV4MaxSeq, "a sequence a thread");
+template <int kTile>
 __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
-    const __grid_constant__ Verify4Args a, int workers, int tile) {
-  constexpr int kSlices = kDim / 4 / kD4;
-  extern __shared__ float2 ml[];   // [parts][rows]: M, l, then the part's weight and l
-  __shared__ int sums[2], own;
-  __shared__ float4 join[kCombineThreads];
-  __shared__ float inv[kV4Lanes];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int slice = blockIdx.x % kSlices, stream = blockIdx.x / kSlices;
-  const int b = stream % a.n_seq, plane = stream / a.n_seq;
-  if (threadIdx.x < 2) sums[threadIdx.x] = 0;
-  __syncthreads();
-  const int lead = tile == kTileN ? kLead<kTileN> : kLead<32>;
-  if (threadIdx.x < kV4MaxSeq) {   // all units, those before sequence b, and its own
-    const int i = threadIdx.x;
+    const __grid_constant__ Verify4Args a, int workers, int slices) {
+  __shared__ int warp_units[kV4MaxSeq / 32], warp_streams[kV4MaxSeq / 32];
+  __shared__ int cut_b, cut_head, cut_u0, cut_n;
+  __shared__ float4 join_o[kCombineThreads];
+  __shared__ float2 join_ml[kCombineThreads];
+  const int tid = threadIdx.x;
+  const int blocks = row_blocks(a.rows), heads = kGroup / blocks, rows = heads * a.rows;
+  // block `at` of a stream's `of`, or of a boundary's; the stream, or the boundary's first worker
+  const int of = slices ? slices : kSplit, at = blockIdx.x % of, rest = blockIdx.x / of;
+  const int block = slices ? rest / (kKvHeads * a.n_seq) : rest % blocks, w = rest / blocks;
+  int tiles = 0;
+  if (tid < a.n_seq) {
     bool refused;
-    const int L = i < a.n_seq ? __ldg(a.seq_len + i) : -1;
-    const int t = tile == kTileN ? seq_tiles<kTileN>(a, L, refused) : seq_tiles<32>(a, L, refused);
-    const int u = t ? t + lead : 0;
-    const int all = __reduce_add_sync(0xffffffffu, u), first = __reduce_add_sync(0xffffffffu, i < b ? u : 0);
-    if (lane == 0) {
-      atomicAdd(&sums[0], all);
-      atomicAdd(&sums[1], first);
+    tiles = seq_tiles<kTile>(a, __ldg(a.seq_len + tid), refused);
+  }
+  if (tid == 0) cut_n = 0;
+  const Units q = scan_units<kTile>(tiles, warp_units, warp_streams);
+  const int total = q.per_head * kKvHeads, share = v4_share(total, workers);
+  if (slices) {
+    if (tid == rest % a.n_seq) {
+      cut_b = tid;
+      cut_head = rest / a.n_seq % kKvHeads;
+      cut_u0 = cut_head * q.per_head + q.before;
+      cut_n = q.n;
     }
-    if (i == b) own = u;
+  } else if (const int u = share * (w + 1); u < total) {   // the stream that the boundary cuts, if any
+    const int head = u / q.per_head, rem = u - head * q.per_head - q.before;
+    if (uncut<kTile>(share) <= rem && rem < q.n) {
+      cut_b = tid;
+      cut_head = head;
+      cut_u0 = u - rem;
+      cut_n = q.n;
+    }
   }
   __syncthreads();
-  const int blocks = row_blocks(a.rows), heads = kGroup / blocks, rows = heads * a.rows;
-  const int share = v4_share(sums[0] * kKvHeads, workers);
-  const int head = plane % kKvHeads, block = plane / kKvHeads;
-  // the stream's units are u0 .. u1 - 1, its first tile is worker c0's, and boundaries cut it from u0 +
-  // uncut on
-  const int u0 = head * sums[0] + sums[1], u1 = u0 + own;
-  const int c0 = own ? (min(u0 + (tile == kTileN ? uncut<kTileN>(share) : uncut<32>(share)), u1) - 1) / share : 0;
-  const int n = own ? (u1 - 1) / share - c0 + 1 : 1;
   grid_wait();   // in every block: the grid's end then stands for the attention kernel's too
-  if (n == 1 || n > kMaxParts) return;   // unused, or one CTA ran the whole stream and wrote it
+  if (cut_n == 0) return;   // none, or unused
+  // its parts: worker c0 has its first tile; boundaries cut it from u0 + uncut on
+  const int b = cut_b, head = cut_head, u0 = cut_u0, u1 = u0 + cut_n;
+  const int c0 = (min(u0 + uncut<kTile>(share), u1) - 1) / share;
+  const int n = (u1 - 1) / share - c0 + 1;
   // part i is of worker c0 + i: its first segment unless the stream began inside the worker's run
   const bool inside = c0 * share < u0;
   auto slot = [&](int i) { return 2 * (blocks * (c0 + i) + block) + (i == 0 && inside ? 1 : 0); };
-  const int items = rows * kD4;
-  // o (relative to the weights' scale s) times the gate, to the output
-  auto finish = [&](int d4, int r, float4 o, float s) {
-    const int rr = r / heads, h = head * kGroup + block * heads + r - rr * heads;
+  if (n == 1) return;   // one CTA ran the whole stream and wrote it
+  // this block's items
+  const long long items = rows * (kDim / 4);
+  const int shares = slices ? of : of * (n - 1), share_at = slices ? at : of * (w - c0) + at;
+  const int lo = (int)(items * share_at / shares), hi = (int)(items * (share_at + 1) / shares);
+  const int count = hi - lo;
+  if (count == 0) return;
+  const int groups = max(1, min((n + 7) / 8, kCombineThreads / count));
+  const int group = groups > 1 ? tid / count : 0;   // (from `groups` on: idle)
+  for (int item = lo + tid - group * count; item < hi; item += kCombineThreads) {
+    const int d4 = item / rows, r = item - d4 * rows;
+    float M = -INFINITY, L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto scale = [&](float top) {   // to a new maximum
+      const float f = M == -INFINITY ? 0.f : exp2f(M - top);
+      M = top;
+      L *= f;
+      o.x *= f;
+      o.y *= f;
+      o.z *= f;
+      o.w *= f;
+    };
+    auto add = [&](float2 x, float4 v) {
+      if (x.x == -INFINITY) return;   // no such part, or no key of it is visible
+      const float f = exp2f(x.x - M);
+      L = fmaf(f, x.y, L);
+      o.x = fmaf(f, v.x, o.x);
+      o.y = fmaf(f, v.y, o.y);
+      o.z = fmaf(f, v.z, o.z);
+      o.w = fmaf(f, v.w, o.w);
+    };
+    for (int i0 = group < groups ? group : n; i0 < n; i0 += 8 * groups) {
+      float2 x[8];
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * groups;
+        x[k] = make_float2(-INFINITY, 0.f);
+        if (i < n) {
+          x[k] = reinterpret_cast<const float2*>(a.part_ml)[(size_t)slot(i) * kV4Lanes + r];
+          v[k] = *part_at(a.part_o, slot(i), d4, r);
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k].x);
+      scale(top);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add(x[k], v[k]);
+    }
+    if (groups > 1) {   // every thread has one item: the loop runs once
+      join_ml[tid] = make_float2(L != L ? L : M, L);
+      join_o[tid] = o;
+      __syncthreads();
+      if (group > 0) return;
+      float top = M;
+      for (int k = 1; k < groups; ++k) top = fmaxf(top, join_ml[k * count + tid].x);
+      scale(top);
+      for (int k = 1; k < groups; ++k) add(join_ml[k * count + tid], join_o[k * count + tid]);
+    }
+    // times the gate, to the output
+    const float inv = 1.0f / L;
+    const int rr = r / heads, h = head * kGroup + block * heads + r - rr * heads, p = 4 * d4;
     const size_t row = ((size_t)b * a.rows + rr) * kHeads + h;
-    const int p = 4 * (slice * kD4 + d4);
-    if (tile != kTileN) {   // place p + k is dim 32 (p % 8 + k) + p / 8
+    const uint16_t* gates = a.qg + row * kQgStride + kDim;
+    uint16_t* out = a.out + row * kDim;
+    if (kTile != kTileN) {   // place p + k is dim 32 (p % 8 + k) + p / 8
       const int d = 32 * (p & 7) + (p >> 3);
-      const uint16_t* g = a.qg + row * kQgStride + kDim + d;
-      uint16_t* to = a.out + row * kDim + d;
       const float x[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        to[32 * k] = (uint16_t)(pack_bf16x2(x[k] * s * sigmoid_f(lo_f(__ldg(g + 32 * k))), 0.f) & 0xFFFFu);
-      return;
+        out[d + 32 * k] = (uint16_t)(pack_bf16x2(x[k] * inv * sigmoid_f(lo_f(__ldg(gates + d + 32 * k))), 0.f) & 0xFFFFu);
+    } else {
+      const uint2 g = __ldg(reinterpret_cast<const uint2*>(gates + p));
+      *reinterpret_cast<uint2*>(out + p) =
+          make_uint2(pack_bf16x2(o.x * inv * sigmoid_f(lo_f(g.x)), o.y * inv * sigmoid_f(hi_f(g.x))),
+                     pack_bf16x2(o.z * inv * sigmoid_f(lo_f(g.y)), o.w * inv * sigmoid_f(hi_f(g.y))));
     }
-    const int d = p;
-    const uint2 g = __ldg(reinterpret_cast<const uint2*>(a.qg + row * kQgStride + kDim + d));
-    *reinterpret_cast<uint2*>(a.out + row * kDim + d) =
-        make_uint2(pack_bf16x2(o.x * s * sigmoid_f(lo_f(g.x)), o.y * s * sigmoid_f(hi_f(g.x))),
-                   pack_bf16x2(o.z * s * sigmoid_f(lo_f(g.y)), o.w * s * sigmoid_f(hi_f(g.y))));
-  };
-  if (n <= kDirectParts) {
-    for (int item = threadIdx.x; item < items; item += kCombineThreads) {
-      const int d4 = item / rows, r = item - d4 * rows;
-      float M = -INFINITY, L = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i0 = 0; i0 < n; i0 += 8) {
-        float2 x[8];
-        float4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int i = i0 + k;
-          x[k] = make_float2(-INFINITY, 0.f);
-          if (i < n) {
-            x[k] = reinterpret_cast<const float2*>(a.part_ml)[(size_t)slot(i) * kV4Lanes + r];
-            v[k] = *part_at(a.part_o, slot(i), slice * kD4 + d4, r);
-          }
-        }
-        float top = M;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k].x);
-        const float f0 = M == -INFINITY ? 0.f : exp2f(M - top);
-        M = top;
-        L *= f0;
-        o.x *= f0;
-        o.y *= f0;
-        o.z *= f0;
-        o.w *= f0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (x[k].x == -INFINITY) continue;   // no such part, or no key of it is visible
-          const float f = exp2f(x[k].x - M);
-          L = fmaf(f, x[k].y, L);
-          o.x = fmaf(f, v[k].x, o.x);
-          o.y = fmaf(f, v[k].y, o.y);
-          o.z = fmaf(f, v[k].z, o.z);
-          o.w = fmaf(f, v[k].w, o.w);
-        }
-      }
-      finish(d4, r, o, 1.0f / L);
-    }
-    return;
-  }
-  for (int k = threadIdx.x; k < n * rows; k += kCombineThreads) {
-    const int i = k / rows;
-    ml[k] = reinterpret_cast<const float2*>(a.part_ml)[(size_t)slot(i) * kV4Lanes + (k - i * rows)];
-  }
-  __syncthreads();
-  for (int r = warp; r < rows; r += kCombineWarps) {
-    float M = -INFINITY, L = 0.f;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[i * rows + r].x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    for (int i = lane; i < n; i += 32) {
-      const float2 x = ml[i * rows + r];
-      const float f = x.x == -INFINITY ? 0.f : exp2f(x.x - M);   // no visible key in the part: none
-      L = fmaf(f, x.y, L);
-      ml[i * rows + r].x = f;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    if (lane == 0) inv[r] = 1.0f / L;
-  }
-  __syncthreads();
-  const int groups = items < kCombineThreads ? kCombineThreads / items : 1;
-  const int group = items < kCombineThreads ? threadIdx.x / items : 0;
-  const int first = items < kCombineThreads ? threadIdx.x - group * items : threadIdx.x;
-  if (groups == 1 && group > 0) return;   // threads past the items (no barrier follows)
-  for (int item = first; item < items; item += kCombineThreads) {
-    const int d4 = item / rows, r = item - d4 * rows;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (group < groups) {
-      for (int i0 = group; i0 < n; i0 += 8 * groups) {
-        float4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int i = i0 + k * groups;
-          if (i < n) v[k] = *part_at(a.part_o, slot(i), slice * kD4 + d4, r);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int i = i0 + k * groups;
-          if (i >= n) continue;
-          const float f = ml[i * rows + r].x;
-          o.x = fmaf(f, v[k].x, o.x);
-          o.y = fmaf(f, v[k].y, o.y);
-          o.z = fmaf(f, v[k].z, o.z);
-          o.w = fmaf(f, v[k].w, o.w);
-        }
-      }
-    }
-    if (groups > 1) {   // items < threads: this loop runs once
-      join[threadIdx.x] = o;
-      __syncthreads();
-      if (group != 0) return;
-      for (int k = 1; k < groups; ++k) {
-        const float4 x = join[k * items + item];
-        o.x += x.x;
-        o.y += x.y;
-        o.z += x.z;
-        o.w += x.w;
-      }
-    }
-    finish(d4, r, o, inv[r]);
   }
 }
 
@@ -715,30 +674,19 @@ size_t verify4_ws_bytes() {
 }
 
 cudaError_t verify4_set_attributes() {
-  const int ml_bytes = kMaxParts * kV4Lanes * (int)sizeof(float2);
-  cudaError_t e = cudaFuncSetAttribute(verify4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(V4Smem));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(verify4_combine_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, ml_bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(verify4_combine_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, ml_bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(verify4_combine_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, ml_bytes);
+  const cudaError_t e = cudaFuncSetAttribute(verify4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)sizeof(V4Smem));
   return e != cudaSuccess ? e : decode4_set_attributes();
 }
 
-cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, int sm_count,
-                                   cudaStream_t s) {
-  const int streams = a.n_seq * kKvHeads * row_blocks(a.rows);
-  const bool few = streams * 2 < sm_count, very_few = streams * 16 < sm_count;
-  const int parts = workers / 2 + 2;
+cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, cudaStream_t s) {
+  const int blocks = row_blocks(a.rows), streams = a.n_seq * kKvHeads * blocks;
+  const int ctas = workers * blocks, slices = streams * 2 >= ctas ? 0 : 2 * ctas / streams < 64 ? 2 * ctas / streams : 64;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = overlapped_launch(
-      (unsigned)(streams * (very_few ? 64 : few ? 16 : 2)), kCombineThreads,
-      (size_t)parts * (a.rows * kGroup / row_blocks(a.rows)) * sizeof(float2), s, attr);
-  if (very_few) return cudaLaunchKernelEx(&cfg, verify4_combine_kernel<1>, a, workers, tile);
-  return few ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<4>, a, workers, tile)
-             : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<32>, a, workers, tile);
+      (unsigned)(slices ? streams * slices : (workers - 1) * blocks * kSplit), kCombineThreads, 0, s, attr);
+  return tile == kTileN ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<kTileN>, a, workers, slices)
+                        : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<32>, a, workers, slices);
 }
 
 cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
@@ -750,7 +698,7 @@ cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_code
   const int blocks = row_blocks(a.rows), workers = ctas / blocks;
   const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)(workers * blocks), kThreads, sizeof(V4Smem), s, attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, verify4_kernel, k_codes, v_codes, k_scales, v_scales, a);
-  return e != cudaSuccess ? e : launch_verify4_combine(a, workers, kTileN, sm_count, s);
+  return e != cudaSuccess ? e : launch_verify4_combine(a, workers, kTileN, s);
 }
 
 }  // namespace ga
