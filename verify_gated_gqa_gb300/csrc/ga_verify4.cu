@@ -103,30 +103,33 @@ __device__ void raw_loader(V4Smem& sm, const CUtensorMap* tm_c, const CUtensorMa
   while (walk.next(sm.cut, a.n_seq, seg)) {
     const int end = cut_len<kTileN>(sm.cut, seg.b, a.rows) + a.rows;
     const int* table = a.page_table + (size_t)seg.b * a.max_pages;
-    // the pool row of this lane's granule of tile kt
-    auto row_of = [&](int kt) -> int {
+    // this lane's granule of a tile, looked up a tile ahead (its page is in flight meanwhile)
+    int page = 0, at = 0;
+    bool in = false;
+    auto look_up = [&](int kt) {
       const int key0 = kt * kTileN + kGranule * (lane & 3);
-      if (key0 >= end) return (int)n_rows;
+      in = key0 < end;
+      if (!in) return;
       const int e = key0 / a.page_size;
-      const int page = __ldg(table + e);
-      if (page < 0 || page >= a.n_pages) {
-        if (lane < 4) record(a.status, kDevBadPage);
-        return (int)n_rows;
-      }
-      return (int)(((long long)page * kKvHeads + seg.head) * a.page_size) + key0 - e * a.page_size;
+      page = __ldg(table + e);
+      at = seg.head * a.page_size + key0 - e * a.page_size;
     };
-    int row = row_of(seg.kt0);
+    look_up(seg.kt0);
     for (int j = 0; j < seg.n; ++j, ++f) {
-      const int here = row;
-      if (j + 1 < seg.n) row = row_of(seg.kt0 + j + 1);   // in flight during the wait
+      int row = (int)n_rows;
+      if (in) {
+        if (page >= 0 && page < a.n_pages) row = page * kKvHeads * a.page_size + at;
+        else if (lane < 4) record(a.status, kDevBadPage);
+      }
       const int st = kStages * is_v + (int)(f % kStages);
       if (!warp_wait(&sm.raw_empty[st], ((f / kStages) & 1) ^ 1, abort)) break;
       if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[st], kRawBytes + kRawScaleBytes);
       __syncwarp();
       if (lane < 4) {
-        tma_load_2d(sm.raw[st] + lane * (kGranule * kQ4RowBytes), tm_c, &sm.raw_full[st], 0, here);
-        tma_load_2d(sm.rsc[st] + lane * (kGranule * kQ4ScaleBytes), tm_s, &sm.raw_full[st], 0, here);
+        tma_load_2d(sm.raw[st] + lane * (kGranule * kQ4RowBytes), tm_c, &sm.raw_full[st], 0, row);
+        tma_load_2d(sm.rsc[st] + lane * (kGranule * kQ4ScaleBytes), tm_s, &sm.raw_full[st], 0, row);
       }
+      if (j + 1 < seg.n) look_up(seg.kt0 + j + 1);
     }
     if (*abort) break;
   }
@@ -297,23 +300,21 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
     {   // Q: dims 0..127 to tensor memory, 128..255 to shared memory. Both places are free: this
         // warp has seen the last S of the segment before, so its Q K^T are done.
       const uint4* qp = reinterpret_cast<const uint4*>(a.q_prep + (row * kHeads + h) * kDim) + 16 * hf;
+      uint32_t x[64];   // all of it in flight at once
 #pragma unroll
-      for (int c0 = 0; c0 < 16; c0 += 8) {
-        uint32_t x[32];
+      for (int i = 0; i < 16; ++i) {
+        const uint4 t = valid ? __ldg(qp + i) : make_uint4(0u, 0u, 0u, 0u);
+        x[4 * i] = t.x; x[4 * i + 1] = t.y; x[4 * i + 2] = t.z; x[4 * i + 3] = t.w;
+      }
+      if (hf == 0) {
+        tc_fence_after();
+        tmem_st32(tmem + kTmemQ + lane_off, *reinterpret_cast<uint32_t(*)[32]>(x));
+        tmem_st32(tmem + kTmemQ + lane_off + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 t = valid ? __ldg(qp + c0 + i) : make_uint4(0u, 0u, 0u, 0u);
-          x[4 * i] = t.x; x[4 * i + 1] = t.y; x[4 * i + 2] = t.z; x[4 * i + 3] = t.w;
-        }
-        if (hf == 0) {
-          tc_fence_after();
-          tmem_st32(tmem + kTmemQ + lane_off + 4 * c0, x);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(sm.qhi[c0 >> 3] + sw128_offset((uint32_t)r, (uint32_t)i)) =
-                make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        }
+        for (int i = 0; i < 16; ++i)
+          *reinterpret_cast<uint4*>(sm.qhi[i >> 3] + sw128_offset((uint32_t)r, (uint32_t)(i & 7))) =
+              make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
       }
       if (hf == 0) {
         tmem_wait_st();
