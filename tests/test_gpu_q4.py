@@ -547,6 +547,50 @@ def test_attention_calls_at_once(rows):
         assert all(torch.equal(x, want[i]) for x in got[i])
 
 
+@pytest.mark.parametrize("rows", [1, 5, 16])
+@pytest.mark.parametrize("graph", [False, True])
+def test_attention_calls_in_a_row_see_fresh_data(rows, graph):
+    """Calls whose blocks are placed while the kernel before them ends: of two batches in turn over
+    one workspace, and with queries, rows, pages and lengths written just before each call."""
+    a, b = Cache([9000, 30], rows, 32, SEED + 94), Cache([7000, 900, 4000], rows, 64, SEED + 95)
+    want = [a.run(), b.run()]
+    ws = torch.empty(B.ga_verify_q4_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    got = [[torch.empty_like(w) for w in want] for _ in range(6)]
+    live = []
+    for c in (a, b):
+        bufs = [c.q, c.qg, *c.pools, _i32(c.table), _i32(c.lens)]
+        empty = [torch.zeros_like(x) for x in bufs]
+        empty[-1].fill_(5)
+        live.append((bufs, empty, [torch.empty_like(x) for x in bufs]))
+
+    def body():
+        for k in range(6):
+            for i, (bufs, empty, use) in enumerate(live):
+                if k % 2:           # other contents first, then the call's own
+                    for src in (empty, bufs):
+                        for to, x in zip(use, src):
+                            to.copy_(x)
+                        B.ga_attn_verify_q4(*use, out=got[k][i], workspace=ws)
+                else:
+                    B.ga_attn_verify_q4(*bufs, out=got[k][i], workspace=ws)
+
+    body()
+    if graph:
+        torch.cuda.synchronize()
+        for pair in got:
+            for x in pair:
+                x.zero_()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            body()
+        for _ in range(3):
+            g.replay()
+    torch.cuda.synchronize()
+    for pair in got:
+        for x, w in zip(pair, want):
+            assert torch.equal(x, w)
+
+
 @pytest.mark.parametrize("rows", [1, 4])
 def test_captured_step_follows_its_lengths(rows):
     """One captured graph, replayed as the device lengths change."""

@@ -99,7 +99,7 @@ __device__ void loader(D4Smem& sm, const CUtensorMap* tm_kc, const CUtensorMap* 
     auto look_up = [&](int j) {
       if (j >= seg.n) return;
       const int key0 = (seg.kt0 + j) * kKeys, e = key0 / a.page_size;
-      page = __ldg(table + e);
+      page = ld_input(table + e);
       at = seg.head * a.page_size + key0 - e * a.page_size;
     };
     look_up(w);
@@ -140,8 +140,8 @@ __device__ void compute(D4Smem& sm, const Verify4Args& a, volatile int* abort) {
     for (int i = 2 * warp; i < 2 * warp + 2; ++i) {
       const uint2* x = reinterpret_cast<const uint2*>(
           a.q_prep + ((size_t)seg.b * kHeads + seg.head * kGroup + g) * kDim + 64 * t + 4 * i);
-      const uint2 lo = __ldg(x);
-      const uint2 hi = g < kGroup - 8 ? __ldg(x + 8 * kDim / 4) : make_uint2(0u, 0u);
+      const uint2 lo = ld_input(x);
+      const uint2 hi = g < kGroup - 8 ? ld_input(x + 8 * kDim / 4) : make_uint2(0u, 0u);
       sm.q[i][lane] = make_uint4(lo.x, hi.x, lo.y, hi.y);
     }
     compute_sync();
@@ -314,7 +314,7 @@ __device__ void compute(D4Smem& sm, const Verify4Args& a, volatile int* abort) {
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              gate[i][k] = lo_f(__ldg(a.qg + out_row * kQgStride + kDim + 32 * (4 * (lane & 1) + k) + 16 * i + (lane >> 1)));
+              gate[i][k] = lo_f(ld_input(a.qg + out_row * kQgStride + kDim + 32 * (4 * (lane & 1) + k) + 16 * i + (lane >> 1)));
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

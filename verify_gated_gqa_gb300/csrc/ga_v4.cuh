@@ -75,6 +75,36 @@ __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// These blocks may be resident while the kernel that writes their inputs still runs, so the inputs
+// are not read-only for a block's whole life: not the non-coherent path, but plain loads that stay
+// behind grid_wait (and may pass the block's own stores).
+__device__ __forceinline__ uint4 ld_input(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_input(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int ld_input(const int* p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint16_t ld_input(const uint16_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+// The merge reads the lengths before its wait (the attention kernel waited for their writer before it
+// let the merge begin): from L2, where they are current.
+__device__ __forceinline__ int ld_len(const int* p) {
+  int v;
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ float sigmoid_f(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
@@ -187,7 +217,7 @@ __device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int wor
   const int b = threadIdx.x;
   int tiles = 0;
   if (b < kV4MaxSeq && b < a.n_seq) {
-    const int L = __ldg(a.seq_len + b);
+    const int L = ld_len(a.seq_len + b);
     bool refused;
     tiles = seq_tiles<kTile>(a, L, refused);
     if (refused && blockIdx.x == 0) record(a.status, kDevBadPosition);

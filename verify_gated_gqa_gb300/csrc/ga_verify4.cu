@@ -111,7 +111,7 @@ __device__ void raw_loader(V4Smem& sm, const CUtensorMap* tm_c, const CUtensorMa
       in = key0 < end;
       if (!in) return;
       const int e = key0 / a.page_size;
-      page = __ldg(table + e);
+      page = ld_input(table + e);
       at = seg.head * a.page_size + key0 - e * a.page_size;
     };
     look_up(seg.kt0);
@@ -303,7 +303,7 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
       uint32_t x[64];   // all of it in flight at once
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const uint4 t = valid ? __ldg(qp + i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 t = valid ? ld_input(qp + i) : make_uint4(0u, 0u, 0u, 0u);
         x[4 * i] = t.x; x[4 * i + 1] = t.y; x[4 * i + 2] = t.z; x[4 * i + 3] = t.w;
       }
       if (hf == 0) {
@@ -408,28 +408,47 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
     const size_t prow = (size_t)seg.slot * kV4Lanes + r;
     const uint4* gp = reinterpret_cast<const uint4*>(a.qg + (row * kHeads + h) * kQgStride + kDim + 128 * hf);
     uint4* op = reinterpret_cast<uint4*>(a.out + (row * kHeads + h) * kDim + 128 * hf);
+    if (seg.whole) {
+      // 16 dims at a time, their gates loaded two steps ahead (loads do not pass the stores)
+      uint4 g[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = valid ? ld_input(gp + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[32];
-      tmem_ld32(o_taddr + 32 * c, o);
-      tmem_wait_ld(o);
-      if (valid && seg.whole) {
+      for (int c = 0; c < 4; ++c) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 gt = __ldg(gp + 4 * c + i);
-          const uint32_t gw[4] = {gt.x, gt.y, gt.z, gt.w};
-          uint32_t res[4];
+        for (int k = 0; k < 2; ++k) {
+          uint32_t o[16];
+          tmem_ld16(o_taddr + 32 * c + 16 * k, o);
+          tmem_wait_ld(o);
+          const uint32_t gw[8] = {g[2 * k].x,     g[2 * k].y,     g[2 * k].z,     g[2 * k].w,
+                                  g[2 * k + 1].x, g[2 * k + 1].y, g[2 * k + 1].z, g[2 * k + 1].w};
+          uint32_t res[8];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            res[q] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * q]) * inv * sigmoid_f(lo_f(gw[q])),
-                                 __uint_as_float(o[8 * i + 2 * q + 1]) * inv * sigmoid_f(hi_f(gw[q])));
-          op[4 * c + i] = make_uint4(res[0], res[1], res[2], res[3]);
+          for (int q = 0; q < 8; ++q)
+            res[q] = pack_bf16x2(__uint_as_float(o[2 * q]) * inv * sigmoid_f(lo_f(gw[q])),
+                                 __uint_as_float(o[2 * q + 1]) * inv * sigmoid_f(hi_f(gw[q])));
+          if (valid) {
+            if (c < 3) {
+              g[2 * k] = ld_input(gp + 4 * c + 2 * k + 4);
+              g[2 * k + 1] = ld_input(gp + 4 * c + 2 * k + 5);
+            }
+            op[4 * c + 2 * k] = make_uint4(res[0], res[1], res[2], res[3]);
+            op[4 * c + 2 * k + 1] = make_uint4(res[4], res[5], res[6], res[7]);
+          }
         }
-      } else if (valid) {
+      }
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld32(o_taddr + 32 * c, o);
+        tmem_wait_ld(o);
+        if (valid) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *part_at(a.part_o, seg.slot, 32 * hf + 8 * c + i, r) = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                      __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+          for (int i = 0; i < 8; ++i)
+            *part_at(a.part_o, seg.slot, 32 * hf + 8 * c + i, r) = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        }
       }
     }
     if (valid && !seg.whole && hf == 0)
@@ -560,7 +579,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   int tiles = 0;
   if (tid < a.n_seq) {
     bool refused;
-    tiles = seq_tiles<kTile>(a, __ldg(a.seq_len + tid), refused);
+    tiles = seq_tiles<kTile>(a, ld_len(a.seq_len + tid), refused);
   }
   if (tid == 0) cut_n = 0;
   const Units q = scan_units<kTile>(tiles, warp_units, warp_streams);
@@ -662,9 +681,9 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
       const float x[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        out[d + 32 * k] = (uint16_t)(pack_bf16x2(x[k] * inv * sigmoid_f(lo_f(__ldg(gates + d + 32 * k))), 0.f) & 0xFFFFu);
+        out[d + 32 * k] = (uint16_t)(pack_bf16x2(x[k] * inv * sigmoid_f(lo_f(ld_input(gates + d + 32 * k))), 0.f) & 0xFFFFu);
     } else {
-      const uint2 g = __ldg(reinterpret_cast<const uint2*>(gates + p));
+      const uint2 g = ld_input(reinterpret_cast<const uint2*>(gates + p));
       *reinterpret_cast<uint2*>(out + p) =
           make_uint2(pack_bf16x2(o.x * inv * sigmoid_f(lo_f(g.x)), o.y * inv * sigmoid_f(hi_f(g.x))),
                      pack_bf16x2(o.z * inv * sigmoid_f(lo_f(g.y)), o.w * inv * sigmoid_f(hi_f(g.y))));
