@@ -6,7 +6,7 @@
 // registers: a lane's codes become its operand fragments where it holds them, and nothing
 // widened is ever stored. What bounds it is the cache's bytes and the instructions that widen
 // them, about equally (288 bytes and some 40 warp instructions a key of a head): 76 sequences of
-// 16,383 keys in 161 us, 4.5 TB/s of codes; 64 of up to 8,192, ragged, in 54; one of 65,536 in 20.
+// 16,383 keys in 161 us, 4.5 TB/s of codes; 64 of up to 8,192, ragged, in 54; one of 65,536 in 21.
 //
 // Work: streams (sequence, KV head) in granules of 32 keys, cut into equal runs, one per CTA, as in
 // ga_v4.cuh. Eight computing warps a CTA; warp w takes a segment's granules w, w + 8, ... on its

@@ -601,8 +601,11 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     }
   }
   __syncthreads();
-  grid_wait();   // in every block: the grid's end then stands for the attention kernel's too
-  if (cut_n == 0) return;   // none, or unused
+  // (every block waits, so that the grid's end stands for the attention kernel's too)
+  if (cut_n == 0) {   // no stream here
+    grid_wait();
+    return;
+  }
   // its parts: worker c0 has its first tile; boundaries cut it from u0 + uncut on
   const int b = cut_b, head = cut_head, u0 = cut_u0, u1 = u0 + cut_n;
   const int c0 = (min(u0 + uncut<kTile>(share), u1) - 1) / share;
@@ -610,15 +613,15 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   // part i is of worker c0 + i: its first segment unless the stream began inside the worker's run
   const bool inside = c0 * share < u0;
   auto slot = [&](int i) { return 2 * (blocks * (c0 + i) + block) + (i == 0 && inside ? 1 : 0); };
-  if (n == 1) return;   // one CTA ran the whole stream and wrote it
   // this block's items
   const long long items = rows * (kDim / 4);
-  const int shares = slices ? of : of * (n - 1), share_at = slices ? at : of * (w - c0) + at;
+  const int shares = slices ? of : of * max(n - 1, 1), share_at = slices ? at : of * (w - c0) + at;
   const int lo = (int)(items * share_at / shares), hi = (int)(items * (share_at + 1) / shares);
   const int count = hi - lo;
-  if (count == 0) return;
-  const int groups = max(1, min((n + 7) / 8, kCombineThreads / count));
+  const int groups = max(1, min((n + 7) / 8, kCombineThreads / max(count, 1)));
   const int group = groups > 1 ? tid / count : 0;   // (from `groups` on: idle)
+  grid_wait();
+  if (n == 1 || count == 0) return;   // (one CTA ran the whole stream and wrote it)
   for (int item = lo + tid - group * count; item < hi; item += kCombineThreads) {
     const int d4 = item / rows, r = item - d4 * rows;
     float M = -INFINITY, L = 0.f;
