@@ -361,21 +361,26 @@ __device__ void softmax_worker(V4Smem& sm, const Verify4Args& a, uint32_t tmem, 
       const bool grow = top > M + kLazyRescale;
       const float newM = grow ? top : M;
       if (__any_sync(0xffffffffu, grow && M != -INFINITY)) {
-        // O must hold every P V before it is scaled (the other half's last store waited for the
-        // P V before the last, and the exchange came after it, so this phase is the next one)
-        if (!warp_wait(&sm.p_empty[1], (g - 1) & 1, abort)) return;
-        tc_fence_after();
         const float sc = (grow && M != -INFINITY) ? exp2f(M - newM) : 1.0f;
+        // Half 0 scales all 256 columns of O: the next P V reads and writes every one of them and
+        // starts when half 0's P is there (p_full[0]), not knowing how far the other half is. With a
+        // half of the columns each, that P V could meet columns that half 1 was still scaling.
+        if (hf == 0) {
+          // O must hold every P V before it is scaled (the other half's last store waited for the
+          // P V before the last, and the exchange came after it, so this phase is the next one)
+          if (!warp_wait(&sm.p_empty[1], (g - 1) & 1, abort)) return;
+          tc_fence_after();
 #pragma unroll 1
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_taddr + c0, o);
-          tmem_wait_ld(o);
+          for (int c0 = 0; c0 < kDim; c0 += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem + kTmemO + lane_off + c0, o);
+            tmem_wait_ld(o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sc);
-          tmem_st32(o_taddr + c0, o);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sc);
+            tmem_st32(tmem + kTmemO + lane_off + c0, o);
+          }
+          tmem_wait_st();
         }
-        tmem_wait_st();
         l *= sc;
       }
       M = newM;
