@@ -34,8 +34,7 @@
 //              (so the next S = Q K^T overlaps this softmax); the two halves exchange their
 //              row maxima through shared memory and take the same M; P = bf16(2^(t - M))
 //              goes to tensor memory, each half its own 64 keys (and the tensor cores read
-//              each half as soon as it is written), and each half rescales its half of O
-//              when needed;
+//              each half as soon as it is written), and half 0 rescales O when needed;
 //   warps 12-15 the edge of each work item: the current item's gate tile from its ring
 //              slot into registers and its bf16 sigmoids while the item's tiles run, the
 //              next item's prepared Q tile (normed and rotated by the query prologue) into
@@ -887,23 +886,27 @@ __device__ void softmax_worker(AttnSmem& sm, const AttnArgs& a, uint32_t tmem, i
         }
       }
       if (__any_sync(0xffffffffu, rescale)) {
-        // O must hold every earlier P.V before it is scaled (the PV of global tile g-1, whose
-        // completion p_empty[1] marks; the P buffer wait below then passes at once). Each
-        // half scales its own 128 of O's 256 columns.
-        if (!warp_wait(&sm.p_empty[1], (g - 1) & 1, abort)) return;
-        tc_fence_after();
         const float f = rescale ? exp2f((float)(M - newM)) : 1.0f;
+        // Half 0 scales all 256 columns of O: the next P V reads and writes every one of them and
+        // starts when half 0's P is there (p_full[0]), not knowing how far the other half is. With
+        // a half of the columns each, that P V could meet columns that half 1 was still scaling.
+        if (hf == 0) {
+          // O must hold every earlier P.V before it is scaled (the PV of global tile g-1, whose
+          // completion p_empty[1] marks; the other half's last store waited for the one before)
+          if (!warp_wait(&sm.p_empty[1], (g - 1) & 1, abort)) return;
+          tc_fence_after();
 #pragma unroll 1
-        for (int c0 = 0; c0 < kDim / 2; c0 += 32) {
-          const uint32_t ta = tmem + kTmemO + lane_off + (kDim / 2) * hf + c0;
-          uint32_t o[32];
-          tmem_ld32(ta, o);
-          tmem_wait_ld(o);
+          for (int c0 = 0; c0 < kDim; c0 += 32) {
+            const uint32_t ta = tmem + kTmemO + lane_off + c0;
+            uint32_t o[32];
+            tmem_ld32(ta, o);
+            tmem_wait_ld(o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-          tmem_st32(ta, o);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st32(ta, o);
+          }
+          tmem_wait_st();
         }
-        tmem_wait_st();
         l *= f;
       }
       M = newM;
