@@ -82,3 +82,60 @@ def test_rows_grow_inside_segments(rows, n_seq, length, page):
     for _ in range(20):   # the same bits, whichever half of a tile's softmax is ahead
         again = B.ga_attn_verify_q4(q, qg, *pools, table, lens)
         assert torch.equal(again.view_as(out), out)
+
+
+@pytest.mark.parametrize("n_seq,length,page", [(64, 3001, 64), (150, 2000, 32)])
+def test_decoding_rows_grow_inside_segments(n_seq, length, page):
+    """One row a sequence: each of eight warps takes every eighth granule of 32 keys and keeps a
+    maximum of its own, so the warp that meets the row's key grows and the others do not."""
+    assert _segment_tiles(n_seq, length + 1, 1) >= 8 * 3
+    q, qg, pools, table, lens, kw, vw = _case(n_seq, length, 1, page, 4200 + n_seq)
+    out = B.ga_attn_verify_q4(q, qg, *pools, table, lens).view(n_seq, 1, 24, 256)
+    worst = 0.0
+    for b in range(n_seq):
+        for kv in range(2):
+            hs = slice(12 * kv, 12 * kv + 12)
+            want = attend64(q[b, :, hs], qg[b, :, hs, 256:], kw[b, :, kv], vw[b, :, kv],
+                            [length + 1])
+            worst = max(worst, float(row_errors(out[b, :, hs], want).max()))
+    assert worst <= ROW_BOUND, worst
+    for _ in range(10):
+        assert torch.equal(B.ga_attn_verify_q4(q, qg, *pools, table, lens).view_as(out), out)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 16])
+def test_every_tile_grows(rows):
+    """Scores that rise by more than 2^8 from one tile (or a warp's granule) to its next, all along
+    segments of many: every step scales O and l, and what is left of the older keys is below the
+    outputs' rounding, so a step that scales too little shows."""
+    n_seq, length, page = 64, 3001, 64
+    keys = length + rows
+    tile = 32 * 8 if rows == 1 else 128       # keys from one step of a running maximum to its next
+    assert _segment_tiles(n_seq, keys, rows) >= (24 if rows == 1 else 8)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4300 + rows)
+    qg = torch.randn(n_seq, rows, 24, 512, generator=g, device="cuda").to(torch.bfloat16)
+    v = torch.randn(n_seq * keys, 2, 256, generator=g, device="cuda").to(torch.bfloat16)
+    # q is 16 in every dim, a key 1 (widened: 63 / 64) in its first 8 s dims, s its step: each step
+    # adds 8 x 16 x 63 / 64 / 16 = 7.9 to the score, 11.4 binary orders
+    q = torch.full((n_seq, rows, 24, 256), 16.0, dtype=torch.bfloat16, device="cuda")
+    t = torch.arange(keys, device="cuda")
+    dims = torch.arange(256, device="cuda")
+    k1 = (dims[None] < 8 * (t // tile)[:, None]).to(torch.bfloat16)      # [keys, 256]
+    k = k1[None, :, None].expand(n_seq, keys, 2, 256).flatten(0, 1)
+    per = -(-keys // page)
+    table = torch.randperm(n_seq * per, generator=g, device="cuda").to(torch.int32).view(n_seq, per)
+    slots = (table.long()[:, t // page] * page + t % page).to(torch.int32).flatten()
+    pools = [torch.zeros(n_seq * per, 2, page, w, dtype=torch.uint8, device="cuda")
+             for w in (128, 16, 128, 16)]
+    B.ga_kv_quantize_q4(k.contiguous(), v, *pools, slots=slots)
+    kw, vw = (x.view(n_seq, keys, 2, 256) for x in B.ga_kv_dequantize_q4(*pools, slots=slots))
+    lens = torch.full((n_seq,), length, dtype=torch.int32, device="cuda")
+    out = B.ga_attn_verify_q4(q, qg, *pools, table, lens).view(n_seq, rows, 24, 256)
+    for b in range(0, n_seq, 7):
+        for kv in range(2):
+            hs = slice(12 * kv, 12 * kv + 12)
+            want = attend64(q[b, :, hs], qg[b, :, hs, 256:], kw[b, :, kv], vw[b, :, kv],
+                            [length + r + 1 for r in range(rows)])
+            worst = float(row_errors(out[b, :, hs], want).max())
+            assert worst <= ROW_BOUND, (b, kv, worst)
