@@ -539,7 +539,9 @@ int ga_attn_prefill_batch(const ga_bf16* qg, const int* row_start, const int* q_
  *   info    [4]: status, tokens, pages taken, pages given back. Status 0: done; 1: more than
  *           max_tokens tokens; 2: a sequence past max_pages * page_size or GA_MAX_TOKENS; 3: not
  *           enough free pages; 4: held or free_count out of range, or more pages given back than
- *           the stack has room for. When it is not 0 nothing is planned: page_table and
+ *           the stack has room for. Of several reasons the first of these counts: held or
+ *           free_count (4), a sequence (2), the stack's room (4), tokens (1), free pages (3).
+ *           When it is not 0 nothing is planned: page_table and
  *           free_pages keep their contents, held_out and free_count_out are copies, row_start
  *           and the totals are 0, every slot is -1.
  * Other than those pairs, no output may overlap an input or another output. The call takes one

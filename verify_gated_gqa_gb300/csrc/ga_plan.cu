@@ -124,11 +124,12 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   // every thread agrees on the outcome before anything is written
   if (total.tok > (unsigned)a.max_tokens) err |= 1;
   if (count >= 0 && total.need > (unsigned)count) err |= 4;
-  if (count >= 0 && (long long)count - total.need + total.rel > a.n_free) err |= 8;
+  if (count >= 0 && (long long)count - total.need + total.rel > a.n_free) err |= 16;
   int any = 0;
   if (__syncthreads_or(err))
-    for (int bit = 1; bit <= 8; bit <<= 1) any |= __syncthreads_or(err & bit) ? bit : 0;
-  const int status = any & 8 ? 4 : any & 2 ? 2 : any & 1 ? 1 : any & 4 ? 3 : 0;
+    for (int bit = 1; bit <= 16; bit <<= 1) any |= __syncthreads_or(err & bit) ? bit : 0;
+  // a sequence past its table (2) comes before the sums' refusals: its pages are not in them
+  const int status = any & 8 ? 4 : any & 2 ? 2 : any & 16 ? 4 : any & 1 ? 1 : any & 4 ? 3 : 0;
   if (status) total = Triple{0u, 0u, 0u};
   Triple at = {before.tok + inc.tok - sum.tok, before.need + inc.need - sum.need,
                before.rel + inc.rel - sum.rel};
