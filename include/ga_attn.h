@@ -562,9 +562,9 @@ int ga_page_plan(const int* seq_len, const int* new_len, int n_seq, int page_siz
  * points are ga_qk_prologue's, and so are the bits where a token's positions are all the same.
  *   k_raw, w_k, k_prep  as in ga_qk_prologue, for n_tok tokens; or all three NULL
  *   qg, w_q, q_prep     as in ga_qk_prologue, for the same n_tok tokens; or all three NULL
- *   positions DEVICE int32 [n_axes][ld_pos], 4-byte aligned; ld_pos >= n_tok. A position outside
- *             0 .. table_rows - 1 is not a fault: status 4 is recorded (ga_device_status) and
- *             the pair turns by position 0.
+ *   positions DEVICE int32 [n_axes][ld_pos], 4-byte aligned; ld_pos >= n_tok, or 0: one row
+ *             [n_tok] for all axes. A position outside 0 .. table_rows - 1 is not a fault:
+ *             status 4 is recorded (ga_device_status) and the pair turns by position 0.
  *   pair_axis HOST array of 32 bytes, each below n_axes (contiguous or interleaved sections)
  *   cos_tab, sin_tab [table_rows][32]
  * Rules: 1 <= n_axes <= 4, 0 <= n_tok <= GA_MAX_TOKENS, table_rows >= 1; no output may overlap an

@@ -1,12 +1,14 @@
 """Calls of the 4-bit serving set that its documentation allows, in the ways that a server makes
-them: several refusals at once."""
+them: several refusals at once, one position row for all axes."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import ga_oracle as O
+from tests.parity import SEED
 from verify_gated_gqa_gb300 import binding as B
 from verify_gated_gqa_gb300 import build as build_mod
+from verify_gated_gqa_gb300 import synth
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +55,19 @@ def test_plan_refusals_in_their_order():
     assert _plan_statuses({**PLAN, "a": [90, 30, -1], "mt": 3, "count": 0}, 0) == 2
     assert _plan_statuses({**PLAN, "a": [4, 0, -1], "count": 5, "mt": 3}, 0) == 4
     assert _plan_statuses({**PLAN, "mt": 3, "count": 0}, 0) == 1
+
+
+# ------------------------------------------------------------------ the prologue over axes
+@pytest.mark.parametrize("n", [1, 37])
+def test_axes_share_one_row_of_positions(n):
+    """Text alone: the same positions on every axis, as one row seen three times."""
+    k = synth.normal_bf16(SEED, "k", (n, 2, 256)).cuda()
+    qg = synth.normal_bf16(SEED, "qg", (n, 24, 512)).cuda()
+    w_k = synth.normal_bf16(SEED, "w_k", (256,), sigma=0.1).cuda()
+    w_q = synth.normal_bf16(SEED, "w_q", (256,), sigma=0.1).cuda()
+    c, s = (t.cuda() for t in B.ga_rope_table_host(512))
+    pos = torch.arange(400, 400 + n, dtype=torch.int32, device="cuda")
+    pairs = [i % 3 for i in range(32)]
+    want = B.ga_qk_prologue_axes(k, w_k, qg, w_q, pos[None].repeat(3, 1), pairs, c, s)
+    got = B.ga_qk_prologue_axes(k, w_k, qg, w_q, pos[None].expand(3, n), pairs, c, s)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))

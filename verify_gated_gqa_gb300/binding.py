@@ -602,7 +602,7 @@ def ga_page_plan(seq_len, new_len, page_table, held, free_pages, free_count, pag
 def ga_qk_prologue_axes(k_raw, w_k, qg, w_q, positions, pair_axis, cos_tab, sin_tab, k_prep=None,
                         q_prep=None):
     """Both prologues at positions of their own: positions int32 [n_tok] or [n_axes, >= n_tok]
-    (unit column stride) on the device, pair_axis 32 axis numbers (rotary pair i turns by axis
+    (unit column stride; one row expanded to all axes will do) on the device, pair_axis 32 axis numbers (rotary pair i turns by axis
     pair_axis[i]; None: axis 0). k_raw (with w_k) or qg (with w_q) may be None. Returns (k_prep
     [n_tok, 2, 256], q_prep [n_tok, 24, 256]), None for a side not given."""
     st, k_prep, q_prep = _native().qk_prologue_axes(k_raw, w_k, qg, w_q, positions, pair_axis,

@@ -1248,7 +1248,8 @@ int ga_qk_prologue_axes(const ga_bf16* k_raw, const ga_bf16* w_k, ga_bf16* k_pre
       (!k_raw && !qg) || !positions || !pair_axis || !cos_tab || !sin_tab)
     return GA_ERR_NULL;
   if (n_tok < 0 || n_axes < 1 || table_rows < 0) return GA_ERR_SHAPE;
-  if (n_tok > GA_MAX_TOKENS || n_axes > 4 || ld_pos < n_tok || ld_pos > (1LL << 40))
+  if (n_tok > GA_MAX_TOKENS || n_axes > 4 || (ld_pos != 0 && ld_pos < n_tok) || ld_pos < 0 ||
+      ld_pos > (1LL << 40))
     return GA_ERR_RANGE;
   AxisPositions ap{};
   for (int i = 0; i < kHalfRot; ++i) {
