@@ -507,6 +507,9 @@ int ga_attn_prefill_batch(const ga_bf16* qg, const int* row_start, const int* q_
  *   ga_kv_quantize_q4     their keys and values into the cache
  *   ga_attn_verify_q4     attention of every sequence's window over its cache
  * and reads no length on the host, so it can be captured once and replayed as they change.
+ * The plan packs its tokens: a sequence that adds fewer moves the ones after it. They lie as the
+ * attention's windows [n_seq][rows] do while every sequence in use adds `rows` tokens and idle
+ * rows of the batch (length -1) stand at its end.
  * ------------------------------------------------------------------------------------------ */
 
 #define GA_PLAN_MAX_SEQ 2048 /* sequences of one ga_page_plan call */
@@ -546,6 +549,8 @@ int ga_attn_prefill_batch(const ga_bf16* qg, const int* row_start, const int* q_
  *           and the totals are 0, every slot is -1.
  * Other than those pairs, no output may overlap an input or another output. The call takes one
  * launch up to 8,192 slots, two above.
+ * With lengths of 0 and the cached lengths as new_len it lists the slots of cached tokens, for
+ * ga_kv_dequantize_q4 to widen whole caches: no page is taken while the rows hold theirs.
  * Rules: 0 <= n_seq <= GA_PLAN_MAX_SEQ, page_size >= 1, 1 <= max_pages, max_pages * page_size
  * < 2^31, n_free * page_size < 2^31, 0 <= max_tokens < 2^30; every array 4-byte aligned. With
  * n_seq = 0, row_start, slot_map, positions and info are still written.
