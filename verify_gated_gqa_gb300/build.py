@@ -37,7 +37,8 @@ def _newest_dep() -> float:
 
 
 def _native_commands(obj: str):
-    """Compile and link commands of the native binding against the installed torch."""
+    """Compile and link commands of the native binding against the installed torch, and a text that
+    changes with everything they depend on beside the sources."""
     import torch
 
     tdir = os.path.dirname(os.path.abspath(torch.__file__))
@@ -50,7 +51,16 @@ def _native_commands(obj: str):
     link = ["g++", "-shared", "-o", NATIVE, obj, "-L", PKG, "-l:libga_attn.so",
             "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
             "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
-    return compile_, link
+    key = "\n".join([torch.__version__, str(sysconfig.get_config_var("SOABI")), " ".join(compile_),
+                     " ".join(link)])
+    return compile_, link, key
+
+
+def _read(path: str) -> str:
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -69,10 +79,14 @@ def build(verbose: bool = False, force: bool = False) -> str:
     native_obj = os.path.join(BUILD, "ga_native.o")
     native_dep = max(os.path.getmtime(NATIVE_SRC),
                      os.path.getmtime(os.path.join(ROOT, "include", "ga_attn.h")))
+    # the module holds torch's and Python's types: the stamp names the ones it was compiled against
+    native_stamp = os.path.join(BUILD, "ga_native.stamp")
+    native_compile, native_link, native_key = _native_commands(native_obj)
     native = (force or not os.path.exists(NATIVE) or not os.path.exists(native_obj) or
-              min(os.path.getmtime(NATIVE), os.path.getmtime(native_obj)) < native_dep)
+              min(os.path.getmtime(NATIVE), os.path.getmtime(native_obj)) < native_dep or
+              _read(native_stamp) != native_key)
+    relink = bool(jobs)
     if native:
-        native_compile, native_link = _native_commands(native_obj)
         jobs.append(native_compile)
 
     def run(cmd):
@@ -84,10 +98,12 @@ def build(verbose: bool = False, force: bool = False) -> str:
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
         list(ex.map(run, jobs))
-    if jobs or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
+    if relink or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         run([nvcc, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"])
     if native:
         run(native_link)
+        with open(native_stamp, "w") as f:
+            f.write(native_key)
     return LIB
 
 
