@@ -58,3 +58,22 @@ def test_native_module_follows_torch_and_python(commands, monkeypatch):
                         lambda name: "other" if name == "SOABI" else real(name))
     build_mod.build()
     assert commands.take() == NATIVE_STEPS
+
+
+def test_library_is_built_without_torch(commands, monkeypatch, capsys):
+    """The C-ABI library needs nvcc alone; the native module is left out, and said to be."""
+    monkeypatch.setitem(build_mod.sys.modules, "torch", None)   # import torch raises ImportError
+    assert build_mod.build() == build_mod.LIB
+    ran = commands.take()
+    assert ("nvcc", "libga_attn.so") in ran and not any(p == "g++" for p, _ in ran)
+    assert "_native.so" in capsys.readouterr().err
+
+
+def test_library_is_linked_before_the_native_module_fails(commands):
+    commands.failing = "ga_native"
+    with pytest.raises(RuntimeError):
+        build_mod.build()
+    assert ("nvcc", "libga_attn.so") in commands.take()
+    commands.failing = None
+    build_mod.build()
+    assert commands.take() == NATIVE_STEPS

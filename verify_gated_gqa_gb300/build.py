@@ -1,7 +1,8 @@
 """Build libga_attn.so in-tree: one nvcc per translation unit (in parallel) for sm_103a,
 then one shared-library link, and beside it the native half of the torch binding
 (_native.so, plain C++ against torch's headers). No CMake; a rebuild only recompiles
-changed units."""
+changed units. The library needs nvcc alone: it is linked whatever becomes of the module, which is
+left out where there is no torch."""
 from __future__ import annotations
 
 import os
@@ -76,18 +77,6 @@ def build(verbose: bool = False, force: bool = False) -> str:
         stale = force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(s), dep_time)
         if stale:
             jobs.append([nvcc, *ARCH, *FLAGS, "-c", s, "-o", o])
-    native_obj = os.path.join(BUILD, "ga_native.o")
-    native_dep = max(os.path.getmtime(NATIVE_SRC),
-                     os.path.getmtime(os.path.join(ROOT, "include", "ga_attn.h")))
-    # the module holds torch's and Python's types: the stamp names the ones it was compiled against
-    native_stamp = os.path.join(BUILD, "ga_native.stamp")
-    native_compile, native_link, native_key = _native_commands(native_obj)
-    native = (force or not os.path.exists(NATIVE) or not os.path.exists(native_obj) or
-              min(os.path.getmtime(NATIVE), os.path.getmtime(native_obj)) < native_dep or
-              _read(native_stamp) != native_key)
-    relink = bool(jobs)
-    if native:
-        jobs.append(native_compile)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -96,14 +85,30 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {cmd[-3]}")
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
+    native_obj = os.path.join(BUILD, "ga_native.o")
+    # the module holds torch's and Python's types: the stamp names the ones it was compiled against
+    native_stamp = os.path.join(BUILD, "ga_native.stamp")
+    native_dep = max(os.path.getmtime(NATIVE_SRC),
+                     os.path.getmtime(os.path.join(ROOT, "include", "ga_attn.h")))
+    try:
+        native_compile, native_link, native_key = _native_commands(native_obj)
+        native = (force or not os.path.exists(NATIVE) or not os.path.exists(native_obj) or
+                  min(os.path.getmtime(NATIVE), os.path.getmtime(native_obj)) < native_dep or
+                  _read(native_stamp) != native_key)
+    except ImportError:
+        native = False
+        sys.stderr.write("torch is not installed: _native.so is not built\n")
+
+    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
+        native_job = ex.submit(run, native_compile) if native else None
         list(ex.map(run, jobs))
-    if relink or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
-        run([nvcc, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"])
-    if native:
-        run(native_link)
-        with open(native_stamp, "w") as f:
-            f.write(native_key)
+        if jobs or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
+            run([nvcc, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"])
+        if native:
+            native_job.result()
+            run(native_link)
+            with open(native_stamp, "w") as f:
+                f.write(native_key)
     return LIB
 
 
