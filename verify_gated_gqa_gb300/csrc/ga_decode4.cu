@@ -23,6 +23,8 @@
 // halves of the words of two keys are joined before they are widened, so a fragment's two keys
 // come out of one operation, with the scales of both in one register. With these choices every
 // 16-byte read of the swizzled codes is free of bank conflicts.
+#include <cstddef>
+
 #include "ga_v4.cuh"
 
 namespace ga {
@@ -54,6 +56,10 @@ struct D4Smem {
   int abort;
 };
 static_assert(sizeof(D4Smem) <= 232448, "227 KiB of shared memory per CTA");
+static_assert(offsetof(D4Smem, codes) % 1024 == 0 && kCodeBytes % 1024 == 0 && offsetof(D4Smem, scales) % 128 == 0,
+              "tiles of the copies");
+static_assert(offsetof(D4Smem, full) % 8 == 0 && offsetof(D4Smem, q) % 16 == 0 && offsetof(D4Smem, join) % 16 == 0,
+              "barriers at 8 bytes, vectors at 16");
 
 __device__ __forceinline__ void compute_sync() {   // the computing warps
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");

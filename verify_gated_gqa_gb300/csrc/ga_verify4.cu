@@ -37,6 +37,8 @@
 // the rows unrolled through registers the widening alone took 3,500 cycles a tile).
 // Tensor memory: O [0, 256), S [256, 384), Q dims 0..127 [384, 448), P [448, 512).
 // Every wait is bounded; a wait that gives up raises the CTA's abort flag, which the others see.
+#include <cstddef>
+
 #include "ga_v4.cuh"
 
 namespace ga {
@@ -74,6 +76,15 @@ struct V4Smem {
   int abort;
 };
 static_assert(sizeof(V4Smem) <= 232448, "227 KiB of shared memory per CTA");
+// What the copies, the descriptors and the barrier instructions need of the addresses.
+static_assert(offsetof(V4Smem, kt) % 1024 == 0 && offsetof(V4Smem, vt) % 1024 == 0 &&
+                  offsetof(V4Smem, qhi) % 1024 == 0 && kQBlockBytes % 1024 == 0 && kBlockBytes % 1024 == 0,
+              "swizzled blocks begin at whole atoms");
+static_assert(offsetof(V4Smem, raw) % 1024 == 0 && offsetof(V4Smem, rsc) % 128 == 0, "tiles of the copies");
+static_assert(offsetof(V4Smem, raw_full) % 8 == 0 && offsetof(V4Smem, full) % 8 == 0 &&
+                  offsetof(V4Smem, q_full) % 8 == 0 && offsetof(V4Smem, drain_pv) % 8 == 0,
+              "every barrier at 8 bytes");
+static_assert(offsetof(V4Smem, vt) + sizeof(V4Smem::vt) <= (1u << 18), "descriptor addresses have 18 bits");
 
 // Two multiply-adds by one operation: a x + b for both x.
 __device__ __forceinline__ void fma_f32x2(float& r0, float& r1, float x0, float x1, float a, float b) {
