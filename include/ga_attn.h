@@ -624,7 +624,8 @@ size_t ga_verify_q4_workspace_bytes(void);
  * lengths on the DEVICE, and it rounds the softmax weights and the output only: scores, O and
  * the gate stay in fp32. The same call gives the same bits; where a sequence's keys are cut
  * among the SMs, and so its last bits, depends on all the lengths of the call. A NaN query (or one
- * whose scores are infinite) makes its own head's row NaN and no other.
+ * whose scores are infinite, or pass 2^29 in magnitude, which fp32 no longer tells apart) makes its
+ * own head's row meaningless, mostly NaN, and no other.
  *   q_prep   [n_seq][rows][24][256] prepared queries (ga_qk_prologue_axes or ga_q_prologue)
  *   qg       [n_seq][rows][24][512] fused rows, read for their gate halves
  *   k_codes, k_scales, v_codes, v_scales, n_pages, page_size: the pools, as ga_kv_quantize_q4

@@ -6,8 +6,8 @@
 //
 // 16 lanes per row, one 16-value group per lane, so a group's maximum needs no exchange between
 // lanes and a row's reads and writes are contiguous runs. Both kernels are bound by the bytes they
-// move (2,624 a token), storing by its instructions nearly as much: 65,536 tokens stored and widened
-// by two calls in 54 us of GPU time, 5.7 TB/s; 8,191 in 8.6. A thread takes the same group
+// move (2,624 a token each), storing by its instructions nearly as much: 65,536 tokens stored and
+// widened by two calls in 54 us of GPU time, 6.3 TB/s; 8,191 in 8.5. A thread takes the same group
 // of a token's four rows (two heads of K and of V), all four in flight before the first is used
 // and the slot looked up and divided once for them; with few tokens, of one row.
 #include <cuda_bf16.h>

@@ -10,7 +10,9 @@
 //
 // Eight dims of a row make a 32-bit little-endian word: nibble p < 4 is dim 2p, nibble 4 + p
 // is dim 2p + 1, so (w >> 4p) & 0x000F000F holds the codes of the pair (2p, 2p + 1) in the
-// halves of a register. OR-ed into 0x4300 (bf16 128, whose last place is 1), a code n becomes
+// halves of a register (integer to float through the exponent field, two values an operation: the
+// published way of widening low-bit weights, Kim et al., "Who Says Elephants Can't Run", 2022). OR-ed
+// into 0x4300 (bf16 128, whose last place is 1), a code n becomes
 // the bf16 value 128 + n, and one fused multiply-add, (128 + n) s - 136 s, gives (n - 8) s
 // with no rounding (136 s = 17 (8 + m) 2^E' has at most 8 significant bits).
 #pragma once

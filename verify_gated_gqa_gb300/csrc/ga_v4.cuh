@@ -130,10 +130,10 @@ __host__ __device__ __forceinline__ int row_blocks(int rows) {
 // A stream's units in the cut: its tiles after kLead units of no work, which stand for what a
 // segment costs beside its tiles (its queries, the first loads, its result). A boundary inside them,
 // or fewer than kFront tiles past them, moves to the stream's beginning: the CTA before is spared a
-// segment. Cut by tiles alone, a CTA that met several short streams took several times as long as one
-// inside a long one: 64 sequences of up to 8,192 keys, one row: 76 us against 61; of up to 300 keys
-// 26 against 15; 5 x 5 rows over up to 12,345 keys 22 against 19. (64 x 4,095 keys lose by
-// it: 52 us against 54.)
+// segment. Cut by tiles alone, a CTA that meets several short streams takes longer than one inside a
+// long one: 64 ragged sequences of up to 8,192 keys, one row: 60 us against 54; of up to 300 keys
+// 24 against 18; 5 x 5 rows over up to 12,345 keys 25 against 21; 200 x 5 rows over up to 2,047 93
+// against 85. (Equal long streams take the same: 64 x 4,095 keys 53 us.)
 template <int kTile>
 constexpr int kLead = kTile == 32 ? 16 : 6;
 template <int kTile>

@@ -16,8 +16,9 @@
 // two per CTA: its first and its last segment), merged by the combine kernel.
 //
 // A tile of 128 keys moves 128 KiB of widened stores, 160 KiB of operand reads and 72 KiB of codes
-// through shared memory, 2,800 cycles of the 2,975 that it takes: 8 x 16 rows over 65,536 keys in 181
-// us (1.14 PFLOP/s), 5 x 6 rows over up to 12,345 in 22.5, of which 5 are launch and fill.
+// through shared memory, 2,800 cycles of the 2,975 that it takes. Whole calls from cold caches: 8 x 16
+// rows over 65,536 keys in 194 us (this kernel alone 173 to 181, 1.14 to 1.19 PFLOP/s), 5 x 6 rows
+// over up to 12,345 in 22.5, of which 5 are launch and fill.
 //
 // Structure (896 threads, 28 warps):
 //   warp 0      issues S = Q K^T (tcgen05, M=128, N=128, K=256; Q dims 0..127 in tensor
