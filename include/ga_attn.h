@@ -103,7 +103,7 @@ unsigned long long ga_debug_cuda_calls(void);
 /* Reads the current device's status word, written by kernels whose bounded waits gave
  * up or whose inputs failed a device-side check (0 = no error, 1 = wait timeout, 2 = bad
  * launch configuration, 3 = a page-table entry or slot outside the page pool, see
- * ga_attn_verify_paged and ga_kv_quantize_q4, 4 = a rotary position outside the table or a
+ * ga_attn_verify_paged, ga_kv_quantize_q4 and the calls over pages, 4 = a rotary position outside the table or a
  * cached length outside the page table, see ga_qk_prologue_axes and ga_attn_verify_q4).
  * Synchronises the device. clear != 0 resets the word afterwards. */
 int ga_device_status(int* status_out, int clear);
@@ -525,7 +525,7 @@ int ga_attn_prefill_batch(const ga_bf16* qg, const int* row_start, const int* q_
  *           then of page (the i-th is free_pages[count - 1 - i]), and appended to its row
  *   new_len[b] < 0:  it is finished: its held pages go back on the stack, on top of what the step
  *           left, in order of sequence and then of column, and it holds none. (Pages that other
- *           rows share must not be given back this way.)
+ *           rows share must not be given back this way: ga_page_release.)
  *   seq_len[b] < 0 (and new_len[b] >= 0): the row is unused and left as it is
  * All arrays are DEVICE int32:
  *   seq_len, new_len, held [n_seq]; page_table [n_seq][max_pages], updated in place
@@ -648,6 +648,176 @@ int ga_attn_verify_q4(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k
                       int n_pages, int page_size, const int* page_table, int max_pages,
                       const int* seq_len, int n_seq, int rows, ga_bf16* out, void* workspace,
                       size_t ws_bytes, ga_stream stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Serving over an 8-bit paged cache: ga_page_plan and ga_qk_prologue_axes as above, then
+ *   ga_kv_quantize_q8     the step's keys and values into the cache
+ *   ga_attn_verify_q8     attention of every sequence's window over its cache
+ * (The e4m3 calls above take contiguous caches, a scale per row and lengths on the host.)
+ * ------------------------------------------------------------------------------------------ */
+
+#define GA_Q8_BLOCK_TOKENS 32 /* tokens of one head that share a scale; pages hold a multiple */
+#define GA_Q8_ROW_BYTES 256   /* code bytes of one (token, KV head) row */
+
+/* 8-bit cache rows: e4m3 codes with a power-of-two scale for each block of 32 tokens (slots 32 i ..
+ * 32 i + 31) and head. A value's code is e4m3(x / 2^e), to nearest, ties to even, saturating; the
+ * widened value code * 2^e is a bf16 value exactly. For the tokens that a call stores into a block,
+ *   e = the least integer in [-32, 31] with max|x| <= 448 * 2^e over their rows (31 if none)
+ * and, unless the block's first slot is among them, no less than the block's exponent was; where it
+ * grows, the block's other codes become e4m3(code / 2^growth), so earlier rows keep their values
+ * but for what falls under the smallest codes. A store of a block's first slot begins it anew: its
+ * other codes are left as they are. So a block is filled from its first slot on, in any number of
+ * calls; writing over its later slots (tokens taken back) is fine. A NaN is stored as 0; an
+ * infinity saturates, and takes the block's exponent to 31. Pools, per keys and values:
+ *   codes   [n_pages][2][page_size][256] uint8, 16-byte aligned (head-major within a page)
+ *   scales  [n_pages][2][page_size / 32] uint8, any alignment: e + 32 in the low six bits (stores
+ *           clear the others)
+ * Slot x is position x % page_size of page x / page_size.
+ * ga_kv_quantize_q8 stores token t's key and value rows at slots[t]:
+ *   k, v    bf16 rows of two heads' 256 values, token t at t * ld_k (ld_v) values; 16-byte
+ *           aligned, leading dimensions >= 512 and multiples of 8 (a slice of a fused projection)
+ *   slots   DEVICE int32 [n_tok], 4-byte aligned, or NULL: token t goes to slot t. A negative
+ *           slot stores nothing; one past the pool stores nothing and records status 3. Slots of
+ *           one call must differ, and the tokens of one block follow one another in the call, as
+ *           ga_page_plan lists them (else that block's rows are unspecified).
+ * Rules: page_size a multiple of 32, n_pages * page_size < 2^30, 0 <= n_tok <= 64 *
+ * GA_MAX_TOKENS; with slots NULL, n_tok <= n_pages * page_size.
+ * Errors: NULL, SHAPE, RANGE, ALIGN, DEVICE, CUDA. */
+int ga_kv_quantize_q8(const ga_bf16* k, long long ld_k, const ga_bf16* v, long long ld_v,
+                      long long n_tok, const int* slots, uint8_t* k_codes, uint8_t* k_scales,
+                      uint8_t* v_codes, uint8_t* v_scales, int n_pages, int page_size,
+                      ga_stream stream);
+
+/* The widened rows of the tokens at slots[0 .. n_tok - 1] (or slots 0 .. n_tok - 1 with NULL).
+ *   k_out, v_out [n_tok][2][256] bf16, 16-byte aligned. Rows of negative or refused slots are
+ *           left as they were. The same slot may appear more than once.
+ * Codes 0x7F and 0xFF, which ga_kv_quantize_q8 never writes, widen to NaN. Everything else as in
+ * ga_kv_quantize_q8.
+ * Errors: NULL, SHAPE, RANGE, ALIGN, DEVICE, CUDA. */
+int ga_kv_dequantize_q8(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                        const uint8_t* v_scales, int n_pages, int page_size, const int* slots,
+                        long long n_tok, ga_bf16* k_out, ga_bf16* v_out, ga_stream stream);
+
+/* Bytes of workspace ga_attn_verify_q8 needs, whatever the sequences and lengths. */
+size_t ga_verify_q8_workspace_bytes(void);
+
+/* Few-row verify windows, and decode (rows = 1), over 8-bit paged caches: ga_attn_verify_q4's
+ * arguments, rules, workspace rules and errors over the pools above (pages of a multiple of 32
+ * tokens). Hidden positions need no initial contents: whatever their codes and scales, NaN codes
+ * included, they do not reach a result. Queries and softmax weights meet the codes as sums of two
+ * 8-bit parts: a query is within 2^-17 of its row's largest magnitude, a weight within 2^-8 of
+ * itself; sums, maxima and O are fp32, and the output is rounded once. A NaN query (or one whose
+ * scores are infinite, or pass 2^29 in magnitude) makes its own head's row meaningless, and no other.
+ * A page-table entry outside the pool records status 3 and its keys are read as zeros.
+ * Errors: NULL, SHAPE, RANGE, ALIGN, WORKSPACE, DEVICE, CUDA. */
+int ga_attn_verify_q8(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k_codes,
+                      const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                      int n_pages, int page_size, const int* page_table, int max_pages,
+                      const int* seq_len, int n_seq, int rows, ga_bf16* out, void* workspace,
+                      size_t ws_bytes, ga_stream stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Pages that several sequences hold (branches over a shared prefix), beside ga_page_plan. Its
+ * page_table, held, free_pages and free_count are these calls' too, with one count more:
+ *   shared  DEVICE int32 [n_free]: the rows beyond the first that hold each page; 0 for a page of
+ *           one row and for a free page, so pages that ga_page_plan takes need no entry
+ * A row may append only to pages that it alone holds: ga_page_fork sees to that at the branch. A row
+ * that is cut back (ga_page_release) into a page that others hold must not go on inside it; fork it
+ * into an unused row and release it instead. ga_page_plan gives back a finished row's pages whoever
+ * else holds them: rows that share pages are finished by ga_page_release.
+ * All arrays are DEVICE int32, 4-byte aligned; an output may be the input of the same kind itself
+ * (held_out held, and so on) and overlap nothing else. Each call reads every length on the device
+ * and so can be captured once. A page-table entry outside the pool is not a fault: it records status
+ * 3 (ga_device_status) and is passed over. info [4] begins with a status; when it is not 0 nothing
+ * is done: tables, stacks and lists of free pages keep their contents, outputs are copies of their
+ * inputs, copy and move lists are -1 throughout and info's other entries 0. Status 4: held or
+ * free_count out of range.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Forks: row child[i] becomes a branch of the first len[i] tokens of row parent[i]. It holds the
+ * parent's whole pages of them with it (shared grows) and, where len[i] % page_size is not 0, a page
+ * of its own, taken from the top of the stack in order of the forks, for the page begun, whose copy
+ * is the caller's to make: ga_page_copy with the lists below, before either row is written to.
+ *   parent, child, len [n_fork]; parent[i] < 0: an unused entry. A parent may appear any number of
+ *           times. A child's row holds no page before (it need not be cleared)
+ *   page_table [n_seq][max_pages], updated in place; held, held_out [n_seq]
+ *   free_pages [n_free], read; free_count, free_count_out [1]; shared, shared_out [n_free]
+ *   copy_src, copy_dst [n_fork]: the pages to copy, -1 for a fork without
+ *   info    {status, forks made, pages taken, pages now held by one row more}. Status 1: a row
+ *           outside 0 .. n_seq - 1, a parent as its own child, a child twice, or one that holds
+ *           pages; 2: len[i] negative or past the pages that the parent holds; 3: not enough free
+ *           pages. Of several reasons the first counts, in the order 4, 1, 2, 3.
+ * The children's cached lengths (ga_page_plan's seq_len) are the caller's to set.
+ * Rules: 0 <= n_fork, n_seq <= GA_PLAN_MAX_SEQ, page_size >= 1, max_pages >= 1, max_pages *
+ * page_size < 2^31, n_seq * max_pages < 2^30, 0 <= n_free, n_free * page_size < 2^31.
+ * Errors: NULL, SHAPE, RANGE, ALIGN, DEVICE, CUDA. */
+int ga_page_fork(const int* parent, const int* child, const int* len, int n_fork, int n_seq,
+                 int page_size, int* page_table, int max_pages, const int* held, int* held_out,
+                 const int* free_pages, int n_free, const int* free_count, int* free_count_out,
+                 const int* shared, int* shared_out, int* copy_src, int* copy_dst, int* info,
+                 ga_stream stream);
+
+/* Pages given back: row b keeps the pages of its first keep[b] tokens and lets the others go (0: a
+ * finished row, negative: a row left as it is). A page that other rows still hold loses a holder;
+ * one that all its holders let go, in this call or before, goes on the stack, in order of row and
+ * then of column (of several places of a page its first).
+ *   keep [n_seq]; page_table [n_seq][max_pages], read; held, held_out [n_seq]
+ *   free_pages [n_free]: entries from free_count on are written; free_count, free_count_out [1]
+ *   shared, shared_out [n_free]
+ *   info    {status, rows that let pages go, pages put on the stack, pages let go}. Status 4 also:
+ *           more pages given back than the stack has room for; 5: a page let go more often than
+ *           `shared` says that it is held. 4 for held or free_count counts first, then 5.
+ * Rules: as ga_page_fork's.
+ * Errors: NULL, SHAPE, RANGE, ALIGN, DEVICE, CUDA. */
+int ga_page_release(const int* keep, int n_seq, int page_size, const int* page_table,
+                    int max_pages, const int* held, int* held_out, int* free_pages, int n_free,
+                    const int* free_count, int* free_count_out, const int* shared,
+                    int* shared_out, int* info, ga_stream stream);
+
+/* Bytes of workspace ga_page_compact needs for a pool of n_free pages; 0 for a negative one. */
+size_t ga_page_compact_workspace_bytes(int n_free);
+
+/* Compaction: pages in use move down into free ones until they fill the front of the pool. With
+ * n_live = n_free - free_count pages in use, move i takes the i-th highest page in use at or past
+ * n_live to the i-th lowest free page below it, for the first max_moves of them (the budget of one
+ * step). The pages' contents are the caller's to move: ga_page_copy with the lists below, before
+ * either row is written to and before a page is taken from the new stack.
+ *   page_table [n_seq][max_pages], its first held[b] columns; page_table_out of the same shape (its
+ *           other columns are copies); held [n_seq], read
+ *   free_pages [n_free], free_count [1]: the stack; its pages differ. free_pages_out [n_free]: the
+ *           stack after, its lowest page on top (entries from free_count on are copies)
+ *   shared, shared_out [n_free]: a page's count moves with it
+ *   move_src, move_dst [max_moves]: the moves, then -1
+ *   info    {status, moves, pages in use, moves left for another call}. Status 4 also: a free page
+ *           outside the pool or twice on the stack.
+ *   workspace >= ga_page_compact_workspace_bytes(n_free) bytes, 16-byte aligned, not shared with a
+ *           concurrent call
+ * Pages that are not on the stack are in use, whether or not a row holds them.
+ * Rules: 0 <= n_seq <= GA_PLAN_MAX_SEQ, max_pages >= 1, n_seq * max_pages < 2^30, 0 <= n_free <
+ * 2^30, max_moves >= 0.
+ * Errors: NULL, SHAPE, RANGE, ALIGN, WORKSPACE, DEVICE, CUDA. */
+int ga_page_compact(int n_seq, const int* page_table, int* page_table_out, int max_pages,
+                    const int* held, const int* free_pages, int* free_pages_out, int n_free,
+                    const int* free_count, const int* shared, int* shared_out, int max_moves,
+                    int* move_src, int* move_dst, int* info, void* workspace, size_t ws_bytes,
+                    ga_stream stream);
+
+#define GA_PAGE_COPY_POOLS 16 /* pools of one ga_page_copy call */
+
+/* Copies whole pages inside each of several pools: page src[i] to page dst[i], in all of them, one
+ * launch. Any pools of pages do: bf16, 4-bit and 8-bit ones, codes and scales.
+ *   pools      HOST array of n_pools DEVICE pointers; page p of pool j begins at byte p * page_bytes[j]
+ *   page_bytes HOST array of n_pools sizes; any size and alignment is right, multiples of 16 at
+ *              16-byte aligned addresses are fast
+ *   src, dst   DEVICE int32 [n_copies], 4-byte aligned. An entry with either negative is passed
+ *              over; one outside the pool is passed over and records status 3. No page is written
+ *              twice, or read and written, in one call (else its contents are unspecified); a page
+ *              may be read many times
+ * Rules: 1 <= n_pools <= GA_PAGE_COPY_POOLS, n_pages >= 0, 1 <= page_bytes[j] <= 2^30, 0 <= n_copies < 2^30. n_copies
+ * or n_pages = 0 is a no-op.
+ * Errors: NULL, SHAPE, RANGE, ALIGN, DEVICE, CUDA. */
+int ga_page_copy(void* const* pools, const size_t* page_bytes, int n_pools, int n_pages,
+                 const int* src, const int* dst, int n_copies, ga_stream stream);
 
 #ifdef __cplusplus
 }

@@ -593,3 +593,159 @@ def verify_q4(q_prep, gate, k, v, seq_len, heads=None):
                 out[b, r, h] = (w @ vb[:T, kv]) * sig[b, r, h]
                 mass[b, r, h] = (w @ np.abs(vb[:T, kv])) * sig[b, r, h]
     return out, mass
+
+
+# ----------------------------------------------------------------------------------
+# Serving over an 8-bit paged cache, and pages that several sequences hold (additions)
+# ----------------------------------------------------------------------------------
+Q8_BLOCK = 32
+Q8_MIN_EXP, Q8_MAX_EXP = -32, 31
+
+
+def q8_exponent(amax):
+    """The least e in [-32, 31] with amax <= 448 * 2^e; 31 if none."""
+    amax = np.asarray(amax, np.float64)
+    m, e = np.frexp(np.where(np.isfinite(amax), amax, 2.0 ** 127))       # 448 = 0.875 * 2^9
+    e = np.where(amax > 0, e - 9 + (m > 0.875), Q8_MIN_EXP)
+    return np.clip(e, Q8_MIN_EXP, Q8_MAX_EXP).astype(np.int64)
+
+
+def e4m3_sat(x):
+    """e4m3 nearest (ties to even), saturating at +-448; NaN counts as 0."""
+    x = np.asarray(x, np.float64)
+    return e4m3(np.clip(np.where(np.isnan(x), 0.0, x), -448.0, 448.0))
+
+
+def q8_store(values, exps, rows, slots):
+    """ga_kv_quantize_q8 for one head: `values` [n_slots, 256] the codes' e4m3 values and `exps`
+    [n_slots / 32] the blocks' exponents, updated in place with rows [n, 256] at slots (-1: none)."""
+    rows = np.asarray(rows, np.float64)
+    rows = np.where(np.isnan(rows), 0.0, rows)
+    blocks = {}
+    for t, s in enumerate(slots):
+        if s >= 0:
+            blocks.setdefault(int(s) // Q8_BLOCK, []).append(t)
+    for b, toks in blocks.items():
+        e = int(q8_exponent(np.max(np.abs(rows[toks]))))
+        mine = [int(slots[t]) for t in toks]
+        if b * Q8_BLOCK not in mine:
+            was = int(exps[b])
+            if e > was:
+                others = [s for s in range(b * Q8_BLOCK, (b + 1) * Q8_BLOCK) if s not in mine]
+                values[others] = e4m3_sat(np.ldexp(values[others], was - e))
+            e = max(e, was)
+        exps[b] = e
+        values[mine] = e4m3_sat(np.ldexp(rows[toks], -e))
+
+
+def q8_widen(values, exps, slots):
+    """The widened rows at slots."""
+    slots = np.asarray(slots, np.int64)
+    return np.ldexp(values[slots], exps[slots // Q8_BLOCK][:, None])
+
+
+def e4m3_codes(values):
+    """The code bytes of e4m3 values (a zero's sign is kept)."""
+    v = np.asarray(values, np.float64)
+    a = np.abs(v)
+    m, e = np.frexp(a)                                # a = m 2^e, m in [0.5, 1)
+    normal = a >= 2.0 ** -6
+    code = np.where(normal, (e - 1 + 7) * 8 + np.rint(m * 16) - 8, np.rint(a * 512))
+    return (code + 128 * np.signbit(v)).astype(np.uint8)
+
+
+def page_fork(parent, child, lens, page_table, held, free_pages, free_count, shared, page_size):
+    """(page_table, held, free_count, shared, copy_src, copy_dst, info)."""
+    n = len(parent)
+    table = np.array(page_table, np.int64)
+    held, shared = np.array(held, np.int64), np.array(shared, np.int64)
+    cap, width = len(free_pages), table.shape[1]
+    src, dst = np.full(n, -1, np.int64), np.full(n, -1, np.int64)
+    count = int(free_count)
+
+    def refuse(status):
+        return table, held, count, shared, src, dst, np.array([status, 0, 0, 0])
+
+    if not 0 <= count <= cap or np.any(held < 0) or np.any(held > width):
+        return refuse(4)
+    used = [i for i in range(n) if parent[i] >= 0]
+    kids = [int(child[i]) for i in used]
+    for i in used:
+        p, c = int(parent[i]), int(child[i])
+        if p >= len(held) or not 0 <= c < len(held) or p == c or held[c] or kids.count(c) > 1:
+            return refuse(1)
+    for i in used:
+        if not 0 <= int(lens[i]) <= int(held[int(parent[i])]) * page_size:
+            return refuse(2)
+    if sum(int(lens[i]) % page_size > 0 for i in used) > count:
+        return refuse(3)
+    pages = taken = 0
+    for i in used:
+        p, c, (whole, tail) = int(parent[i]), int(child[i]), divmod(int(lens[i]), page_size)
+        table[c, :whole] = table[p, :whole]
+        for x in table[p, :whole]:
+            shared[x] += 1
+        pages += whole
+        held[c] = whole
+        if tail:
+            src[i], dst[i] = table[p, whole], free_pages[count - 1 - taken]
+            table[c, whole] = dst[i]
+            held[c] += 1
+            taken += 1
+    return table, held, count - taken, shared, src, dst, np.array([0, len(used), taken, pages])
+
+
+def page_release(keep, page_table, held, free_pages, free_count, shared, page_size):
+    """(held, free_pages, free_count, shared, info)."""
+    table = np.asarray(page_table, np.int64)
+    held, shared = np.array(held, np.int64), np.array(shared, np.int64)
+    stack, count = np.array(free_pages, np.int64), int(free_count)
+    cap, width = len(stack), table.shape[1]
+
+    def refuse(status):
+        return held, stack, count, shared, np.array([status, 0, 0, 0])
+
+    if not 0 <= count <= cap or np.any(held < 0) or np.any(held > width):
+        return refuse(4)
+    left = [int(h) if k < 0 else min(int(h), -(-int(k) // page_size)) for k, h in zip(keep, held)]
+    gone = [int(x) for b in range(len(left)) for x in table[b, left[b]:held[b]]]
+    times = {}
+    for x in gone:
+        times[x] = times.get(x, 0) + 1
+    if any(t > shared[x] + 1 for x, t in times.items()):
+        return refuse(5)
+    back = [x for x in dict.fromkeys(gone) if times[x] == shared[x] + 1]
+    if count + len(back) > cap:
+        return refuse(4)
+    rows = sum(a < int(b) for a, b in zip(left, held))
+    for x, t in times.items():
+        shared[x] = 0 if times[x] == shared[x] + 1 else shared[x] - t
+    stack[count:count + len(back)] = back
+    return (np.array(left, np.int64), stack, count + len(back), shared,
+            np.array([0, rows, len(back), len(gone)]))
+
+
+def page_compact(page_table, held, free_pages, free_count, shared, max_moves):
+    """(page_table, free_pages, shared, move_src, move_dst, info)."""
+    table = np.array(page_table, np.int64)
+    stack, shared = np.array(free_pages, np.int64), np.array(shared, np.int64)
+    n, count = len(stack), int(free_count)
+    src, dst = np.full(max_moves, -1, np.int64), np.full(max_moves, -1, np.int64)
+    free = [int(x) for x in stack[:max(count, 0)]]
+    if (not 0 <= count <= n or any(not 0 <= int(h) <= table.shape[1] for h in held)
+            or any(not 0 <= x < n for x in free) or len(set(free)) < len(free)):
+        return table, stack, shared, src, dst, np.array([4, 0, 0, 0])
+    live, is_free = n - count, set(free)
+    holes = [p for p in range(live) if p in is_free]
+    movers = [p for p in range(n - 1, live - 1, -1) if p not in is_free]
+    k = min(max_moves, len(holes))
+    src[:k], dst[:k] = movers[:k], holes[:k]
+    to = dict(zip(movers[:k], holes[:k]))
+    for b in range(len(held)):
+        for c in range(int(held[b])):
+            table[b, c] = to.get(int(table[b, c]), int(table[b, c]))
+    for s, d in to.items():
+        shared[d], shared[s] = shared[s], 0
+    left = (is_free - set(holes[:k])) | set(movers[:k])
+    stack[:count] = sorted(left, reverse=True)
+    return table, stack, shared, src, dst, np.array([0, k, live, len(holes) - k])

@@ -77,6 +77,18 @@ _SIGS = {
     "ga_verify_q4_workspace_bytes": (_SZ, []),
     "ga_attn_verify_q4": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _SZ,
                                _P]),
+    "ga_kv_quantize_q8": (_I, [_P, _LL, _P, _LL, _LL, _P, _P, _P, _P, _P, _I, _I, _P]),
+    "ga_kv_dequantize_q8": (_I, [_P, _P, _P, _P, _I, _I, _P, _LL, _P, _P, _P]),
+    "ga_verify_q8_workspace_bytes": (_SZ, []),
+    "ga_attn_verify_q8": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _P, _SZ,
+                               _P]),
+    "ga_page_fork": (_I, [_P, _P, _P, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P,
+                          _P]),
+    "ga_page_release": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P]),
+    "ga_page_compact_workspace_bytes": (_SZ, [_I]),
+    "ga_page_compact": (_I, [_I, _P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _SZ,
+                             _P]),
+    "ga_page_copy": (_I, [_P, _P, _I, _I, _P, _P, _I, _P]),
 }
 
 
@@ -645,3 +657,94 @@ def ga_attn_verify_q4(q_prep, qg, k_codes, k_scales, v_codes, v_scales, page_tab
                                        seq_len, out, workspace)
     _check(st, "ga_attn_verify_q4")
     return out
+
+
+# ------------------------------------------------------------------ serving over 8-bit pages
+Q8_ROW_BYTES, Q8_BLOCK_TOKENS = 256, 32
+
+
+def ga_kv_quantize_q8(k, v, k_codes, k_scales, v_codes, v_scales, slots=None):
+    """Stores bf16 rows k, v [n_tok, 2, 256] (the token stride may be larger) as 8-bit rows at slots
+    int32 [n_tok] (None: token t at slot t) of the pools k_codes, v_codes uint8 [n_pages, 2,
+    page_size, 256], k_scales, v_scales uint8 [n_pages, 2, page_size / 32]. Tokens of one block of 32
+    slots follow one another; negative slots are skipped. A block's first slot begins it anew; later
+    ones may raise its scale, to which its other codes are then moved."""
+    _check(_native().kv_quantize_q8(k, v, k_codes, k_scales, v_codes, v_scales, slots)[0],
+           "ga_kv_quantize_q8")
+
+
+def ga_kv_dequantize_q8(k_codes, k_scales, v_codes, v_scales, slots=None, n_tok=None, k_out=None,
+                        v_out=None):
+    """The widened rows at slots int32 [n_tok] (None: slots 0 .. n_tok - 1, by default the whole
+    pool) of 8-bit pools, (k_out, v_out) bf16 [n_tok, 2, 256]. Rows of negative slots are left as
+    they were (unspecified in outputs allocated here)."""
+    st, k_out, v_out = _native().kv_dequantize_q8(k_codes, k_scales, v_codes, v_scales, slots, n_tok,
+                                                  k_out, v_out)
+    _check(st, "ga_kv_dequantize_q8")
+    return k_out, v_out
+
+
+def ga_verify_q8_workspace_bytes() -> int:
+    return lib().ga_verify_q8_workspace_bytes()
+
+
+def ga_attn_verify_q8(q_prep, qg, k_codes, k_scales, v_codes, v_scales, page_table, seq_len,
+                      out=None, workspace=None):
+    """Decode (rows = 1) or verify windows over 8-bit paged caches: ga_attn_verify_q4's arguments
+    over the pools of ga_kv_quantize_q8. Returns out [n_seq, rows, 24*256]."""
+    st, out = _native().attn_verify_q8(q_prep, qg, k_codes, k_scales, v_codes, v_scales, page_table,
+                                       seq_len, out, workspace)
+    _check(st, "ga_attn_verify_q8")
+    return out
+
+
+# ------------------------------------------------------------------ pages of several sequences
+# `shared` int32 [n_free] counts the rows beyond the first that hold each page, beside ga_page_plan's
+# page_table, held, free_pages and free_count. What an *_out argument does not take is updated in
+# place. info[0] is a status; when it is not 0 nothing is done.
+def ga_page_fork(parent, child, lens, page_table, held, free_pages, free_count, shared, page_size,
+                 held_out=None, free_count_out=None, shared_out=None, copy_src=None, copy_dst=None,
+                 info=None):
+    """Row child[i] becomes a branch of the first lens[i] tokens of row parent[i] (negative: unused
+    entry): their whole pages are held by both, a page begun is taken from the stack and to be copied
+    (ga_page_copy). Returns (copy_src [n_fork], copy_dst [n_fork], info [4]: status, forks, pages
+    taken, pages shared)."""
+    st, *outputs = _native().page_fork(parent, child, lens, page_table, held, free_pages, free_count,
+                                       shared, page_size, held_out, free_count_out, shared_out,
+                                       copy_src, copy_dst, info)
+    _check(st, "ga_page_fork")
+    return tuple(outputs)
+
+
+def ga_page_release(keep, page_table, held, free_pages, free_count, shared, page_size, held_out=None,
+                    free_count_out=None, shared_out=None, info=None):
+    """Row b keeps the pages of its first keep[b] tokens (0: finished, negative: as it is); pages that
+    no row holds any more go on the stack. Returns info [4]: status, rows that let pages go, pages put
+    on the stack, pages let go."""
+    st, info = _native().page_release(keep, page_table, held, free_pages, free_count, shared, page_size,
+                                      held_out, free_count_out, shared_out, info)
+    _check(st, "ga_page_release")
+    return info
+
+
+def ga_page_compact_workspace_bytes(n_free: int) -> int:
+    return lib().ga_page_compact_workspace_bytes(n_free)
+
+
+def ga_page_compact(page_table, held, free_pages, free_count, shared, max_moves, page_table_out=None,
+                    free_pages_out=None, shared_out=None, move_src=None, move_dst=None, info=None,
+                    workspace=None):
+    """At most max_moves moves of the highest pages in use to the lowest free ones, until the pages in
+    use fill the front of the pool; their contents are to be copied (ga_page_copy). Returns (move_src
+    [max_moves], move_dst [max_moves], info [4]: status, moves, pages in use, moves left)."""
+    st, *outputs = _native().page_compact(page_table, held, free_pages, free_count, shared, max_moves,
+                                          page_table_out, free_pages_out, shared_out, move_src,
+                                          move_dst, info, workspace)
+    _check(st, "ga_page_compact")
+    return tuple(outputs)
+
+
+def ga_page_copy(pools, src, dst):
+    """Copies page src[i] to page dst[i] in each of up to 16 pools (contiguous tensors [n_pages, ...]
+    of any type); src, dst int32 [n] on the device, entries with a negative one are passed over."""
+    _check(_native().page_copy(pools, src, dst)[0], "ga_page_copy")

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstring>
 #include <algorithm>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -1413,6 +1414,235 @@ int ga_attn_verify_q4(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k
     if (e != cudaSuccess) return fail_cuda(e);
   }
   return GA_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- 8-bit paged serving
+namespace ga {
+namespace {
+// The checks that the 8-bit cache calls share (no CUDA call).
+int check_q8_pools(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                   const uint8_t* v_scales, int n_pages, int page_size) {
+  if (!k_codes || !k_scales || !v_codes || !v_scales) return GA_ERR_NULL;
+  if (n_pages < 1 || page_size < 1) return GA_ERR_SHAPE;
+  if (page_size % GA_Q8_BLOCK_TOKENS != 0 || page_size > GA_MAX_TOKENS ||
+      (long long)n_pages * page_size >= (1LL << 30))
+    return GA_ERR_RANGE;
+  if (!aligned(k_codes, 16) || !aligned(v_codes, 16)) return GA_ERR_ALIGN;
+  return GA_OK;
+}
+// The checks that the calls over pages share.
+int check_pages(int n_seq, int max_pages, int n_free, std::initializer_list<const void*> arrays) {
+  for (const void* p : arrays)
+    if (!p) return GA_ERR_NULL;
+  if (n_seq < 0 || max_pages < 1 || n_free < 0) return GA_ERR_SHAPE;
+  if (n_seq > GA_PLAN_MAX_SEQ || (long long)n_seq * max_pages >= (1LL << 30) || n_free >= (1 << 30))
+    return GA_ERR_RANGE;
+  for (const void* p : arrays)
+    if (!aligned(p, 4)) return GA_ERR_ALIGN;
+  return GA_OK;
+}
+// Of the page size, between the shapes and the alignments of check_pages.
+int check_page_size(int page_size, int max_pages, int n_free) {
+  if (page_size < 1) return GA_ERR_SHAPE;
+  if ((long long)max_pages * page_size > 0x7FFFFFFFLL || (long long)n_free * page_size > 0x7FFFFFFFLL)
+    return GA_ERR_RANGE;
+  return GA_OK;
+}
+}  // namespace
+}  // namespace ga
+
+extern "C" {
+
+int ga_kv_quantize_q8(const ga_bf16* k, long long ld_k, const ga_bf16* v, long long ld_v,
+                      long long n_tok, const int* slots, uint8_t* k_codes, uint8_t* k_scales,
+                      uint8_t* v_codes, uint8_t* v_scales, int n_pages, int page_size,
+                      ga_stream stream) {
+  if (!k || !v) return GA_ERR_NULL;
+  int st = check_q8_pools(k_codes, k_scales, v_codes, v_scales, n_pages, page_size);
+  if (st != GA_OK) return st;
+  st = check_q4_tokens(n_tok, slots, n_pages, page_size);
+  if (st != GA_OK) return st;
+  if (ld_k < kKvHeads * kDim || ld_v < kKvHeads * kDim || ld_k > (1LL << 32) || ld_v > (1LL << 32))
+    return GA_ERR_RANGE;
+  if (!aligned(k, 16) || !aligned(v, 16) || ld_k % 8 != 0 || ld_v % 8 != 0) return GA_ERR_ALIGN;
+  if (n_tok == 0) return GA_OK;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != GA_OK) return st;
+  Kv8Args a{};
+  a.k = k; a.v = v; a.ld_k = ld_k; a.ld_v = ld_v;
+  a.k_codes = k_codes; a.k_scales = k_scales; a.v_codes = v_codes; a.v_scales = v_scales;
+  a.slots = slots; a.n_tok = n_tok;
+  a.n_slots = (long long)n_pages * page_size; a.page_size = page_size;
+  a.status = dev->status_word;
+  const cudaError_t e = GA_CUDA(launch_quantize_q8(a, (cudaStream_t)stream));
+  return e == cudaSuccess ? GA_OK : fail_cuda(e);
+}
+
+int ga_kv_dequantize_q8(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                        const uint8_t* v_scales, int n_pages, int page_size, const int* slots,
+                        long long n_tok, ga_bf16* k_out, ga_bf16* v_out, ga_stream stream) {
+  if (!k_out || !v_out) return GA_ERR_NULL;
+  int st = check_q8_pools(k_codes, k_scales, v_codes, v_scales, n_pages, page_size);
+  if (st != GA_OK) return st;
+  st = check_q4_tokens(n_tok, slots, n_pages, page_size);
+  if (st != GA_OK) return st;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return GA_ERR_ALIGN;
+  if (n_tok == 0) return GA_OK;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != GA_OK) return st;
+  Kv8Args a{};
+  a.k_codes = const_cast<uint8_t*>(k_codes); a.k_scales = const_cast<uint8_t*>(k_scales);
+  a.v_codes = const_cast<uint8_t*>(v_codes); a.v_scales = const_cast<uint8_t*>(v_scales);
+  a.slots = slots; a.n_tok = n_tok;
+  a.n_slots = (long long)n_pages * page_size; a.page_size = page_size;
+  a.k_out = k_out; a.v_out = v_out;
+  a.status = dev->status_word;
+  const cudaError_t e = GA_CUDA(launch_dequantize_q8(a, (cudaStream_t)stream));
+  return e == cudaSuccess ? GA_OK : fail_cuda(e);
+}
+
+size_t ga_verify_q8_workspace_bytes(void) { return verify4_ws_bytes(); }
+
+int ga_attn_verify_q8(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k_codes,
+                      const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                      int n_pages, int page_size, const int* page_table, int max_pages,
+                      const int* seq_len, int n_seq, int rows, ga_bf16* out, void* workspace,
+                      size_t ws_bytes, ga_stream stream) {
+  if (!q_prep || !qg || !page_table || !seq_len || !out) return GA_ERR_NULL;
+  int st = check_q8_pools(k_codes, k_scales, v_codes, v_scales, n_pages, page_size);
+  if (st != GA_OK) return st;
+  if (n_seq < 0 || rows < 0 || max_pages < 1) return GA_ERR_SHAPE;
+  if (rows > kVerifyMaxRows || n_seq > GA_MAX_TOKENS) return GA_ERR_RANGE;
+  if (!aligned(q_prep, 16) || !aligned(qg, 16) || !aligned(out, 16) || !aligned(page_table, 4) ||
+      !aligned(seq_len, 4))
+    return GA_ERR_ALIGN;
+  if (n_seq == 0 || rows == 0) return GA_OK;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < ga_verify_q8_workspace_bytes())
+    return GA_ERR_WORKSPACE;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != GA_OK) return st;
+  Verify8Args a{};
+  a.q_prep = q_prep; a.qg = qg; a.out = out;
+  a.k_codes = k_codes; a.k_scales = k_scales; a.v_codes = v_codes; a.v_scales = v_scales;
+  a.page_table = page_table; a.seq_len = seq_len;
+  a.n_seq = n_seq; a.rows = rows; a.page_size = page_size; a.max_pages = max_pages; a.n_pages = n_pages;
+  a.status = dev->status_word;
+  const cudaError_t e = GA_CUDA(launch_verify8(a, (cudaStream_t)stream));
+  return e == cudaSuccess ? GA_OK : fail_cuda(e);
+}
+
+// ---------------------------------------------------------------- pages of several sequences
+int ga_page_fork(const int* parent, const int* child, const int* len, int n_fork, int n_seq,
+                 int page_size, int* page_table, int max_pages, const int* held, int* held_out,
+                 const int* free_pages, int n_free, const int* free_count, int* free_count_out,
+                 const int* shared, int* shared_out, int* copy_src, int* copy_dst, int* info,
+                 ga_stream stream) {
+  int st = check_pages(n_seq, max_pages, n_free,
+                       {parent, child, len, page_table, held, held_out, free_pages, free_count,
+                        free_count_out, shared, shared_out, copy_src, copy_dst, info});
+  if (st != GA_OK) return st;
+  if (n_fork < 0) return GA_ERR_SHAPE;
+  if (n_fork > GA_PLAN_MAX_SEQ) return GA_ERR_RANGE;
+  if ((st = check_page_size(page_size, max_pages, n_free)) != GA_OK) return st;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != GA_OK) return st;
+  ForkArgs a{};
+  a.parent = parent; a.child = child; a.len = len;
+  a.n_fork = n_fork; a.n_seq = n_seq; a.page_size = page_size; a.max_pages = max_pages;
+  a.page_table = page_table; a.held = held; a.held_out = held_out;
+  a.free_pages = free_pages; a.n_free = n_free;
+  a.free_count = free_count; a.free_count_out = free_count_out;
+  a.shared = shared; a.shared_out = shared_out;
+  a.copy_src = copy_src; a.copy_dst = copy_dst; a.info = info;
+  a.status = dev->status_word;
+  const cudaError_t e = GA_CUDA(launch_page_fork(a, (cudaStream_t)stream));
+  return e == cudaSuccess ? GA_OK : fail_cuda(e);
+}
+
+int ga_page_release(const int* keep, int n_seq, int page_size, const int* page_table,
+                    int max_pages, const int* held, int* held_out, int* free_pages, int n_free,
+                    const int* free_count, int* free_count_out, const int* shared,
+                    int* shared_out, int* info, ga_stream stream) {
+  int st = check_pages(n_seq, max_pages, n_free,
+                       {keep, page_table, held, held_out, free_pages, free_count, free_count_out,
+                        shared, shared_out, info});
+  if (st != GA_OK) return st;
+  if ((st = check_page_size(page_size, max_pages, n_free)) != GA_OK) return st;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != GA_OK) return st;
+  ReleaseArgs a{};
+  a.keep = keep; a.n_seq = n_seq; a.page_size = page_size; a.max_pages = max_pages;
+  a.page_table = page_table; a.held = held; a.held_out = held_out;
+  a.free_pages = free_pages; a.n_free = n_free;
+  a.free_count = free_count; a.free_count_out = free_count_out;
+  a.shared = shared; a.shared_out = shared_out; a.info = info;
+  a.status = dev->status_word;
+  const cudaError_t e = GA_CUDA(launch_page_release(a, (cudaStream_t)stream));
+  return e == cudaSuccess ? GA_OK : fail_cuda(e);
+}
+
+size_t ga_page_compact_workspace_bytes(int n_free) {
+  return n_free < 0 ? 0 : ((size_t)n_free * sizeof(int) + 255) / 256 * 256;
+}
+
+int ga_page_compact(int n_seq, const int* page_table, int* page_table_out, int max_pages,
+                    const int* held, const int* free_pages, int* free_pages_out, int n_free,
+                    const int* free_count, const int* shared, int* shared_out, int max_moves,
+                    int* move_src, int* move_dst, int* info, void* workspace, size_t ws_bytes,
+                    ga_stream stream) {
+  int st = check_pages(n_seq, max_pages, n_free,
+                       {page_table, page_table_out, held, free_pages, free_pages_out, free_count,
+                        shared, shared_out, move_src, move_dst, info});
+  if (st != GA_OK) return st;
+  if (max_moves < 0) return GA_ERR_SHAPE;
+  if (ws_bytes < ga_page_compact_workspace_bytes(n_free) ||
+      (n_free > 0 && (!workspace || !aligned(workspace, 16))))
+    return GA_ERR_WORKSPACE;
+  DeviceState* dev = nullptr;
+  st = current_device(&dev);
+  if (st != GA_OK) return st;
+  CompactArgs a{};
+  a.n_seq = n_seq; a.max_pages = max_pages;
+  a.page_table = page_table; a.page_table_out = page_table_out; a.held = held;
+  a.free_pages = free_pages; a.free_pages_out = free_pages_out; a.n_free = n_free;
+  a.free_count = free_count; a.shared = shared; a.shared_out = shared_out;
+  a.max_moves = max_moves; a.move_src = move_src; a.move_dst = move_dst; a.info = info;
+  a.map = static_cast<int*>(workspace);
+  a.status = dev->status_word;
+  const cudaError_t e = GA_CUDA(launch_page_compact(a, (cudaStream_t)stream));
+  return e == cudaSuccess ? GA_OK : fail_cuda(e);
+}
+
+int ga_page_copy(void* const* pools, const size_t* page_bytes, int n_pools, int n_pages,
+                 const int* src, const int* dst, int n_copies, ga_stream stream) {
+  if (!pools || !page_bytes || !src || !dst) return GA_ERR_NULL;
+  if (n_pools < 1 || n_pages < 0 || n_copies < 0) return GA_ERR_SHAPE;
+  if (n_pools > GA_PAGE_COPY_POOLS || n_copies >= (1 << 30)) return GA_ERR_RANGE;
+  PageCopyArgs a{};
+  for (int j = 0; j < n_pools; ++j) {
+    if (!pools[j]) return GA_ERR_NULL;
+    if (page_bytes[j] < 1) return GA_ERR_SHAPE;
+    if (page_bytes[j] > ((size_t)1 << 30)) return GA_ERR_RANGE;
+    a.pool[j].base = static_cast<uint8_t*>(pools[j]);
+    a.pool[j].bytes = (long long)page_bytes[j];
+  }
+  if (!aligned(src, 4) || !aligned(dst, 4)) return GA_ERR_ALIGN;
+  if (n_copies == 0 || n_pages == 0) return GA_OK;
+  DeviceState* dev = nullptr;
+  const int st = current_device(&dev);
+  if (st != GA_OK) return st;
+  a.n_pools = n_pools; a.n_pages = n_pages; a.n_copies = n_copies;
+  a.src = src; a.dst = dst;
+  a.status = dev->status_word;
+  const cudaError_t e = GA_CUDA(launch_page_copy(a, dev->sm_count, (cudaStream_t)stream));
+  return e == cudaSuccess ? GA_OK : fail_cuda(e);
 }
 
 }  // extern "C"

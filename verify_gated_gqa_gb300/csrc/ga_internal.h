@@ -224,6 +224,91 @@ cudaError_t launch_decode4(const CUtensorMap& k_codes, const CUtensorMap& v_code
                            const CUtensorMap& k_scales, const CUtensorMap& v_scales,
                            const Verify4Args& a, int ctas, cudaStream_t s);
 
+// Pages that several sequences hold (ga_pages.cu).
+struct ForkArgs {
+  const int *parent, *child, *len;
+  int n_fork, n_seq, page_size, max_pages;
+  int* page_table;
+  const int* held;
+  int* held_out;
+  const int* free_pages;
+  int n_free;
+  const int* free_count;
+  int* free_count_out;
+  const int* shared;
+  int *shared_out, *copy_src, *copy_dst, *info;
+  int* status;
+};
+cudaError_t launch_page_fork(const ForkArgs& a, cudaStream_t s);
+struct ReleaseArgs {
+  const int* keep;
+  int n_seq, page_size, max_pages;
+  const int* page_table;
+  const int* held;
+  int* held_out;
+  int* free_pages;
+  int n_free;
+  const int* free_count;
+  int* free_count_out;
+  const int* shared;
+  int *shared_out, *info;
+  int* status;
+};
+cudaError_t launch_page_release(const ReleaseArgs& a, cudaStream_t s);
+struct CompactArgs {
+  int n_seq, max_pages;
+  const int* page_table;
+  int* page_table_out;
+  const int* held;
+  const int* free_pages;
+  int* free_pages_out;
+  int n_free;
+  const int* free_count;
+  const int* shared;
+  int* shared_out;
+  int max_moves;
+  int *move_src, *move_dst, *info;
+  int* map;                   // workspace: [n_free]
+  int* status;
+};
+cudaError_t launch_page_compact(const CompactArgs& a, cudaStream_t s);
+struct PageCopyArgs {
+  struct Pool {
+    uint8_t* base;
+    long long bytes;          // of a page
+    int width, first, pieces; // set by the launcher
+  } pool[GA_PAGE_COPY_POOLS];
+  int n_pools, n_pages, n_copies, pieces;
+  const int *src, *dst;
+  int* status;
+};
+cudaError_t launch_page_copy(PageCopyArgs a, int sm_count, cudaStream_t s);
+
+// 8-bit cache rows of n_tok tokens by slot (ga_kv8.cu; slots null: token t is slot t).
+struct Kv8Args {
+  const uint16_t *k, *v;      // storing: rows of 2 x 256 values, ld_k / ld_v values apart
+  long long ld_k, ld_v;
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const int* slots;
+  long long n_tok, n_slots;
+  int page_size;
+  uint16_t *k_out, *v_out;    // widening: [n_tok][2][256]
+  int* status;
+};
+cudaError_t launch_quantize_q8(const Kv8Args& a, cudaStream_t s);
+cudaError_t launch_dequantize_q8(const Kv8Args& a, cudaStream_t s);
+
+// Attention over 8-bit paged caches (ga_verify8.cu).
+struct Verify8Args {
+  const uint16_t *q_prep, *qg;
+  uint16_t* out;
+  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const int *page_table, *seq_len;
+  int n_seq, rows, page_size, max_pages, n_pages;
+  int* status;
+};
+cudaError_t launch_verify8(const Verify8Args& a, cudaStream_t s);
+
 cudaError_t attn_set_smem_attribute();
 // Clusters of two attention CTAs (the e4m3 verify variant) that can run at once.
 cudaError_t attn_max_pair_clusters(int* n);

@@ -1,5 +1,5 @@
 // Native half of the binding for the calls that run once a decode step (ga_page_plan,
-// ga_qk_prologue_axes, ga_kv_quantize_q4, ga_kv_dequantize_q4, ga_attn_verify_q4): the checks of
+// ga_qk_prologue_axes, the 4-bit and 8-bit cache calls, the calls over pages): the checks of
 // their torch tensors, the outputs that the caller did not give, and the call of the C ABI, in one
 // step. In Python the same checks and calls took 18 to 25 microseconds of host time, longer than
 // the kernels of a small step; here 4 to 9 (12 for the attention on one host).
@@ -78,18 +78,25 @@ struct Call {
   void* stream() const { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 };
 
+// The four pools of a quantised cache: codes [n_pages, 2, page_size, row_bytes]; scales [n_pages, 2,
+// page_size, 16] beside 4-bit codes, [n_pages, 2, page_size / 32] beside 8-bit ones.
 struct Pools {
   uint8_t *kc, *ks, *vc, *vs;
   int n_pages, page_size;
-  Pools(const Call& c, PyObject* const* a) {
+  Pools(const Call& c, PyObject* const* a, bool q8) {
     const Tensor& t = tensor(a[0], "k_codes");
-    if (t.dim() != 4) value_error("k_codes must be [n_pages, 2, page_size, 128]");
+    const int64_t row = q8 ? GA_Q8_ROW_BYTES : GA_Q4_ROW_BYTES;
+    if (t.dim() != 4) value_error("k_codes must be [n_pages, 2, page_size, " + std::to_string(row) + "]");
     const int64_t n = t.size(0), page = t.size(2);
     if (n > INT32_MAX || page > INT32_MAX) value_error("k_codes is too large");
-    kc = c.at<uint8_t>(t, "k_codes", kU8, {n, kHeadsKv, page, GA_Q4_ROW_BYTES});
-    ks = c.at<uint8_t>(a[1], "k_scales", kU8, {n, kHeadsKv, page, GA_Q4_SCALE_BYTES});
-    vc = c.at<uint8_t>(a[2], "v_codes", kU8, {n, kHeadsKv, page, GA_Q4_ROW_BYTES});
-    vs = c.at<uint8_t>(a[3], "v_scales", kU8, {n, kHeadsKv, page, GA_Q4_SCALE_BYTES});
+    auto scales = [&](PyObject* o, const char* name) {
+      return q8 ? c.at<uint8_t>(o, name, kU8, {n, kHeadsKv, page / GA_Q8_BLOCK_TOKENS})
+                : c.at<uint8_t>(o, name, kU8, {n, kHeadsKv, page, GA_Q4_SCALE_BYTES});
+    };
+    kc = c.at<uint8_t>(t, "k_codes", kU8, {n, kHeadsKv, page, row});
+    ks = scales(a[1], "k_scales");
+    vc = c.at<uint8_t>(a[2], "v_codes", kU8, {n, kHeadsKv, page, row});
+    vs = scales(a[3], "v_scales");
     n_pages = (int)n;
     page_size = (int)page;
   }
@@ -239,30 +246,32 @@ const uint16_t* kv_rows(const Call& c, PyObject* o, const char* name, int64_t n,
 }
 
 // (k, v, k_codes, k_scales, v_codes, v_scales, slots)
-PyObject* kv_quantize_q4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+template <bool kQ8>
+PyObject* kv_quantize(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   HANDLE_TH_ERRORS
   expect(n_args, 7);
   const Tensor& k = tensor(a[0], "k");
   const Call c(k, "k");
   if (k.dim() != 3) value_error("k must be [n_tok, 2, 256]");
   const int64_t n = k.size(0);
-  const Pools p(c, a + 2);
+  const Pools p(c, a + 2, kQ8);
   int64_t ld_k, ld_v;
   const uint16_t *k_at = kv_rows(c, a[0], "k", n, ld_k), *v_at = kv_rows(c, a[1], "v", n, ld_v);
   const int st = without_gil(
-      ga_kv_quantize_q4, k_at, ld_k, v_at, ld_v, n,
-                                   a[6] == Py_None ? nullptr : c.at<int>(a[6], "slots", kI32, {n}),
-                                   p.kc, p.ks, p.vc, p.vs, p.n_pages, p.page_size, c.stream());
+      kQ8 ? ga_kv_quantize_q8 : ga_kv_quantize_q4, k_at, ld_k, v_at, ld_v, n,
+      a[6] == Py_None ? nullptr : c.at<int>(a[6], "slots", kI32, {n}), p.kc, p.ks, p.vc, p.vs, p.n_pages,
+      p.page_size, c.stream());
   return result(st, {});
   END_HANDLE_TH_ERRORS
 }
 
 // (k_codes, k_scales, v_codes, v_scales, slots, n_tok, k_out, v_out)
-PyObject* kv_dequantize_q4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+template <bool kQ8>
+PyObject* kv_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   HANDLE_TH_ERRORS
   expect(n_args, 8);
   const Call c(tensor(a[0], "k_codes"), "k_codes");
-  const Pools p(c, a);
+  const Pools p(c, a, kQ8);
   int64_t n = (int64_t)p.n_pages * p.page_size;
   const int* slots = nullptr;
   if (a[4] != Py_None) {
@@ -278,32 +287,32 @@ PyObject* kv_dequantize_q4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   const Tensor k_out = c.output(a[6], "k_out", kBf16, {n, kHeadsKv, kDim}),
                v_out = c.output(a[7], "v_out", kBf16, {n, kHeadsKv, kDim});
   const int st = without_gil(
-      ga_kv_dequantize_q4, p.kc, p.ks, p.vc, p.vs, p.n_pages, p.page_size, slots, n,
-                                     c.at<uint16_t>(k_out, "k_out", kBf16, {n, kHeadsKv, kDim}),
-                                     c.at<uint16_t>(v_out, "v_out", kBf16, {n, kHeadsKv, kDim}),
-                                     c.stream());
+      kQ8 ? ga_kv_dequantize_q8 : ga_kv_dequantize_q4, p.kc, p.ks, p.vc, p.vs, p.n_pages, p.page_size, slots,
+      n, c.at<uint16_t>(k_out, "k_out", kBf16, {n, kHeadsKv, kDim}),
+      c.at<uint16_t>(v_out, "v_out", kBf16, {n, kHeadsKv, kDim}), c.stream());
   return result(st, {k_out, v_out});
   END_HANDLE_TH_ERRORS
 }
 
 // (q_prep, qg, k_codes, k_scales, v_codes, v_scales, page_table, seq_len, out, workspace)
-PyObject* attn_verify_q4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+template <bool kQ8>
+PyObject* attn_verify(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   HANDLE_TH_ERRORS
   expect(n_args, 10);
   const Tensor& q = tensor(a[0], "q_prep");
   const Call c(q, "q_prep");
   if (q.dim() != 4) value_error("q_prep must be [n_seq, rows, 24, 256]");
   const int64_t n = q.size(0), rows = q.size(1);
-  const Pools p(c, a + 2);
+  const Pools p(c, a + 2, kQ8);
   const Tensor& table = tensor(a[6], "page_table");
   if (table.dim() != 2) value_error("page_table must be [n_seq, max_pages]");
   const int64_t width = table.size(1);
   const Tensor out = c.output(a[8], "out", kBf16, {n, rows, kHeadsQ * kDim});
-  const Tensor ws = c.output(a[9], "workspace", kU8, {(int64_t)ga_verify_q4_workspace_bytes()});
+  const Tensor ws = c.output(a[9], "workspace", kU8, {(int64_t)(kQ8 ? ga_verify_q8_workspace_bytes() : ga_verify_q4_workspace_bytes())});
   if (!ws.is_cuda() || ws.get_device() != c.dev || !ws.is_contiguous())
     value_error("workspace must be a contiguous tensor on the current CUDA device");
   const int st = without_gil(
-      ga_attn_verify_q4,
+      kQ8 ? ga_attn_verify_q8 : ga_attn_verify_q4,
       c.at<uint16_t>(q, "q_prep", kBf16, {n, rows, kHeadsQ, kDim}),
       c.at<uint16_t>(a[1], "qg", kBf16, {n, rows, kHeadsQ, 2 * kDim}), p.kc, p.ks, p.vc, p.vs, p.n_pages,
       p.page_size, c.at<int>(table, "page_table", kI32, {n, width}), extent(width, "page_table"),
@@ -314,12 +323,146 @@ PyObject* attn_verify_q4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   END_HANDLE_TH_ERRORS
 }
 
+// An input's own address where no output was given.
+int* or_input(const Call& c, PyObject* o, const char* name, std::initializer_list<int64_t> shape, int* in) {
+  return o == Py_None ? in : c.at<int>(o, name, kI32, shape);
+}
+// What the calls over pages share.
+struct PageState {
+  int64_t n, width, n_free;
+  int *table, *held, *free, *count, *shared;
+  PageState(const Call& c, PyObject* table_, PyObject* held_, PyObject* free_, PyObject* count_, PyObject* shared_) {
+    const Tensor &t = tensor(table_, "page_table"), &f = tensor(free_, "free_pages");
+    if (t.dim() != 2 || f.dim() != 1)
+      value_error("page_table must be [n_seq, max_pages] and free_pages [n_free]");
+    n = t.size(0);
+    width = t.size(1);
+    n_free = f.size(0);
+    table = c.at<int>(t, "page_table", kI32, {n, width});
+    held = c.at<int>(held_, "held", kI32, {n});
+    free = c.at<int>(f, "free_pages", kI32, {n_free});
+    count = c.at<int>(count_, "free_count", kI32, {1});
+    shared = c.at<int>(shared_, "shared", kI32, {n_free});
+  }
+};
+
+// (parent, child, lens, page_table, held, free_pages, free_count, shared, page_size, held_out,
+//  free_count_out, shared_out, copy_src, copy_dst, info)
+PyObject* page_fork(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  expect(n_args, 15);
+  const Tensor& parent = tensor(a[0], "parent");
+  const Call c(parent, "parent");
+  if (parent.dim() != 1) value_error("parent must be [n_fork]");
+  const int64_t m = parent.size(0);
+  const PageState s(c, a[3], a[4], a[5], a[6], a[7]);
+  const Tensor src = c.output(a[12], "copy_src", kI32, {m}), dst = c.output(a[13], "copy_dst", kI32, {m}),
+               info = c.output(a[14], "info", kI32, {4});
+  const int st = without_gil(
+      ga_page_fork, c.at<int>(parent, "parent", kI32, {m}), c.at<int>(a[1], "child", kI32, {m}),
+      c.at<int>(a[2], "lens", kI32, {m}), extent(m, "parent"), extent(s.n, "page_table"),
+      to_int(a[8], "page_size"), s.table, extent(s.width, "page_table"), s.held,
+      or_input(c, a[9], "held_out", {s.n}, s.held), s.free, extent(s.n_free, "free_pages"), s.count,
+      or_input(c, a[10], "free_count_out", {1}, s.count), s.shared,
+      or_input(c, a[11], "shared_out", {s.n_free}, s.shared), c.at<int>(src, "copy_src", kI32, {m}),
+      c.at<int>(dst, "copy_dst", kI32, {m}), c.at<int>(info, "info", kI32, {4}), c.stream());
+  return result(st, {src, dst, info});
+  END_HANDLE_TH_ERRORS
+}
+
+// (keep, page_table, held, free_pages, free_count, shared, page_size, held_out, free_count_out,
+//  shared_out, info)
+PyObject* page_release(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  expect(n_args, 11);
+  const Tensor& keep = tensor(a[0], "keep");
+  const Call c(keep, "keep");
+  const PageState s(c, a[1], a[2], a[3], a[4], a[5]);
+  const Tensor info = c.output(a[10], "info", kI32, {4});
+  const int st = without_gil(
+      ga_page_release, c.at<int>(keep, "keep", kI32, {s.n}), extent(s.n, "page_table"),
+      to_int(a[6], "page_size"), s.table, extent(s.width, "page_table"), s.held,
+      or_input(c, a[7], "held_out", {s.n}, s.held), s.free, extent(s.n_free, "free_pages"), s.count,
+      or_input(c, a[8], "free_count_out", {1}, s.count), s.shared,
+      or_input(c, a[9], "shared_out", {s.n_free}, s.shared), c.at<int>(info, "info", kI32, {4}), c.stream());
+  return result(st, {info});
+  END_HANDLE_TH_ERRORS
+}
+
+// (page_table, held, free_pages, free_count, shared, max_moves, page_table_out, free_pages_out,
+//  shared_out, move_src, move_dst, info, workspace)
+PyObject* page_compact(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  expect(n_args, 13);
+  const Call c(tensor(a[0], "page_table"), "page_table");
+  const PageState s(c, a[0], a[1], a[2], a[3], a[4]);
+  const int64_t m = to_int(a[5], "max_moves");
+  if (m < 0) value_error("max_moves must not be negative");
+  const Tensor src = c.output(a[9], "move_src", kI32, {m}), dst = c.output(a[10], "move_dst", kI32, {m}),
+               info = c.output(a[11], "info", kI32, {4});
+  const Tensor ws = c.output(a[12], "workspace", kU8,
+                             {(int64_t)ga_page_compact_workspace_bytes(extent(s.n_free, "free_pages"))});
+  if (!ws.is_cuda() || ws.get_device() != c.dev || !ws.is_contiguous())
+    value_error("workspace must be a contiguous tensor on the current CUDA device");
+  const int st = without_gil(
+      ga_page_compact, extent(s.n, "page_table"), s.table,
+      or_input(c, a[6], "page_table_out", {s.n, s.width}, s.table), extent(s.width, "page_table"), s.held,
+      s.free, or_input(c, a[7], "free_pages_out", {s.n_free}, s.free), extent(s.n_free, "free_pages"), s.count,
+      s.shared, or_input(c, a[8], "shared_out", {s.n_free}, s.shared), (int)m,
+      c.at<int>(src, "move_src", kI32, {m}), c.at<int>(dst, "move_dst", kI32, {m}),
+      c.at<int>(info, "info", kI32, {4}), ws.data_ptr(), ws.nbytes(), c.stream());
+  return result(st, {src, dst, info});
+  END_HANDLE_TH_ERRORS
+}
+
+// (pools, src, dst)
+PyObject* page_copy(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  expect(n_args, 3);
+  const Tensor& src = tensor(a[1], "src");
+  const Call c(src, "src");
+  if (src.dim() != 1) value_error("src must be [n_copies]");
+  const int64_t m = src.size(0);
+  THPObjectPtr seq(PySequence_Fast(a[0], "pools must be a sequence of tensors"));
+  if (!seq) throw python_error();
+  const Py_ssize_t n_pools = PySequence_Fast_GET_SIZE(seq.get());
+  if (n_pools < 1 || n_pools > GA_PAGE_COPY_POOLS)
+    value_error("pools must be 1 to " + std::to_string(GA_PAGE_COPY_POOLS) + " tensors");
+  void* base[GA_PAGE_COPY_POOLS];
+  size_t bytes[GA_PAGE_COPY_POOLS];
+  int64_t n_pages = 0;
+  for (Py_ssize_t i = 0; i < n_pools; ++i) {
+    const Tensor& t = tensor(PySequence_Fast_GET_ITEM(seq.get(), i), "pools");
+    if (t.dim() < 2 || !t.is_cuda() || t.get_device() != c.dev || !t.is_contiguous() ||
+        (i > 0 && t.size(0) != n_pages))
+      value_error("pools must be contiguous tensors [n_pages, ...] of the same n_pages on the current "
+                  "CUDA device");
+    n_pages = t.size(0);
+    bytes[i] = (size_t)t.element_size();
+    for (int64_t d = 1; d < t.dim(); ++d) bytes[i] *= (size_t)t.size(d);
+    void* p = t.data_ptr();
+    base[i] = p ? p : reinterpret_cast<void*>(256);
+  }
+  const int st = without_gil(ga_page_copy, base, bytes, (int)n_pools, extent(n_pages, "pools"),
+                             c.at<int>(src, "src", kI32, {m}), c.at<int>(a[2], "dst", kI32, {m}),
+                             extent(m, "src"), c.stream());
+  return result(st, {});
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef kMethods[] = {
     {"page_plan", (PyCFunction)(void*)page_plan, METH_FASTCALL, nullptr},
     {"qk_prologue_axes", (PyCFunction)(void*)qk_prologue_axes, METH_FASTCALL, nullptr},
-    {"kv_quantize_q4", (PyCFunction)(void*)kv_quantize_q4, METH_FASTCALL, nullptr},
-    {"kv_dequantize_q4", (PyCFunction)(void*)kv_dequantize_q4, METH_FASTCALL, nullptr},
-    {"attn_verify_q4", (PyCFunction)(void*)attn_verify_q4, METH_FASTCALL, nullptr},
+    {"kv_quantize_q4", (PyCFunction)(void*)kv_quantize<false>, METH_FASTCALL, nullptr},
+    {"kv_dequantize_q4", (PyCFunction)(void*)kv_dequantize<false>, METH_FASTCALL, nullptr},
+    {"attn_verify_q4", (PyCFunction)(void*)attn_verify<false>, METH_FASTCALL, nullptr},
+    {"kv_quantize_q8", (PyCFunction)(void*)kv_quantize<true>, METH_FASTCALL, nullptr},
+    {"kv_dequantize_q8", (PyCFunction)(void*)kv_dequantize<true>, METH_FASTCALL, nullptr},
+    {"attn_verify_q8", (PyCFunction)(void*)attn_verify<true>, METH_FASTCALL, nullptr},
+    {"page_fork", (PyCFunction)(void*)page_fork, METH_FASTCALL, nullptr},
+    {"page_release", (PyCFunction)(void*)page_release, METH_FASTCALL, nullptr},
+    {"page_compact", (PyCFunction)(void*)page_compact, METH_FASTCALL, nullptr},
+    {"page_copy", (PyCFunction)(void*)page_copy, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods};
 

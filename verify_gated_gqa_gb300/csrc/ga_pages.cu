@@ -1,0 +1,551 @@
+// Pages that several sequences hold: forks, pages given back, compaction, and the copies of pages
+// that forks and compactions ask for.
+//
+// The first three are bookkeeping over page tables, a stack of free pages and a count of further
+// holders a page. They move a few kilobytes and are bound by latency: a chain of dependent loads
+// (a length, an entry, a count) and the barriers between the steps that read and the ones that
+// write. Each is one launch of a team, one CTA of 1,024 threads or a cluster of eight, which every
+// step deals its entries to; the cluster's hardware barrier stands between the steps.
+// The order of what they write is fixed by the inputs alone: sums and counts, no race, decide
+// every place.
+#include <climits>
+
+#include "ga_internal.h"
+#include "ga_sm100.cuh"
+
+namespace ga {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kTeamCtas = 8;
+constexpr int kExchanges = 2;
+static_assert(GA_PLAN_MAX_SEQ == 2 * kThreads, "two rows a thread");
+
+__device__ __forceinline__ void record_page(int* status) { atomicCAS(status, 0, (int)kDevBadPage); }
+
+struct Pair {
+  unsigned a, b;
+};
+struct TeamSmem {
+  Pair warp_sum[kThreads / 32];
+  Pair sums[kExchanges][kTeamCtas];
+};
+
+template <int kCtas>
+struct Team {
+  TeamSmem& sm;
+  int rank, gid, size;
+  __device__ __forceinline__ explicit Team(TeamSmem& s)
+      : sm(s), rank(kCtas > 1 ? (int)cluster_ctarank() : 0), gid(rank * kThreads + (int)threadIdx.x),
+        size(kCtas * kThreads) {}
+  // All of the team; what was written before is seen after.
+  __device__ __forceinline__ void sync() const {
+    if (kCtas == 1) {
+      __syncthreads();
+    } else {
+      asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    }
+  }
+  // Sums over the threads of this CTA before this one, and over all of it.
+  __device__ __forceinline__ Pair block_scan(Pair v, Pair& total) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Pair inc = warp_scan(v, lane);
+    if (lane == 31) sm.warp_sum[warp] = inc;
+    __syncthreads();
+    const Pair w = sm.warp_sum[lane];
+    const Pair winc = warp_scan(w, lane);
+    const Pair before = {__shfl_sync(~0u, winc.a - w.a, warp) + inc.a - v.a,
+                         __shfl_sync(~0u, winc.b - w.b, warp) + inc.b - v.b};
+    total = {__shfl_sync(~0u, winc.a, 31), __shfl_sync(~0u, winc.b, 31)};
+    __syncthreads();   // warp_sum may be written again
+    return before;
+  }
+  // The same over the team; a sync. Exchange x is used once in a kernel (a CTA may still be reading
+  // its copy while another is past it).
+  __device__ __forceinline__ Pair scan(int x, Pair v, Pair& total) const {
+    Pair before = block_scan(v, total);
+    if (kCtas == 1) return before;
+    publish(x, total);
+    sync();
+    total = {0u, 0u};
+#pragma unroll
+    for (int r = 0; r < kCtas; ++r) {
+      const Pair o = sm.sums[x][r];
+      if (r < rank) before = {before.a + o.a, before.b + o.b};
+      total = {total.a + o.a, total.b + o.b};
+    }
+    return before;
+  }
+  // Whether v is set anywhere in the team; a sync.
+  __device__ __forceinline__ bool any(int x, bool v) const {
+    int r = __syncthreads_or(v);
+    if (kCtas == 1) return r != 0;
+    publish(x, Pair{(unsigned)r, 0u});
+    sync();
+#pragma unroll
+    for (int i = 0; i < kCtas; ++i) r |= (int)sm.sums[x][i].a;
+    return r != 0;
+  }
+
+ private:
+  __device__ __forceinline__ static Pair warp_scan(Pair v, int lane) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const unsigned a = __shfl_up_sync(~0u, v.a, off), b = __shfl_up_sync(~0u, v.b, off);
+      if (lane >= off) v = {v.a + a, v.b + b};
+    }
+    return v;
+  }
+  // This CTA's value into every CTA's copy.
+  __device__ __forceinline__ void publish(int x, Pair v) const {
+    if (threadIdx.x < kCtas) {
+      const uint32_t at = mapa_shared(smem_u32(&sm.sums[x][rank]), threadIdx.x);
+      asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(v.a), "r"(v.b) : "memory");
+    }
+  }
+};
+
+// n entries of one array to another, unless they are the same.
+template <int kCtas>
+__device__ __forceinline__ void copy_array(const Team<kCtas>& t, const int* from, int* to, int n) {
+  if (from == to) return;
+  for (int i = t.gid; i < n; i += t.size) to[i] = from[i];
+}
+
+// ------------------------------------------------------------------ forks
+// Every CTA checks all forks (two a thread) and forms the same sums; the whole pages of all forks,
+// end to end, are then dealt to the team's threads.
+template <int kCtas>
+__global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ ForkArgs a) {
+  __shared__ TeamSmem tsm;
+  __shared__ unsigned start[GA_PLAN_MAX_SEQ], named[GA_PLAN_MAX_SEQ / 32];
+  const Team<kCtas> team(tsm);
+  const int tid = threadIdx.x;
+  if (tid < GA_PLAN_MAX_SEQ / 32) named[tid] = 0u;
+  const int count = *a.free_count;
+  int err = count < 0 || count > a.n_free ? 8 : 0;
+  __syncthreads();
+  int parent[2], child[2], len[2], held_c[2] = {0, 0};
+  Pair need[2];   // whole pages, a page begun
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = 2 * tid + k;
+    parent[k] = -1;
+    need[k] = {0u, 0u};
+    if (i >= a.n_fork) continue;
+    parent[k] = a.parent[i];
+    child[k] = a.child[i];
+    len[k] = a.len[i];
+    if (parent[k] < 0) continue;
+    if (parent[k] >= a.n_seq || child[k] < 0 || child[k] >= a.n_seq || parent[k] == child[k]) {
+      err |= 1;
+      continue;
+    }
+    const int held_p = a.held[parent[k]];
+    held_c[k] = a.held[child[k]];
+    if (held_p < 0 || held_p > a.max_pages || held_c[k] < 0 || held_c[k] > a.max_pages) err |= 8;
+    if (held_c[k] != 0 || (atomicOr(&named[child[k] >> 5], 1u << (child[k] & 31)) >> (child[k] & 31) & 1u))
+      err |= 1;
+    if (len[k] < 0 || (long long)len[k] > (long long)held_p * a.page_size) {
+      err |= 2;
+      continue;
+    }
+    need[k] = {(unsigned)(len[k] / a.page_size), len[k] % a.page_size ? 1u : 0u};
+  }
+  Pair total;
+  const Pair before = team.block_scan(Pair{need[0].a + need[1].a, need[0].b + need[1].b}, total);
+  if (count >= 0 && total.b > (unsigned)count) err |= 4;
+  for (int b = tid; b < a.n_seq; b += kThreads)   // rows that no fork names count too
+    if (a.held[b] < 0 || a.held[b] > a.max_pages) err |= 8;
+  int all = 0;
+  for (int bit = 1; bit <= 8; bit <<= 1) all |= __syncthreads_or(err & bit) ? bit : 0;
+  const int status = all & 8 ? 4 : all & 1 ? 1 : all & 2 ? 2 : all & 4 ? 3 : 0;
+  int forks = 0;
+  if (status) total = {0u, 0u};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    start[2 * tid + k] = k ? before.a + need[0].a : before.a;
+    forks += parent[k] >= 0 && !status;
+  }
+  const int made = __syncthreads_count(forks > 0) + __syncthreads_count(forks > 1);
+  team.sync();   // every CTA has read what is written from here on
+  copy_array(team, a.held, a.held_out, a.n_seq);
+  copy_array(team, a.shared, a.shared_out, a.n_free);
+  team.sync();
+  if (team.rank == 0) {
+    if (tid == 0) {
+      *a.free_count_out = count - (int)total.b;
+      a.info[0] = status;
+      a.info[1] = made;
+      a.info[2] = (int)total.b;
+      a.info[3] = (int)total.a;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = 2 * tid + k;
+      if (i >= a.n_fork) continue;
+      int src = -1, dst = -1;
+      if (parent[k] >= 0 && !status) {
+        a.held_out[child[k]] = (int)(need[k].a + need[k].b);
+        if (need[k].b) {
+          src = a.page_table[(long long)parent[k] * a.max_pages + need[k].a];
+          dst = a.free_pages[count - 1 - (int)(k ? before.b + need[0].b : before.b)];
+          a.page_table[(long long)child[k] * a.max_pages + need[k].a] = dst;
+          if (src < 0 || src >= a.n_free || dst < 0 || dst >= a.n_free) {
+            record_page(a.status);
+            src = dst = -1;
+          }
+        }
+      }
+      a.copy_src[i] = src;
+      a.copy_dst[i] = dst;
+    }
+  }
+  for (unsigned i = team.gid; i < total.a; i += team.size) {
+    const int f = find_seq(start, a.n_fork, i);
+    const unsigned col = i - start[f];
+    const int page = a.page_table[(long long)a.parent[f] * a.max_pages + col];
+    a.page_table[(long long)a.child[f] * a.max_pages + col] = page;
+    if (page < 0 || page >= a.n_free) record_page(a.status);
+    else atomicAdd(a.shared_out + page, 1);
+  }
+}
+
+// ------------------------------------------------------------------ pages given back
+// The pages that the rows let go, end to end in order of row and column, are dealt to the team's
+// threads in runs. `shared` counts a page's holders less one, so once each place has taken one off,
+// a page is free where -1 is left, and one that found less than 0 was let go too often. A free page's
+// first place is found by a minimum over its places' numbers in the same word, from INT_MIN up.
+template <int kCtas>
+__global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant__ ReleaseArgs a) {
+  __shared__ TeamSmem tsm;
+  __shared__ unsigned start[GA_PLAN_MAX_SEQ];
+  __shared__ int kept[GA_PLAN_MAX_SEQ];
+  const Team<kCtas> team(tsm);
+  const int tid = threadIdx.x;
+  const int count = *a.free_count;
+  int err = count < 0 || count > a.n_free ? 8 : 0;
+  unsigned gone[2], rows = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int b = 2 * tid + k;
+    gone[k] = 0u;
+    if (b >= a.n_seq) continue;
+    const int held = a.held[b], keep = a.keep[b];
+    int left = held;
+    if (held < 0 || held > a.max_pages) {
+      err |= 8;
+    } else if (keep >= 0) {
+      left = min(held, (int)(((long long)keep + a.page_size - 1) / a.page_size));
+      gone[k] = (unsigned)(held - left);   // n_seq * max_pages < 2^30
+    }
+    kept[b] = left;
+    rows += gone[k] > 0;
+  }
+  Pair total;
+  const Pair before = team.block_scan(Pair{gone[0] + gone[1], rows}, total);
+  start[2 * tid] = before.a;
+  start[2 * tid + 1] = before.a + gone[0];
+  const bool range = __syncthreads_or(err) != 0;   // the same in every CTA
+  team.sync();   // every CTA has read what is written from here on
+  copy_array(team, a.shared, a.shared_out, a.n_free);
+  int status = range ? 4 : 0;
+  unsigned freed = 0;
+  if (!status && total.a > 0u) {
+    if (a.shared != a.shared_out) team.sync();
+    // this thread's places
+    const unsigned per = (total.a + team.size - 1) / team.size;
+    const unsigned lo = min(total.a, per * team.gid), hi = min(total.a, lo + per);
+    const int row0 = lo < hi ? find_seq(start, a.n_seq, lo) : 0;
+    // f(place, page) over them
+    auto each = [&](auto f) {
+      int b = row0;
+      for (unsigned i = lo; i < hi; ++i) {
+        while (b + 1 < a.n_seq && start[b + 1] <= i) ++b;
+        const int page = a.page_table[(long long)b * a.max_pages + kept[b] + (int)(i - start[b])];
+        if (page >= 0 && page < a.n_free) f(i, page);
+        else record_page(a.status);
+      }
+    };
+    volatile int* left = a.shared_out;
+    bool bad = false;
+    each([&](unsigned, int page) { bad |= atomicSub(a.shared_out + page, 1) < 0; });
+    if (team.any(0, bad)) {
+      status = 5;
+      each([&](unsigned, int page) { atomicAdd(a.shared_out + page, 1); });
+    } else {
+      each([&](unsigned i, int page) {
+        if (left[page] < 0) atomicMin(a.shared_out + page, INT_MIN + (int)i);
+      });
+      team.sync();
+      Pair own = {0u, 0u}, sum;
+      each([&](unsigned i, int page) { own.a += left[page] == INT_MIN + (int)i; });
+      unsigned to = team.scan(1, own, sum).a;
+      if ((long long)count + sum.a > a.n_free) {   // as it was
+        status = 4;
+        each([&](unsigned i, int page) {
+          if (left[page] == INT_MIN + (int)i) left[page] = -1;
+        });
+        team.sync();
+        each([&](unsigned, int page) { atomicAdd(a.shared_out + page, 1); });
+      } else {
+        freed = sum.a;
+        each([&](unsigned i, int page) {
+          if (left[page] != INT_MIN + (int)i) return;
+          a.free_pages[count + (int)to++] = page;
+          left[page] = 0;
+        });
+      }
+    }
+  }
+  for (int b = team.gid; b < a.n_seq; b += team.size)
+    if (status == 0) a.held_out[b] = kept[b];
+    else if (a.held_out != a.held) a.held_out[b] = a.held[b];
+  if (team.gid == 0) {
+    *a.free_count_out = count + (int)freed;
+    a.info[0] = status;
+    a.info[1] = status ? 0 : (int)total.b;
+    a.info[2] = (int)freed;
+    a.info[3] = status ? 0 : (int)total.a;
+  }
+}
+
+// ------------------------------------------------------------------ compaction
+// map[p] first tells whether page p is free, then where its contents go. Each thread has a run of
+// pages, in order, so that sums of free pages below n_live and of pages in use from it on give the
+// moves their numbers, and those give every place on the new stack.
+template <int kCtas>
+__global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ CompactArgs a, int remap) {
+  __shared__ TeamSmem tsm;
+  const Team<kCtas> team(tsm);
+  const int n = a.n_free, count = *a.free_count;
+  bool err = count < 0 || count > n;
+  for (int b = team.gid; b < a.n_seq; b += team.size) err |= a.held[b] < 0 || a.held[b] > a.max_pages;
+  for (int p = team.gid; p < n; p += team.size) a.map[p] = 0;
+  team.sync();
+  if (count >= 0 && count <= n) {
+    for (int i = team.gid; i < count; i += team.size) {
+      const int p = a.free_pages[i];
+      if (p < 0 || p >= n || atomicExch(a.map + p, 1) != 0) err = true;
+    }
+  }
+  const long long entries = (long long)a.n_seq * a.max_pages;
+  if (team.any(0, err)) {
+    if (a.page_table != a.page_table_out && remap)
+      for (long long i = team.gid; i < entries; i += team.size) a.page_table_out[i] = a.page_table[i];
+    copy_array(team, a.free_pages, a.free_pages_out, n);
+    copy_array(team, a.shared, a.shared_out, n);
+    for (int i = team.gid; i < a.max_moves; i += team.size) a.move_src[i] = a.move_dst[i] = -1;
+    if (team.gid < 4) a.info[team.gid] = team.gid == 0 ? 4 : 0;
+    return;
+  }
+  volatile int* map = a.map;
+  const int live = n - count;
+  const unsigned per = ((unsigned)n + team.size - 1) / team.size;
+  const int lo = (int)min((unsigned)n, per * team.gid), hi = (int)min((unsigned)n, lo + per);
+  Pair own = {0u, 0u}, sum;   // free pages below live, pages in use from it on: as many of each
+  for (int p = lo; p < hi; ++p) {
+    const int free = map[p];
+    own.a += p < live && free;
+    own.b += p >= live && !free;
+  }
+  const Pair at = team.scan(1, own, sum);
+  const int all = (int)sum.b, moves = min(a.max_moves, all);
+  {
+    int hole = (int)at.a, mover = all - 1 - (int)at.b;
+    for (int p = lo; p < hi; ++p) {
+      const int free = map[p];
+      if (p < live && free) {
+        if (hole < moves) a.move_dst[hole] = p;
+        ++hole;
+      } else if (p >= live && !free) {
+        if (mover < moves) a.move_src[mover] = p;
+        --mover;
+      }
+    }
+  }
+  for (int i = moves + team.gid; i < a.max_moves; i += team.size) a.move_src[i] = a.move_dst[i] = -1;
+  team.sync();
+  volatile int* dst = a.move_dst;
+  int hole = (int)at.a, mover = all - 1 - (int)at.b;
+  // free pages before p afterwards: the holes left, and past live every page but those still in use
+  for (int p = lo; p < hi; ++p) {
+    const int free = map[p];
+    const int past = max(p - live, 0), in_use = all - 1 - mover;   // movers before p
+    const int moved = max(0, in_use - (all - moves));              // and moved away
+    const int rank = max(hole - moves, 0) + past - in_use + moved;
+    int to = p;
+    bool free_after = free != 0;
+    bool keep_count = true;
+    if (p < live && free) {
+      if (hole < moves) {
+        free_after = false;
+        keep_count = false;
+      }
+      ++hole;
+    } else if (p >= live && !free) {
+      if (mover < moves) {
+        to = dst[mover];
+        free_after = true;
+        keep_count = false;
+        a.shared_out[to] = a.shared[p];
+        a.shared_out[p] = 0;
+      }
+      --mover;
+    }
+    map[p] = to;
+    if (keep_count && a.shared != a.shared_out) a.shared_out[p] = a.shared[p];
+    if (free_after) a.free_pages_out[count - 1 - rank] = p;
+  }
+  if (a.free_pages != a.free_pages_out)
+    for (int i = count + team.gid; i < n; i += team.size) a.free_pages_out[i] = a.free_pages[i];
+  if (team.gid == 0) {
+    a.info[0] = 0;
+    a.info[1] = moves;
+    a.info[2] = live;
+    a.info[3] = all - moves;
+  }
+  if (!remap) return;
+  team.sync();
+  for (long long i = team.gid; i < entries; i += team.size) {
+    const int b = (int)(i / a.max_pages), col = (int)(i - (long long)b * a.max_pages);
+    int p = a.page_table[i];
+    if (col < a.held[b]) {
+      if (p >= 0 && p < n) p = map[p];
+      else record_page(a.status);
+    }
+    a.page_table_out[i] = p;
+  }
+}
+
+// The table of a large batch: a CTA per kRemapEntries of it, after compact_kernel.
+constexpr int kRemapThreads = 256, kRemapEntries = 1024;
+__global__ void __launch_bounds__(kRemapThreads) remap_kernel(const __grid_constant__ CompactArgs a) {
+  const long long entries = (long long)a.n_seq * a.max_pages;
+  const bool refused = a.info[0] != 0;
+#pragma unroll
+  for (int k = 0; k < kRemapEntries / kRemapThreads; ++k) {
+    const long long i = (long long)blockIdx.x * kRemapEntries + k * kRemapThreads + threadIdx.x;
+    if (i >= entries) return;
+    const int b = (int)(i / a.max_pages), col = (int)(i - (long long)b * a.max_pages);
+    int p = a.page_table[i];
+    if (!refused && col < a.held[b]) {
+      if (p >= 0 && p < a.n_free) p = a.map[p];
+      else record_page(a.status);
+    }
+    a.page_table_out[i] = p;
+  }
+}
+
+// ------------------------------------------------------------------ copies of pages
+// An item is a 16 KiB piece of a copied page of one pool (256 threads x 4 x 16 bytes), or all of a
+// page in the pools whose pages are small (scales). Bound by the bytes, in and out.
+constexpr int kCopyThreads = 256, kCopyLoads = 4;
+
+template <typename T>
+__device__ __forceinline__ void copy_piece(const uint8_t* from, uint8_t* to, long long bytes, long long off) {
+  T v[kCopyLoads];
+#pragma unroll
+  for (int k = 0; k < kCopyLoads; ++k) {
+    const long long at = off + ((long long)k * kCopyThreads + threadIdx.x) * sizeof(T);
+    if (at < bytes) v[k] = *reinterpret_cast<const T*>(from + at);
+  }
+#pragma unroll
+  for (int k = 0; k < kCopyLoads; ++k) {
+    const long long at = off + ((long long)k * kCopyThreads + threadIdx.x) * sizeof(T);
+    if (at < bytes) *reinterpret_cast<T*>(to + at) = v[k];
+  }
+}
+__device__ __forceinline__ void copy_piece(const uint8_t* from, uint8_t* to, long long bytes, long long off, int width) {
+  switch (width) {
+    case 16: return copy_piece<uint4>(from, to, bytes, off);
+    case 8: return copy_piece<uint2>(from, to, bytes, off);
+    case 4: return copy_piece<uint32_t>(from, to, bytes, off);
+    case 2: return copy_piece<uint16_t>(from, to, bytes, off);
+    default: return copy_piece<uint8_t>(from, to, bytes, off);
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ PageCopyArgs a) {
+  const long long items = (long long)a.n_copies * a.pieces;
+  for (long long w = blockIdx.x; w < items; w += gridDim.x) {
+    const int i = (int)(w / a.pieces);
+    int piece = (int)(w - (long long)i * a.pieces);
+    const int src = a.src[i], dst = a.dst[i];
+    if (src < 0 || dst < 0) continue;
+    if (src >= a.n_pages || dst >= a.n_pages) {
+      if (threadIdx.x == 0) record_page(a.status);
+      continue;
+    }
+    for (int j = 0; j < a.n_pools; ++j) {
+      const PageCopyArgs::Pool& p = a.pool[j];
+      const uint8_t* from = p.base + src * p.bytes;
+      uint8_t* to = p.base + dst * p.bytes;
+      const int step = kCopyThreads * kCopyLoads * p.width;
+      if (p.pieces == 0) {   // small: with piece 0
+        if (piece == 0)
+          for (long long off = 0; off < p.bytes; off += step) copy_piece(from, to, p.bytes, off, p.width);
+      } else if (piece >= p.first && piece < p.first + p.pieces) {
+        copy_piece(from, to, p.bytes, (long long)(piece - p.first) * step, p.width);
+      }
+    }
+  }
+}
+
+// One CTA while a step's entries are few (its barriers are cheaper), else the cluster.
+constexpr long long kOneCtaEntries = 4096;
+template <typename K1, typename K8, typename... A>
+cudaError_t launch_team(K1 one, K8 eight, bool large, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(large ? kTeamCtas : 1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kTeamCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = large ? 1 : 0;
+  return large ? cudaLaunchKernelEx(&cfg, eight, args...) : cudaLaunchKernelEx(&cfg, one, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_page_fork(const ForkArgs& a, cudaStream_t s) {
+  const bool large = (long long)a.n_fork * a.max_pages > kOneCtaEntries || a.n_free > 4 * kOneCtaEntries;
+  return launch_team(fork_kernel<1>, fork_kernel<kTeamCtas>, large, s, a);
+}
+
+cudaError_t launch_page_release(const ReleaseArgs& a, cudaStream_t s) {
+  const bool large = (long long)a.n_seq * a.max_pages > kOneCtaEntries || a.n_free > 4 * kOneCtaEntries;
+  return launch_team(release_kernel<1>, release_kernel<kTeamCtas>, large, s, a);
+}
+
+cudaError_t launch_page_compact(const CompactArgs& a, cudaStream_t s) {
+  const long long entries = (long long)a.n_seq * a.max_pages;
+  const int remap = entries <= 16 * kOneCtaEntries ? 1 : 0;
+  const bool large = a.n_free > kOneCtaEntries || (remap && entries > kOneCtaEntries);
+  const cudaError_t e = launch_team(compact_kernel<1>, compact_kernel<kTeamCtas>, large, s, a, remap);
+  if (e != cudaSuccess || remap) return e;
+  remap_kernel<<<(unsigned)((entries + kRemapEntries - 1) / kRemapEntries), kRemapThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_page_copy(PageCopyArgs a, int sm_count, cudaStream_t s) {
+  a.pieces = 0;
+  for (int j = 0; j < a.n_pools; ++j) {
+    PageCopyArgs::Pool& p = a.pool[j];
+    const size_t both = reinterpret_cast<size_t>(p.base) | (size_t)p.bytes;
+    p.width = both % 16 == 0 ? 16 : both % 8 == 0 ? 8 : both % 4 == 0 ? 4 : both % 2 == 0 ? 2 : 1;
+    const long long step = (long long)kCopyThreads * kCopyLoads * p.width;
+    p.first = a.pieces;
+    p.pieces = p.bytes < 2048 ? 0 : (int)((p.bytes + step - 1) / step);
+    a.pieces += p.pieces;
+  }
+  if (a.pieces == 0) a.pieces = 1;
+  const long long items = (long long)a.n_copies * a.pieces, most = 8LL * sm_count;
+  copy_kernel<<<(unsigned)(items < most ? items : most), kCopyThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace ga

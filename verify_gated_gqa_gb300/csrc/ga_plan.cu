@@ -24,18 +24,6 @@ static_assert(kSeqPerThread == 2 && kSeqPerThread * kThreads == GA_PLAN_MAX_SEQ,
 constexpr int kSlotThreads = 256;
 constexpr int kSlotsPerThread = 4;
 
-// The last b with start[b] <= x, over start[0 .. n - 1] ascending with start[0] = 0 (so
-// entries without any item, whose start equals the next one's, are passed over).
-__device__ __forceinline__ int find_seq(const unsigned* start, int n, unsigned x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (start[mid] <= x) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-
 // Slot and position of packed token t; padding past the last token is -1 and 0.
 __device__ __forceinline__ void write_slot(const PlanArgs& a, const unsigned* start, int t,
                                            unsigned tokens) {

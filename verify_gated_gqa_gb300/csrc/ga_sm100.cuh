@@ -501,6 +501,17 @@ __device__ __forceinline__ void tmem_wait_st() {
 }
 
 // ------------------------------------------------------------------ small helpers
+// The last b with start[b] <= x, over start[0 .. n - 1] ascending with start[0] = 0 (so
+// entries without any item, whose start equals the next one's, are passed over).
+__device__ __forceinline__ int find_seq(const unsigned* start, int n, unsigned x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
 // Pack two floats into bf16x2 (round to nearest even): lo -> bits 0..15, hi -> 16..31.
 // Two bf16 products, each the exact product rounded once to bf16: the same bits as the
 // fp32 product (exact for two bf16 values) converted to bf16 (checked on the device over
