@@ -91,6 +91,7 @@ int current_device(DeviceState** out) {
       if ((e = GA_CUDA(attn_set_smem_attribute())) != cudaSuccess) return fail_cuda(e);
       if ((e = GA_CUDA(probe_set_smem_attribute())) != cudaSuccess) return fail_cuda(e);
       if ((e = GA_CUDA(verify4_set_attributes())) != cudaSuccess) return fail_cuda(e);
+      if ((e = GA_CUDA(verify8_set_attributes())) != cudaSuccess) return fail_cuda(e);
       if ((e = GA_CUDA(attn_max_pair_clusters(&d.pair_clusters))) != cudaSuccess) return fail_cuda(e);
       if ((e = GA_CUDA(attn_max_gated_pair_clusters(&d.gated_pair_clusters))) != cudaSuccess)
         return fail_cuda(e);
@@ -220,11 +221,11 @@ int encode_q4_map(CUtensorMap* map, const void* base, long long n_rows, int row_
   if (st != GA_OK) return st;
   cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)n_rows};
   cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-  cuuint32_t box[2] = {(cuuint32_t)row_bytes, GA_Q4_PAGE_TOKENS};
+  cuuint32_t box[2] = {(cuuint32_t)std::min(row_bytes, 128), GA_Q4_PAGE_TOKENS};
   cuuint32_t es[2] = {1, 1};
   CUresult r = GA_CUDA(enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
                            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                           row_bytes >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
   if (r != CUDA_SUCCESS) {
     t_last_cuda_error = (int)r;
@@ -1303,6 +1304,23 @@ void set_page_division(Kv4Args& a) {
   a.page_shift = 25 + log2;
   a.page_mul = (unsigned)(((1ULL << a.page_shift) + d - 1) / d);
 }
+// The sequences g0 .. of a call over a quantised cache, as many as one launch takes.
+Verify4Args verify_args(const ga_bf16* q_prep, const ga_bf16* qg, const int* page_table, const int* seq_len,
+                        int g0, int n_seq, int rows, int page_size, int max_pages, int n_pages, ga_bf16* out,
+                        void* workspace, int* status) {
+  Verify4Args a{};
+  a.n_seq = n_seq - g0 < kV4MaxSeq ? n_seq - g0 : kV4MaxSeq;
+  a.rows = rows; a.page_size = page_size; a.max_pages = max_pages; a.n_pages = n_pages;
+  a.q_prep = q_prep + (size_t)g0 * rows * kOutRow;
+  a.qg = qg + (size_t)g0 * rows * kRowElems;
+  a.out = out + (size_t)g0 * rows * kOutRow;
+  a.page_table = page_table + (size_t)g0 * max_pages;
+  a.seq_len = seq_len + g0;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + (size_t)2 * kV4MaxCtas * kV4Lanes * kDim;
+  a.status = status;
+  return a;
+}
 int check_q4_tokens(long long n_tok, const int* slots, int n_pages, int page_size) {
   if (n_tok < 0) return GA_ERR_SHAPE;
   if (n_tok > 64LL * GA_MAX_TOKENS || (!slots && n_tok > (long long)n_pages * page_size))
@@ -1398,17 +1416,8 @@ int ga_attn_verify_q4(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k
       (st = encode_q4_map(&vs, v_scales, n_rows, GA_Q4_SCALE_BYTES)) != GA_OK)
     return st;
   for (int g0 = 0; g0 < n_seq; g0 += kV4MaxSeq) {
-    Verify4Args a{};
-    a.n_seq = n_seq - g0 < kV4MaxSeq ? n_seq - g0 : kV4MaxSeq;
-    a.rows = rows; a.page_size = page_size; a.max_pages = max_pages; a.n_pages = n_pages;
-    a.q_prep = q_prep + (size_t)g0 * rows * kOutRow;
-    a.qg = qg + (size_t)g0 * rows * kRowElems;
-    a.out = out + (size_t)g0 * rows * kOutRow;
-    a.page_table = page_table + (size_t)g0 * max_pages;
-    a.seq_len = seq_len + g0;
-    a.part_o = static_cast<float*>(workspace);
-    a.part_ml = a.part_o + (size_t)2 * kV4MaxCtas * kV4Lanes * kDim;
-    a.status = dev->status_word;
+    const Verify4Args a = verify_args(q_prep, qg, page_table, seq_len, g0, n_seq, rows, page_size, max_pages,
+                                      n_pages, out, workspace, dev->status_word);
     const cudaError_t e =
         GA_CUDA(launch_verify4(kc, vc, ks, vs, a, dev->sm_count, (cudaStream_t)stream));
     if (e != cudaSuccess) return fail_cuda(e);
@@ -1505,6 +1514,8 @@ int ga_kv_dequantize_q8(const uint8_t* k_codes, const uint8_t* k_scales, const u
   return e == cudaSuccess ? GA_OK : fail_cuda(e);
 }
 
+static_assert(GA_Q8_BLOCK_TOKENS == GA_Q4_PAGE_TOKENS, "the boxes of both caches' maps are 32 rows high");
+
 size_t ga_verify_q8_workspace_bytes(void) { return verify4_ws_bytes(); }
 
 int ga_attn_verify_q8(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k_codes,
@@ -1526,14 +1537,20 @@ int ga_attn_verify_q8(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k
   DeviceState* dev = nullptr;
   st = current_device(&dev);
   if (st != GA_OK) return st;
-  Verify8Args a{};
-  a.q_prep = q_prep; a.qg = qg; a.out = out;
-  a.k_codes = k_codes; a.k_scales = k_scales; a.v_codes = v_codes; a.v_scales = v_scales;
-  a.page_table = page_table; a.seq_len = seq_len;
-  a.n_seq = n_seq; a.rows = rows; a.page_size = page_size; a.max_pages = max_pages; a.n_pages = n_pages;
-  a.status = dev->status_word;
-  const cudaError_t e = GA_CUDA(launch_verify8(a, (cudaStream_t)stream));
-  return e == cudaSuccess ? GA_OK : fail_cuda(e);
+  const long long n_rows = (long long)n_pages * kKvHeads * page_size;
+  CUtensorMap kc, vc;
+  if ((st = encode_q4_map(&kc, k_codes, n_rows, GA_Q8_ROW_BYTES)) != GA_OK ||
+      (st = encode_q4_map(&vc, v_codes, n_rows, GA_Q8_ROW_BYTES)) != GA_OK)
+    return st;
+  for (int g0 = 0; g0 < n_seq; g0 += kV4MaxSeq) {
+    Verify8Args a{};
+    a.v = verify_args(q_prep, qg, page_table, seq_len, g0, n_seq, rows, page_size, max_pages, n_pages, out,
+                      workspace, dev->status_word);
+    a.k_scales = k_scales; a.v_scales = v_scales;
+    const cudaError_t e = GA_CUDA(launch_verify8(kc, vc, a, dev->sm_count, (cudaStream_t)stream));
+    if (e != cudaSuccess) return fail_cuda(e);
+  }
+  return GA_OK;
 }
 
 // ---------------------------------------------------------------- pages of several sequences

@@ -224,6 +224,16 @@ cudaError_t launch_decode4(const CUtensorMap& k_codes, const CUtensorMap& v_code
                            const CUtensorMap& k_scales, const CUtensorMap& v_scales,
                            const Verify4Args& a, int ctas, cudaStream_t s);
 
+// Attention over 8-bit paged caches (ga_verify8.cu). Maps: the code pools as [rows][256] bytes (box 32
+// rows x 128, 128-byte swizzle).
+struct Verify8Args {
+  Verify4Args v;
+  const uint8_t *k_scales, *v_scales;
+};
+cudaError_t verify8_set_attributes();
+cudaError_t launch_verify8(const CUtensorMap& k_codes, const CUtensorMap& v_codes, const Verify8Args& a,
+                           int sm_count, cudaStream_t s);
+
 // Pages that several sequences hold (ga_pages.cu).
 struct ForkArgs {
   const int *parent, *child, *len;
@@ -297,17 +307,6 @@ struct Kv8Args {
 };
 cudaError_t launch_quantize_q8(const Kv8Args& a, cudaStream_t s);
 cudaError_t launch_dequantize_q8(const Kv8Args& a, cudaStream_t s);
-
-// Attention over 8-bit paged caches (ga_verify8.cu).
-struct Verify8Args {
-  const uint16_t *q_prep, *qg;
-  uint16_t* out;
-  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
-  const int *page_table, *seq_len;
-  int n_seq, rows, page_size, max_pages, n_pages;
-  int* status;
-};
-cudaError_t launch_verify8(const Verify8Args& a, cudaStream_t s);
 
 cudaError_t attn_set_smem_attribute();
 // Clusters of two attention CTAs (the e4m3 verify variant) that can run at once.

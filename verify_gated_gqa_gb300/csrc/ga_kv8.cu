@@ -41,20 +41,6 @@ __device__ __forceinline__ int exp_for(uint32_t top) {
   const int e = (int)(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0);
   return min(max(e, kQ8MinExp), kQ8MaxExp);
 }
-__device__ __forceinline__ uint32_t top_of(const uint4& x) {
-  const uint32_t w[4] = {x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu};
-  const uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
-  uint32_t top = max(m & 0xFFFFu, m >> 16);
-  if (top > 0x7F80u) {   // a NaN counts as 0
-    top = 0u;
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = w[i] & 0xFFFFu, hi = w[i] >> 16;
-      if (lo <= 0x7F80u) top = max(top, lo);
-      if (hi <= 0x7F80u) top = max(top, hi);
-    }
-  }
-  return top;
-}
 __device__ __forceinline__ float scaled(uint32_t bf16_bits, float inv) {
   const float x = __uint_as_float(bf16_bits);
   return x != x ? 0.f : x * inv;   // x inv is exact, or past +-448 either way

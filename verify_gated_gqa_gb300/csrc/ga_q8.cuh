@@ -18,6 +18,21 @@ constexpr int kQ8MinExp = -32, kQ8MaxExp = 31;   // stored as e + 32 in six bits
 __device__ __forceinline__ int q8_exp(uint32_t byte) { return (int)(byte & 63u) + kQ8MinExp; }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// The largest magnitude of 8 bf16 values, as its bits (ordered as the magnitudes are).
+__device__ __forceinline__ uint32_t top_of(const uint4& x) {
+  const uint32_t w[4] = {x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu};
+  const uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+  uint32_t top = max(m & 0xFFFFu, m >> 16);
+  if (top > 0x7F80u) {   // a NaN counts as 0
+    top = 0u;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = w[i] & 0xFFFFu, hi = w[i] >> 16;
+      if (lo <= 0x7F80u) top = max(top, lo);
+      if (hi <= 0x7F80u) top = max(top, hi);
+    }
+  }
+  return top;
+}
 // Two codes, to nearest even, saturating at +-448 (lo in bits 0..7); a NaN gives the code 0x7F.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;

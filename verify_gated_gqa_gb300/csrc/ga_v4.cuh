@@ -93,6 +93,11 @@ __device__ __forceinline__ int ld_input(const int* p) {
   asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
+__device__ __forceinline__ uint32_t ld_input(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ uint16_t ld_input(const uint16_t* p) {
   uint16_t v;
   asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
@@ -311,8 +316,9 @@ __device__ __forceinline__ float4* part_at(float* part_o, int slot, int d4, int 
   return reinterpret_cast<float4*>(part_o) + ((size_t)slot * (kDim / 4) + d4) * kV4Lanes + row;
 }
 
-// The log-sum-exp merge of the streams that the cut over `workers` left in parts, after either
-// kernel with tiles of `tile` keys (128 or 32).
-cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, cudaStream_t s);
+// The log-sum-exp merge of the streams that the cut over `workers` left in parts, after either 4-bit
+// kernel with tiles of `tile` keys (128 or 32), or the 8-bit one (128), whose parts lie row after row
+// (by_row).
+cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, bool by_row, cudaStream_t s);
 
 }  // namespace ga

@@ -570,8 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The streams that the cut left in parts: o = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i over a
 // stream's parts, times the gate.
 //
-// A stream's items are (row, four dims), rows innermost, as the parts lie; a block takes an equal
-// share of them. With few streams each has `slices` blocks, about twice the device's CTAs in all (32
+// A stream's items are (row, four dims), in the order in which the parts lie (rows innermost, or dims:
+// kByRow); a block takes an equal share of them. With few streams each has `slices` blocks, about twice the device's CTAs in all (32
 // sequences of up to 4,096 keys, one row: a whole call of 22 us; with twice the blocks 25). With many
 // (slices 0), most of them whole or of two parts, blocks go by the boundaries that cut streams, n - 1
 // to a stream of n parts, kSplit to each, so that one long stream among many short ones is not left to
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // turned into weights in shared memory first, 76 parts of 96 rows took 28 us.)
 constexpr int kCombineThreads = 384, kSplit = 2;
 static_assert(kCombineThreads >= kV4MaxSeq, "a sequence a thread");
-template <int kTile>
+template <int kTile, bool kByRow>
 __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     const __grid_constant__ Verify4Args a, int workers, int slices) {
   __shared__ int warp_units[kV4MaxSeq / 32], warp_streams[kV4MaxSeq / 32];
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   grid_wait();
   if (n == 1 || count == 0) return;   // (one CTA ran the whole stream and wrote it)
   for (int item = lo + tid - group * count; item < hi; item += kCombineThreads) {
-    const int d4 = item / rows, r = item - d4 * rows;
+    const int d4 = kByRow ? item % (kDim / 4) : item / rows, r = kByRow ? item / (kDim / 4) : item - d4 * rows;
     float M = -INFINITY, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     auto scale = [&](float top) {   // to a new maximum
@@ -670,7 +670,8 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
         x[k] = make_float2(-INFINITY, 0.f);
         if (i < n) {
           x[k] = reinterpret_cast<const float2*>(a.part_ml)[(size_t)slot(i) * kV4Lanes + r];
-          v[k] = *part_at(a.part_o, slot(i), d4, r);
+          v[k] = kByRow ? reinterpret_cast<const float4*>(a.part_o)[((size_t)slot(i) * kV4Lanes + r) * (kDim / 4) + d4]
+                        : *part_at(a.part_o, slot(i), d4, r);
         }
       }
       float top = M;
@@ -723,14 +724,15 @@ cudaError_t verify4_set_attributes() {
   return e != cudaSuccess ? e : decode4_set_attributes();
 }
 
-cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, cudaStream_t s) {
+cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, bool by_row, cudaStream_t s) {
   const int blocks = row_blocks(a.rows), streams = a.n_seq * kKvHeads * blocks;
   const int ctas = workers * blocks, slices = streams * 2 >= ctas ? 0 : 2 * ctas / streams < 64 ? 2 * ctas / streams : 64;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = overlapped_launch(
       (unsigned)(slices ? streams * slices : (workers - 1) * blocks * kSplit), kCombineThreads, 0, s, attr);
-  return tile == kTileN ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<kTileN>, a, workers, slices)
-                        : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<32>, a, workers, slices);
+  if (by_row) return cudaLaunchKernelEx(&cfg, verify4_combine_kernel<kTileN, true>, a, workers, slices);
+  return tile == kTileN ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<kTileN, false>, a, workers, slices)
+                        : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<32, false>, a, workers, slices);
 }
 
 cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
@@ -742,7 +744,7 @@ cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_code
   const int blocks = row_blocks(a.rows), workers = ctas / blocks;
   const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)(workers * blocks), kThreads, sizeof(V4Smem), s, attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, verify4_kernel, k_codes, v_codes, k_scales, v_scales, a);
-  return e != cudaSuccess ? e : launch_verify4_combine(a, workers, kTileN, s);
+  return e != cudaSuccess ? e : launch_verify4_combine(a, workers, kTileN, false, s);
 }
 
 }  // namespace ga
