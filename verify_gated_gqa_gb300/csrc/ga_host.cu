@@ -221,11 +221,32 @@ int encode_q4_map(CUtensorMap* map, const void* base, long long n_rows, int row_
   if (st != GA_OK) return st;
   cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)n_rows};
   cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-  cuuint32_t box[2] = {(cuuint32_t)std::min(row_bytes, 128), GA_Q4_PAGE_TOKENS};
+  cuuint32_t box[2] = {(cuuint32_t)row_bytes, GA_Q4_PAGE_TOKENS};
   cuuint32_t es[2] = {1, 1};
   CUresult r = GA_CUDA(enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
                            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           row_bytes >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                           row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
+  if (r != CUDA_SUCCESS) {
+    t_last_cuda_error = (int)r;
+    return GA_ERR_CUDA;
+  }
+  return GA_OK;
+}
+
+// An 8-bit cache pool's rows, [n_rows][256] bytes, as a TMA tensor [2 halves][n_rows][128 bytes]: box =
+// box_rows rows of one half, or both where that is a whole tile of 128 keys, with the 128-byte
+// swizzle, so that a tile lands as two blocks [128 keys][128 dims]; rows past the pool read as zeros.
+int encode_q8_map(CUtensorMap* map, const void* base, long long n_rows, int box_rows) {
+  EncodeTiledFn enc;
+  int st = get_encode(&enc);
+  if (st != GA_OK) return st;
+  cuuint64_t dims[3] = {128, (cuuint64_t)n_rows, 2};
+  cuuint64_t strides[2] = {GA_Q8_ROW_BYTES, 128};
+  cuuint32_t box[3] = {128, (cuuint32_t)box_rows, box_rows == kTileN ? 2u : 1u};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = GA_CUDA(enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims,
+                           strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
   if (r != CUDA_SUCCESS) {
     t_last_cuda_error = (int)r;
@@ -1514,8 +1535,6 @@ int ga_kv_dequantize_q8(const uint8_t* k_codes, const uint8_t* k_scales, const u
   return e == cudaSuccess ? GA_OK : fail_cuda(e);
 }
 
-static_assert(GA_Q8_BLOCK_TOKENS == GA_Q4_PAGE_TOKENS, "the boxes of both caches' maps are 32 rows high");
-
 size_t ga_verify_q8_workspace_bytes(void) { return verify4_ws_bytes(); }
 
 int ga_attn_verify_q8(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k_codes,
@@ -1539,8 +1558,9 @@ int ga_attn_verify_q8(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k
   if (st != GA_OK) return st;
   const long long n_rows = (long long)n_pages * kKvHeads * page_size;
   CUtensorMap kc, vc;
-  if ((st = encode_q4_map(&kc, k_codes, n_rows, GA_Q8_ROW_BYTES)) != GA_OK ||
-      (st = encode_q4_map(&vc, v_codes, n_rows, GA_Q8_ROW_BYTES)) != GA_OK)
+  const int box = verify8_box_keys(page_size);
+  if ((st = encode_q8_map(&kc, k_codes, n_rows, box)) != GA_OK ||
+      (st = encode_q8_map(&vc, v_codes, n_rows, box)) != GA_OK)
     return st;
   for (int g0 = 0; g0 < n_seq; g0 += kV4MaxSeq) {
     Verify8Args a{};

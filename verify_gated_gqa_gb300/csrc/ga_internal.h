@@ -224,12 +224,13 @@ cudaError_t launch_decode4(const CUtensorMap& k_codes, const CUtensorMap& v_code
                            const CUtensorMap& k_scales, const CUtensorMap& v_scales,
                            const Verify4Args& a, int ctas, cudaStream_t s);
 
-// Attention over 8-bit paged caches (ga_verify8.cu). Maps: the code pools as [rows][256] bytes (box 32
-// rows x 128, 128-byte swizzle).
+// Attention over 8-bit paged caches (ga_verify8.cu). Maps: the code pools' rows of 256 bytes as [2][rows]
+// [128] (boxes of verify8_box_keys rows, both halves where that is a whole tile; 128-byte swizzle).
 struct Verify8Args {
   Verify4Args v;
   const uint8_t *k_scales, *v_scales;
 };
+int verify8_box_keys(int page_size);
 cudaError_t verify8_set_attributes();
 cudaError_t launch_verify8(const CUtensorMap& k_codes, const CUtensorMap& v_codes, const Verify8Args& a,
                            int sm_count, cudaStream_t s);

@@ -13,7 +13,7 @@ __device__ __forceinline__ void record(int* status, int code) {
 // mbar_wait with a time hint on every try after the first, so that a waiting warp is suspended by
 // the hardware: most warps of these kernels wait most of the time, and spinning they took a third of
 // the SM's issue slots.
-__device__ __forceinline__ bool v4_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool v4_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
@@ -23,7 +23,7 @@ __device__ __forceinline__ bool v4_wait(uint64_t* bar, uint32_t parity, volatile
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}\n"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)   // ns
+        : "r"(bar), "r"(parity), "r"(20000u)   // ns
         : "memory");
     if (ok) return true;
     if (*abort) return false;
@@ -34,9 +34,15 @@ __device__ __forceinline__ bool v4_wait(uint64_t* bar, uint32_t parity, volatile
   }
 }
 // The same in all 32 lanes, which agree on the outcome.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   const bool ok = v4_wait(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool v4_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return v4_wait(smem_u32(bar), parity, abort);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return warp_wait(smem_u32(bar), parity, abort);
 }
 __device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
   uint32_t v;
