@@ -92,6 +92,7 @@ int current_device(DeviceState** out) {
       if ((e = GA_CUDA(probe_set_smem_attribute())) != cudaSuccess) return fail_cuda(e);
       if ((e = GA_CUDA(verify4_set_attributes())) != cudaSuccess) return fail_cuda(e);
       if ((e = GA_CUDA(verify8_set_attributes())) != cudaSuccess) return fail_cuda(e);
+      if ((e = GA_CUDA(pages_set_attributes())) != cudaSuccess) return fail_cuda(e);
       if ((e = GA_CUDA(attn_max_pair_clusters(&d.pair_clusters))) != cudaSuccess) return fail_cuda(e);
       if ((e = GA_CUDA(attn_max_gated_pair_clusters(&d.gated_pair_clusters))) != cudaSuccess)
         return fail_cuda(e);

@@ -287,12 +287,16 @@ struct PageCopyArgs {
   struct Pool {
     uint8_t* base;
     long long bytes;          // of a page
-    int width, first, pieces; // set by the launcher
+    // by the launcher: widest access, first piece and number of pieces of a page that go by bulk copies
+    int width, first, pieces;
   } pool[GA_PAGE_COPY_POOLS];
-  int n_pools, n_pages, n_copies, pieces;
+  int n_pools, n_pages, n_copies;
+  int pieces, piece_bytes;    // by the launcher: of all pools; whether some pool goes without
+  bool small;
   const int *src, *dst;
   int* status;
 };
+cudaError_t pages_set_attributes();
 cudaError_t launch_page_copy(PageCopyArgs a, int sm_count, cudaStream_t s);
 
 // 8-bit cache rows of n_tok tokens by slot (ga_kv8.cu; slots null: token t is slot t).

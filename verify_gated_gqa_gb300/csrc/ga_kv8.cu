@@ -11,8 +11,10 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kChunk = 32;                       // tokens whose runs a CTA stores
-constexpr int kSpan = 2 * kChunk;                // a run goes at most 31 tokens past them
-constexpr int kRowsPerWarp = kSpan / kWarps;
+constexpr int kTokRows = 2 * kKvHeads;           // a token's rows: K heads 0, 1, V heads 0, 1
+constexpr int kStoreThreads = 512;
+constexpr int kRowWarps = kStoreThreads / 32 / kTokRows;   // warps of each
+constexpr int kKept = kChunk / kRowWarps;                  // rows that a warp keeps in registers
 
 struct Slot {
   long long row;    // pool row of head 0; head 1's is page_size on
@@ -28,7 +30,7 @@ __device__ __forceinline__ Slot slot_place(const Kv8Args& a, int slot) {
 // the pool, which is recorded, or no token).
 __device__ __forceinline__ int slot_of(const Kv8Args& a, long long t) {
   if (t < 0 || t >= a.n_tok) return -1;
-  const int s = a.slots ? __ldg(a.slots + t) : (int)t;
+  const int s = a.slots ? ld_input(a.slots + t) : (int)t;
   if (s >= a.n_slots) {
     atomicCAS(a.status, 0, (int)kDevBadPage);
     return -1;
@@ -53,21 +55,20 @@ __device__ __forceinline__ uint2 encode(const uint4& x, float inv) {
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
-// A run is a row of tokens of one block. CTA (c, u) stores, for K or V (u / 2) and head u % 2, the
-// runs that begin among tokens 32 c .. 32 c + 31: a prompt's chunk has one or two, a decode batch
-// 32 of one token. Its tokens are dealt to the warps row by row, 8 values a lane, and stay in
-// registers from the search for the maxima to their codes, so every row is read once.
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constant__ Kv8Args a) {
-  __shared__ uint32_t top[kChunk], written[kChunk];
-  __shared__ int exps[kChunk], shift[kChunk], first[kChunk];
+// A run is a row of tokens of one block. CTA c stores the runs that begin among tokens 32 c .. 32 c +
+// 31: a prompt's chunk has one or two, a decode batch 32 of one token. Four warps take each of a
+// token's four rows, 8 values a lane. A chunk's rows stay in registers from the search for the maxima
+// to their codes; those of a run that goes on past the chunk (31 at most) are read again. Bound by
+// the bytes it moves.
+__global__ void __launch_bounds__(kStoreThreads, 2) quantize_kernel(const __grid_constant__ Kv8Args a) {
+  __shared__ uint32_t top[kTokRows][kChunk], written[kChunk];
+  __shared__ int exps[kTokRows][kChunk], shift[kTokRows][kChunk], first[kChunk];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kv = blockIdx.y >> 1, head = blockIdx.y & 1;
+  const int row = warp / kRowWarps, part = warp % kRowWarps;
   const long long t0 = (long long)blockIdx.x * kChunk;
-  const uint16_t* in = (kv ? a.v : a.k) + head * kDim;
-  const long long ld = kv ? a.ld_v : a.ld_k;
-  uint8_t* codes = kv ? a.v_codes : a.k_codes;
-  uint8_t* scales = kv ? a.v_scales : a.k_scales;
-  if (tid < kChunk) top[tid] = written[tid] = 0u;
+  if (tid < kTokRows * kChunk) top[tid / kChunk][tid % kChunk] = 0u;
+  grid_wait();
+  grid_launch_dependents();
   // every warp finds the runs: this lane's tokens are t0 + lane and t0 + 32 + lane
   const int s0 = slot_of(a, t0 + lane), s1 = slot_of(a, t0 + kChunk + lane);
   int before = __shfl_up_sync(0xffffffffu, s0, 1);
@@ -80,61 +81,74 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
   const uint32_t goes_on = __ballot_sync(0xffffffffu, last >= 0 && s1 >= 0 && (s1 >> 5) == (last >> 5));
   const int runs = __popc(leads), last_lead = 31 - __clz(leads);
   const int more = min(__ffs(~goes_on) ? __ffs(~goes_on) - 1 : 32, last_lead);
-  if (warp == 0 && lead) first[__popc(leads & ((1u << lane) - 1u))] = s0;
-  __syncthreads();
-  uint4 x[kRowsPerWarp];
-  int slot[kRowsPerWarp];
-#pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i) {
-    const int at = warp + kWarps * i;
-    const int s = __shfl_sync(0xffffffffu, at < kChunk ? s0 : s1, at & 31);
-    const bool mine = at < kChunk ? (leads & ((2u << at) - 1u)) != 0u : at - kChunk < more;
-    slot[i] = mine ? s : -1;
-    if (slot[i] >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(in + (t0 + at) * ld) + lane);
+  const int run0 = __popc(leads & ((2u << lane) - 1u)) - 1;   // of token t0 + lane, or -1
+  if (warp == 0) {   // which slots of its block a run writes
+    if (lead) first[run0] = s0;
+    written[lane] = 0u;
+    __syncwarp();
+    if (s0 >= 0 && run0 >= 0) atomicOr(&written[run0], 1u << (s0 & 31));
+    if (lane < more) atomicOr(&written[runs - 1], 1u << (s1 & 31));
   }
-  auto run_of = [&](int i) {
-    const int at = warp + kWarps * i;
-    return at < kChunk ? __popc(leads & ((2u << at) - 1u)) - 1 : runs - 1;
-  };
+  const int head = row & 1, kv = row >> 1;
+  const uint16_t* in = (kv ? a.v : a.k) + head * kDim;
+  const long long ld = kv ? a.ld_v : a.ld_k;
+  uint8_t* codes = kv ? a.v_codes : a.k_codes;
+  auto load = [&](int at) { return ld_input(reinterpret_cast<const uint4*>(in + (t0 + at) * ld) + lane); };
+  uint4 x[kKept];
 #pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i) {
-    if (slot[i] < 0) continue;
+  for (int i = 0; i < kKept; ++i) {
+    const int at = part + kRowWarps * i;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (__shfl_sync(0xffffffffu, s0, at) >= 0 && __shfl_sync(0xffffffffu, run0, at) >= 0) x[i] = load(at);
+  }
+  __syncthreads();   // top is zero
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const int at = part + kRowWarps * i, run = __shfl_sync(0xffffffffu, run0, at);
     const uint32_t m = __reduce_max_sync(0xffffffffu, top_of(x[i]));
-    if (lane == 0) {
-      atomicMax(&top[run_of(i)], m);
-      atomicOr(&written[run_of(i)], 1u << (slot[i] & 31));
-    }
+    if (lane == 0 && m != 0u && run >= 0) atomicMax(&top[row][run], m);
+  }
+  for (int at = part; at < more; at += kRowWarps) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, top_of(load(kChunk + at)));
+    if (lane == 0) atomicMax(&top[row][runs - 1], m);
   }
   __syncthreads();
-  if (tid < runs) {
-    uint8_t* at = scales + slot_place(a, first[tid]).scale + head * (a.page_size / kQ8Block);
-    int e = exp_for(top[tid]);
-    int grown = 0;
-    if ((written[tid] & 1u) == 0u) {   // the block goes on
+  bool grows = false;
+  if (tid < kTokRows * kChunk && tid % kChunk < runs) {
+    const int r = tid / kChunk, run = tid % kChunk;   // (its own row, kv and head: not this warp's)
+    uint8_t* at = (r >> 1 ? a.v_scales : a.k_scales) + slot_place(a, first[run]).scale + (r & 1) * (a.page_size / kQ8Block);
+    int e = exp_for(top[r][run]), grown = 0;
+    if ((written[run] & 1u) == 0u) {   // the block goes on
       const int was = q8_exp(*at);
       grown = max(e - was, 0);
       e = max(e, was);
     }
     *at = (uint8_t)(e - kQ8MinExp);
-    exps[tid] = e;
-    shift[tid] = grown;
+    exps[r][run] = e;
+    shift[r][run] = grown;
+    grows = grown > 0;
   }
-  const bool any = __syncthreads_or(tid < runs && shift[tid] > 0);
+  const bool any = __syncthreads_or(grows);
+  auto store = [&](int slot, int run, const uint4& v) {
+    const long long at = slot_place(a, slot).row + head * a.page_size;
+    reinterpret_cast<uint2*>(codes + at * kQ8RowBytes)[lane] = encode(v, pow2i(-exps[row][run]));
+  };
 #pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i) {
-    if (slot[i] < 0) continue;
-    const long long row = slot_place(a, slot[i]).row + head * a.page_size;
-    reinterpret_cast<uint2*>(codes + row * kQ8RowBytes)[lane] = encode(x[i], pow2i(-exps[run_of(i)]));
+  for (int i = 0; i < kKept; ++i) {
+    const int at = part + kRowWarps * i;
+    const int slot = __shfl_sync(0xffffffffu, s0, at), run = __shfl_sync(0xffffffffu, run0, at);
+    if (slot >= 0 && run >= 0) store(slot, run, x[i]);
   }
+  for (int at = part; at < more; at += kRowWarps) store(__shfl_sync(0xffffffffu, s1, at), runs - 1, load(kChunk + at));
   if (!any) return;
   // the other rows of blocks that grew
-  for (int i = warp; i < runs * kQ8Block; i += kWarps) {
-    const int r = i / kQ8Block, off = i % kQ8Block;
-    if (shift[r] == 0 || (written[r] >> off & 1u)) continue;
-    const long long row = slot_place(a, (first[r] & ~31) + off).row + head * a.page_size;
-    uint2* p = reinterpret_cast<uint2*>(codes + row * kQ8RowBytes) + lane;
+  for (int i = part; i < runs * kQ8Block; i += kRowWarps) {
+    const int run = i / kQ8Block, off = i % kQ8Block;
+    if (shift[row][run] == 0 || (written[run] >> off & 1u)) continue;
+    const long long at = slot_place(a, (first[run] & ~31) + off).row + head * a.page_size;
+    uint2* p = reinterpret_cast<uint2*>(codes + at * kQ8RowBytes) + lane;
     const uint2 c = *p;
-    const float inv = pow2i(-shift[r]);
+    const float inv = pow2i(-shift[row][run]);
     uint32_t w[2] = {c.x, c.y}, o[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -151,6 +165,8 @@ constexpr int kWidenTokens = 2;
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_constant__ Kv8Args a) {
   const int lane = threadIdx.x & 31;
   const long long t0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kWidenTokens;
+  grid_wait();
+  grid_launch_dependents();
   uint2 c[kWidenTokens][4];
   uint32_t sc[kWidenTokens][4];
   bool live[kWidenTokens];
@@ -163,8 +179,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const long long row = p.row + (u & 1) * a.page_size;
-      c[i][u] = __ldg(reinterpret_cast<const uint2*>((u < 2 ? a.k_codes : a.v_codes) + row * kQ8RowBytes) + lane);
-      sc[i][u] = __ldg((u < 2 ? a.k_scales : a.v_scales) + p.scale + (u & 1) * (a.page_size / kQ8Block));
+      c[i][u] = ld_input(reinterpret_cast<const uint2*>((u < 2 ? a.k_codes : a.v_codes) + row * kQ8RowBytes) + lane);
+      sc[i][u] = ld_input((u < 2 ? a.k_scales : a.v_scales) + p.scale + (u & 1) * (a.page_size / kQ8Block));
     }
   }
 #pragma unroll
@@ -189,14 +205,16 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
 }  // namespace
 
 cudaError_t launch_quantize_q8(const Kv8Args& a, cudaStream_t s) {
-  quantize_kernel<<<dim3((unsigned)((a.n_tok + kChunk - 1) / kChunk), 2 * kKvHeads), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)((a.n_tok + kChunk - 1) / kChunk), kStoreThreads, 0, s, attr);
+  return cudaLaunchKernelEx(&cfg, quantize_kernel, a);
 }
 
 cudaError_t launch_dequantize_q8(const Kv8Args& a, cudaStream_t s) {
   constexpr int kPer = kWarps * kWidenTokens;
-  dequantize_kernel<<<(unsigned)((a.n_tok + kPer - 1) / kPer), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)((a.n_tok + kPer - 1) / kPer), kThreads, 0, s, attr);
+  return cudaLaunchKernelEx(&cfg, dequantize_kernel, a);
 }
 
 }  // namespace ga

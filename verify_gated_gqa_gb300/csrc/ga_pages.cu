@@ -121,6 +121,8 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
   __shared__ unsigned start[GA_PLAN_MAX_SEQ], named[GA_PLAN_MAX_SEQ / 32];
   const Team<kCtas> team(tsm);
   const int tid = threadIdx.x;
+  grid_wait();
+  grid_launch_dependents();
   if (tid < GA_PLAN_MAX_SEQ / 32) named[tid] = 0u;
   const int count = *a.free_count;
   int err = count < 0 || count > a.n_free ? 8 : 0;
@@ -223,6 +225,8 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
   __shared__ int kept[GA_PLAN_MAX_SEQ];
   const Team<kCtas> team(tsm);
   const int tid = threadIdx.x;
+  grid_wait();
+  grid_launch_dependents();
   const int count = *a.free_count;
   int err = count < 0 || count > a.n_free ? 8 : 0;
   unsigned gone[2], rows = 0;
@@ -253,45 +257,71 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
   unsigned freed = 0;
   if (!status && total.a > 0u) {
     if (a.shared != a.shared_out) team.sync();
-    // this thread's places
+    // this thread's places; as many of their pages as fit stay in registers, so that the loads of a step
+    // are all in flight at once (one by one, 31,000 pages took 21 us)
+    constexpr unsigned kKeep = 8;
     const unsigned per = (total.a + team.size - 1) / team.size;
     const unsigned lo = min(total.a, per * team.gid), hi = min(total.a, lo + per);
     const int row0 = lo < hi ? find_seq(start, a.n_seq, lo) : 0;
-    // f(place, page) over them
-    auto each = [&](auto f) {
-      int b = row0;
-      for (unsigned i = lo; i < hi; ++i) {
-        while (b + 1 < a.n_seq && start[b + 1] <= i) ++b;
-        const int page = a.page_table[(long long)b * a.max_pages + kept[b] + (int)(i - start[b])];
-        if (page >= 0 && page < a.n_free) f(i, page);
+    auto page_at = [&](unsigned i, int& b) {
+      while (b + 1 < a.n_seq && start[b + 1] <= i) ++b;
+      return a.page_table[(long long)b * a.max_pages + kept[b] + (int)(i - start[b])];
+    };
+    int pages[kKeep], b1 = row0;
+#pragma unroll
+    for (unsigned k = 0; k < kKeep; ++k) pages[k] = lo + k < hi ? page_at(lo + k, b1) : -1;
+#pragma unroll
+    for (unsigned k = 0; k < kKeep; ++k)
+      if (lo + k < hi && (unsigned)pages[k] >= (unsigned)a.n_free) {   // passed over
+        record_page(a.status);
+        pages[k] = -1;
+      }
+    // f(place, page) over them, load(page) first for a batch
+    auto each = [&](auto load, auto f) {
+      int got[kKeep];
+#pragma unroll
+      for (unsigned k = 0; k < kKeep; ++k)
+        if (pages[k] >= 0) got[k] = load(pages[k]);
+#pragma unroll
+      for (unsigned k = 0; k < kKeep; ++k)
+        if (pages[k] >= 0) f(lo + k, pages[k], got[k]);
+      int b = b1;
+      for (unsigned i = lo + kKeep; i < hi; ++i) {
+        const int page = page_at(i, b);
+        if ((unsigned)page < (unsigned)a.n_free) f(i, page, load(page));
         else record_page(a.status);
       }
     };
     volatile int* left = a.shared_out;
+    auto read = [&](int page) { return left[page]; };
+    auto nothing = [](int) { return 0; };
+    auto put_back = [&]() {   // as it was
+      each(nothing, [&](unsigned, int page, int) { atomicAdd(a.shared_out + page, 1); });
+    };
     bool bad = false;
-    each([&](unsigned, int page) { bad |= atomicSub(a.shared_out + page, 1) < 0; });
+    each([&](int page) { return atomicSub(a.shared_out + page, 1); }, [&](unsigned, int, int was) { bad |= was < 0; });
     if (team.any(0, bad)) {
       status = 5;
-      each([&](unsigned, int page) { atomicAdd(a.shared_out + page, 1); });
+      put_back();
     } else {
-      each([&](unsigned i, int page) {
-        if (left[page] < 0) atomicMin(a.shared_out + page, INT_MIN + (int)i);
+      each(read, [&](unsigned i, int page, int v) {
+        if (v < 0) atomicMin(a.shared_out + page, INT_MIN + (int)i);
       });
       team.sync();
       Pair own = {0u, 0u}, sum;
-      each([&](unsigned i, int page) { own.a += left[page] == INT_MIN + (int)i; });
+      each(read, [&](unsigned i, int, int v) { own.a += v == INT_MIN + (int)i; });
       unsigned to = team.scan(1, own, sum).a;
-      if ((long long)count + sum.a > a.n_free) {   // as it was
+      if ((long long)count + sum.a > a.n_free) {
         status = 4;
-        each([&](unsigned i, int page) {
-          if (left[page] == INT_MIN + (int)i) left[page] = -1;
+        each(read, [&](unsigned i, int page, int v) {
+          if (v == INT_MIN + (int)i) left[page] = -1;
         });
         team.sync();
-        each([&](unsigned, int page) { atomicAdd(a.shared_out + page, 1); });
+        put_back();
       } else {
         freed = sum.a;
-        each([&](unsigned i, int page) {
-          if (left[page] != INT_MIN + (int)i) return;
+        each(read, [&](unsigned i, int page, int v) {
+          if (v != INT_MIN + (int)i) return;
           a.free_pages[count + (int)to++] = page;
           left[page] = 0;
         });
@@ -318,6 +348,8 @@ template <int kCtas>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ CompactArgs a, int remap) {
   __shared__ TeamSmem tsm;
   const Team<kCtas> team(tsm);
+  grid_wait();
+  grid_launch_dependents();
   const int n = a.n_free, count = *a.free_count;
   bool err = count < 0 || count > n;
   for (int b = team.gid; b < a.n_seq; b += team.size) err |= a.held[b] < 0 || a.held[b] > a.max_pages;
@@ -438,78 +470,194 @@ __global__ void __launch_bounds__(kRemapThreads) remap_kernel(const __grid_const
 }
 
 // ------------------------------------------------------------------ copies of pages
-// An item is a 16 KiB piece of a copied page of one pool (256 threads x 4 x 16 bytes), or all of a
-// page in the pools whose pages are small (scales). Bound by the bytes, in and out.
+// An item is a piece of a copied page of one pool. Pools whose pages are 16-byte aligned and not small
+// go in pieces of up to 32 KiB through shared memory by bulk copies, three loads and three stores in
+// flight from one thread of each CTA; the others (scales, odd sizes) through registers by the other
+// warps, a page an item. Bound by the bytes, in and out.
 constexpr int kCopyThreads = 256, kCopyLoads = 4;
+constexpr int kPieceBytes = 32768, kCopyStages = 6, kCopyAhead = 3;
+constexpr int kBulkLeast = 2048;     // smaller pages go through registers
 
 template <typename T>
-__device__ __forceinline__ void copy_piece(const uint8_t* from, uint8_t* to, long long bytes, long long off) {
-  T v[kCopyLoads];
+__device__ __forceinline__ void copy_page(const uint8_t* from, uint8_t* to, long long bytes, int tid, int threads) {
+  for (long long off = 0; off < bytes; off += (long long)kCopyLoads * threads * sizeof(T)) {
+    T v[kCopyLoads];
 #pragma unroll
-  for (int k = 0; k < kCopyLoads; ++k) {
-    const long long at = off + ((long long)k * kCopyThreads + threadIdx.x) * sizeof(T);
-    if (at < bytes) v[k] = *reinterpret_cast<const T*>(from + at);
-  }
+    for (int k = 0; k < kCopyLoads; ++k) {
+      const long long at = off + ((long long)k * threads + tid) * sizeof(T);
+      if (at < bytes) v[k] = *reinterpret_cast<const T*>(from + at);
+    }
 #pragma unroll
-  for (int k = 0; k < kCopyLoads; ++k) {
-    const long long at = off + ((long long)k * kCopyThreads + threadIdx.x) * sizeof(T);
-    if (at < bytes) *reinterpret_cast<T*>(to + at) = v[k];
+    for (int k = 0; k < kCopyLoads; ++k) {
+      const long long at = off + ((long long)k * threads + tid) * sizeof(T);
+      if (at < bytes) *reinterpret_cast<T*>(to + at) = v[k];
+    }
   }
 }
-__device__ __forceinline__ void copy_piece(const uint8_t* from, uint8_t* to, long long bytes, long long off, int width) {
-  switch (width) {
-    case 16: return copy_piece<uint4>(from, to, bytes, off);
-    case 8: return copy_piece<uint2>(from, to, bytes, off);
-    case 4: return copy_piece<uint32_t>(from, to, bytes, off);
-    case 2: return copy_piece<uint16_t>(from, to, bytes, off);
-    default: return copy_piece<uint8_t>(from, to, bytes, off);
+
+// Copy i's pages, or src -1: an entry to pass over (a page outside the pool is recorded).
+__device__ __forceinline__ int2 copy_entry(const PageCopyArgs& a, long long i) {
+  int2 e = make_int2(a.src[i], a.dst[i]);
+  if (e.x < 0 || e.y < 0) {
+    e.x = -1;
+  } else if (e.x >= a.n_pages || e.y >= a.n_pages) {
+    record_page(a.status);
+    e.x = -1;
   }
+  return e;
+}
+
+struct CopySmem {
+  uint8_t stages[kCopyStages][kPieceBytes];
+  uint64_t full[kCopyStages];
+  uint8_t* to[kCopyStages];   // of the loads in flight
+  int bytes[kCopyStages], abort;
+};
+
+// The bulk pieces of this CTA, by one warp: items blockIdx.x, + gridDim.x, ...
+__device__ void copy_bulk(const PageCopyArgs& a, CopySmem& sm) {
+  const int lane = threadIdx.x & 31;
+  const long long items = (long long)a.n_copies * a.pieces;
+  long long next = blockIdx.x;
+  // 32 items at a time, an item a lane; those to be done are gathered in the lanes 0 .. have - 1
+  const uint8_t* from = nullptr;
+  uint8_t* to = nullptr;
+  int bytes = 0, have = 0, at = 0;
+  auto fetch = [&]() {   // whether there is another item: lane `at`'s
+    while (at == have && next < items) {
+      const long long w = next + (long long)lane * gridDim.x;
+      bytes = 0;
+      if (w < items) {
+        const long long i = w / a.pieces;
+        const int piece = (int)(w - i * a.pieces);
+        int j = 0;
+        while (piece < a.pool[j].first || piece >= a.pool[j].first + a.pool[j].pieces) ++j;
+        const PageCopyArgs::Pool& p = a.pool[j];
+        const int2 e = copy_entry(a, i);
+        if (e.x >= 0) {
+          const long long off = (long long)(piece - p.first) * a.piece_bytes;
+          from = p.base + e.x * p.bytes + off;
+          to = p.base + e.y * p.bytes + off;
+          bytes = (int)min((long long)a.piece_bytes, p.bytes - off);
+        }
+      }
+      next += 32LL * gridDim.x;
+      const uint32_t live = __ballot_sync(~0u, bytes > 0);
+      have = __popc(live);
+      at = 0;
+      const int pick = lane < have ? (int)__fns(live, 0, lane + 1) : 0;
+      from = (const uint8_t*)__shfl_sync(~0u, (unsigned long long)from, pick);
+      to = (uint8_t*)__shfl_sync(~0u, (unsigned long long)to, pick);
+      bytes = __shfl_sync(~0u, bytes, pick);
+    }
+    return at < have;
+  };
+  unsigned n = 0, m = 0;   // loaded, stored
+  volatile int* abort = &sm.abort;
+  while (true) {
+    while (n - m < kCopyAhead && fetch()) {
+      const unsigned st = n % kCopyStages;
+      const uint8_t* src = (const uint8_t*)__shfl_sync(~0u, (unsigned long long)from, at);
+      uint8_t* dst = (uint8_t*)__shfl_sync(~0u, (unsigned long long)to, at);
+      const int size = __shfl_sync(~0u, bytes, at);
+      if (lane == 0) {
+        // the stage's last store, one of those before the last kCopyStages - kCopyAhead, has read it
+        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kCopyStages - kCopyAhead) : "memory");
+        sm.to[st] = dst;
+        sm.bytes[st] = size;
+        mbar_arrive_expect_tx(&sm.full[st], (uint32_t)size);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                smem_u32(sm.stages[st])),
+            "l"(src), "r"(size), "r"(smem_u32(&sm.full[st]))
+            : "memory");
+      }
+      ++at;
+      ++n;
+      __syncwarp();
+    }
+    if (m == n) break;
+    const unsigned st = m % kCopyStages;
+    if (!__all_sync(~0u, mbar_wait(&sm.full[st], (m / kCopyStages) & 1u, abort))) {
+      for (unsigned k = m; k < n; ++k)   // the loads in flight land before the CTA leaves
+        mbar_wait_quiet(&sm.full[k % kCopyStages], (k / kCopyStages) & 1u, 100000000LL);
+      if (lane == 0) atomicCAS(a.status, 0, *abort);
+      break;
+    }
+    if (lane == 0) {
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(sm.to[st]),
+                   "r"(smem_u32(sm.stages[st])), "r"(sm.bytes[st])
+                   : "memory");
+      bulk_commit_group();
+    }
+    ++m;
+    __syncwarp();
+  }
+  if (lane == 0) bulk_wait_group0();
 }
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ PageCopyArgs a) {
-  const long long items = (long long)a.n_copies * a.pieces;
-  for (long long w = blockIdx.x; w < items; w += gridDim.x) {
-    const int i = (int)(w / a.pieces);
-    int piece = (int)(w - (long long)i * a.pieces);
-    const int src = a.src[i], dst = a.dst[i];
-    if (src < 0 || dst < 0) continue;
-    if (src >= a.n_pages || dst >= a.n_pages) {
-      if (threadIdx.x == 0) record_page(a.status);
-      continue;
-    }
+  extern __shared__ __align__(128) uint8_t raw[];
+  CopySmem& sm = *reinterpret_cast<CopySmem*>(raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    sm.abort = 0;
+    for (int i = 0; i < kCopyStages; ++i) mbar_init(&sm.full[i], 1);
+    mbar_fence_init();
+  }
+  __syncthreads();
+  grid_wait();
+  grid_launch_dependents();
+  if (warp == 0) {
+    if (a.pieces > 0) copy_bulk(a, sm);
+    return;
+  }
+  if (!a.small) return;
+  constexpr int kWarps = kCopyThreads / 32 - 1;
+  for (long long i = (long long)blockIdx.x * kWarps + warp - 1; i < a.n_copies; i += (long long)gridDim.x * kWarps) {
+    const int2 e = copy_entry(a, i);
+    if (e.x < 0) continue;
     for (int j = 0; j < a.n_pools; ++j) {
       const PageCopyArgs::Pool& p = a.pool[j];
-      const uint8_t* from = p.base + src * p.bytes;
-      uint8_t* to = p.base + dst * p.bytes;
-      const int step = kCopyThreads * kCopyLoads * p.width;
-      if (p.pieces == 0) {   // small: with piece 0
-        if (piece == 0)
-          for (long long off = 0; off < p.bytes; off += step) copy_piece(from, to, p.bytes, off, p.width);
-      } else if (piece >= p.first && piece < p.first + p.pieces) {
-        copy_piece(from, to, p.bytes, (long long)(piece - p.first) * step, p.width);
+      if (p.pieces > 0) continue;
+      const uint8_t* from = p.base + e.x * p.bytes;
+      uint8_t* to = p.base + e.y * p.bytes;
+      switch (p.width) {
+        case 16: copy_page<uint4>(from, to, p.bytes, lane, 32); break;
+        case 8: copy_page<uint2>(from, to, p.bytes, lane, 32); break;
+        case 4: copy_page<uint32_t>(from, to, p.bytes, lane, 32); break;
+        case 2: copy_page<uint16_t>(from, to, p.bytes, lane, 32); break;
+        default: copy_page<uint8_t>(from, to, p.bytes, lane, 32);
       }
     }
   }
 }
 
-// One CTA while a step's entries are few (its barriers are cheaper), else the cluster.
-constexpr long long kOneCtaEntries = 4096;
+// One CTA while a step's entries are few (its barriers are cheaper), else the cluster. All may be placed
+// while the kernel before them ends.
+constexpr long long kOneCtaEntries = 2048;
 template <typename K1, typename K8, typename... A>
 cudaError_t launch_team(K1 one, K8 eight, bool large, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kTeamCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(large ? kTeamCtas : 1);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kTeamCtas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = large ? 1 : 0;
+  cfg.numAttrs = large ? 2 : 1;
   return large ? cudaLaunchKernelEx(&cfg, eight, args...) : cudaLaunchKernelEx(&cfg, one, args...);
 }
 
 }  // namespace
+
+cudaError_t pages_set_attributes() {
+  return cudaFuncSetAttribute(copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(CopySmem));
+}
 
 cudaError_t launch_page_fork(const ForkArgs& a, cudaStream_t s) {
   const bool large = (long long)a.n_fork * a.max_pages > kOneCtaEntries || a.n_free > 4 * kOneCtaEntries;
@@ -523,7 +671,7 @@ cudaError_t launch_page_release(const ReleaseArgs& a, cudaStream_t s) {
 
 cudaError_t launch_page_compact(const CompactArgs& a, cudaStream_t s) {
   const long long entries = (long long)a.n_seq * a.max_pages;
-  const int remap = entries <= 16 * kOneCtaEntries ? 1 : 0;
+  const int remap = entries <= 32 * kOneCtaEntries ? 1 : 0;
   const bool large = a.n_free > kOneCtaEntries || (remap && entries > kOneCtaEntries);
   const cudaError_t e = launch_team(compact_kernel<1>, compact_kernel<kTeamCtas>, large, s, a, remap);
   if (e != cudaSuccess || remap) return e;
@@ -532,20 +680,27 @@ cudaError_t launch_page_compact(const CompactArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_page_copy(PageCopyArgs a, int sm_count, cudaStream_t s) {
-  a.pieces = 0;
-  for (int j = 0; j < a.n_pools; ++j) {
-    PageCopyArgs::Pool& p = a.pool[j];
-    const size_t both = reinterpret_cast<size_t>(p.base) | (size_t)p.bytes;
-    p.width = both % 16 == 0 ? 16 : both % 8 == 0 ? 8 : both % 4 == 0 ? 4 : both % 2 == 0 ? 2 : 1;
-    const long long step = (long long)kCopyThreads * kCopyLoads * p.width;
-    p.first = a.pieces;
-    p.pieces = p.bytes < 2048 ? 0 : (int)((p.bytes + step - 1) / step);
-    a.pieces += p.pieces;
+  // pieces of 32 KiB when they fill the device, else of 8 KiB, which more SMs share
+  for (a.piece_bytes = kPieceBytes;; a.piece_bytes = kPieceBytes / 4) {
+    a.pieces = 0;
+    a.small = false;
+    for (int j = 0; j < a.n_pools; ++j) {
+      PageCopyArgs::Pool& p = a.pool[j];
+      const size_t both = reinterpret_cast<size_t>(p.base) | (size_t)p.bytes;
+      p.width = both % 16 == 0 ? 16 : both % 8 == 0 ? 8 : both % 4 == 0 ? 4 : both % 2 == 0 ? 2 : 1;
+      p.first = a.pieces;
+      p.pieces = p.width < 16 || p.bytes < kBulkLeast ? 0 : (int)((p.bytes + a.piece_bytes - 1) / a.piece_bytes);
+      a.pieces += p.pieces;
+      a.small |= p.pieces == 0;
+    }
+    if (a.piece_bytes < kPieceBytes || (long long)a.n_copies * a.pieces >= sm_count) break;
   }
-  if (a.pieces == 0) a.pieces = 1;
-  const long long items = (long long)a.n_copies * a.pieces, most = 8LL * sm_count;
-  copy_kernel<<<(unsigned)(items < most ? items : most), kCopyThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const long long bulk = (long long)a.n_copies * a.pieces, small = a.small ? (a.n_copies + 6LL) / 7 : 0;
+  const long long ctas = bulk > small ? bulk : small;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)(ctas < sm_count ? ctas : sm_count), kCopyThreads,
+                                                   sizeof(CopySmem), s, attr);
+  return cudaLaunchKernelEx(&cfg, copy_kernel, a);
 }
 
 }  // namespace ga

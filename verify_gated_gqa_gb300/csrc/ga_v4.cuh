@@ -75,40 +75,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
       : "memory");
 }
-// Programmatic dependent launch: the next kernel's blocks may be placed from here on; they wait
-// (grid_wait) for this one's end before they read what it wrote.
-__device__ __forceinline__ void grid_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// These blocks may be resident while the kernel that writes their inputs still runs, so the inputs
-// are not read-only for a block's whole life: not the non-coherent path, but plain loads that stay
-// behind grid_wait (and may pass the block's own stores).
-__device__ __forceinline__ uint4 ld_input(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 ld_input(const uint2* p) {
-  uint2 v;
-  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ int ld_input(const int* p) {
-  int v;
-  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_input(const uint8_t* p) {
-  uint32_t v;
-  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint16_t ld_input(const uint16_t* p) {
-  uint16_t v;
-  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
-  return v;
-}
 // The merge reads the lengths before its wait (the attention kernel waited for their writer before it
 // let the merge begin): from L2, where they are current.
 __device__ __forceinline__ int ld_len(const int* p) {
@@ -145,18 +111,19 @@ __host__ __device__ __forceinline__ int row_blocks(int rows) {
 // long one: 64 ragged sequences of up to 8,192 keys, one row: 60 us against 54; of up to 300 keys
 // 24 against 18; 5 x 5 rows over up to 12,345 keys 25 against 21; 200 x 5 rows over up to 2,047 93
 // against 85. (Equal long streams take the same: 64 x 4,095 keys 53 us.)
-template <int kTile>
-constexpr int kLead = kTile == 32 ? 16 : 6;
-template <int kTile>
+// (The 8-bit form, kQ8, has cheaper segments for its tiles.)
+template <int kTile, bool kQ8 = false>
+constexpr int kLead = kTile == 32 ? 16 : kQ8 ? 3 : 6;
+template <int kTile, bool kQ8 = false>
 constexpr int kFront = kTile == 32 ? 8 : 2;
-template <int kTile>
+template <int kTile, bool kQ8 = false>
 __device__ __forceinline__ int stream_units(int tiles) {
-  return tiles ? tiles + kLead<kTile> : 0;
+  return tiles ? tiles + kLead<kTile, kQ8> : 0;
 }
 // A stream's units that no boundary cuts off from its beginning (few streams are cut finely).
-template <int kTile>
+template <int kTile, bool kQ8 = false>
 __device__ __forceinline__ int uncut(int share) {
-  return kLead<kTile> + min(kFront<kTile>, share);
+  return kLead<kTile, kQ8> + min(kFront<kTile, kQ8>, share);
 }
 
 // A worker's share of the streams' units: `left` units from unit `at` of stream (head, b) on.
@@ -188,11 +155,11 @@ struct Units {
 // By a whole block of at least kV4MaxSeq threads, a sequence each (`tiles` is 0 past the last); one
 // block barrier. Short on purpose: this code runs once, from a cold instruction cache, before
 // anything can be loaded (a warp's search over the sequences took 2.5 us here).
-template <int kTile>
+template <int kTile, bool kQ8 = false>
 __device__ __forceinline__ Units scan_units(int tiles, int (&warp_units)[kV4MaxSeq / 32],
                                             int (&warp_streams)[kV4MaxSeq / 32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = stream_units<kTile>(tiles);
+  const int n = stream_units<kTile, kQ8>(tiles);
   int sum = n, streams = 0;
   if (threadIdx.x < kV4MaxSeq) {
 #pragma unroll
@@ -223,7 +190,7 @@ __device__ __forceinline__ Units scan_units(int tiles, int (&warp_units)[kV4MaxS
 
 // The sequences' tiles and the part of the cut of worker `me` of `workers`: both heads' sequences,
 // end to end. A refused length is recorded by the first block. Two block barriers.
-template <int kTile>
+template <int kTile, bool kQ8 = false>
 __device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int workers, int me) {
   const int b = threadIdx.x;
   int tiles = 0;
@@ -235,7 +202,7 @@ __device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int wor
     c.tiles[b] = (uint16_t)tiles;
     c.spare[b] = (uint8_t)(tiles * kTile - L - a.rows);
   }
-  const Units q = scan_units<kTile>(tiles, c.warp_units, c.warp_streams);
+  const Units q = scan_units<kTile, kQ8>(tiles, c.warp_units, c.warp_streams);
   const int total = q.per_head * kKvHeads, share = v4_share(total, workers);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -243,16 +210,16 @@ __device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int wor
     if (u >= total) {
       if (b == 0) {
         c.at[i] = total;
-        c.tiles_at[i] = total - kLead<kTile> * kKvHeads * q.all_streams;
+        c.tiles_at[i] = total - kLead<kTile, kQ8> * kKvHeads * q.all_streams;
       }
       continue;
     }
     const int head = u / q.per_head, rem = u - head * q.per_head - q.before;
     if (0 <= rem && rem < q.n) {   // one sequence's thread (n is 0 past the last)
-      const int rel = rem < uncut<kTile>(share) ? 0 : rem;
+      const int rel = rem < uncut<kTile, kQ8>(share) ? 0 : rem;
       const int at = head * q.per_head + q.before + rel;
       c.at[i] = at;
-      c.tiles_at[i] = at - kLead<kTile> * (head * q.all_streams + q.streams) - min(rel, kLead<kTile>);
+      c.tiles_at[i] = at - kLead<kTile, kQ8> * (head * q.all_streams + q.streams) - min(rel, kLead<kTile, kQ8>);
       if (i == 0) {
         c.head0 = head;
         c.b0 = b;
@@ -267,25 +234,25 @@ template <int kTile>
 __device__ __forceinline__ int cut_len(const V4Cut& c, int b, int rows) {
   return (int)c.tiles[b] * kTile - (int)c.spare[b] - rows;
 }
-template <int kTile>
+template <int kTile, bool kQ8 = false>
 struct Walk {
   int head, b, at, left, seen;
   __device__ __forceinline__ explicit Walk(const V4Cut& c)
       : head(c.head0), b(c.b0), at(c.at0), left(c.at[1] - c.at[0]), seen(0) {}
   __device__ __forceinline__ bool next(const V4Cut& c, int n_seq, Seg& s) {
     if (left <= 0) return false;
-    int total = stream_units<kTile>(c.tiles[b]);
+    int total = stream_units<kTile, kQ8>(c.tiles[b]);
     while (at >= total) {   // the next stream with tiles
       at = 0;
       if (++b == n_seq) {
         b = 0;
         ++head;
       }
-      total = stream_units<kTile>(c.tiles[b]);
+      total = stream_units<kTile, kQ8>(c.tiles[b]);
     }
     const int n = min(left, total - at);   // past the lead: no boundary lies in one
-    s.kt0 = max(at - kLead<kTile>, 0);
-    s.n = at + n - kLead<kTile> - s.kt0;
+    s.kt0 = max(at - kLead<kTile, kQ8>, 0);
+    s.n = at + n - kLead<kTile, kQ8> - s.kt0;
     s.whole = n == total;
     s.head = head;
     s.b = b;
@@ -297,22 +264,6 @@ struct Walk {
     return true;
   }
 };
-
-// Launch that may be placed while the kernel before it in the stream ends (its blocks call
-// grid_wait before they touch memory that one may use).
-inline cudaLaunchConfig_t overlapped_launch(unsigned grid, unsigned block, size_t smem, cudaStream_t s,
-                                            cudaLaunchAttribute (&attr)[1]) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cfg;
-}
 
 // A part's O in the workspace: float4 of four dims at (slot, dims / 4, row), rows innermost, so that
 // the attention kernel, whose threads hold a row each, writes whole sectors (row after row of 1

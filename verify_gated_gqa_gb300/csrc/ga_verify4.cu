@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     tiles = seq_tiles<kTile>(a, ld_len(a.seq_len + tid), refused);
   }
   if (tid == 0) cut_n = 0;
-  const Units q = scan_units<kTile>(tiles, warp_units, warp_streams);
+  const Units q = scan_units<kTile, kByRow>(tiles, warp_units, warp_streams);
   const int total = q.per_head * kKvHeads, share = v4_share(total, workers);
   if (slices) {
     if (tid == rest % a.n_seq) {
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     }
   } else if (const int u = share * (w + 1); u < total) {   // the stream that the boundary cuts, if any
     const int head = u / q.per_head, rem = u - head * q.per_head - q.before;
-    if (uncut<kTile>(share) <= rem && rem < q.n) {
+    if (uncut<kTile, kByRow>(share) <= rem && rem < q.n) {
       cut_b = tid;
       cut_head = head;
       cut_u0 = u - rem;
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   }
   // its parts: worker c0 has its first tile; boundaries cut it from u0 + uncut on
   const int b = cut_b, head = cut_head, u0 = cut_u0, u1 = u0 + cut_n;
-  const int c0 = (min(u0 + uncut<kTile>(share), u1) - 1) / share;
+  const int c0 = (min(u0 + uncut<kTile, kByRow>(share), u1) - 1) / share;
   const int n = (u1 - 1) / share - c0 + 1;
   // part i is of worker c0 + i: its first segment unless the stream began inside the worker's run
   const bool inside = c0 * share < u0;

@@ -233,7 +233,7 @@ __device__ void load_tiles(const Cta& c, const CUtensorMap* map, bool is_v) {
   const uint8_t* scale_pool = is_v ? c.a.v_scales : c.a.k_scales;
   Ring ring(c.lay.stages);
   uint32_t issued = 0;
-  Walk<kTileN> walk(c.ctl.cut);
+  Walk<kTileN, true> walk(c.ctl.cut);
   Seg seg;
   while (walk.next(c.ctl.cut, a.n_seq, seg)) {
     const int end = cut_len<kTileN>(c.ctl.cut, seg.b, a.rows) + a.rows;
@@ -369,7 +369,7 @@ struct Issue {
 __device__ void issue_mma(const Cta& c) {
   const Verify4Args& a = c.a.v;
   Issue is(c);
-  Walk<kTileN> walk(c.ctl.cut);
+  Walk<kTileN, true> walk(c.ctl.cut);
   Seg seg;
   uint32_t done = 0;
   while (walk.next(c.ctl.cut, a.n_seq, seg)) {
@@ -505,7 +505,7 @@ __device__ void softmax_worker(const Cta& c) {
   const uint32_t sf0 = smem_u32(c.smem + c.lay.sf(0)) + quarter;
   const uint32_t scales0 = smem_u32(c.ctl.scales[0][quarter]), scales_full = smem_u32(c.ctl.scales_full);
   const uint32_t s_full = smem_u32(c.ctl.s_full), s_free = smem_u32(c.ctl.s_free), p_full = smem_u32(c.ctl.p_full);
-  Walk<kTileN> walk(c.ctl.cut);
+  Walk<kTileN, true> walk(c.ctl.cut);
   Seg seg, next;
   bool more = walk.next(c.ctl.cut, a.n_seq, seg);
   if (more) load_queries(seg);
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   tc_fence_before();
   {   // two block barriers
     const int blocks = row_blocks(a.v.rows);
-    make_cut<kTileN>(a.v, ctl.cut, (int)gridDim.x / blocks, (int)blockIdx.x / blocks);
+    make_cut<kTileN, true>(a.v, ctl.cut, (int)gridDim.x / blocks, (int)blockIdx.x / blocks);
   }
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
