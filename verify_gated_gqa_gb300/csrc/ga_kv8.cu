@@ -11,9 +11,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kChunk = 32;                       // tokens whose runs a CTA stores
-constexpr int kTokRows = 2 * kKvHeads;           // a token's rows: K heads 0, 1, V heads 0, 1
-constexpr int kStoreThreads = 512;
-constexpr int kRowWarps = kStoreThreads / 32 / kTokRows;   // warps of each
+constexpr int kRowWarps = kWarps / kKvHeads;               // warps of each head
 constexpr int kKept = kChunk / kRowWarps;                  // rows that a warp keeps in registers
 
 struct Slot {
@@ -55,20 +53,32 @@ __device__ __forceinline__ uint2 encode(const uint4& x, float inv) {
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
-// A run is a row of tokens of one block. CTA c stores the runs that begin among tokens 32 c .. 32 c +
-// 31: a prompt's chunk has one or two, a decode batch 32 of one token. Four warps take each of a
-// token's four rows, 8 values a lane. A chunk's rows stay in registers from the search for the maxima
+// A run is a row of tokens of one block. CTA (c, kv) stores the keys' or values' runs that begin among
+// tokens 32 c .. 32 c + 31: a prompt's chunk has one or two, a decode batch 32 of one token. Four warps
+// take each head, 8 values a lane. The rows are on their way before the slots are known. A chunk's stay in registers from the search for the maxima
 // to their codes; those of a run that goes on past the chunk (31 at most) are read again. Bound by
 // the bytes it moves.
-__global__ void __launch_bounds__(kStoreThreads, 2) quantize_kernel(const __grid_constant__ Kv8Args a) {
-  __shared__ uint32_t top[kTokRows][kChunk], written[kChunk];
-  __shared__ int exps[kTokRows][kChunk], shift[kTokRows][kChunk], first[kChunk];
+__global__ void __launch_bounds__(kThreads, 5) quantize_kernel(const __grid_constant__ Kv8Args a) {
+  __shared__ uint32_t top[kKvHeads][kChunk], written[kChunk];
+  __shared__ int exps[kKvHeads][kChunk], shift[kKvHeads][kChunk], first[kChunk];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = warp / kRowWarps, part = warp % kRowWarps;
+  const int head = warp / kRowWarps, part = warp % kRowWarps, kv = blockIdx.y;
   const long long t0 = (long long)blockIdx.x * kChunk;
-  if (tid < kTokRows * kChunk) top[tid / kChunk][tid % kChunk] = 0u;
+  const uint16_t* in = (kv ? a.v : a.k) + head * kDim;
+  const long long ld = kv ? a.ld_v : a.ld_k;
+  uint8_t* codes = kv ? a.v_codes : a.k_codes;
+  uint8_t* scales = kv ? a.v_scales : a.k_scales;
+  if (tid < kKvHeads * kChunk) top[tid / kChunk][tid % kChunk] = 0u;
   grid_wait();
   grid_launch_dependents();
+  auto load = [&](int at) { return ld_input(reinterpret_cast<const uint4*>(in + (t0 + at) * ld) + lane); };
+  uint4 x[kKept];
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const int at = part + kRowWarps * i;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (t0 + at < a.n_tok) x[i] = load(at);
+  }
   // every warp finds the runs: this lane's tokens are t0 + lane and t0 + 32 + lane
   const int s0 = slot_of(a, t0 + lane), s1 = slot_of(a, t0 + kChunk + lane);
   int before = __shfl_up_sync(0xffffffffu, s0, 1);
@@ -89,34 +99,23 @@ __global__ void __launch_bounds__(kStoreThreads, 2) quantize_kernel(const __grid
     if (s0 >= 0 && run0 >= 0) atomicOr(&written[run0], 1u << (s0 & 31));
     if (lane < more) atomicOr(&written[runs - 1], 1u << (s1 & 31));
   }
-  const int head = row & 1, kv = row >> 1;
-  const uint16_t* in = (kv ? a.v : a.k) + head * kDim;
-  const long long ld = kv ? a.ld_v : a.ld_k;
-  uint8_t* codes = kv ? a.v_codes : a.k_codes;
-  auto load = [&](int at) { return ld_input(reinterpret_cast<const uint4*>(in + (t0 + at) * ld) + lane); };
-  uint4 x[kKept];
-#pragma unroll
-  for (int i = 0; i < kKept; ++i) {
-    const int at = part + kRowWarps * i;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (__shfl_sync(0xffffffffu, s0, at) >= 0 && __shfl_sync(0xffffffffu, run0, at) >= 0) x[i] = load(at);
-  }
   __syncthreads();   // top is zero
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
-    const int at = part + kRowWarps * i, run = __shfl_sync(0xffffffffu, run0, at);
+    const int at = part + kRowWarps * i;
+    const int slot = __shfl_sync(0xffffffffu, s0, at), run = __shfl_sync(0xffffffffu, run0, at);
     const uint32_t m = __reduce_max_sync(0xffffffffu, top_of(x[i]));
-    if (lane == 0 && m != 0u && run >= 0) atomicMax(&top[row][run], m);
+    if (lane == 0 && slot >= 0 && run >= 0) atomicMax(&top[head][run], m);
   }
   for (int at = part; at < more; at += kRowWarps) {
     const uint32_t m = __reduce_max_sync(0xffffffffu, top_of(load(kChunk + at)));
-    if (lane == 0) atomicMax(&top[row][runs - 1], m);
+    if (lane == 0) atomicMax(&top[head][runs - 1], m);
   }
   __syncthreads();
   bool grows = false;
-  if (tid < kTokRows * kChunk && tid % kChunk < runs) {
-    const int r = tid / kChunk, run = tid % kChunk;   // (its own row, kv and head: not this warp's)
-    uint8_t* at = (r >> 1 ? a.v_scales : a.k_scales) + slot_place(a, first[run]).scale + (r & 1) * (a.page_size / kQ8Block);
+  if (tid < kKvHeads * kChunk && tid % kChunk < runs) {
+    const int r = tid / kChunk, run = tid % kChunk;   // (a head of its own: not this warp's)
+    uint8_t* at = scales + slot_place(a, first[run]).scale + r * (a.page_size / kQ8Block);
     int e = exp_for(top[r][run]), grown = 0;
     if ((written[run] & 1u) == 0u) {   // the block goes on
       const int was = q8_exp(*at);
@@ -131,7 +130,7 @@ __global__ void __launch_bounds__(kStoreThreads, 2) quantize_kernel(const __grid
   const bool any = __syncthreads_or(grows);
   auto store = [&](int slot, int run, const uint4& v) {
     const long long at = slot_place(a, slot).row + head * a.page_size;
-    reinterpret_cast<uint2*>(codes + at * kQ8RowBytes)[lane] = encode(v, pow2i(-exps[row][run]));
+    reinterpret_cast<uint2*>(codes + at * kQ8RowBytes)[lane] = encode(v, pow2i(-exps[head][run]));
   };
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
@@ -144,11 +143,11 @@ __global__ void __launch_bounds__(kStoreThreads, 2) quantize_kernel(const __grid
   // the other rows of blocks that grew
   for (int i = part; i < runs * kQ8Block; i += kRowWarps) {
     const int run = i / kQ8Block, off = i % kQ8Block;
-    if (shift[row][run] == 0 || (written[run] >> off & 1u)) continue;
+    if (shift[head][run] == 0 || (written[run] >> off & 1u)) continue;
     const long long at = slot_place(a, (first[run] & ~31) + off).row + head * a.page_size;
     uint2* p = reinterpret_cast<uint2*>(codes + at * kQ8RowBytes) + lane;
     const uint2 c = *p;
-    const float inv = pow2i(-shift[row][run]);
+    const float inv = pow2i(-shift[head][run]);
     uint32_t w[2] = {c.x, c.y}, o[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -206,7 +205,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
 
 cudaError_t launch_quantize_q8(const Kv8Args& a, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)((a.n_tok + kChunk - 1) / kChunk), kStoreThreads, 0, s, attr);
+  cudaLaunchConfig_t cfg = overlapped_launch((unsigned)((a.n_tok + kChunk - 1) / kChunk), kThreads, 0, s, attr);
+  cfg.gridDim.y = 2;   // keys, values
   return cudaLaunchKernelEx(&cfg, quantize_kernel, a);
 }
 

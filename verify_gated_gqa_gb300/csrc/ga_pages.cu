@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
   grid_wait();
   grid_launch_dependents();
   if (tid < GA_PLAN_MAX_SEQ / 32) named[tid] = 0u;
+  copy_array(team, a.shared, a.shared_out, a.n_free);
   const int count = *a.free_count;
   int err = count < 0 || count > a.n_free ? 8 : 0;
   __syncthreads();
@@ -170,10 +171,8 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
     forks += parent[k] >= 0 && !status;
   }
   const int made = __syncthreads_count(forks > 0) + __syncthreads_count(forks > 1);
-  team.sync();   // every CTA has read what is written from here on
   copy_array(team, a.held, a.held_out, a.n_seq);
-  copy_array(team, a.shared, a.shared_out, a.n_free);
-  team.sync();
+  team.sync();   // every CTA has read what is written from here on
   if (team.rank == 0) {
     if (tid == 0) {
       *a.free_count_out = count - (int)total.b;
@@ -227,6 +226,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
   const int tid = threadIdx.x;
   grid_wait();
   grid_launch_dependents();
+  copy_array(team, a.shared, a.shared_out, a.n_free);
   const int count = *a.free_count;
   int err = count < 0 || count > a.n_free ? 8 : 0;
   unsigned gone[2], rows = 0;
@@ -252,11 +252,9 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
   start[2 * tid + 1] = before.a + gone[0];
   const bool range = __syncthreads_or(err) != 0;   // the same in every CTA
   team.sync();   // every CTA has read what is written from here on
-  copy_array(team, a.shared, a.shared_out, a.n_free);
   int status = range ? 4 : 0;
   unsigned freed = 0;
   if (!status && total.a > 0u) {
-    if (a.shared != a.shared_out) team.sync();
     // this thread's places; as many of their pages as fit stay in registers, so that the loads of a step
     // are all in flight at once (one by one, 31,000 pages took 21 us)
     constexpr unsigned kKeep = 8;
@@ -308,8 +306,14 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
         if (v < 0) atomicMin(a.shared_out + page, INT_MIN + (int)i);
       });
       team.sync();
+      // first places: those in registers are remembered, later ones read again
       Pair own = {0u, 0u}, sum;
-      each(read, [&](unsigned i, int, int v) { own.a += v == INT_MIN + (int)i; });
+      uint32_t firsts = 0u;
+      each(read, [&](unsigned i, int, int v) {
+        const bool is = v == INT_MIN + (int)i;
+        own.a += is;
+        if (i - lo < kKeep) firsts |= (uint32_t)is << (i - lo);
+      });
       unsigned to = team.scan(1, own, sum).a;
       if ((long long)count + sum.a > a.n_free) {
         status = 4;
@@ -320,8 +324,9 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
         put_back();
       } else {
         freed = sum.a;
-        each(read, [&](unsigned i, int page, int v) {
-          if (v != INT_MIN + (int)i) return;
+        const auto again = [&](int page) { return hi - lo > kKeep ? left[page] : 0; };
+        each(again, [&](unsigned i, int page, int v) {
+          if (i - lo < kKeep ? !(firsts >> (i - lo) & 1u) : v != INT_MIN + (int)i) return;
           a.free_pages[count + (int)to++] = page;
           left[page] = 0;
         });
