@@ -20,8 +20,9 @@ NATIVE_SRC = os.path.join(CSRC, "ga_native.cpp")
 NATIVE = os.path.join(PKG, "_native.so")
 SOURCES = ["ga_host.cu", "ga_prologue.cu", "ga_attn.cu", "ga_mask.cu", "ga_quant.cu",
            "ga_select.cu", "ga_kv4.cu", "ga_plan.cu", "ga_verify4.cu", "ga_decode4.cu",
-           "ga_pages.cu", "ga_kv8.cu", "ga_verify8.cu", "ga_debug.cu"]
-HEADERS = ["ga_internal.h", "ga_numerics.cuh", "ga_q4.cuh", "ga_q8.cuh", "ga_sm100.cuh", "ga_v4.cuh"]
+           "ga_pages.cu", "ga_kv8.cu", "ga_verify8.cu", "ga_verify8_rows.cu",
+           "ga_debug.cu"]
+HEADERS = ["ga_internal.h", "ga_numerics.cuh", "ga_q4.cuh", "ga_q8.cuh", "ga_sm100.cuh", "ga_v4.cuh", "ga_v8.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "-I", os.path.join(ROOT, "include")]

@@ -234,6 +234,10 @@ int verify8_box_keys(int page_size);
 cudaError_t verify8_set_attributes();
 cudaError_t launch_verify8(const CUtensorMap& k_codes, const CUtensorMap& v_codes, const Verify8Args& a,
                            int sm_count, cudaStream_t s);
+// The form for five rows and more (ga_verify8_rows.cu), called by launch_verify8.
+cudaError_t verify8_rows_set_attributes();
+cudaError_t launch_verify8_rows(const CUtensorMap& k_codes, const CUtensorMap& v_codes, const Verify8Args& a,
+                                int ctas, cudaStream_t s);
 
 // Pages that several sequences hold (ga_pages.cu).
 struct ForkArgs {

@@ -273,9 +273,10 @@ __device__ __forceinline__ float4* part_at(float* part_o, int slot, int d4, int 
   return reinterpret_cast<float4*>(part_o) + ((size_t)slot * (kDim / 4) + d4) * kV4Lanes + row;
 }
 
-// The log-sum-exp merge of the streams that the cut over `workers` left in parts, after either 4-bit
-// kernel with tiles of `tile` keys (128 or 32), or the 8-bit one (128), whose parts lie row after row
+// The log-sum-exp merge of the streams that the cut over `workers` left in parts, after a kernel with
+// tiles of `tile` keys (128 or 32), of either cache (q8), whose parts lie as above or row after row
 // (by_row).
-cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, bool by_row, cudaStream_t s);
+cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, bool q8, bool by_row,
+                                   cudaStream_t s);
 
 }  // namespace ga

@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // turned into weights in shared memory first, 76 parts of 96 rows took 28 us.)
 constexpr int kCombineThreads = 384, kSplit = 2;
 static_assert(kCombineThreads >= kV4MaxSeq, "a sequence a thread");
-template <int kTile, bool kByRow>
+template <int kTile, bool kQ8, bool kByRow>
 __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     const __grid_constant__ Verify4Args a, int workers, int slices) {
   __shared__ int warp_units[kV4MaxSeq / 32], warp_streams[kV4MaxSeq / 32];
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     tiles = seq_tiles<kTile>(a, ld_len(a.seq_len + tid), refused);
   }
   if (tid == 0) cut_n = 0;
-  const Units q = scan_units<kTile, kByRow>(tiles, warp_units, warp_streams);
+  const Units q = scan_units<kTile, kQ8>(tiles, warp_units, warp_streams);
   const int total = q.per_head * kKvHeads, share = v4_share(total, workers);
   if (slices) {
     if (tid == rest % a.n_seq) {
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     }
   } else if (const int u = share * (w + 1); u < total) {   // the stream that the boundary cuts, if any
     const int head = u / q.per_head, rem = u - head * q.per_head - q.before;
-    if (uncut<kTile, kByRow>(share) <= rem && rem < q.n) {
+    if (uncut<kTile, kQ8>(share) <= rem && rem < q.n) {
       cut_b = tid;
       cut_head = head;
       cut_u0 = u - rem;
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   }
   // its parts: worker c0 has its first tile; boundaries cut it from u0 + uncut on
   const int b = cut_b, head = cut_head, u0 = cut_u0, u1 = u0 + cut_n;
-  const int c0 = (min(u0 + uncut<kTile, kByRow>(share), u1) - 1) / share;
+  const int c0 = (min(u0 + uncut<kTile, kQ8>(share), u1) - 1) / share;
   const int n = (u1 - 1) / share - c0 + 1;
   // part i is of worker c0 + i: its first segment unless the stream began inside the worker's run
   const bool inside = c0 * share < u0;
@@ -724,15 +724,16 @@ cudaError_t verify4_set_attributes() {
   return e != cudaSuccess ? e : decode4_set_attributes();
 }
 
-cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, bool by_row, cudaStream_t s) {
+cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, bool q8, bool by_row, cudaStream_t s) {
   const int blocks = row_blocks(a.rows), streams = a.n_seq * kKvHeads * blocks;
   const int ctas = workers * blocks, slices = streams * 2 >= ctas ? 0 : 2 * ctas / streams < 64 ? 2 * ctas / streams : 64;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = overlapped_launch(
       (unsigned)(slices ? streams * slices : (workers - 1) * blocks * kSplit), kCombineThreads, 0, s, attr);
-  if (by_row) return cudaLaunchKernelEx(&cfg, verify4_combine_kernel<kTileN, true>, a, workers, slices);
-  return tile == kTileN ? cudaLaunchKernelEx(&cfg, verify4_combine_kernel<kTileN, false>, a, workers, slices)
-                        : cudaLaunchKernelEx(&cfg, verify4_combine_kernel<32, false>, a, workers, slices);
+  auto* kernel = q8 ? by_row ? verify4_combine_kernel<kTileN, true, true> : verify4_combine_kernel<kTileN, true, false>
+                 : tile == kTileN ? verify4_combine_kernel<kTileN, false, false>
+                                  : verify4_combine_kernel<32, false, false>;
+  return cudaLaunchKernelEx(&cfg, kernel, a, workers, slices);
 }
 
 cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_codes,
@@ -744,7 +745,7 @@ cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_code
   const int blocks = row_blocks(a.rows), workers = ctas / blocks;
   const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)(workers * blocks), kThreads, sizeof(V4Smem), s, attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, verify4_kernel, k_codes, v_codes, k_scales, v_scales, a);
-  return e != cudaSuccess ? e : launch_verify4_combine(a, workers, kTileN, false, s);
+  return e != cudaSuccess ? e : launch_verify4_combine(a, workers, kTileN, false, false, s);
 }
 
 }  // namespace ga
