@@ -1,0 +1,208 @@
+"""The attention over 8-bit caches where its reference exponents move inside a segment, captured and
+replayed, on two streams at once, next to the other caches' calls, and its refusals through the
+binding."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import ga_oracle as O
+from tests.parity import SEED, np64
+from tests.q4_bounds import attend64, row_errors
+from tests.q8_bounds import ROW_BOUND, allowed, rest_of, score_error
+from verify_gated_gqa_gb300 import binding as B
+from verify_gated_gqa_gb300 import build as build_mod
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build_mod.build()
+    B.lib()
+    yield
+    assert B.ga_device_status() == 0
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(SEED + seed)
+    return g
+
+
+def _normal(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+
+def _pools(n_pages, page):
+    u8 = lambda *s: torch.full((n_pages, 2) + s, 0x7F, dtype=torch.uint8, device="cuda")  # noqa: E731
+    return [u8(page, 256), u8(page // 32), u8(page, 256), u8(page // 32)]
+
+
+def _slots(table, page, keys):
+    t = torch.arange(keys, device="cuda")
+    return (table.long()[:, t // page] * page + t % page).to(torch.int32)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 4, 5, 8, 11, 16])
+def test_references_that_move_inside_a_segment(rows):
+    """So many sequences that the CTAs run whole streams. Every query row has two keys of its own, at
+    places of its own, whose scores are about 60 and 120 nats above the rest: a block there passes the
+    row's reference by more than 2^64, for some rows of a warp and not for others, with products in O
+    already. A factor left out, or given to part of O only, would leave what came before 2^80 too large."""
+    g, rng = _gen(rows), np.random.default_rng(SEED + rows)
+    n, length, page = 160, 1250, 64
+    keys = length + rows
+    per = -(-keys // page)
+    table = _i32(rng.permutation(n * per).reshape(n, per))
+    q, qg = _normal(g, n, rows, 24, 256), _normal(g, n, rows, 24, 512)
+    k = torch.randn(n, keys, 2, 256, generator=g, device="cuda") * 0.3
+    v = _normal(g, n, keys, 2, 256)
+    for b in range(n):
+        for kv in range(2):
+            at = rng.permutation(length - 600)[:12 * rows]
+            own = q[b, :, 12 * kv:12 * kv + 12].reshape(12 * rows, 256).float()
+            k[b, torch.tensor(at + 200, device="cuda"), kv] = 3.75 * own
+            k[b, torch.tensor(at + 600, device="cuda"), kv] = 7.5 * own
+    pools = _pools(n * per, page)
+    slots = _slots(table, page, keys)
+    B.ga_kv_quantize_q8(k.flatten(0, 1).to(torch.bfloat16), v.flatten(0, 1), *pools, slots=slots.flatten())
+    out = B.ga_attn_verify_q8(q, qg, *pools, table, _i32([length] * n)).view(n, rows, 24, 256)
+    for b in (0, 3, 77, 120, 159):
+        kw, vw = B.ga_kv_dequantize_q8(*pools, slots=slots[b])
+        kb, vb = np64(kw), np64(vw)
+        heads = [0, 5, 11, 12, 23]
+        want, mass = O.verify_q4(np64(q[b])[None], np64(qg[b])[None, ..., 256:], [kb], [vb], [length], heads)
+        rest = rest_of(np64(q[b]), np64(qg[b])[..., 256:], kb, vb, length)
+        x = score_error(np64(q[b]), kb[:, 0])
+        bad = np.abs(np64(out[b]) - want[0]) > allowed(want[0], mass[0], x, rest)
+        assert not bad[:, heads].any(), (b, bad[:, heads].sum())
+
+
+def _serving(g, lens, rows, page):
+    width = max(-(-(x + rows + 40) // page) for x in lens)
+    table = torch.randperm(len(lens) * width, generator=g, device="cuda").to(torch.int32).view(len(lens), width)
+    pools = _pools(len(lens) * width, page)
+    slots = _slots(table, page, width * page)
+    n = len(lens) * width * page
+    B.ga_kv_quantize_q8(_normal(g, n, 2, 256), _normal(g, n, 2, 256), *pools, slots=slots.flatten())
+    return pools, table, _normal(g, len(lens), rows, 24, 256), _normal(g, len(lens), rows, 24, 512)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 6, 16])
+def test_captured_and_replayed_with_other_lengths(rows):
+    g = _gen(20 + rows)
+    pools, table, q, qg = _serving(g, [900, 40, 2000, 300], rows, 32)
+    lens, out = _i32([5, 6, 7, 8]), torch.zeros(4, rows, 6144, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(B.ga_verify_q8_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    run = lambda o: B.ga_attn_verify_q8(q, qg, *pools, table, lens, out=o, workspace=ws)  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(out)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(out)
+    for new in ([900, 40, 2000, 300], [0, 0, 0, 0], [31, -1, 1999, -1], [-1] * 4, [1, 63, 64, 65]):
+        lens.copy_(_i32(new))
+        q.copy_(_normal(g, *q.shape))
+        ws.fill_(0xFF)
+        out.fill_(3.0)
+        graph.replay()
+        want = torch.full_like(out, 3.0)
+        ws.fill_(0xFF)
+        run(want)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        for b, x in enumerate(new):
+            assert bool((out[b] == 3).all()) == (x < 0)
+    for b, x in enumerate(new):
+        kw, vw = B.ga_kv_dequantize_q8(*pools, slots=_slots(table[b:b + 1], 32, x + rows)[0])
+        for kv in range(2):
+            hs = slice(12 * kv, 12 * kv + 12)
+            w = attend64(q[b, :, hs], qg[b, :, hs, 256:], kw[:, kv], vw[:, kv], [x + r + 1 for r in range(rows)])
+            # few keys: an element's own bound times the row's, as in ROW_BOUND's derivation
+            assert float(row_errors(out.view(4, rows, 24, 256)[b, :, hs], w).max()) <= 3 * ROW_BOUND
+
+
+@pytest.mark.parametrize("rows", [1, 7])
+def test_two_streams_with_a_workspace_each(rows):
+    g = _gen(40 + rows)
+    sets = [_serving(g, [3000, 100, 1700], rows, 64) for _ in range(2)]
+    lens = _i32([3000, 100, 1700])
+    want = [B.ga_attn_verify_q8(q, qg, *p, t, lens) for p, t, q, qg in sets]
+    ws = [torch.empty(B.ga_verify_q8_workspace_bytes(), dtype=torch.uint8, device="cuda") for _ in sets]
+    got = [[torch.empty_like(w) for _ in range(6)] for w in want]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for k, (p, t, q, qg) in enumerate(sets):
+            with torch.cuda.stream(streams[k]):
+                B.ga_attn_verify_q8(q, qg, *p, t, lens, out=got[k][i], workspace=ws[k])
+    torch.cuda.synchronize()
+    for k, w in enumerate(want):
+        assert all(torch.equal(w.view(torch.int16), x.view(torch.int16)) for x in got[k])
+
+
+def test_calls_in_a_row_of_both_forms_and_caches():
+    """Launches that may overlap the ones before them, over one workspace: every call's result is its own."""
+    g = _gen(60)
+    pools, table, q, qg = _serving(g, [700, 1500, 64], 16, 32)
+    lens = _i32([700, 1500, 64])
+    ws = torch.empty(B.ga_verify_q8_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    parts = [(q[:, :r].contiguous(), qg[:, :r].contiguous()) for r in (1, 16, 4, 5, 2, 9)]
+    want = [B.ga_attn_verify_q8(a, b, *pools, table, lens) for a, b in parts]
+    got = []
+    for _ in range(3):
+        for a, b in parts:
+            got.append(B.ga_attn_verify_q8(a, b, *pools, table, lens, workspace=ws))
+    for i, x in enumerate(got):
+        assert torch.equal(x.view(torch.int16), want[i % len(parts)].view(torch.int16))
+
+
+def test_widened_prefix_serves_a_prefill():
+    """A prompt's next chunk over a prefix of the 8-bit cache, widened for the bf16 call."""
+    g = _gen(61)
+    T, rows, page = 320, 64, 64
+    pools, table, _, _ = _serving(g, [T], 1, page)
+    k, v = B.ga_kv_dequantize_q8(*pools, slots=_slots(table, page, T)[0])
+    qg, w = _normal(g, rows, 24, 512), (0.1 * _normal(g, 256).float()).to(torch.bfloat16)
+    c, s = (t.cuda() for t in B.ga_rope_table_host(512))
+    got = B.ga_attn_prefill(qg, k, v, w, c, s, q_base=T - rows)
+    q = B.ga_q_prologue(qg, w, c, s, q_base=T - rows)
+    # the same rows as verify windows of 16
+    for r in range(0, rows, 16):
+        x = B.ga_attn_verify_q8(q[None, r:r + 16].contiguous(), qg[None, r:r + 16].contiguous(), *pools, table,
+                                _i32([T - rows + r]))
+        # the prefill rounds scores, weights and the gate to bf16, each up to 2^-8
+        assert float(row_errors(x.view(16, 24, 256), got[r:r + 16].view(16, 24, 256)).max()) <= 16 * 2.0 ** -8
+
+
+def test_refusals_through_the_binding():
+    g = _gen(62)
+    pools, table, q, qg = _serving(g, [100], 2, 32)
+    lens = _i32([100])
+    with pytest.raises(B.GaError) as e:
+        B.ga_attn_verify_q8(q, qg, *pools, table, lens, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == -6
+    with pytest.raises(B.GaError) as e:
+        B.ga_attn_verify_q8(q[:, :1].repeat(1, 17, 1, 1), qg[:, :1].repeat(1, 17, 1, 1), *pools, table, lens)
+    assert e.value.status == -4
+    for bad in (dict(k=pools[0][:, :, :16]), dict(ks=pools[1][..., None]), dict(v=pools[2].float()),
+                dict(vs=pools[3][:, :1]), dict(table=table.long()), dict(lens=lens[:0]), dict(q=q[..., ::2]),
+                dict(qg=qg[:, :1])):
+        a = {**dict(q=q, qg=qg, k=pools[0], ks=pools[1], v=pools[2], vs=pools[3], table=table, lens=lens), **bad}
+        with pytest.raises(ValueError):
+            B.ga_attn_verify_q8(a["q"], a["qg"], a["k"], a["ks"], a["v"], a["vs"], a["table"], a["lens"])
+    x = _normal(g, 4, 2, 256)
+    with pytest.raises(ValueError):
+        B.ga_kv_quantize_q8(x, x[:3], *pools)
+    with pytest.raises(ValueError):
+        B.ga_page_copy([pools[0], pools[0][:1]], _i32([0]), _i32([1]))
+    with pytest.raises(ValueError):
+        B.ga_page_copy([pools[0].transpose(0, 1)], _i32([0]), _i32([1]))
+    with pytest.raises(ValueError):
+        B.ga_page_copy([], _i32([0]), _i32([1]))
