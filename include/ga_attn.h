@@ -705,8 +705,9 @@ size_t ga_verify_q8_workspace_bytes(void);
  * arguments, rules, workspace rules and errors over the pools above (pages of a multiple of 32
  * tokens). Hidden positions need no initial contents: whatever their codes and scales, NaN codes
  * included, they do not reach a result. Queries and softmax weights meet the codes as sums of two
- * 8-bit parts: a query is within 2^-17 of its row's largest magnitude, a weight within 2^-8 of
- * itself; sums, maxima and O are fp32, and the output is rounded once. A NaN query (or one whose
+ * 8-bit parts: a query is within 2^-17 of its row's largest magnitude, a weight within 2^-9 of
+ * itself or 2^-22 of the largest of its block of 32 keys; sums, maxima and O are fp32, and the output
+ * is rounded once. A NaN query (or one whose
  * scores are infinite, or pass 2^29 in magnitude) makes its own head's row meaningless, and no other.
  * A page-table entry outside the pool records status 3 and its keys are read as zeros.
  * Errors: NULL, SHAPE, RANGE, ALIGN, WORKSPACE, DEVICE, CUDA. */

@@ -346,9 +346,11 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------ compaction
-// map[p] first tells whether page p is free, then where its contents go. Each thread has a run of
-// pages, in order, so that sums of free pages below n_live and of pages in use from it on give the
+// map[p] first tells whether page p is free, then where its contents go. Each warp has a run of pages,
+// in order, so that its loads are whole lines (with a run a thread 262,144 pages took 197 us, so they take
+// 61; 1,024 pages 5.0 and 6.0). Sums of free pages below n_live and of pages in use from it on give the
 // moves their numbers, and those give every place on the new stack.
+constexpr int kMapBatch = 2;   // times 32 pages, loaded together; 1: 262,144 pages 66 us, 4: 59, but 4,096 9.8 for 9.7
 template <int kCtas>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ CompactArgs a, int remap) {
   __shared__ TeamSmem tsm;
@@ -378,62 +380,73 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
   }
   volatile int* map = a.map;
   const int live = n - count;
-  const unsigned per = ((unsigned)n + team.size - 1) / team.size;
-  const int lo = (int)min((unsigned)n, per * team.gid), hi = (int)min((unsigned)n, lo + per);
-  Pair own = {0u, 0u}, sum;   // free pages below live, pages in use from it on: as many of each
-  for (int p = lo; p < hi; ++p) {
-    const int free = map[p];
-    own.a += p < live && free;
-    own.b += p >= live && !free;
-  }
-  const Pair at = team.scan(1, own, sum);
-  const int all = (int)sum.b, moves = min(a.max_moves, all);
-  {
-    int hole = (int)at.a, mover = all - 1 - (int)at.b;
-    for (int p = lo; p < hi; ++p) {
-      const int free = map[p];
-      if (p < live && free) {
-        if (hole < moves) a.move_dst[hole] = p;
-        ++hole;
-      } else if (p >= live && !free) {
-        if (mover < moves) a.move_src[mover] = p;
-        --mover;
+  const int lane = threadIdx.x & 31;
+  const uint32_t before_lane = (1u << lane) - 1u;
+  const int warps = team.size / 32, per = (n + warps - 1) / warps;
+  const int lo = (int)min((long long)n, (long long)per * (team.gid / 32)), hi = min(n, lo + per);
+  // f(page or -1, whether it is free) in order of the warp's run; all lanes call it
+  auto each = [&](auto f) {
+    for (int p0 = lo; p0 < hi; p0 += 32 * kMapBatch) {
+      int free[kMapBatch];
+#pragma unroll
+      for (int k = 0; k < kMapBatch; ++k) free[k] = p0 + 32 * k + lane < hi ? map[p0 + 32 * k + lane] : 0;
+#pragma unroll
+      for (int k = 0; k < kMapBatch; ++k) {
+        const int p = p0 + 32 * k + lane;
+        if (p - lane < hi) f(p < hi ? p : -1, free[k] != 0);
       }
     }
-  }
+  };
+  // free pages below live, and pages in use from it on: as many of each
+  auto is_hole = [&](int p, bool free) { return p >= 0 && p < live && free; };
+  auto is_mover = [&](int p, bool free) { return p >= live && !free; };
+  Pair own = {0u, 0u}, sum;
+  each([&](int p, bool free) {
+    own.a += is_hole(p, free);
+    own.b += is_mover(p, free);
+  });
+  own = {__reduce_add_sync(~0u, own.a), __reduce_add_sync(~0u, own.b)};
+  if (lane != 0) own = {0u, 0u};
+  Pair at = team.scan(1, own, sum);
+  at = {__shfl_sync(~0u, at.a, 0), __shfl_sync(~0u, at.b, 0)};
+  const int all = (int)sum.b, moves = min(a.max_moves, all);
+  // f(page or -1, free, holes before it, movers before it)
+  auto each_numbered = [&](auto f) {
+    int holes = (int)at.a, movers = (int)at.b;
+    each([&](int p, bool free) {
+      const uint32_t h = __ballot_sync(~0u, is_hole(p, free)), m = __ballot_sync(~0u, is_mover(p, free));
+      if (p >= 0) f(p, free, holes + __popc(h & before_lane), movers + __popc(m & before_lane));
+      holes += __popc(h);
+      movers += __popc(m);
+    });
+  };
+  // the lowest holes take the highest movers, highest first
+  each_numbered([&](int p, bool free, int holes, int movers) {
+    if (is_hole(p, free) && holes < moves) a.move_dst[holes] = p;
+    if (is_mover(p, free) && all - 1 - movers < moves) a.move_src[all - 1 - movers] = p;
+  });
   for (int i = moves + team.gid; i < a.max_moves; i += team.size) a.move_src[i] = a.move_dst[i] = -1;
   team.sync();
   volatile int* dst = a.move_dst;
-  int hole = (int)at.a, mover = all - 1 - (int)at.b;
-  // free pages before p afterwards: the holes left, and past live every page but those still in use
-  for (int p = lo; p < hi; ++p) {
-    const int free = map[p];
-    const int past = max(p - live, 0), in_use = all - 1 - mover;   // movers before p
-    const int moved = max(0, in_use - (all - moves));              // and moved away
-    const int rank = max(hole - moves, 0) + past - in_use + moved;
+  each_numbered([&](int p, bool free, int holes, int movers) {
+    // free pages before p afterwards: the holes left, and past live every page but those still in use
+    const int rank = max(holes - moves, 0) + max(p - live, 0) - movers + max(0, movers - (all - moves));
     int to = p;
-    bool free_after = free != 0;
-    bool keep_count = true;
-    if (p < live && free) {
-      if (hole < moves) {
-        free_after = false;
-        keep_count = false;
-      }
-      ++hole;
-    } else if (p >= live && !free) {
-      if (mover < moves) {
-        to = dst[mover];
-        free_after = true;
-        keep_count = false;
-        a.shared_out[to] = a.shared[p];
-        a.shared_out[p] = 0;
-      }
-      --mover;
+    bool free_after = free;
+    const int number = all - 1 - movers;
+    if (is_hole(p, free) && holes < moves) {
+      free_after = false;   // its count comes with its contents
+    } else if (is_mover(p, free) && number < moves) {
+      to = dst[number];
+      free_after = true;
+      a.shared_out[to] = a.shared[p];
+      a.shared_out[p] = 0;
+    } else if (a.shared != a.shared_out) {
+      a.shared_out[p] = a.shared[p];
     }
     map[p] = to;
-    if (keep_count && a.shared != a.shared_out) a.shared_out[p] = a.shared[p];
     if (free_after) a.free_pages_out[count - 1 - rank] = p;
-  }
+  });
   if (a.free_pages != a.free_pages_out)
     for (int i = count + team.gid; i < n; i += team.size) a.free_pages_out[i] = a.free_pages[i];
   if (team.gid == 0) {
@@ -455,7 +468,10 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
   }
 }
 
-// The table of a large batch: a CTA per kRemapEntries of it, after compact_kernel.
+// The table of a large batch: a CTA per kRemapEntries of it, after compact_kernel, whose cluster would take
+// longer over it than a launch costs: 65,536 entries 10.8 us for 13.2 within, a million 35 for 96, but 8,192
+// 12.5 for 11.0.
+constexpr long long kRemapInside = 32768;
 constexpr int kRemapThreads = 256, kRemapEntries = 1024;
 __global__ void __launch_bounds__(kRemapThreads) remap_kernel(const __grid_constant__ CompactArgs a) {
   const long long entries = (long long)a.n_seq * a.max_pages;
@@ -481,7 +497,9 @@ __global__ void __launch_bounds__(kRemapThreads) remap_kernel(const __grid_const
 // warps, a page an item. Bound by the bytes, in and out.
 constexpr int kCopyThreads = 256, kCopyLoads = 4;
 constexpr int kPieceBytes = 32768, kCopyStages = 6, kCopyAhead = 3;
-constexpr int kBulkLeast = 2048;     // smaller pages go through registers
+// Smaller pages go through registers: 512 pages of 2 KiB take 2.3 us there, 4.0 by bulk copies (one thread
+// issues a CTA's), 8 of 4 KiB 2.8 against 2.1.
+constexpr int kBulkLeast = 4096;
 
 template <typename T>
 __device__ __forceinline__ void copy_page(const uint8_t* from, uint8_t* to, long long bytes, int tid, int threads) {
@@ -638,9 +656,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
   }
 }
 
-// One CTA while a step's entries are few (its barriers are cheaper), else the cluster. All may be placed
-// while the kernel before them ends.
-constexpr long long kOneCtaEntries = 2048;
+// One CTA while a step's entries are few (its barriers are cheaper), else the cluster of eight: 1,024 table
+// entries let go 7.8 us against 10.0, 2,048 10.7 against 10.2 and 4,096 17.3 against 10.5; forks of 1,008
+// entries 5.1 against 5.4, of 2,016 6.3 against 5.5. Copying an array of 8,192 pages costs one CTA as much
+// as its barriers save (forks of 252 entries 5.4 against 4.8), and a compaction of 2,048 pages takes 6.9
+// against 9.0, of 4,096 11.6 against 9.2. All may be placed while the kernel before them ends.
+constexpr long long kOneCtaEntries = 1024, kOneCtaCopies = 8192, kOneCtaPages = 2048;
 template <typename K1, typename K8, typename... A>
 cudaError_t launch_team(K1 one, K8 eight, bool large, cudaStream_t s, A... args) {
   cudaLaunchAttribute attr[2];
@@ -665,19 +686,19 @@ cudaError_t pages_set_attributes() {
 }
 
 cudaError_t launch_page_fork(const ForkArgs& a, cudaStream_t s) {
-  const bool large = (long long)a.n_fork * a.max_pages > kOneCtaEntries || a.n_free > 4 * kOneCtaEntries;
+  const bool large = (long long)a.n_fork * a.max_pages > kOneCtaEntries || a.n_free >= kOneCtaCopies;
   return launch_team(fork_kernel<1>, fork_kernel<kTeamCtas>, large, s, a);
 }
 
 cudaError_t launch_page_release(const ReleaseArgs& a, cudaStream_t s) {
-  const bool large = (long long)a.n_seq * a.max_pages > kOneCtaEntries || a.n_free > 4 * kOneCtaEntries;
+  const bool large = (long long)a.n_seq * a.max_pages > kOneCtaEntries || a.n_free >= kOneCtaCopies;
   return launch_team(release_kernel<1>, release_kernel<kTeamCtas>, large, s, a);
 }
 
 cudaError_t launch_page_compact(const CompactArgs& a, cudaStream_t s) {
   const long long entries = (long long)a.n_seq * a.max_pages;
-  const int remap = entries <= 32 * kOneCtaEntries ? 1 : 0;
-  const bool large = a.n_free > kOneCtaEntries || (remap && entries > kOneCtaEntries);
+  const int remap = entries <= kRemapInside ? 1 : 0;
+  const bool large = a.n_free > kOneCtaPages || (remap && entries > kOneCtaPages);
   const cudaError_t e = launch_team(compact_kernel<1>, compact_kernel<kTeamCtas>, large, s, a, remap);
   if (e != cudaSuccess || remap) return e;
   remap_kernel<<<(unsigned)((entries + kRemapEntries - 1) / kRemapEntries), kRemapThreads, 0, s>>>(a);
@@ -685,7 +706,8 @@ cudaError_t launch_page_compact(const CompactArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_page_copy(PageCopyArgs a, int sm_count, cudaStream_t s) {
-  // pieces of 32 KiB when they fill the device, else of 8 KiB, which more SMs share
+  // pieces of 32 KiB when there is one for every other SM, else of 8 KiB, which more SMs share: 64 pieces of
+  // 32 KiB take 2.7 us whole and 2.5 as quarters, 128 2.8 against 3.1, 256 3.5 against 4.2
   for (a.piece_bytes = kPieceBytes;; a.piece_bytes = kPieceBytes / 4) {
     a.pieces = 0;
     a.small = false;
@@ -698,7 +720,7 @@ cudaError_t launch_page_copy(PageCopyArgs a, int sm_count, cudaStream_t s) {
       a.pieces += p.pieces;
       a.small |= p.pieces == 0;
     }
-    if (a.piece_bytes < kPieceBytes || (long long)a.n_copies * a.pieces >= sm_count) break;
+    if (a.piece_bytes < kPieceBytes || 2LL * a.n_copies * a.pieces >= sm_count) break;
   }
   const long long bulk = (long long)a.n_copies * a.pieces, small = a.small ? (a.n_copies + 6LL) / 7 : 0;
   const long long ctas = bulk > small ? bulk : small;
