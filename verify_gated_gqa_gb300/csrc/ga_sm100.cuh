@@ -536,9 +536,9 @@ __device__ __forceinline__ uint32_t ld_input(const uint8_t* p) {
   asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint16_t ld_input(const uint16_t* p) {
-  uint16_t v;
-  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+__device__ __forceinline__ uint32_t ld_input(const uint16_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 // Launch that may be placed while the kernel before it in the stream ends (its blocks call
