@@ -111,12 +111,13 @@ __host__ __device__ __forceinline__ int row_blocks(int rows) {
 // long one: 64 ragged sequences of up to 8,192 keys, one row: 60 us against 54; of up to 300 keys
 // 24 against 18; 5 x 5 rows over up to 12,345 keys 25 against 21; 200 x 5 rows over up to 2,047 93
 // against 85. (Equal long streams take the same: 64 x 4,095 keys 53 us.)
-// The 8-bit form's (kQ8) segments cost less beside its tiles: 64 ragged sequences of up to 8,192 keys 63.5
-// us with a lead of 3, 68.6 with none, 65.5 with 6; 5 x 6 rows over up to 12,345 keys 32.8, 42 with none.
+// The 8-bit form's (kQ8) segments cost less beside its tiles: 64 ragged sequences of up to 8,192 keys 53.5
+// us with a lead of 3, 54.6 with 4; 256 of up to 1,000 keys 51.4, with 2 52.5 and with 4 54.2; 5 x 6 rows
+// over up to 12,345 keys 22.7, with 2 24.3.
 template <int kTile, bool kQ8 = false>
 constexpr int kLead = kTile == 32 ? 16 : kQ8 ? 3 : 6;
 template <int kTile, bool kQ8 = false>
-constexpr int kFront = kTile == 32 ? 8 : 2;
+constexpr int kFront = kTile == 32 ? 8 : kQ8 ? 1 : 2;
 template <int kTile, bool kQ8 = false>
 __device__ __forceinline__ int stream_units(int tiles) {
   return tiles ? tiles + kLead<kTile, kQ8> : 0;
