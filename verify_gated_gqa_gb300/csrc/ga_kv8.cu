@@ -41,24 +41,48 @@ __device__ __forceinline__ int exp_for(uint32_t top) {
   const int e = (int)(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0);
   return min(max(e, kQ8MinExp), kQ8MaxExp);
 }
-__device__ __forceinline__ float scaled(uint32_t bf16_bits, float inv) {
-  const float x = __uint_as_float(bf16_bits);
-  return x != x ? 0.f : x * inv;   // x inv is exact, or past +-448 either way
+// NaNs of x made 0, which is what is stored for them. The largest magnitude's bits.
+__device__ __forceinline__ uint32_t clear_nan(uint4& x) {
+  auto top = [&]() {
+    const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+    return max(m & 0xFFFFu, m >> 16);
+  };
+  auto clear = [](uint32_t w) {
+    return ((w & 0x7FFFu) > 0x7F80u ? 0u : w & 0xFFFFu) | ((w >> 16 & 0x7FFFu) > 0x7F80u ? 0u : w & 0xFFFF0000u);
+  };
+  uint32_t t = top();
+  if (t > 0x7F80u) {
+    x = make_uint4(clear(x.x), clear(x.y), clear(x.z), clear(x.w));
+    t = top();
+  }
+  return t;
 }
+// x inv is exact, or past +-448 either way.
 __device__ __forceinline__ uint2 encode(const uint4& x, float inv) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = e4m3x2(scaled(w[i] << 16, inv), scaled(w[i] & 0xFFFF0000u, inv));
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;   // both by one instruction
+    asm("{\n\t.reg .b64 x, s;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmul.rn.f32x2 x, x, s;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(w[i] << 16), "r"(w[i] & 0xFFFF0000u), "f"(inv));
+    c[i] = e4m3x2(lo, hi);
+  }
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
 // A run is a row of tokens of one block. CTA (c, kv) stores the keys' or values' runs that begin among
 // tokens 32 c .. 32 c + 31: a prompt's chunk has one or two, a decode batch 32 of one token. Four warps
-// take each head, 8 values a lane. The rows are on their way before the slots are known. A chunk's stay in registers from the search for the maxima
-// to their codes; those of a run that goes on past the chunk (31 at most) are read again. Bound by
-// the bytes it moves.
-__global__ void __launch_bounds__(kThreads, 5) quantize_kernel(const __grid_constant__ Kv8Args a) {
+// take each head, 8 values a lane. The rows are on their way before the slots are known. A chunk's stay
+// in registers from the search for the maxima to their codes; those of a run that goes on past the
+// chunk (31 at most) are read again. Bound by the bytes it moves (131,072 tokens 74 us, 5.4 TB/s) and by
+// instruction issue: with a test for NaN and a division by the page size at every use it was at 70 % of
+// the issue slots and took 93 us. Four CTAs an SM keep everything in registers; five spill and take as
+// long.
+__global__ void __launch_bounds__(kThreads, 4) quantize_kernel(const __grid_constant__ Kv8Args a) {
   __shared__ uint32_t top[kKvHeads][kChunk], written[kChunk];
   __shared__ int exps[kKvHeads][kChunk], shift[kKvHeads][kChunk], first[kChunk];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -89,6 +113,8 @@ __global__ void __launch_bounds__(kThreads, 5) quantize_kernel(const __grid_cons
   const int last = __shfl_sync(0xffffffffu, s0, 31);
   // the last run's tokens past the chunk, 32 in all at most
   const uint32_t goes_on = __ballot_sync(0xffffffffu, last >= 0 && s1 >= 0 && (s1 >> 5) == (last >> 5));
+  // codes' places of this lane's tokens (a division each: found once, and handed on)
+  const int row0 = s0 >= 0 ? (int)slot_place(a, s0).row : -1;   // below 2^31, as the pool's rows
   const int runs = __popc(leads), last_lead = 31 - __clz(leads);
   const int more = min(__ffs(~goes_on) ? __ffs(~goes_on) - 1 : 32, last_lead);
   const int run0 = __popc(leads & ((2u << lane) - 1u)) - 1;   // of token t0 + lane, or -1
@@ -104,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 5) quantize_kernel(const __grid_cons
   for (int i = 0; i < kKept; ++i) {
     const int at = part + kRowWarps * i;
     const int slot = __shfl_sync(0xffffffffu, s0, at), run = __shfl_sync(0xffffffffu, run0, at);
-    const uint32_t m = __reduce_max_sync(0xffffffffu, top_of(x[i]));
+    const uint32_t m = __reduce_max_sync(0xffffffffu, clear_nan(x[i]));
     if (lane == 0 && slot >= 0 && run >= 0) atomicMax(&top[head][run], m);
   }
   for (int at = part; at < more; at += kRowWarps) {
@@ -128,17 +154,21 @@ __global__ void __launch_bounds__(kThreads, 5) quantize_kernel(const __grid_cons
     grows = grown > 0;
   }
   const bool any = __syncthreads_or(grows);
-  auto store = [&](int slot, int run, const uint4& v) {
-    const long long at = slot_place(a, slot).row + head * a.page_size;
+  auto store = [&](long long row, int run, const uint4& v) {
+    const long long at = row + head * a.page_size;
     reinterpret_cast<uint2*>(codes + at * kQ8RowBytes)[lane] = encode(v, pow2i(-exps[head][run]));
   };
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
     const int at = part + kRowWarps * i;
-    const int slot = __shfl_sync(0xffffffffu, s0, at), run = __shfl_sync(0xffffffffu, run0, at);
-    if (slot >= 0 && run >= 0) store(slot, run, x[i]);
+    const int row = __shfl_sync(0xffffffffu, row0, at), run = __shfl_sync(0xffffffffu, run0, at);
+    if (row >= 0 && run >= 0) store(row, run, x[i]);
   }
-  for (int at = part; at < more; at += kRowWarps) store(__shfl_sync(0xffffffffu, s1, at), runs - 1, load(kChunk + at));
+  for (int at = part; at < more; at += kRowWarps) {
+    uint4 v = load(kChunk + at);
+    clear_nan(v);
+    store(slot_place(a, __shfl_sync(0xffffffffu, s1, at)).row, runs - 1, v);
+  }
   if (!any) return;
   // the other rows of blocks that grew
   for (int i = part; i < runs * kQ8Block; i += kRowWarps) {
