@@ -104,6 +104,9 @@ __host__ __device__ __forceinline__ int row_blocks(int rows) {
   return rows * kGroup > kV4Lanes ? 2 : 1;
 }
 
+// Forms over the 8-bit cache: query rows on the columns of the MMAs, or on their rows.
+constexpr int kQ8Columns = 1, kQ8Rows = 2;
+
 // A stream's units in the cut: its tiles after kLead units of no work, which stand for what a
 // segment costs beside its tiles (its queries, the first loads, its result). A boundary inside them,
 // or fewer than kFront tiles past them, moves to the stream's beginning: the CTA before is spared a
@@ -111,19 +114,20 @@ __host__ __device__ __forceinline__ int row_blocks(int rows) {
 // long one: 64 ragged sequences of up to 8,192 keys, one row: 60 us against 54; of up to 300 keys
 // 24 against 18; 5 x 5 rows over up to 12,345 keys 25 against 21; 200 x 5 rows over up to 2,047 93
 // against 85. (Equal long streams take the same: 64 x 4,095 keys 53 us.)
-// The 8-bit form's (kQ8) segments cost less beside its tiles: 64 ragged sequences of up to 8,192 keys 53.5
-// us with a lead of 3, 54.6 with 4; 256 of up to 1,000 keys 51.4, with 2 52.5 and with 4 54.2; 5 x 6 rows
-// over up to 12,345 keys 22.7, with 2 24.3.
-template <int kTile, bool kQ8 = false>
-constexpr int kLead = kTile == 32 ? 16 : kQ8 ? 3 : 6;
-template <int kTile, bool kQ8 = false>
+// Over the 8-bit cache segments cost less beside their tiles. kQ8Columns: 64 ragged sequences of up to 8,192
+// keys 53.5 us with a lead of 3, 54.6 with 4; 256 of up to 1,000 keys 51.4, with 2 52.5 and with 4 54.2.
+// kQ8Rows: 64 x 16 rows over up to 4,096 keys 84.0 us with 5, 88.0 with 3 and 86.8 with 8; 64 x 8 rows 62.7,
+// with 3 65.2; 20 x 12 rows over up to 3,000 35.4, with 3 37.3.
+template <int kTile, int kQ8 = 0>
+constexpr int kLead = kTile == 32 ? 16 : kQ8 == kQ8Rows ? 5 : kQ8 ? 3 : 6;
+template <int kTile, int kQ8 = 0>
 constexpr int kFront = kTile == 32 ? 8 : kQ8 ? 1 : 2;
-template <int kTile, bool kQ8 = false>
+template <int kTile, int kQ8 = 0>
 __device__ __forceinline__ int stream_units(int tiles) {
   return tiles ? tiles + kLead<kTile, kQ8> : 0;
 }
 // A stream's units that no boundary cuts off from its beginning (few streams are cut finely).
-template <int kTile, bool kQ8 = false>
+template <int kTile, int kQ8 = 0>
 __device__ __forceinline__ int uncut(int share) {
   return kLead<kTile, kQ8> + min(kFront<kTile, kQ8>, share);
 }
@@ -157,7 +161,7 @@ struct Units {
 // By a whole block of at least kV4MaxSeq threads, a sequence each (`tiles` is 0 past the last); one
 // block barrier. Short on purpose: this code runs once, from a cold instruction cache, before
 // anything can be loaded (a warp's search over the sequences took 2.5 us here).
-template <int kTile, bool kQ8 = false>
+template <int kTile, int kQ8 = 0>
 __device__ __forceinline__ Units scan_units(int tiles, int (&warp_units)[kV4MaxSeq / 32],
                                             int (&warp_streams)[kV4MaxSeq / 32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -192,7 +196,7 @@ __device__ __forceinline__ Units scan_units(int tiles, int (&warp_units)[kV4MaxS
 
 // The sequences' tiles and the part of the cut of worker `me` of `workers`: both heads' sequences,
 // end to end. A refused length is recorded by the first block. Two block barriers.
-template <int kTile, bool kQ8 = false>
+template <int kTile, int kQ8 = 0>
 __device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int workers, int me) {
   const int b = threadIdx.x;
   int tiles = 0;
@@ -236,7 +240,7 @@ template <int kTile>
 __device__ __forceinline__ int cut_len(const V4Cut& c, int b, int rows) {
   return (int)c.tiles[b] * kTile - (int)c.spare[b] - rows;
 }
-template <int kTile, bool kQ8 = false>
+template <int kTile, int kQ8 = 0>
 struct Walk {
   int head, b, at, left, seen;
   __device__ __forceinline__ explicit Walk(const V4Cut& c)
@@ -276,9 +280,7 @@ __device__ __forceinline__ float4* part_at(float* part_o, int slot, int d4, int 
 }
 
 // The log-sum-exp merge of the streams that the cut over `workers` left in parts, after a kernel with
-// tiles of `tile` keys (128 or 32), of either cache (q8), whose parts lie as above or row after row
-// (by_row).
-cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, bool q8, bool by_row,
-                                   cudaStream_t s);
+// tiles of `tile` keys (128 or 32), or of a form over the 8-bit cache (q8, or 0).
+cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, int q8, cudaStream_t s);
 
 }  // namespace ga

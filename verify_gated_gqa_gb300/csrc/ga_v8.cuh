@@ -116,6 +116,7 @@ __device__ __forceinline__ void load_box_warp(uint32_t dst, const CUtensorMap* m
 // box, or a box for each half of the dims). Boxes without a key of the sequence are not loaded; on a
 // page outside the pool (recorded) they are read past its end, which gives zeros. The warp's lanes
 // look after a block of 32 keys each, lane b % 4 after block b.
+template <int kForm>
 __device__ __forceinline__ void load_tiles(const Verify8Args& args, V4Cut& cut, const CUtensorMap* map,
                                            const uint8_t* scale_pool, int is_v, uint8_t* tiles, int stages,
                                            int box_keys, uint64_t* full, uint64_t* empty, TileScales& scales,
@@ -125,7 +126,7 @@ __device__ __forceinline__ void load_tiles(const Verify8Args& args, V4Cut& cut, 
   const int n_rows = a.n_pages * kKvHeads * a.page_size;   // below 2^31
   Ring ring(stages);
   uint32_t issued = 0;
-  Walk<kTileN, true> walk(cut);
+  Walk<kTileN, kForm> walk(cut);
   Seg seg;
   while (walk.next(cut, a.n_seq, seg)) {
     const int end = cut_len<kTileN>(cut, seg.b, a.rows) + a.rows;

@@ -571,19 +571,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // stream's parts, times the gate.
 //
 // A stream's items are (row, four dims), in the order in which the parts lie (rows innermost, or dims:
-// kByRow); a block takes an equal share of them. With few streams each has `slices` blocks, about twice the device's CTAs in all (32
-// sequences of up to 4,096 keys, one row: a whole call of 22 us; with twice the blocks 25). With many
-// (slices 0), most of them whole or of two parts, blocks go by the boundaries that cut streams, n - 1
-// to a stream of n parts, kSplit to each, so that one long stream among many short ones is not left to
-// few blocks (5 rows of one sequence of 65,536 keys and 63 of 200: 34 us, by streams 76). A thread merges eight parts of an item at
-// a time, as they come; where a share has fewer items than the block has threads, a stream of more
+// kByRow); a block takes an equal share of them. With few streams each has `slices` blocks, about twice
+// the device's CTAs in all (32 sequences of up to 4,096 keys, one row: a whole call of 22 us; with twice the
+// blocks 25). With many (slices 0), most of them whole or of two parts, blocks go by the boundaries that
+// cut streams, n - 1 to a stream of n parts, kSplit to each, so that one long stream among many short
+// ones is not left to few blocks (5 rows of one sequence of 65,536 keys and 63 of 200: 34 us, by streams
+// 76). A thread merges eight parts of an item at a time, as they come; where a share has fewer items than the block has threads, a stream of more
 // than eight parts is dealt to groups of threads, merged through shared memory. (With all (M, l)
 // turned into weights in shared memory first, 76 parts of 96 rows took 28 us.)
 constexpr int kCombineThreads = 384, kSplit = 2;
 static_assert(kCombineThreads >= kV4MaxSeq, "a sequence a thread");
-template <int kTile, bool kQ8, bool kByRow>
+template <int kTile, int kQ8>
 __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     const __grid_constant__ Verify4Args a, int workers, int slices) {
+  constexpr bool kByRow = kQ8 == kQ8Columns;   // how the parts lie
   __shared__ int warp_units[kV4MaxSeq / 32], warp_streams[kV4MaxSeq / 32];
   __shared__ int cut_b, cut_head, cut_u0, cut_n;
   __shared__ float4 join_o[kCombineThreads];
@@ -724,15 +725,16 @@ cudaError_t verify4_set_attributes() {
   return e != cudaSuccess ? e : decode4_set_attributes();
 }
 
-cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, bool q8, bool by_row, cudaStream_t s) {
+cudaError_t launch_verify4_combine(const Verify4Args& a, int workers, int tile, int q8, cudaStream_t s) {
   const int blocks = row_blocks(a.rows), streams = a.n_seq * kKvHeads * blocks;
   const int ctas = workers * blocks, slices = streams * 2 >= ctas ? 0 : 2 * ctas / streams < 64 ? 2 * ctas / streams : 64;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = overlapped_launch(
       (unsigned)(slices ? streams * slices : (workers - 1) * blocks * kSplit), kCombineThreads, 0, s, attr);
-  auto* kernel = q8 ? by_row ? verify4_combine_kernel<kTileN, true, true> : verify4_combine_kernel<kTileN, true, false>
-                 : tile == kTileN ? verify4_combine_kernel<kTileN, false, false>
-                                  : verify4_combine_kernel<32, false, false>;
+  auto* kernel = q8 == kQ8Columns ? verify4_combine_kernel<kTileN, kQ8Columns>
+                 : q8 == kQ8Rows  ? verify4_combine_kernel<kTileN, kQ8Rows>
+                 : tile == kTileN ? verify4_combine_kernel<kTileN, 0>
+                                  : verify4_combine_kernel<32, 0>;
   return cudaLaunchKernelEx(&cfg, kernel, a, workers, slices);
 }
 
@@ -745,7 +747,7 @@ cudaError_t launch_verify4(const CUtensorMap& k_codes, const CUtensorMap& v_code
   const int blocks = row_blocks(a.rows), workers = ctas / blocks;
   const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)(workers * blocks), kThreads, sizeof(V4Smem), s, attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, verify4_kernel, k_codes, v_codes, k_scales, v_scales, a);
-  return e != cudaSuccess ? e : launch_verify4_combine(a, workers, kTileN, false, false, s);
+  return e != cudaSuccess ? e : launch_verify4_combine(a, workers, kTileN, 0, s);
 }
 
 }  // namespace ga

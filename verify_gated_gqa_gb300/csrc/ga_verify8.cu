@@ -203,7 +203,7 @@ __device__ void issue_mma(const Cta<kGroups>& c) {
   const Verify4Args& a = c.a.v;
   using Lay = Layout<kGroups>;
   Issue<kGroups> is(c);
-  Walk<kTileN, true> walk(c.ctl.cut);
+  Walk<kTileN, kQ8Columns> walk(c.ctl.cut);
   Seg seg;
   uint32_t done = 0;
   while (walk.next(c.ctl.cut, a.n_seq, seg)) {
@@ -250,7 +250,7 @@ __device__ void softmax_worker(const Cta<kGroups>& c) {
   const uint32_t slab_buf = Lay::p(1) - Lay::p(0), part_step = Lay::p_part;
   const uint32_t sf0 = smem_u32(c.smem + Lay::sf(0)) + quarter;
   const uint32_t s_full = smem_u32(c.ctl.s_full), s_free = smem_u32(c.ctl.s_free), p_full = smem_u32(c.ctl.p_full);
-  Walk<kTileN, true> walk(c.ctl.cut);
+  Walk<kTileN, kQ8Columns> walk(c.ctl.cut);
   Seg seg;
   for (; walk.next(c.ctl.cut, a.n_seq, seg); ++done) {
     const int L = cut_len<kTileN>(c.ctl.cut, seg.b, a.rows);
@@ -434,7 +434,7 @@ __device__ void segment_worker(const Cta<kGroups>& c) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&c.ctl.q_full);
   };
-  Walk<kTileN, true> walk(c.ctl.cut);
+  Walk<kTileN, kQ8Columns> walk(c.ctl.cut);
   Seg seg, next;
   bool more = walk.next(c.ctl.cut, a.n_seq, seg);
   if (more) {
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(128 + 256 * kGroups, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  make_cut<kTileN, true>(a.v, ctl.cut, (int)gridDim.x, (int)blockIdx.x);   // two block barriers
+  make_cut<kTileN, kQ8Columns>(a.v, ctl.cut, (int)gridDim.x, (int)blockIdx.x);   // two block barriers
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   if (warp >= 4 && warp < 8) {   // the values' scale factors: 1 beside the weights' first part, 2^-5
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(128 + 256 * kGroups, 1)
       mbar_wait_quiet(&ctl.drain, 0, 100000000LL);
     } else if (warp == 2 || warp == 3) {
       const bool v = warp == 3;
-      load_tiles(a, ctl.cut, v ? &tm_v : &tm_k, v ? a.v_scales : a.k_scales, v, smem + (v ? Lay::v(0) : Lay::k(0)),
+      load_tiles<kQ8Columns>(a, ctl.cut, v ? &tm_v : &tm_k, v ? a.v_scales : a.k_scales, v, smem + (v ? Lay::v(0) : Lay::k(0)),
                  v ? Lay::v_stages : kStages, box_keys, v ? ctl.v_full : ctl.k_full, v ? ctl.v_empty : ctl.k_empty,
                  ctl.scales, &ctl.abort);
     } else if (warp >= 4 + 4 * kGroups) {
@@ -628,7 +628,7 @@ cudaError_t launch_verify8(const CUtensorMap& k_codes, const CUtensorMap& v_code
   const cudaError_t e = groups == 1   ? launch_groups<1>(k_codes, v_codes, a, ctas, s)
                         : groups == 2 ? launch_groups<2>(k_codes, v_codes, a, ctas, s)
                                       : launch_groups<3>(k_codes, v_codes, a, ctas, s);
-  return e != cudaSuccess ? e : launch_verify4_combine(a.v, ctas, kTileN, true, true, s);
+  return e != cudaSuccess ? e : launch_verify4_combine(a.v, ctas, kTileN, kQ8Columns, s);
 }
 
 }  // namespace ga

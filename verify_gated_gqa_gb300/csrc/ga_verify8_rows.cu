@@ -152,7 +152,7 @@ struct Issue {
 
 __device__ void issue_mma(Smem& sm, const Verify4Args& a, uint32_t tmem) {
   Issue is(sm, tmem);
-  Walk<kTileN, true> walk(sm.cut);
+  Walk<kTileN, kQ8Rows> walk(sm.cut);
   Seg seg;
   uint32_t done = 0;
   while (walk.next(sm.cut, a.n_seq, seg)) {
@@ -252,7 +252,7 @@ __device__ void softmax_worker(Smem& sm, const Verify4Args& a, uint32_t tmem) {
   };
   const uint32_t s_at = tmem + kTmemS + lanes + 32 * block, w_at = tmem + kTmemW + lanes + 8 * block;
   const uint32_t sf_at = smem_u32(sm.sf_w) + (r & 31) * 16 + (r >> 5) * 4 + block;
-  Walk<kTileN, true> walk(sm.cut);
+  Walk<kTileN, kQ8Rows> walk(sm.cut);
   Seg seg, next;
   bool more = walk.next(sm.cut, a.n_seq, seg);
   if (more) load_queries(seg);
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   {   // two block barriers
     const int blocks = row_blocks(a.v.rows);
-    make_cut<kTileN, true>(a.v, sm.cut, (int)gridDim.x / blocks, (int)blockIdx.x / blocks);
+    make_cut<kTileN, kQ8Rows>(a.v, sm.cut, (int)gridDim.x / blocks, (int)blockIdx.x / blocks);
   }
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
@@ -462,9 +462,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit_warp(&sm.drain);
       mbar_wait_quiet(&sm.drain, 0, 100000000LL);
     } else if (warp == 7) {
-      load_tiles(a, sm.cut, &tm_k, a.k_scales, 0, sm.k[0], kKStages, box_keys, sm.k_full, sm.k_empty, sm.scales, &sm.abort);
+      load_tiles<kQ8Rows>(a, sm.cut, &tm_k, a.k_scales, 0, sm.k[0], kKStages, box_keys, sm.k_full, sm.k_empty, sm.scales, &sm.abort);
     } else if (warp == 11) {
-      load_tiles(a, sm.cut, &tm_v, a.v_scales, 1, sm.v[0], kVStages, box_keys, sm.v_full, sm.v_empty, sm.scales, &sm.abort);
+      load_tiles<kQ8Rows>(a, sm.cut, &tm_v, a.v_scales, 1, sm.v[0], kVStages, box_keys, sm.v_full, sm.v_empty, sm.scales, &sm.abort);
     } else if ((warp & 3) < quarters) {
       softmax_worker(sm, a.v, tmem);
     }
@@ -492,7 +492,7 @@ cudaError_t launch_verify8_rows(const CUtensorMap& k_codes, const CUtensorMap& v
   const cudaLaunchConfig_t cfg = overlapped_launch((unsigned)(workers * blocks), kThreads, kSmemLimit, s, attr);
   const cudaError_t e =
       cudaLaunchKernelEx(&cfg, verify8_rows_kernel, k_codes, v_codes, a, verify8_box_keys(a.v.page_size));
-  return e != cudaSuccess ? e : launch_verify4_combine(a.v, workers, kTileN, true, false, s);
+  return e != cudaSuccess ? e : launch_verify4_combine(a.v, workers, kTileN, kQ8Rows, s);
 }
 
 }  // namespace ga
