@@ -638,10 +638,28 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   const int count = hi - lo;
   const int groups = max(1, min((n + 7) / 8, kCombineThreads / max(count, 1)));
   const int group = groups > 1 ? tid / count : 0;   // (from `groups` on: idle)
+  // an item's row among the call's, and its four gates (place p + k of 32-key tiles' parts is dim
+  // 32 (p % 8 + k) + p / 8); the first item's are loaded before the wait, which is for the parts alone
+  auto dims_of = [&](int item) { return kByRow ? item % (kDim / 4) : item / rows; };
+  auto row_of = [&](int item) {
+    const int r = kByRow ? item / (kDim / 4) : item % rows, rr = r / heads;
+    return ((size_t)b * a.rows + rr) * kHeads + head * kGroup + block * heads + r - rr * heads;
+  };
+  auto gates_of = [&](int item) {
+    const int p = 4 * dims_of(item);
+    const uint16_t* at = a.qg + row_of(item) * kQgStride + kDim;
+    if (kTile == kTileN) return ld_input(reinterpret_cast<const uint2*>(at + p));
+    at += 32 * (p & 7) + (p >> 3);
+    return make_uint2(ld_input(at) | ld_input(at + 32) << 16, ld_input(at + 64) | ld_input(at + 96) << 16);
+  };
+  const int item0 = lo + tid - group * count;
+  const bool merges = n > 1 && count > 0;
+  uint2 g = make_uint2(0u, 0u);
+  if (merges && group == 0 && item0 < hi) g = gates_of(item0);
   grid_wait();
-  if (n == 1 || count == 0) return;   // (one CTA ran the whole stream and wrote it)
-  for (int item = lo + tid - group * count; item < hi; item += kCombineThreads) {
-    const int d4 = kByRow ? item % (kDim / 4) : item / rows, r = kByRow ? item / (kDim / 4) : item - d4 * rows;
+  if (!merges) return;   // (one CTA ran the whole stream and wrote it)
+  for (int item = item0; item < hi; item += kCombineThreads) {
+    const int d4 = dims_of(item), r = kByRow ? item / (kDim / 4) : item - d4 * rows;
     float M = -INFINITY, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     auto scale = [&](float top) {   // to a new maximum
@@ -694,22 +712,20 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
     }
     // times the gate, to the output
     const float inv = 1.0f / L;
-    const int rr = r / heads, h = head * kGroup + block * heads + r - rr * heads, p = 4 * d4;
-    const size_t row = ((size_t)b * a.rows + rr) * kHeads + h;
-    const uint16_t* gates = a.qg + row * kQgStride + kDim;
-    uint16_t* out = a.out + row * kDim;
-    if (kTile != kTileN) {   // place p + k is dim 32 (p % 8 + k) + p / 8
-      const int d = 32 * (p & 7) + (p >> 3);
-      const float x[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        out[d + 32 * k] = (uint16_t)(pack_bf16x2(x[k] * inv * sigmoid_f(lo_f(ld_input(gates + d + 32 * k))), 0.f) & 0xFFFFu);
+    uint16_t* out = a.out + row_of(item) * kDim;
+    const uint32_t lo2 = pack_bf16x2(o.x * inv * sigmoid_f(lo_f(g.x)), o.y * inv * sigmoid_f(hi_f(g.x)));
+    const uint32_t hi2 = pack_bf16x2(o.z * inv * sigmoid_f(lo_f(g.y)), o.w * inv * sigmoid_f(hi_f(g.y)));
+    const int p = 4 * d4;
+    if (kTile != kTileN) {
+      out += 32 * (p & 7) + (p >> 3);
+      out[0] = (uint16_t)lo2;
+      out[32] = (uint16_t)(lo2 >> 16);
+      out[64] = (uint16_t)hi2;
+      out[96] = (uint16_t)(hi2 >> 16);
     } else {
-      const uint2 g = ld_input(reinterpret_cast<const uint2*>(gates + p));
-      *reinterpret_cast<uint2*>(out + p) =
-          make_uint2(pack_bf16x2(o.x * inv * sigmoid_f(lo_f(g.x)), o.y * inv * sigmoid_f(hi_f(g.x))),
-                     pack_bf16x2(o.z * inv * sigmoid_f(lo_f(g.y)), o.w * inv * sigmoid_f(hi_f(g.y))));
+      *reinterpret_cast<uint2*>(out + p) = make_uint2(lo2, hi2);
     }
+    if (item + kCombineThreads < hi) g = gates_of(item + kCombineThreads);
   }
 }
 
