@@ -678,8 +678,9 @@ int ga_attn_verify_q4(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k
  *           aligned, leading dimensions >= 512 and multiples of 8 (a slice of a fused projection)
  *   slots   DEVICE int32 [n_tok], 4-byte aligned, or NULL: token t goes to slot t. A negative
  *           slot stores nothing; one past the pool stores nothing and records status 3. Slots of
- *           one call must differ, and the tokens of one block follow one another in the call, as
- *           ga_page_plan lists them (else that block's rows are unspecified).
+ *           one call must differ, and the tokens of one block follow one another in the call, with no
+ *           other token and no skipped one between them, as ga_page_plan lists them (else that
+ *           block's rows are unspecified).
  * Rules: page_size a multiple of 32, n_pages * page_size < 2^30, 0 <= n_tok <= 64 *
  * GA_MAX_TOKENS; with slots NULL, n_tok <= n_pages * page_size.
  * Errors: NULL, SHAPE, RANGE, ALIGN, DEVICE, CUDA. */
@@ -706,9 +707,9 @@ size_t ga_verify_q8_workspace_bytes(void);
  * tokens). Hidden positions need no initial contents: whatever their codes and scales, NaN codes
  * included, they do not reach a result. Queries and softmax weights meet the codes as sums of two
  * 8-bit parts: a query is within 2^-17 of its row's largest magnitude, a weight within 2^-9 of
- * itself or 2^-22 of the largest of its block of 32 keys; sums, maxima and O are fp32, and the output
- * is rounded once. A NaN query (or one whose
- * scores are infinite, or pass 2^29 in magnitude) makes its own head's row meaningless, and no other.
+ * itself or 2^-22 of the largest of its block of 32 keys; sums, maxima and O are fp32, and the
+ * output is rounded once. A NaN query (or one whose scores are infinite, or pass 2^29 in magnitude)
+ * makes its own head's row meaningless, and no other.
  * A page-table entry outside the pool records status 3 and its keys are read as zeros.
  * Errors: NULL, SHAPE, RANGE, ALIGN, WORKSPACE, DEVICE, CUDA. */
 int ga_attn_verify_q8(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k_codes,
@@ -814,8 +815,8 @@ int ga_page_compact(int n_seq, const int* page_table, int* page_table_out, int m
  *              over; one outside the pool is passed over and records status 3. No page is written
  *              twice, or read and written, in one call (else its contents are unspecified); a page
  *              may be read many times
- * Rules: 1 <= n_pools <= GA_PAGE_COPY_POOLS, n_pages >= 0, 1 <= page_bytes[j] <= 2^30, 0 <= n_copies < 2^30. n_copies
- * or n_pages = 0 is a no-op.
+ * Rules: 1 <= n_pools <= GA_PAGE_COPY_POOLS, n_pages >= 0, 1 <= page_bytes[j] <= 2^30, 0 <=
+ * n_copies < 2^30. n_copies or n_pages = 0 is a no-op.
  * Errors: NULL, SHAPE, RANGE, ALIGN, DEVICE, CUDA. */
 int ga_page_copy(void* const* pools, const size_t* page_bytes, int n_pools, int n_pages,
                  const int* src, const int* dst, int n_copies, ga_stream stream);

@@ -350,7 +350,8 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const __grid_constant
 // in order, so that its loads are whole lines (with a run a thread 262,144 pages took 197 us, so they take
 // 61; 1,024 pages 5.0 and 6.0). Sums of free pages below n_live and of pages in use from it on give the
 // moves their numbers, and those give every place on the new stack.
-constexpr int kMapBatch = 2;   // times 32 pages, loaded together; 1: 262,144 pages 66 us, 4: 59, but 4,096 9.8 for 9.7
+// Batches of 32 pages loaded together (1: 262,144 pages 66 us; 4: 59, but 2,048 7.5 for 7.1).
+constexpr int kMapBatch = 2;
 template <int kCtas>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ CompactArgs a, int remap) {
   __shared__ TeamSmem tsm;

@@ -103,7 +103,8 @@ struct TileScales {
 // ------------------------------------------------------------------ loading
 // A box of the tile's dims 128 half .. + 127 (all of them where the box covers the tile), by one lane of
 // a converged warp.
-__device__ __forceinline__ void load_box_warp(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int row, int half) {
+__device__ __forceinline__ void load_box_warp(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int row,
+                                              int half) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"

@@ -576,9 +576,9 @@ __global__ void __launch_bounds__(128 + 256 * kGroups, 1)
       mbar_wait_quiet(&ctl.drain, 0, 100000000LL);
     } else if (warp == 2 || warp == 3) {
       const bool v = warp == 3;
-      load_tiles<kQ8Columns>(a, ctl.cut, v ? &tm_v : &tm_k, v ? a.v_scales : a.k_scales, v, smem + (v ? Lay::v(0) : Lay::k(0)),
-                 v ? Lay::v_stages : kStages, box_keys, v ? ctl.v_full : ctl.k_full, v ? ctl.v_empty : ctl.k_empty,
-                 ctl.scales, &ctl.abort);
+      load_tiles<kQ8Columns>(a, ctl.cut, v ? &tm_v : &tm_k, v ? a.v_scales : a.k_scales, v,
+                             smem + (v ? Lay::v(0) : Lay::k(0)), v ? Lay::v_stages : kStages, box_keys,
+                             v ? ctl.v_full : ctl.k_full, v ? ctl.v_empty : ctl.k_empty, ctl.scales, &ctl.abort);
     } else if (warp >= 4 + 4 * kGroups) {
       segment_worker<kGroups>(c);
     } else if (warp >= 4) {
