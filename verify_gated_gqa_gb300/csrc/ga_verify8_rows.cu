@@ -9,8 +9,10 @@
 // softmax thread has a query row of its own (its maximum, its sum and its scale need no exchange), and
 // a tile costs 64 KiB + 48 KiB of operands for S and 64 KiB for O beside the 64 KiB that are loaded:
 // bound by the tensor cores, 2,048 cycles a tile whatever the rows, which is why few rows take the
-// other form: 8 x 65,536 keys with 3 rows 98 us there and 100 here, 4 rows 98 and 104, 5 rows 121 and 105,
-// 8 rows 137 and 110, 16 rows 213 and 176; 64 x 8,192 keys with 4 rows 107 and 115.
+// other form: 8 x 65,536 keys with 4 rows 94.0 us there and 96.0 here, 64 x 8,192 keys 101 and 107, 256
+// ragged sequences of up to 1,000 keys 65 and 78, 5 of up to 12,345 19.1 and 21.1 (3 rows: 93.1 and 94.5, 99
+// and 105, 62 and 74, 18.6 and 20.6). With more rows, both as they were when they were compared, over 65,536
+// keys: 5 rows 121 and 105, 8 rows 137 and 110, 16 rows 213 and 176.
 //
 // Structure (512 threads, 16 warps; the softmax's on three of the SM's four quarters):
 //   warps w % 4 < 3  softmax: query rows 32 (w % 4) .. + 31, a row a lane, of the tile's keys 32 (w / 4) ..
