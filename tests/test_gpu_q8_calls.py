@@ -124,7 +124,8 @@ def test_captured_and_replayed_with_other_lengths(rows):
         for kv in range(2):
             hs = slice(12 * kv, 12 * kv + 12)
             w = attend64(q[b, :, hs], qg[b, :, hs, 256:], kw[:, kv], vw[:, kv], [x + r + 1 for r in range(rows)])
-            # few keys: an element's own bound times the row's, as in ROW_BOUND's derivation
+            # with few keys the weights' errors do not average out: 2^-9 + 2^-10 + 2 x with x below 2^-9
+            # here, under 3 x 2^-8, beside the outputs' 2^-8; 3 x ROW_BOUND is 6.75 x 2^-8
             assert float(row_errors(out.view(4, rows, 24, 256)[b, :, hs], w).max()) <= 3 * ROW_BOUND
 
 
@@ -177,7 +178,9 @@ def test_widened_prefix_serves_a_prefill():
     for r in range(0, rows, 16):
         x = B.ga_attn_verify_q8(q[None, r:r + 16].contiguous(), qg[None, r:r + 16].contiguous(), *pools, table,
                                 _i32([T - rows + r]))
-        # the prefill rounds scores, weights and the gate to bf16, each up to 2^-8
+        # the prefill rounds q . k, below 128 in magnitude here, to bf16: by 0.25 at most, 4 x 2^-8 of a weight
+        # once divided by 16 and twice that with the sum; weights, gate and output another 2^-8 each, and
+        # the same for this call's: 13 x 2^-8
         assert float(row_errors(x.view(16, 24, 256), got[r:r + 16].view(16, 24, 256)).max()) <= 16 * 2.0 ** -8
 
 
