@@ -243,6 +243,7 @@ __device__ void softmax_worker(const Cta<kGroups>& c) {
   uint32_t f = 0, done = 0;
   // the four warps of the team meet
   auto meet = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + team) : "memory"); };
+  auto factor_of = [](uint32_t scales) { return pow2i(q8_exp(scales)) * kLog2eOver16; };   // from S to exponents
   // places of buffer 0 of S, of this warp's part of the weights (a place for exchanges until they are
   // written), of its columns' scales, what buffer 1 is on
   const uint32_t s_at = c.tmem + kTmemS + lanes + col0;
@@ -260,9 +261,8 @@ __device__ void softmax_worker(const Cta<kGroups>& c) {
     for (int j = 0; j < seg.n; ++j, ++f) {
       const uint32_t buf = f & 1u, slab = slab0 + (buf ? slab_buf : 0u);
       const int kt = seg.kt0 + j;
-      const uint32_t scales = c.ctl.scales.wait(f, quarter, c.abort);
-      const float factor = pow2i(q8_exp(scales)) * kLog2eOver16;   // from S to exponents
-      const int v_exp = q8_exp(scales >> 8);
+      uint32_t scales = c.ctl.scales.wait(f, quarter, c.abort);
+      const float factor = factor_of(scales);
       warp_wait(s_full + 8 * buf, (f >> 1) & 1u, c.abort);
       tc_fence_after();
       uint32_t s[kCols];
@@ -292,8 +292,15 @@ __device__ void softmax_worker(const Cta<kGroups>& c) {
         if (lane == 0) sts_v4(slab + 4 * i, m);
       }
       __syncwarp();
-      const float E = fmaxf(ceilf(lds_f32(slab + 4 * (lane & 15)) * factor), kNone);
-      if (team_any(1 + team, E > R + kMove)) {
+      const float top = lds_f32(slab + 4 * (lane & 15));
+      float E = fmaxf(ceilf(top * factor), kNone), d = kTop - E;
+      if (__any_sync(0xffffffffu, is_far(E))) {
+        far_exponent(E, d, top, factor);
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+          s[i] = __float_as_uint(__uint_as_float(s[i]) - far_base(lds_f32(slab + 4 * i)));
+      }
+      if (team_any(1 + team, E - R > kMove)) {
         // R moves, for all of the team (a segment's first tile: from nothing)
         if (lane < kCols) sts_f32(slab + 4 * lane, E);
         meet();
@@ -325,24 +332,27 @@ __device__ void softmax_worker(const Cta<kGroups>& c) {
         tc_fence_before();
         meet();   // every warp has read the exchange
       }
-      const float x = E - kTop - R;
+      asm volatile("" : "+r"(scales));   // formed anew: both kept from above, three groups' would be spilled
+      const float factor2 = factor_of(scales);
+      const int v_exp = q8_exp(scales >> 8);
+      const float x = E - R - kTop;   // (E - R is exact where it matters, E - kTop is not for every E)
       if (lane < kCols) {
         const int col = col0 + lane;
         asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf0 + 512 * buf + (col & 31) * 16 + (col >> 5) * 4),
                      "r"(max(0, (int)x + v_exp + kSfBias))
                      : "memory");
-        sts_f32(slab + 4 * lane, kTop - E);
+        sts_f32(slab + 4 * lane, d);
         sts_f32(slab + 4 * kCols + 4 * lane, ex2_approx(x));
       }
       __syncwarp();
       uint32_t hi[kCols / 4], lo[kCols / 4];
 #pragma unroll
       for (int i = 0; i < kCols; i += 4) {
-        const float4 d = lds_f32x4(slab + 4 * i), g = lds_f32x4(slab + 4 * kCols + 4 * i);
-        const float p0 = ex2_approx(fmaf(__uint_as_float(s[i]), factor, d.x));
-        const float p1 = ex2_approx(fmaf(__uint_as_float(s[i + 1]), factor, d.y));
-        const float p2 = ex2_approx(fmaf(__uint_as_float(s[i + 2]), factor, d.z));
-        const float p3 = ex2_approx(fmaf(__uint_as_float(s[i + 3]), factor, d.w));
+        const float4 a = lds_f32x4(slab + 4 * i), g = lds_f32x4(slab + 4 * kCols + 4 * i);
+        const float p0 = ex2_approx(fmaf(__uint_as_float(s[i]), factor2, a.x));
+        const float p1 = ex2_approx(fmaf(__uint_as_float(s[i + 1]), factor2, a.y));
+        const float p2 = ex2_approx(fmaf(__uint_as_float(s[i + 2]), factor2, a.z));
+        const float p3 = ex2_approx(fmaf(__uint_as_float(s[i + 3]), factor2, a.w));
         l[i] = fmaf(p0, g.x, l[i]);
         l[i + 1] = fmaf(p1, g.y, l[i + 1]);
         l[i + 2] = fmaf(p2, g.z, l[i + 2]);

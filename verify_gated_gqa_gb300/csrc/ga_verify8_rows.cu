@@ -292,8 +292,13 @@ __device__ void softmax_worker(Smem& sm, const Verify4Args& a, uint32_t tmem) {
         m1 = max3(m1, v(i + 2), v(i + 3));
       }
       const float top = fmaxf(max3(m0, m1, v(30)), v(31));
-      const float E = fmaxf(ceilf(top * factor), kNone);   // what the block's weights are scaled by
-      if (meet_any(E > R + kMove)) {
+      float E = fmaxf(ceilf(top * factor), kNone), d = kTop - E;   // what the block's weights are scaled by
+      if (is_far(E)) {
+        far_exponent(E, d, top, factor);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(v(i) - far_base(top));
+      }
+      if (meet_any(E - R > kMove)) {
         // R moves, for the rows of these warps (a segment's first tile: from nothing)
         sm.exchange[block][r] = E;
         meet();
@@ -321,7 +326,7 @@ __device__ void softmax_worker(Smem& sm, const Verify4Args& a, uint32_t tmem) {
         }
         meet();   // the exchange is read
       }
-      const float x = E - kTop - R, d = kTop - E;
+      const float x = E - R - kTop;   // (E - R is exact where it matters, E - kTop is not for every E)
       float l0 = 0.f, l1 = 0.f;
       uint32_t hi[8], lo[8];
 #pragma unroll
