@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   int tiles = 0;
   if (tid < a.n_seq) {
     bool refused;
-    tiles = seq_tiles<kTile>(a, ld_len(a.seq_len + tid), refused);
+    tiles = seq_tiles<kTile>(a, ld_ahead(a.seq_len + tid), refused);
   }
   if (tid == 0) cut_n = 0;
   const Units q = scan_units<kTile, kQ8>(tiles, warp_units, warp_streams);
@@ -648,9 +648,9 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   auto gates_of = [&](int item) {
     const int p = 4 * dims_of(item);
     const uint16_t* at = a.qg + row_of(item) * kQgStride + kDim;
-    if (kTile == kTileN) return ld_input(reinterpret_cast<const uint2*>(at + p));
+    if (kTile == kTileN) return ld_ahead(reinterpret_cast<const uint2*>(at + p));
     at += 32 * (p & 7) + (p >> 3);
-    return make_uint2(ld_input(at) | ld_input(at + 32) << 16, ld_input(at + 64) | ld_input(at + 96) << 16);
+    return make_uint2(ld_ahead(at) | ld_ahead(at + 32) << 16, ld_ahead(at + 64) | ld_ahead(at + 96) << 16);
   };
   const int item0 = lo + tid - group * count;
   const bool merges = n > 1 && count > 0;
