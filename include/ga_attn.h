@@ -798,7 +798,7 @@ size_t ga_page_compact_workspace_bytes(int n_free);
  *           concurrent call
  * Pages that are not on the stack are in use, whether or not a row holds them.
  * Rules: 0 <= n_seq <= GA_PLAN_MAX_SEQ, max_pages >= 1, n_seq * max_pages < 2^30, 0 <= n_free <
- * 2^30, max_moves >= 0.
+ * 2^30, 0 <= max_moves < 2^30.
  * Errors: NULL, SHAPE, RANGE, ALIGN, WORKSPACE, DEVICE, CUDA. */
 int ga_page_compact(int n_seq, const int* page_table, int* page_table_out, int max_pages,
                     const int* held, const int* free_pages, int* free_pages_out, int n_free,

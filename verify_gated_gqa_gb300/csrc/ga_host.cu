@@ -1640,6 +1640,7 @@ int ga_page_compact(int n_seq, const int* page_table, int* page_table_out, int m
                         shared, shared_out, move_src, move_dst, info});
   if (st != GA_OK) return st;
   if (max_moves < 0) return GA_ERR_SHAPE;
+  if (max_moves >= (1 << 30)) return GA_ERR_RANGE;
   if (ws_bytes < ga_page_compact_workspace_bytes(n_free) ||
       (n_free > 0 && (!workspace || !aligned(workspace, 16))))
     return GA_ERR_WORKSPACE;

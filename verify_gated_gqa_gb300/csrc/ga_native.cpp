@@ -397,7 +397,7 @@ PyObject* page_compact(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   const Call c(tensor(a[0], "page_table"), "page_table");
   const PageState s(c, a[0], a[1], a[2], a[3], a[4]);
   const int64_t m = to_int(a[5], "max_moves");
-  if (m < 0) value_error("max_moves must not be negative");
+  if (m < 0 || m >= 1 << 30) value_error("max_moves must be 0 .. 2^30 - 1");
   const Tensor src = c.output(a[9], "move_src", kI32, {m}), dst = c.output(a[10], "move_dst", kI32, {m}),
                info = c.output(a[11], "info", kI32, {4});
   const Tensor ws = c.output(a[12], "workspace", kU8,
