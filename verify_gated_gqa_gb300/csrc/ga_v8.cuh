@@ -248,6 +248,12 @@ __device__ __forceinline__ void split_weights(uint32_t& hi, uint32_t& lo, float 
       : "=&r"(hi), "=r"(lo)
       : "f"(p0), "f"(p1), "f"(p2), "f"(p3));
 }
+// The scale byte of a block's weights, 2^x of what O is relative to, for values of exponent v_exp: 0 (2^-127)
+// from there down. (x is about kNone for a block that the row does not see: more than an int holds.)
+__host__ __device__ __forceinline__ uint32_t scale_byte(float x, int v_exp) {
+  const int e = (int)fmaxf(x, -512.f) + v_exp + kSfBias;
+  return e > 0 ? (uint32_t)e : 0u;
+}
 __device__ __forceinline__ float lds_f32(uint32_t addr) { return __uint_as_float(lds_u32(addr)); }
 __device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");

@@ -339,7 +339,7 @@ __device__ void softmax_worker(const Cta<kGroups>& c) {
       if (lane < kCols) {
         const int col = col0 + lane;
         asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf0 + 512 * buf + (col & 31) * 16 + (col >> 5) * 4),
-                     "r"(max(0, (int)x + v_exp + kSfBias))
+                     "r"(scale_byte(x, v_exp))
                      : "memory");
         sts_f32(slab + 4 * lane, d);
         sts_f32(slab + 4 * kCols + 4 * lane, ex2_approx(x));

@@ -343,7 +343,7 @@ __device__ void softmax_worker(Smem& sm, const Verify4Args& a, uint32_t tmem) {
       tc_fence_after();
       tmem_st8(w_at, hi);
       tmem_st8(w_at + 32, lo);
-      asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf_at), "r"(max(0, (int)x + v_exp + kSfBias)) : "memory");
+      asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf_at), "r"(scale_byte(x, v_exp)) : "memory");
       tmem_wait_st();
       tc_fence_before();
       fence_async_smem();
