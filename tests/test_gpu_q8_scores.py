@@ -62,12 +62,12 @@ def scored_case(g, n, length, rows, power, sign, top):
     return pools, table, q, qg, slots
 
 
-def check_top_values(out, pools, qg, slots, top, rows):
+def check_top_values(out, pools, qg, slots, top, rows, only=None):
     """The mean of the top keys' values, times the gate. Equal scores have equal weights, each off by
     2^-9 at most (`mass` is the mean of their values' magnitudes), and no other key has any."""
     n = len(top)
     out, gate = np64(out).reshape(n, rows, 24, 256), 1 / (1 + np.exp(-np64(qg)[..., 256:]))
-    for b in range(n):
+    for b in only or range(n):
         kw, vw = (np64(x) for x in B.ga_kv_dequantize_q8(*pools, slots=slots[b][top[b]]))
         assert (kw == kw[:1]).all()
         for kv in range(2):
@@ -110,3 +110,17 @@ def test_a_sequence_of_one_key(power):
     for sign in (1, -1):
         pools, table, q, qg, slots = scored_case(g, 9, 0, 1, power, sign, top)
         check_top_values(B.ga_attn_verify_q8(q, qg, *pools, table, _i32([0] * 9)), pools, qg, slots, top, 1)
+
+
+@pytest.mark.parametrize("power", [12, 21, 23, 25, 27, 29])
+@pytest.mark.parametrize("rows", [1, 4, 5, 16])
+def test_far_scores_in_long_streams(rows, power):
+    """Streams cut into parts, whose references are far apart, and whole ones, whose reference moves when
+    the largest score comes by: at the stream's beginning, inside, and in its last whole block."""
+    g = _gen(7000 + 100 * rows + power)
+    for n, length in ((3, 9000), (160, 1250)):
+        top = torch.tensor([[0], [length // 2], [length - 1]], device="cuda").repeat(-(-n // 3), 1)[:n]
+        for sign in (1, -1) if power < 28 else (1,):
+            pools, table, q, qg, slots = scored_case(g, n, length, rows, power, sign, top)
+            out = B.ga_attn_verify_q8(q, qg, *pools, table, _i32([length] * n))
+            check_top_values(out, pools, qg, slots, top, rows, None if n == 3 else (0, 1, 2, 76, 77, 78, 157, 158, 159))
