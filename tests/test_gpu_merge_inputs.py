@@ -1,6 +1,6 @@
 """Calls queued one behind the other over one buffer of fused query and gate rows that is written
-anew before each: the merge of streams that were cut into parts reads its gates ahead of the parts, and
-has to see the ones of its own call."""
+anew before each: the merge of streams that were cut into parts is launched ahead of the parts, and has
+to see the gates of its own call."""
 import numpy as np
 import pytest
 import torch

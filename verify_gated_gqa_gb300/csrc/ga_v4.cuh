@@ -75,21 +75,11 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
       : "memory");
 }
-// The merge reads the lengths and its first gates before its wait (the attention kernel waited for their
-// writers before it let the merge begin): from L2, where they are current. L1 may hold a line from before.
-__device__ __forceinline__ int ld_ahead(const int* p) {
+// The merge reads the lengths before its wait (the attention kernel waited for their writer before it
+// let the merge begin): from L2, where they are current.
+__device__ __forceinline__ int ld_len(const int* p) {
   int v;
   asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 ld_ahead(const uint2* p) {
-  uint2 v;
-  asm volatile("ld.relaxed.gpu.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_ahead(const uint16_t* p) {
-  uint32_t v;
-  asm volatile("ld.relaxed.gpu.global.u16 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
 __device__ __forceinline__ float sigmoid_f(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
@@ -211,7 +201,7 @@ __device__ __forceinline__ void make_cut(const Verify4Args& a, V4Cut& c, int wor
   const int b = threadIdx.x;
   int tiles = 0;
   if (b < kV4MaxSeq && b < a.n_seq) {
-    const int L = ld_ahead(a.seq_len + b);
+    const int L = ld_len(a.seq_len + b);
     bool refused;
     tiles = seq_tiles<kTile>(a, L, refused);
     if (refused && blockIdx.x == 0) record(a.status, kDevBadPosition);

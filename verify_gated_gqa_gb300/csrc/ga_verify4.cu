@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   int tiles = 0;
   if (tid < a.n_seq) {
     bool refused;
-    tiles = seq_tiles<kTile>(a, ld_ahead(a.seq_len + tid), refused);
+    tiles = seq_tiles<kTile>(a, ld_len(a.seq_len + tid), refused);
   }
   if (tid == 0) cut_n = 0;
   const Units q = scan_units<kTile, kQ8>(tiles, warp_units, warp_streams);
@@ -639,7 +639,9 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   const int groups = max(1, min((n + 7) / 8, kCombineThreads / max(count, 1)));
   const int group = groups > 1 ? tid / count : 0;   // (from `groups` on: idle)
   // an item's row among the call's, and its four gates (place p + k of 32-key tiles' parts is dim
-  // 32 (p % 8 + k) + p / 8); the first item's are loaded before the wait, which is for the parts alone
+  // 32 (p % 8 + k) + p / 8). Behind the wait: ahead of it they would have to come from L2, which won 0.1 us
+  // over the 8-bit cache (32 x 4 rows of up to 4,096 keys 28.1 for 28.2) and cost 1.0 over the 4-bit one, whose
+  // two-byte loads live on L1 (64 ragged decoding 55.1 for 54.0).
   auto dims_of = [&](int item) { return kByRow ? item % (kDim / 4) : item / rows; };
   auto row_of = [&](int item) {
     const int r = kByRow ? item / (kDim / 4) : item % rows, rr = r / heads;
@@ -648,16 +650,16 @@ __global__ void __launch_bounds__(kCombineThreads) verify4_combine_kernel(
   auto gates_of = [&](int item) {
     const int p = 4 * dims_of(item);
     const uint16_t* at = a.qg + row_of(item) * kQgStride + kDim;
-    if (kTile == kTileN) return ld_ahead(reinterpret_cast<const uint2*>(at + p));
+    if (kTile == kTileN) return ld_input(reinterpret_cast<const uint2*>(at + p));
     at += 32 * (p & 7) + (p >> 3);
-    return make_uint2(ld_ahead(at) | ld_ahead(at + 32) << 16, ld_ahead(at + 64) | ld_ahead(at + 96) << 16);
+    return make_uint2(ld_input(at) | ld_input(at + 32) << 16, ld_input(at + 64) | ld_input(at + 96) << 16);
   };
   const int item0 = lo + tid - group * count;
   const bool merges = n > 1 && count > 0;
   uint2 g = make_uint2(0u, 0u);
-  if (merges && group == 0 && item0 < hi) g = gates_of(item0);
   grid_wait();
   if (!merges) return;   // (one CTA ran the whole stream and wrote it)
+  if (group == 0 && item0 < hi) g = gates_of(item0);
   for (int item = item0; item < hi; item += kCombineThreads) {
     const int d4 = dims_of(item), r = kByRow ? item / (kDim / 4) : item - d4 * rows;
     float M = -INFINITY, L = 0.f;
