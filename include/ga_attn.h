@@ -707,11 +707,11 @@ size_t ga_verify_q8_workspace_bytes(void);
  * tokens). Hidden positions need no initial contents: whatever their codes and scales, NaN codes
  * included, they do not reach a result. Queries and softmax weights meet the codes as sums of two
  * 8-bit parts: a query is within 2^-17 of its row's largest magnitude, a weight within 2^-9 of
- * itself or 2^-22 of the largest of its block of 32 keys (2^-15 where the scores pass 2^20); sums,
- * maxima and O are fp32, and the output is rounded once. Scores are fp32 too: those past 2^20 are
- * known to the nearest eighth or worse, and their weights to match, but up to 2^29 a row's weights
- * are the same in its sum as in its output. A NaN query (or one whose scores are infinite, or pass
- * 2^29 in magnitude) makes its own head's row meaningless, and no other.
+ * itself or 2^-22 of the largest of its block of 32 keys (2^-15 where the scores pass 2^23); sums,
+ * maxima and O are fp32, and the output is rounded once. Scores are fp32 too: large ones are known to
+ * a few of their last steps (an eighth at 2^20), and their weights to match, but up to 2^29 a row's
+ * weights are the same in its sum as in its output. A NaN query (or one whose scores are infinite, or
+ * pass 2^29 in magnitude) makes its own head's row meaningless, and no other.
  * A page-table entry outside the pool records status 3 and its keys are read as zeros.
  * Errors: NULL, SHAPE, RANGE, ALIGN, WORKSPACE, DEVICE, CUDA. */
 int ga_attn_verify_q8(const ga_bf16* q_prep, const ga_bf16* qg, const uint8_t* k_codes,

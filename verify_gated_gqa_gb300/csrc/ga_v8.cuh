@@ -10,7 +10,7 @@ constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kBoxBytes = kQ8Block * 128;              // 32 keys x 128 dims
 constexpr int kSmemLimit = 232448;
 constexpr float kLog2eOver16 = 1.4426950408889634f / 16.0f;
-constexpr float kTop = 8.0f;          // a block's largest weight becomes at most 2^8 (far_exponent)
+constexpr float kTop = 8.0f;          // a block's largest weight becomes at most 2^8 (block_exponent)
 constexpr float kMove = 64.0f;        // R moves when a block passes it by more than 2^64
 constexpr float kNone = -1e30f;       // the exponent of a block without a visible key
 constexpr int kSfBias = 127;          // of a scale factor's 8 exponent bits
@@ -207,28 +207,26 @@ __device__ __forceinline__ void hide_values(uint8_t* tile, int keys, int steps) 
 }
 
 // ------------------------------------------------------------------ numerics
-// A block's weights are 2^(t - E + 8) with t = s factor, the scores as exponents, and E = ceil of the largest t.
-// The product in fma(s, factor, 8 - E) is exact, E is of the rounded one; up to 2^21 they differ by 1/16 at
-// most. The largest weight is then 267 at most, which two parts hold (256 + 14: the second part of 256 to
-// 512 saturates from a remainder of 14 on). Past 2^21 E is made no less than t, and the weights are formed
-// from the differences to the block's largest score, 2^((s - top) factor + c + 8) with c = t - E, since 8 - E
-// would be rounded from 2^24 on. E is a multiple of its own step, 8 below 2^27: c is down to -8, the largest
-// weight from 1 to 256. From there on E stands for t with the rounding that fp32 gives t, and c stays at -8.
-// Rare, so the first loop over the weights pays one comparison for it.
-constexpr float kFar = 2097152.0f;   // 2^21
-__device__ __forceinline__ bool is_far(float E) { return fabsf(E) > kFar && E > kNone; }
-// What is taken off the scores of a block whose largest is `top` (-inf: no visible key).
-__device__ __forceinline__ float far_base(float top) { return top == -INFINITY ? 0.f : top; }
-// E, and d, what is added to the differences' products. (A row or column that is not far may go through it
-// beside others.)
-__device__ __forceinline__ void far_exponent(float& E, float& d, float top, float factor) {
-  const float base = far_base(top);
-  float c = fmaf(base, factor, -E);
-  if (c > 0.f && is_far(E)) {   // to the next integer, or the next value
+// A block's weights are 2^(t - E + 8), t = s factor (the scores as exponents), E about the largest t; they are
+// formed as 2^fma(s, factor, a), whose product is exact. Two parts hold a weight up to 2^8 and little more
+// (from a remainder of 14 on, at 270, the second part saturates, and the sum would not see it), so E has to be
+// an integer no less than t itself. The ceil of the rounded product may be less: E is moved up then. Past
+// 2^23 E is a multiple of its own step, so below 2^27, where that is at most 8, a = 8 - E is exact, and the
+// largest weight is between 1 (2^7 below 2^24) and 2^8. From kFar on neither holds, and scores that differ at
+// all are half that step apart: E is t rounded down, and the caller sees to it that the largest score has the
+// weight 2^8.
+constexpr float kFar = 134217728.0f;   // 2^27
+__device__ __forceinline__ float block_exponent(float top, float factor) {
+  float E = fmaxf(ceilf(top * factor), kNone);
+  if (fmaf(top, factor, -E) > 0.f)   // to the next integer, or the next value (E = 0: NaN, which is passed over)
     E = fmaxf(E + 1.f, __int_as_float(__float_as_int(E) + (E > 0.f ? 1 : -1)));
-    c = fmaf(base, factor, -E);
-  }
-  d = kTop + fmaxf(c, -8.f);
+  if (fabsf(E) >= kFar) E = fmaxf(__fmul_rd(top, factor), kNone);
+  return E;
+}
+__device__ __forceinline__ float min_or_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 // Four weights as two e4m3 parts: hi, to nearest, and lo = 32 (p - hi), which is exact before it is
