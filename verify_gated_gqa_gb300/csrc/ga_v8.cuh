@@ -10,7 +10,7 @@ constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kBoxBytes = kQ8Block * 128;              // 32 keys x 128 dims
 constexpr int kSmemLimit = 232448;
 constexpr float kLog2eOver16 = 1.4426950408889634f / 16.0f;
-constexpr float kTop = 8.0f;          // a block's largest weight becomes at most 2^8 (block_exponent)
+constexpr float kTop = 8.0f;          // a block's largest weight becomes at most 2^8 (large_exponent)
 constexpr float kMove = 64.0f;        // R moves when a block passes it by more than 2^64
 constexpr float kNone = -1e30f;       // the exponent of a block without a visible key
 constexpr int kSfBias = 127;          // of a scale factor's 8 exponent bits
@@ -209,19 +209,22 @@ __device__ __forceinline__ void hide_values(uint8_t* tile, int keys, int steps) 
 // ------------------------------------------------------------------ numerics
 // A block's weights are 2^(t - E + 8), t = s factor (the scores as exponents), E about the largest t; they are
 // formed as 2^fma(s, factor, a), whose product is exact. Two parts hold a weight up to 2^8 and little more
-// (from a remainder of 14 on, at 270, the second part saturates, and the sum would not see it), so E has to be
-// an integer no less than t itself. The ceil of the rounded product may be less: E is moved up then. Past
-// 2^23 E is a multiple of its own step, so below 2^27, where that is at most 8, a = 8 - E is exact, and the
+// (from a remainder of 14 on, at 270, the second part saturates, and the sum would not see it). E is ceil of
+// the rounded product, which up to 2^20 is less than t by 1/32 at most: 262. Past it E is moved up where it is
+// less. It is a multiple of its own step, so below 2^27, where that is at most 8, a = 8 - E is exact, and the
 // largest weight is between 1 (2^7 below 2^24) and 2^8. From kFar on neither holds, and scores that differ at
 // all are half that step apart: E is t rounded down, and the caller sees to it that the largest score has the
 // weight 2^8.
-constexpr float kFar = 134217728.0f;   // 2^27
-__device__ __forceinline__ float block_exponent(float top, float factor) {
-  float E = fmaxf(ceilf(top * factor), kNone);
+// first_exponent is what serves up to 2^20 (is_large: past it), large_exponent what serves at any magnitude.
+constexpr float kLarge = 1048576.0f, kFar = 134217728.0f;   // 2^20, 2^27
+__device__ __forceinline__ float first_exponent(float top, float factor) {
+  return fmaxf(ceilf(top * factor), kNone);
+}
+__device__ __forceinline__ bool is_large(float E) { return fabsf(E) > kLarge && E > kNone; }
+__device__ __forceinline__ float large_exponent(float E, float top, float factor) {
   if (fmaf(top, factor, -E) > 0.f)   // to the next integer, or the next value (E = 0: NaN, which is passed over)
     E = fmaxf(E + 1.f, __int_as_float(__float_as_int(E) + (E > 0.f ? 1 : -1)));
-  if (fabsf(E) >= kFar) E = fmaxf(__fmul_rd(top, factor), kNone);
-  return E;
+  return fabsf(E) >= kFar ? fmaxf(__fmul_rd(top, factor), kNone) : E;
 }
 __device__ __forceinline__ float min_or_nan(float a, float b) {
   float r;
@@ -230,7 +233,10 @@ __device__ __forceinline__ float min_or_nan(float a, float b) {
 }
 
 // Four weights as two e4m3 parts: hi, to nearest, and lo = 32 (p - hi), which is exact before it is
-// rounded.
+// rounded. 9 bits, so that the codes of V meet them in 8-bit MMAs, two for each product; one part alone would
+// keep 4; bf16 weights, which V would have to be widened for, keep 8. The sums take p itself: rounded
+// weights would cost a conversion each, and be nearer only where one key has nearly all the weight, by 2^-9
+// of the output at most.
 __device__ __forceinline__ void split_weights(uint32_t& hi, uint32_t& lo, float p0, float p1, float p2, float p3) {
   asm("{\n\t.reg .b16 a, b, x, y, m;\n\t.reg .b32 h, g;\n\t.reg .f32 r0, r1, r2, r3;\n\t"
       "cvt.rn.satfinite.e4m3x2.f32 a, %3, %2;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %5, %4;\n\t"

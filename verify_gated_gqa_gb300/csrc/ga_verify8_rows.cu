@@ -292,12 +292,15 @@ __device__ void softmax_worker(Smem& sm, const Verify4Args& a, uint32_t tmem) {
         m1 = max3(m1, v(i + 2), v(i + 3));
       }
       const float top = fmaxf(max3(m0, m1, v(30)), v(31));
-      const float E = block_exponent(top, factor);   // what the block's weights are scaled by
-      float d = kTop - E;
-      if (fabsf(E) >= kFar && top != -INFINITY) {   // the differences to the largest score
+      float E = first_exponent(top, factor), d = kTop - E;   // what the block's weights are scaled by
+      if (is_large(E)) {
+        E = large_exponent(E, top, factor);
+        d = kTop - E;
+        if (fabsf(E) >= kFar) {   // the differences to the largest score
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(v(i) - top);
-        d = kTop;
+          for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(v(i) - top);
+          d = kTop;
+        }
       }
       if (meet_any(E - R > kMove)) {
         // R moves, for the rows of these warps (a segment's first tile: from nothing)
