@@ -79,9 +79,9 @@ __device__ __forceinline__ uint2 encode(const uint4& x, float inv) {
 // take each head, 8 values a lane. The rows are on their way before the slots are known. A chunk's stay
 // in registers from the search for the maxima to their codes; those of a run that goes on past the
 // chunk (31 at most) are read again. Bound by the bytes it moves (131,072 tokens 74 us, 5.4 TB/s) and by
-// instruction issue: with a test for NaN and a division by the page size at every use it was at 70 % of
-// the issue slots and took 93 us. Four CTAs an SM keep everything in registers; five spill and take as
-// long.
+// how much of the waiting for them its warps cover: 29 of 64 an SM, 61 % of the issue slots used (40,001
+// tokens). With a test for NaN and a division by the page size at every use 131,072 tokens took 93 us. Four
+// CTAs an SM keep everything in registers; five spill and take as long.
 __global__ void __launch_bounds__(kThreads, 4) quantize_kernel(const __grid_constant__ Kv8Args a) {
   __shared__ uint32_t top[kKvHeads][kChunk], written[kChunk];
   __shared__ int exps[kKvHeads][kChunk], shift[kKvHeads][kChunk], first[kChunk];
